@@ -18,11 +18,13 @@ LIB_PATH = os.path.join(_HERE, "libeaglespec_timeline.so" if os.environ.get("EAG
 
 c_i32 = ctypes.c_int32
 c_u64 = ctypes.c_uint64
+c_i64 = ctypes.c_int64
 c_vp = ctypes.c_void_p
 c_size = ctypes.c_size_t
 
 DTYPE_F32 = 0
 DTYPE_BF16 = 1
+DTYPES = {"f32": 0, "bf16": 1, "f16": 2, "e4m3": 3}     # names as in configs.Workload.dtype
 
 
 class SpecError(RuntimeError):
@@ -64,6 +66,18 @@ class TreeIO(ctypes.Structure):
                                      "tree_score", "tree_mask"]]
 
 
+class AttnDesc(ctypes.Structure):
+    _fields_ = [("n_q_heads", c_i32), ("n_kv_heads", c_i32), ("head_dim", c_i32), ("dtype", c_i32),
+                ("kv_dtype", c_i32), ("window", c_i32), ("scale", ctypes.c_float), ("k_scale", ctypes.c_float),
+                ("v_scale", ctypes.c_float)]
+
+
+class BeamState(ctypes.Structure):
+    _fields_ = ([(n, c_i32) for n in ["B", "W", "block_size", "max_blocks", "owned_ld", "hist_ld"]]
+                + [(n, c_vp) for n in ["parent", "tok", "seq_len", "prompt_blocks", "owned", "table_in", "table_out",
+                                       "spare_in", "spare_out", "slots", "hist_in", "hist_out"]])
+
+
 EXPORTS = {
     # name: (restype, argtypes)
     "spec_status_string": (ctypes.c_char_p, [c_i32]),
@@ -96,6 +110,18 @@ EXPORTS = {
     "spec_verify_greedy_static_capacity": (c_size, []),
     "spec_verify_greedy_static_bytes": (c_size, [c_i32, c_i32, c_i32]),
     "spec_verify_greedy_static_error": (c_i32, [ctypes.POINTER(c_i32), c_vp]),
+    "spec_block_tables_workspace_bytes": (c_size, [c_i32]),
+    "spec_block_tables": (c_i32, [c_i32, c_i32, c_i32, c_i32, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp,
+                                  c_vp, c_vp, c_vp, c_i32, c_vp, c_size, c_vp]),
+    "spec_cache_append": (c_i32, [ctypes.POINTER(AttnDesc), c_vp, c_vp, c_i64, c_vp, c_i32, ctypes.POINTER(KV), c_vp,
+                                  c_vp]),
+    "spec_attention_workspace_bytes": (c_size, [ctypes.POINTER(AttnDesc), c_i32]),
+    "spec_paged_attention": (c_i32, [ctypes.POINTER(AttnDesc), c_vp, c_i64, ctypes.POINTER(KV), c_vp, c_i32, c_i32,
+                                     c_vp, c_i64, c_vp, c_vp, c_size, c_vp]),
+    "spec_beam_workspace_bytes": (c_size, [c_i32, c_i32, c_i32]),
+    "spec_beam_select": (c_i32, [c_i32, c_i32, c_i32, c_i32, c_vp, c_i64, c_vp, c_vp, c_i32, c_vp, c_vp, c_vp, c_vp,
+                                 c_vp, c_size, c_vp]),
+    "spec_beam_reorder": (c_i32, [ctypes.POINTER(BeamState), c_i32, ctypes.POINTER(KV), c_i32, c_vp, c_vp]),
 }
 
 _LIB = None
@@ -174,6 +200,30 @@ def make_tree_io(frontier_tok, frontier_pos, frontier_kv_idx, frontier_mask, fro
     io = TreeIO(*[_p(t) for t in ts])
     io._keep = ts
     return io
+
+
+def make_attn_desc(n_q_heads, n_kv_heads, head_dim, dtype, kv_dtype=None, window=0, scale=0.0, k_scale=1.0,
+                   v_scale=1.0) -> AttnDesc:
+    """AttnDesc of the cache's append and attention; types by name (DTYPES)."""
+    return AttnDesc(n_q_heads, n_kv_heads, head_dim, DTYPES[dtype], DTYPES[kv_dtype or dtype], window, scale, k_scale,
+                    v_scale)
+
+
+def make_kv_layers(kvs) -> ctypes.Array:
+    """Array of KV structs, one per layer, from the dicts make_kv takes."""
+    items = [make_kv(kv) for kv in kvs]
+    a = (KV * len(items))(*items)
+    a._keep = [k._keep for k in items]
+    return a
+
+
+def make_beam_state(B, W, block_size, max_blocks, parent, tok, seq_len, prompt_blocks, owned, table_in, table_out,
+                    spare_in, spare_out, slots, hist_in=None, hist_out=None) -> BeamState:
+    ts = (parent, tok, seq_len, prompt_blocks, owned, table_in, table_out, spare_in, spare_out, slots, hist_in, hist_out)
+    st = BeamState(B, W, block_size, max_blocks, owned.shape[-1],
+                   hist_in.shape[-1] if hist_in is not None else 0, *[_p(t) for t in ts])
+    st._keep = ts
+    return st
 
 
 # ------------------------------------------------------------------ entry points
@@ -286,3 +336,45 @@ def spec_prefill_inputs(B, R, input_ids, next_token, last_idx, ctx_len, tok, pos
 def spec_gather_rows(src, n_src, row_bytes, rows, n, dst, ws=None):
     _check(_lib().spec_gather_rows(_p(src), n_src, row_bytes, _p(rows), n, _p(dst), _p(ws), _stream()),
            "spec_gather_rows")
+
+
+def spec_block_tables_workspace_bytes(B):
+    return _lib().spec_block_tables_workspace_bytes(B)
+
+
+def spec_block_tables(B, block_size, max_blocks, num_blocks, len_old, len_new, table_in, table_out, free_in, n_free_in,
+                      free_out, n_free_out, len_out, cu_new, slots, pos, slots_cap, ws):
+    _check(_lib().spec_block_tables(B, block_size, max_blocks, num_blocks, _p(len_old), _p(len_new), _p(table_in),
+                                    _p(table_out), _p(free_in), _p(n_free_in), _p(free_out), _p(n_free_out),
+                                    _p(len_out), _p(cu_new), _p(slots), _p(pos), slots_cap, _p(ws),
+                                    ws.numel() * ws.element_size(), _stream()), "spec_block_tables")
+
+
+def spec_cache_append(desc, k, v, ld, slots, n, kv, ws=None):
+    _check(_lib().spec_cache_append(ctypes.byref(desc), _p(k), _p(v), ld, _p(slots), n, ctypes.byref(kv), _p(ws),
+                                    _stream()), "spec_cache_append")
+
+
+def spec_attention_workspace_bytes(desc, max_B):
+    return _lib().spec_attention_workspace_bytes(ctypes.byref(desc), max_B)
+
+
+def spec_paged_attention(desc, q, kv, seq_len, B, out, lse, ws, max_len=0, q_ld=0, out_ld=0):
+    _check(_lib().spec_paged_attention(ctypes.byref(desc), _p(q), q_ld, ctypes.byref(kv), _p(seq_len), B, max_len,
+                                       _p(out), out_ld, _p(lse), _p(ws), ws.numel() * ws.element_size(), _stream()),
+           "spec_paged_attention")
+
+
+def spec_beam_workspace_bytes(B, W, V):
+    return _lib().spec_beam_workspace_bytes(B, W, V)
+
+
+def spec_beam_select(B, W, V, dtype, logits, score, done, eos, parent, tok, score_out, done_out, ws, ld=0):
+    _check(_lib().spec_beam_select(B, W, V, DTYPES[dtype], _p(logits), ld, _p(score), _p(done), eos, _p(parent), _p(tok),
+                                   _p(score_out), _p(done_out), _p(ws), ws.numel() * ws.element_size(), _stream()),
+           "spec_beam_select")
+
+
+def spec_beam_reorder(state, kv_layers, row_bytes, ws=None):
+    _check(_lib().spec_beam_reorder(ctypes.byref(state), len(kv_layers), kv_layers, row_bytes, _p(ws), _stream()),
+           "spec_beam_reorder")

@@ -1,0 +1,391 @@
+// Block tables and slot maps from request lengths, and the K/V append that the
+// slots are for.
+//
+// [NEURON] "KV Cache Sharing" and "EagleProposer": a paged cache addressed by
+// block tables, slot_mapping built from them for the tokens of a step.
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include <algorithm>
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace spec {
+
+enum : unsigned { kTLTables = 24, kTLAppend = 25 };   // after common.cuh's ids
+
+// ---------------------------------------------------------------- block tables
+constexpr int kTabThreads = 512;
+constexpr int kTabMaxB = 8192;
+
+struct TabArgs {
+  int B, bs, mb, num_blocks, cap;
+  const int32_t *len_old, *len_new, *table_in, *free_in, *n_free_in;
+  int32_t *table_out, *free_out, *n_free_out, *len_out, *cu_new, *slots, *pos;
+  void* ws;
+};
+
+// index of the first entry of the ascending a[0, n) above x (n if none)
+SPEC_DEV int first_above(const int* a, int n, int x) {
+  int lo = 0, hi = n;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (a[mid] > x) hi = mid;
+    else lo = mid + 1;
+  }
+  return lo;
+}
+
+// One launch.  Every CTA computes the prefix sums of all requests for itself (a
+// few thousand integers, read from L2), then takes its share of the pool
+// entries, table entries and tokens.  A block taken from the pool is *delivered*
+// by the thread that reads it: it finds the request that the block goes to by
+// bisection of the prefix sums and writes that table entry and the slots of the
+// block's tokens.  So every pool entry and every released table entry is read by
+// one thread only, which writes to it afterwards, and the update is safe in
+// place without a grid-wide barrier.  What all CTAs read and one of them
+// replaces (len_old, n_free_in) is written by the last CTA to have read it.
+__global__ void __launch_bounds__(kTabThreads) block_tables_kernel(const TabArgs g) {
+  SPEC_TL(kTLTables);
+  pdl_wait();
+  pdl_trigger();
+  extern __shared__ int tab_sm[];
+  const int B = g.B, bs = g.bs, mb = g.mb;
+  int* s_old = tab_sm;             // clamped lengths
+  int* s_new = s_old + B;
+  int* s_rel = s_new + B;          // inclusive prefix sums: blocks released,
+  int* s_need = s_rel + B;         // blocks asked for,
+  int* s_cnt = s_need + B;         // tokens asked for
+  __shared__ int wsum[3][kTabThreads / 32];
+  __shared__ int s_last;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const bool first_cta = blockIdx.x == 0;
+
+  int n_free = *g.n_free_in;
+  if (n_free < 0 || n_free > g.num_blocks) {
+    if (first_cta && tid == 0) report(g.ws, SPEC_ERR_DEVICE, -1, n_free);
+    n_free = n_free < 0 ? 0 : g.num_blocks;
+  }
+  int carry[3] = {0, 0, 0};
+  for (int base = 0; base < B; base += kTabThreads) {
+    const int b = base + tid;
+    int x[3] = {0, 0, 0};
+    if (b < B) {
+      int o = g.len_old[b], n = g.len_new[b];
+      const int most = mb * bs;
+      if (o < 0 || o > most || n < 0 || n > most) {
+        if (first_cta) report(g.ws, SPEC_ERR_DEVICE, b, n);
+        o = o < 0 ? 0 : (o > most ? most : o);
+        n = o;
+      }
+      s_old[b] = o;
+      s_new[b] = n;
+      const int have = (o + bs - 1) / bs, want = (n + bs - 1) / bs;
+      x[0] = max(have - want, 0);
+      x[1] = max(want - have, 0);
+      x[2] = max(n - o, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x[i], o);
+        if (lane >= o) x[i] += y;
+      }
+      if (lane == 31) wsum[i][warp] = x[i];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      const int w = lane < kTabThreads / 32 ? wsum[i][lane] : 0;
+      const int before = __reduce_add_sync(0xffffffffu, lane < warp ? w : 0);
+      const int all = __reduce_add_sync(0xffffffffu, w);
+      x[i] += carry[i] + before;
+      carry[i] += all;
+    }
+    if (b < B) {
+      s_rel[b] = x[0];
+      s_need[b] = x[1];
+      s_cnt[b] = x[2];
+    }
+    __syncthreads();
+  }
+  const int avail = n_free + carry[0], total = carry[2];
+  // requests are served while their needs fit; the needs' prefix sums ascend, so the
+  // served ones (and those that need nothing) are the requests before `cut`
+  const int cut = carry[1] <= avail ? B : first_above(s_need, B, avail);
+  const int taken = cut > 0 ? s_need[cut - 1] : 0;
+  const int left = avail - taken;
+  auto have_of = [&](int b) { return (s_old[b] + bs - 1) / bs; };
+  auto is_served = [&](int b) { return b < cut || (b > 0 && s_need[b] == s_need[b - 1]); };
+  auto want_of = [&](int b) { return is_served(b) ? (s_new[b] + bs - 1) / bs : have_of(b); };
+
+  if (tid == 0) {
+    if (gridDim.x == 1) {
+      s_last = 1;
+    } else {
+      int* ctr = reinterpret_cast<int*>(static_cast<char*>(g.ws) + kWsHeader);
+      __threadfence();
+      s_last = atomicAdd(ctr, 1) == (int)gridDim.x - 1;
+      if (s_last) *ctr = 0;
+    }
+  }
+  __syncthreads();
+  if (s_last) {
+    if (tid == 0) {
+      *g.n_free_out = min(left, g.num_blocks);
+      if (carry[1] > avail || total > g.cap) report(g.ws, SPEC_ERR_CAPACITY, carry[1], avail);
+      if (left > g.num_blocks) report(g.ws, SPEC_ERR_DEVICE, left, g.num_blocks);
+      g.cu_new[0] = 0;
+    }
+    for (int b = tid; b < B; b += kTabThreads) {
+      g.cu_new[b + 1] = s_cnt[b];
+      g.len_out[b] = is_served(b) ? s_new[b] : s_old[b];
+    }
+  }
+
+  const int gt = blockIdx.x * kTabThreads + tid, gn = gridDim.x * kTabThreads;
+  const bool out_of_place = g.table_out != g.table_in, pool_moves = g.free_out != g.free_in;
+  // the j-th id of the pool with the released blocks on top
+  auto pool_id = [&](int j) {
+    int id;
+    if (j < n_free) {
+      id = g.free_in[j];
+    } else {
+      const int r = j - n_free, b = first_above(s_rel, B, r);
+      const int start = b > 0 ? s_rel[b - 1] : 0;
+      const long long e = (long long)b * mb + (s_new[b] + bs - 1) / bs + (r - start);
+      id = g.table_in[e];
+      if (!out_of_place) g.table_out[e] = -1;
+    }
+    if ((unsigned)id >= (unsigned)g.num_blocks) {
+      report(g.ws, SPEC_ERR_DEVICE, j, id);
+      id = -1;
+    }
+    return id;
+  };
+  // what stays in the pool (an entry of the free list that stays where it is is not
+  // written in place), and -1 past its end
+  for (int j = gt; j < g.num_blocks; j += gn) {
+    if (j < left) {
+      if (j >= n_free) g.free_out[j] = pool_id(j);
+      else if (pool_moves) g.free_out[j] = g.free_in[j];
+    } else if (pool_moves) {
+      g.free_out[j] = -1;
+    }
+  }
+  // deliveries: 2^lg lanes a block, so that a block's slots are written together
+  int lg = 0;
+  while (lg < 5 && (1 << lg) < bs) ++lg;
+  const int part = lane & ((1 << lg) - 1), lead = lane & ~((1 << lg) - 1);
+  for (int base = (gt & ~31) >> lg; base < taken; base += gn >> lg) {
+    const int i = base + (lane >> lg);               // the i-th block taken
+    int id = -1;
+    if (i < taken && part == 0) {
+      const int j = avail - 1 - i;
+      id = pool_id(j);
+      if (!pool_moves && j < n_free) g.free_out[j] = -1;
+    }
+    id = __shfl_sync(0xffffffffu, id, lead);
+    if (i >= taken) continue;
+    const int b = first_above(s_need, B, i);
+    const int e = have_of(b) + i - (b > 0 ? s_need[b - 1] : 0);
+    if (part == 0) g.table_out[(long long)b * mb + e] = id;
+    const int off = (b > 0 ? s_cnt[b - 1] : 0) - s_old[b];
+    const int end = min(s_new[b], (e + 1) * bs);
+    for (int t = max(s_old[b], e * bs) + part; t < end; t += 1 << lg)
+      if (off + t < g.cap) {
+        g.slots[off + t] = id < 0 ? -1 : id * bs + (t - e * bs);
+        if (g.pos) g.pos[off + t] = t;
+      }
+  }
+  // kept entries, and -1 past a request's blocks
+  if (out_of_place) {
+    const int entries = B * mb;
+    for (int k = gt; k < entries; k += gn) {
+      const int b = k / mb, i = k - b * mb, want = want_of(b);
+      if (i < min(have_of(b), want)) g.table_out[k] = g.table_in[k];
+      else if (i >= want) g.table_out[k] = -1;
+    }
+  }
+  // tokens of blocks that were there before, a warp a request; all tokens of a request
+  // that is not served
+  for (int b = gt >> 5; b < B; b += gn >> 5) {
+    const int o = s_old[b], off = (b > 0 ? s_cnt[b - 1] : 0) - o;
+    const bool ok = is_served(b);
+    const int end = ok ? min(s_new[b], have_of(b) * bs) : s_new[b];
+    if (o >= end) continue;
+    int id = -1;
+    if (ok) {
+      id = g.table_in[(long long)b * mb + o / bs];
+      if ((unsigned)id >= (unsigned)g.num_blocks) {
+        if (lane == 0) report(g.ws, SPEC_ERR_DEVICE, b, id);
+        id = -1;
+      }
+    }
+    for (int t = o + lane; t < end; t += 32)
+      if (off + t < g.cap) {
+        g.slots[off + t] = id < 0 ? -1 : id * bs + t % bs;
+        if (g.pos) g.pos[off + t] = t;
+      }
+  }
+  for (int k = total + gt; k < g.cap; k += gn) {
+    g.slots[k] = -1;
+    if (g.pos) g.pos[k] = 0;
+  }
+}
+
+// ---------------------------------------------------------------- K/V append
+template <typename T> struct alignas(sizeof(T) == 1 ? 8 : 16) Vec8 { T v[8]; };   // eight elements: 32, 16 or 8 bytes
+
+SPEC_DEV float to_f(float x) { return x; }
+SPEC_DEV float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
+SPEC_DEV float to_f(__half x) { return __half2float(x); }
+
+// value in the cache's type.  E4M3: x / scale in fp32 (the quotient, not a product
+// with the reciprocal, so that values next to a rounding border go the way the
+// definition says), then one rounding to nearest even, saturating
+template <typename T, typename C> SPEC_DEV C stored(T x, float scale) {
+  if constexpr (sizeof(C) == 1) {
+    return __nv_cvt_float_to_fp8(__fdiv_rn(to_f(x), scale), __NV_SATFINITE, __NV_E4M3);
+  } else {
+    return x;
+  }
+}
+
+// Rows to slots, bound by the bytes moved.  2^lg lanes share a row (as many as it
+// has vectors of eight elements, at most a warp), blockIdx.y picks K or V.
+template <typename T, typename C, bool VEC>
+__global__ void __launch_bounds__(256) cache_append_kernel(const T* __restrict__ k, const T* __restrict__ v,
+                                                           long long ld, const int32_t* __restrict__ slots, int n,
+                                                           C* __restrict__ ck, C* __restrict__ cv, int width,
+                                                           int num_slots, float k_scale, float v_scale, int lg,
+                                                           void* ws) {
+  SPEC_TL(kTLAppend);
+  pdl_wait();
+  pdl_trigger();
+  const T* __restrict__ src = blockIdx.y ? v : k;
+  C* __restrict__ dst = blockIdx.y ? cv : ck;
+  const float scale = blockIdx.y ? v_scale : k_scale;
+  const int per = 1 << lg, part = threadIdx.x & (per - 1);
+  const long long row = (long long)blockIdx.x * (256 >> lg) + (threadIdx.x >> lg);
+  if (row >= n) return;
+  const int slot = slots[row];
+  if (slot < 0 || slot >= num_slots) {
+    if (slot != -1 && part == 0) report(ws, SPEC_ERR_DEVICE, (int)row, slot);
+    return;
+  }
+  const T* s = src + row * ld;
+  C* d = dst + (long long)slot * width;
+  if constexpr (VEC) {
+    const int nv = width >> 3;
+#pragma unroll 4
+    for (int i = part; i < nv; i += per) {
+      const Vec8<T> x = [&] {
+        Vec8<T> y;
+        const uint4* p = reinterpret_cast<const uint4*>(s + 8 * i);
+        uint4* q = reinterpret_cast<uint4*>(&y);
+        q[0] = __ldcs(p);
+        if constexpr (sizeof(T) == 4) q[1] = __ldcs(p + 1);
+        return y;
+      }();
+      Vec8<C> o;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) o.v[j] = stored<T, C>(x.v[j], scale);
+      if constexpr (sizeof(C) == 1) {
+        *reinterpret_cast<uint2*>(d + 8 * i) = *reinterpret_cast<uint2*>(&o);
+      } else {
+        uint4* q = reinterpret_cast<uint4*>(d + 8 * i);
+        q[0] = reinterpret_cast<uint4*>(&o)[0];
+        if constexpr (sizeof(C) == 4) q[1] = reinterpret_cast<uint4*>(&o)[1];
+      }
+    }
+  } else {
+    for (int i = part; i < width; i += per) d[i] = stored<T, C>(s[i], scale);
+  }
+}
+
+template <typename T, typename C>
+static void launch_append(const spec_attn_desc& d, const void* k, const void* v, long long ld, const int32_t* slots,
+                          int n, const spec_kv& kv, void* ws, cudaStream_t st) {
+  const int width = d.n_kv_heads * d.head_dim;
+  int lg = 0;
+  while (lg < 5 && (8 << lg) < width) ++lg;
+  const bool vec = (ld * (long long)sizeof(T)) % 16 == 0 && aligned(k, 16) && aligned(v, 16) && aligned(kv.k, 16) &&
+                   aligned(kv.v, 16);
+  const int rows = 256 >> lg;
+  const dim3 grid((n + rows - 1) / rows, 2);
+  auto* kern = vec ? cache_append_kernel<T, C, true> : cache_append_kernel<T, C, false>;
+  launch_pdl(kern, grid, dim3(256), 0, st, (const T*)k, (const T*)v, ld, slots, n, (C*)kv.k, (C*)kv.v, width,
+             (int)kv.num_slots, d.k_scale, d.v_scale, lg, ws);
+}
+
+}  // namespace spec
+
+using namespace spec;
+
+extern "C" size_t spec_block_tables_workspace_bytes(int32_t B) {
+  return B <= 0 || B > kTabMaxB ? 0 : kWsHeader + 256;
+}
+
+extern "C" spec_status spec_block_tables(int32_t B, int32_t block_size, int32_t max_blocks, int32_t num_blocks,
+                                         const int32_t* len_old, const int32_t* len_new, const int32_t* table_in,
+                                         int32_t* table_out, const int32_t* free_in, const int32_t* n_free_in,
+                                         int32_t* free_out, int32_t* n_free_out, int32_t* len_out, int32_t* cu_new,
+                                         int32_t* slots, int32_t* pos, int32_t slots_cap, void* ws, size_t ws_bytes,
+                                         spec_stream_t stream) {
+  if (B <= 0 || block_size <= 0 || max_blocks <= 0 || num_blocks <= 0 || slots_cap <= 0) return SPEC_ERR_SHAPE;
+  if (!len_old || !len_new || !table_in || !table_out || !free_in || !n_free_in || !free_out || !n_free_out ||
+      !len_out || !cu_new || !slots)
+    return SPEC_ERR_ARG;
+  // token indices, slots and pool positions (free and released ids together) are 32-bit integers
+  const long long limit = 1ll << 30;
+  if (B > kTabMaxB || (long long)max_blocks * block_size >= limit ||
+      (long long)B * ((long long)max_blocks * block_size) >= limit || (long long)num_blocks * block_size >= limit)
+    return SPEC_ERR_CAPACITY;
+  if (!ws || !aligned(ws, 256) || ws_bytes < spec_block_tables_workspace_bytes(B)) return SPEC_ERR_WORKSPACE;
+  TabArgs a{B, block_size, max_blocks, num_blocks, slots_cap, len_old, len_new, table_in, free_in, n_free_in,
+            table_out, free_out, n_free_out, len_out, cu_new, slots, pos, ws};
+  // a CTA per 8192 items it may have to touch: below that a second CTA's scan costs more than its share saves
+  const long long items = (table_out != table_in ? (long long)B * max_blocks : 0) + num_blocks + slots_cap;
+  const int grid = (int)std::min<long long>(std::max<long long>(1, items / 8192), sm_count());
+  const size_t smem = (size_t)5 * B * 4;
+  if (smem > 48 * 1024 &&
+      cudaFuncSetAttribute(block_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+    return SPEC_ERR_CUDA;
+  launch_pdl(block_tables_kernel, dim3(grid), dim3(kTabThreads), smem, stream, a);
+  return last_launch();
+}
+
+extern "C" spec_status spec_cache_append(const spec_attn_desc* desc, const void* k, const void* v, int64_t ld,
+                                         const int32_t* slots, int32_t n, const spec_kv* kv, void* ws,
+                                         spec_stream_t stream) {
+  if (!desc || !k || !v || !slots || !kv || !kv->k || !kv->v) return SPEC_ERR_ARG;
+  const spec_attn_desc& d = *desc;
+  if (d.n_kv_heads <= 0 || d.head_dim <= 0 || d.head_dim % 16 || d.head_dim > 256 || n <= 0 || kv->num_slots <= 0)
+    return SPEC_ERR_SHAPE;
+  if (d.dtype < SPEC_DTYPE_F32 || d.dtype > SPEC_DTYPE_F16) return SPEC_ERR_UNSUPPORTED;
+  const bool e4m3 = d.kv_dtype == SPEC_DTYPE_E4M3 && d.dtype != SPEC_DTYPE_F32;
+  if (d.kv_dtype != d.dtype && !e4m3) return SPEC_ERR_UNSUPPORTED;
+  if (e4m3 && !(d.k_scale > 0 && d.v_scale > 0)) return SPEC_ERR_ARG;
+  const long long width = (long long)d.n_kv_heads * d.head_dim;
+  if (width >= (1ll << 30)) return SPEC_ERR_SHAPE;
+  if (ld == 0) ld = width;
+  if (ld < width) return SPEC_ERR_SHAPE;
+  const size_t es = d.dtype == SPEC_DTYPE_F32 ? 4 : 2;
+  if (!aligned(k, es) || !aligned(v, es) || (!e4m3 && (!aligned(kv->k, es) || !aligned(kv->v, es))))
+    return SPEC_ERR_ALIGN;
+  if (ws && !aligned(ws, 256)) return SPEC_ERR_WORKSPACE;
+  if (d.dtype == SPEC_DTYPE_F32) launch_append<float, float>(d, k, v, ld, slots, n, *kv, ws, stream);
+  else if (d.dtype == SPEC_DTYPE_BF16 && !e4m3)
+    launch_append<__nv_bfloat16, __nv_bfloat16>(d, k, v, ld, slots, n, *kv, ws, stream);
+  else if (d.dtype == SPEC_DTYPE_BF16)
+    launch_append<__nv_bfloat16, uint8_t>(d, k, v, ld, slots, n, *kv, ws, stream);
+  else if (!e4m3) launch_append<__half, __half>(d, k, v, ld, slots, n, *kv, ws, stream);
+  else launch_append<__half, uint8_t>(d, k, v, ld, slots, n, *kv, ws, stream);
+  return last_launch();
+}
+
+// per-unit log setter of the instrumented build (no-op otherwise)
+SPEC_TL_SETTER(tables)

@@ -22,7 +22,10 @@ NAMES = [None, "tc_kernel (GEMMs, LM head)", "attn_ws_kernel", "attn_mma_kernel"
          "cand_best_kernel", "lm_merge_kernel", "tree_expand_kernel", "verify_greedy_kernel",
          "verify_rejection_kernel", "reject_threshold_kernel", "prefill_inputs_kernel", "spec_metadata_kernel",
          "gather_rows_kernel"]
-UNITS = ("layer", "lmhead", "metadata", "prefill", "tc_gemm", "tree", "verify")
+# ids of the decoding kernels, which their own files declare
+DECODE_NAMES = {24: "block_tables_kernel", 25: "cache_append_kernel", 26: "paged_attention_kernel",
+                27: "beam_select_kernel", 28: "beam_reorder_kernel"}
+UNITS = ("beam", "layer", "lmhead", "metadata", "paged_attn", "prefill", "tables", "tc_gemm", "tree", "verify")
 SLOTS = 1 << 20
 LOG_WORDS = 8 + 4 * SLOTS
 
@@ -54,7 +57,7 @@ def launches(log):
             ends = e[blk, 2]
             out.append({"start": int(e[blk, 0].min()), "end": int(ends.max()),
                         "tail": int(ends.max() - np.median(ends)),
-                        "name": NAMES[int(k)] if int(k) < len(NAMES) else "kernel %d" % k,
+                        "name": NAMES[int(k)] if int(k) < len(NAMES) else DECODE_NAMES.get(int(k), "kernel %d" % k),
                         "blocks": len(blk), "grid": g})
             i += g
     out.sort(key=lambda x: x["start"])

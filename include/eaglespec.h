@@ -58,7 +58,9 @@ typedef enum {
   SPEC_ERR_ALIGN = -9         /* a pointer lacks the alignment the kernels need */
 } spec_status;
 
-enum { SPEC_DTYPE_F32 = 0, SPEC_DTYPE_BF16 = 1 };
+/* F16 and E4M3 (8-bit float, 4 exponent and 3 mantissa bits, no infinities) are
+ * types of the decoding calls below only; the draft step takes F32 and BF16. */
+enum { SPEC_DTYPE_F32 = 0, SPEC_DTYPE_BF16 = 1, SPEC_DTYPE_F16 = 2, SPEC_DTYPE_E4M3 = 3 };
 
 /* Shape of the single-layer EAGLE-3 draft model ([NEURON] "Eagle3 Draft Model
  * Architecture"; window, rank and num_candidates from [EAGLE4]
@@ -192,7 +194,7 @@ int spec_version(void);
 size_t spec_workspace_bytes(const spec_model_desc *desc, int32_t max_rows, int32_t max_ctx);
 
 /* Reads the device error word of a workspace (synchronises ``stream``):
- * SPEC_OK, SPEC_ERR_DEVICE or SPEC_ERR_TIMEOUT in *code_out. */
+ * SPEC_OK, SPEC_ERR_DEVICE, SPEC_ERR_TIMEOUT or SPEC_ERR_CAPACITY in *code_out. */
 spec_status spec_get_device_error(const void *ws, int32_t *code_out, spec_stream_t stream);
 /* Clears the device error word (asynchronous). */
 spec_status spec_clear_device_error(void *ws, spec_stream_t stream);
@@ -408,6 +410,176 @@ spec_status spec_prefill_inputs(int32_t B, int32_t R, const int32_t *input_ids, 
  * error word of ws (if not NULL) and leaves that row untouched. */
 spec_status spec_gather_rows(const void *src, int32_t n_src, int32_t row_bytes, const int32_t *rows,
                              int32_t n, void *dst, void *ws, spec_stream_t stream);
+
+/* ------------------------------------------------------------------ */
+/* Decoding without speculation over the paged cache: block tables, K/V */
+/* append, attention of one new token, beam search.  The sources describe */
+/* the cache and its slot mapping ([NEURON] "KV Cache Sharing",          */
+/* "EagleProposer": slot_mapping from the block table); these calls make */
+/* the tables, fill the cache and decode the requests that are not       */
+/* speculated on.                                                        */
+
+/* Workspace of spec_block_tables: 256-byte header (error word first) and a
+ * completion counter.  Zero-filled before its first use; every call leaves the
+ * counter at zero.  Calls that share a workspace must not overlap. */
+size_t spec_block_tables_workspace_bytes(int32_t B);
+
+/* Block tables and slot map of one scheduler tick, from request lengths.
+ * Request b holds len_old[b] tokens and is to hold len_new[b]: more (new tokens:
+ * accepted drafts, a prompt chunk), fewer, or 0 (finished).  With
+ * have = ceil(len_old / block_size) and want = ceil(len_new / block_size):
+ *   - blocks past want go back to the pool, in request order and then block
+ *     order, on top of the free ids: P = free_in[0 .. n_free) ++ released;
+ *   - blocks to add are taken off the top of P, in request order and then block
+ *     order (the i-th taken is P[size - 1 - i]);
+ *   - a request that adds blocks is served only if all that it and the requests
+ *     before it ask for fit the pool; one that is not served keeps its blocks
+ *     and its length, and its new tokens get slot -1.
+ * Outputs:
+ *   table_out [B, max_blocks]  entries past a request's blocks are -1;
+ *   free_out [num_blocks], n_free_out [1]  the pool left, -1 past its end;
+ *   len_out [B]    len_new, or len_old of a request that was not served;
+ *   cu_new [B + 1] prefix sums of the tokens each request asked to add;
+ *   slots [slots_cap]  token t of request b at cu_new[b] + t - len_old[b]:
+ *                  table_out[b][t / block_size] * block_size + t % block_size;
+ *                  -1 from cu_new[B] on (so a padded batch appends nothing);
+ *   pos [slots_cap] or NULL  t of each new token, 0 past the end.
+ * table_out / free_out / n_free_out / len_out may be table_in / free_in /
+ * n_free_in / len_old (an update in place) or must not overlap them; in place,
+ * entries that do not change are not written.  Ids are 0 <= id < num_blocks.
+ * Error word: SPEC_ERR_CAPACITY when a request was not served or slots_cap is
+ * less than cu_new[B]; SPEC_ERR_DEVICE for a length outside
+ * [0, max_blocks * block_size] (the request is left as it is), an n_free_in
+ * outside [0, num_blocks], or an id out of range.
+ * B <= 8192; B * max_blocks * block_size and num_blocks * block_size < 2^30
+ * (SPEC_ERR_CAPACITY). */
+spec_status spec_block_tables(int32_t B, int32_t block_size, int32_t max_blocks, int32_t num_blocks,
+                              const int32_t *len_old, const int32_t *len_new, const int32_t *table_in,
+                              int32_t *table_out, const int32_t *free_in, const int32_t *n_free_in,
+                              int32_t *free_out, int32_t *n_free_out, int32_t *len_out, int32_t *cu_new,
+                              int32_t *slots, int32_t *pos, int32_t slots_cap,
+                              void *ws, size_t ws_bytes, spec_stream_t stream);
+
+/* Shape and types of the cache's append and attention. */
+typedef struct {
+  int32_t n_q_heads;   /* a multiple of n_kv_heads, at most 128 times it */
+  int32_t n_kv_heads;
+  int32_t head_dim;    /* a multiple of 16, at most 256 */
+  int32_t dtype;       /* of queries, outputs and new rows: F32, BF16 or F16 */
+  int32_t kv_dtype;    /* of the cache: dtype, or E4M3 (with BF16 or F16) */
+  int32_t window;      /* keys a token attends to, itself included; 0 = all */
+  float scale;         /* of q.k; 0 = 1 / sqrt(head_dim) */
+  float k_scale;       /* E4M3: a stored key stands for k_scale * it; > 0 */
+  float v_scale;
+} spec_attn_desc;
+
+/* Writes n new K/V rows into the cache: k, v [n, n_kv_heads, head_dim] with ld
+ * elements from one row to the next (0 = n_kv_heads * head_dim; slices of a
+ * fused QKV product), row i to slot slots[i] of kv.  A slot of -1 skips its row;
+ * another one outside [0, num_slots) sets SPEC_ERR_DEVICE in ws (if not NULL)
+ * and is skipped.  Slots are distinct.  With an E4M3 cache the stored value is
+ * k / k_scale rounded to nearest even and saturated at +-448 (NaN stays NaN).
+ * kv->block_table is not read.  Rows of any alignment. */
+spec_status spec_cache_append(const spec_attn_desc *desc, const void *k, const void *v, int64_t ld,
+                              const int32_t *slots, int32_t n, const spec_kv *kv, void *ws, spec_stream_t stream);
+
+/* Workspace of spec_paged_attention for at most max_B requests: header,
+ * counters, partial results.  Zero-filled before its first use; every call
+ * leaves the counters at zero.  Calls that share a workspace must not overlap
+ * on the GPU.  0 for an invalid descriptor. */
+size_t spec_attention_workspace_bytes(const spec_attn_desc *desc, int32_t max_B);
+
+/* Attention of one new token per request over the paged cache (the decode step
+ * of a request that is not speculated on): query head h of request b attends
+ * to the keys of kv head h / (n_q_heads / n_kv_heads) at cache indices
+ * max(0, seq_len - window) .. seq_len[b] - 1 (the new token's own K/V row is
+ * appended before the call):
+ *   s_j = scale * q . k_j;  lse = log(sum_j exp(s_j));
+ *   out = sum_j exp(s_j - lse) v_j.
+ * A request with seq_len 0 gets out = 0 and lse = -infinity.
+ * q, out [B, n_q_heads, head_dim] in desc->dtype, q_ld / out_ld elements from
+ * one request to the next (0 = n_q_heads * head_dim); lse [B, n_q_heads] fp32 or
+ * NULL.  max_len: an upper bound of seq_len over the batch, or 0 if unknown; it
+ * only chooses how work is laid out.  Any block_size.  q, the cache and, with
+ * ld's, every row of q 16-byte aligned (SPEC_ERR_ALIGN).
+ * Sums and softmax statistics are fp32.  Error word: SPEC_ERR_DEVICE for a
+ * seq_len outside [0, max_blocks * block_size] (clamped) or a block id out of
+ * range (its keys are left out). */
+spec_status spec_paged_attention(const spec_attn_desc *desc, const void *q, int64_t q_ld, const spec_kv *kv,
+                                 const int32_t *seq_len, int32_t B, int32_t max_len, void *out, int64_t out_ld,
+                                 float *lse, void *ws, size_t ws_bytes, spec_stream_t stream);
+
+/* Workspace of spec_beam_select: header, counters, per-chunk records.
+ * Zero-filled before its first use; every call leaves the counters at zero.
+ * Calls that share a workspace must not overlap on the GPU. */
+size_t spec_beam_workspace_bytes(int32_t B, int32_t W, int32_t V);
+
+/* One selection step of beam search: the W best continuations of the W beams of
+ * each request.  logits [B, W, V] in dtype (F32, BF16 or F16), ld elements from
+ * one row to the next (0 = V).  A logit that is not finite is masked: it is no
+ * candidate and adds nothing to the row's log-sum-exp.  Candidates of request b:
+ *   a live beam j (done = 0, score finite): (j, v) for every finite logit, score
+ *     score[j] + logit - lse_j;
+ *   a finished beam (done != 0, score finite): (j, eos) with score[j] as it is;
+ *   a beam whose score is not finite: none.
+ * The W best by score, equal scores by j * V + v (the smaller first), go to
+ * parent / tok / score_out / done_out [B, W]; done_out is 1 where the parent was
+ * finished or tok == eos (eos < 0: no end token; finished beams then emit -1).
+ * Fewer candidates than W leave parent = the slot's own index, tok = -1,
+ * score = -infinity, done = 1.  Logits and beam scores are compared in fp64 with
+ * an fp32-accurate lse; score_out is the fp32 rounding.
+ * 1 <= W <= 32, W * V < 2^30.  score_out / done_out must not alias inputs. */
+spec_status spec_beam_select(int32_t B, int32_t W, int32_t V, int32_t dtype, const void *logits, int64_t ld,
+                             const float *score, const int32_t *done, int32_t eos, int32_t *parent,
+                             int32_t *tok, float *score_out, int32_t *done_out,
+                             void *ws, size_t ws_bytes, spec_stream_t stream);
+
+/* The states of the beams of a batch (spec_beam_reorder); row b * W + j is beam
+ * j of request b.  A request owns its blocks (owned: a row of a table that
+ * spec_block_tables made); its beams only index them.  With P =
+ * prompt_blocks[b] full blocks before the beams part, owned holds
+ *   [0, P)                    the shared blocks,
+ *   [P, P + W)                one spare block a beam,
+ *   P + W + g * W + j         the g-th block of beam j after the shared ones. */
+typedef struct {
+  int32_t B, W;
+  int32_t block_size;
+  int32_t max_blocks;             /* entries of a beam's table row */
+  int32_t owned_ld;               /* entries of a request's owned row */
+  int32_t hist_ld;                /* entries of a history row */
+  const int32_t *parent;          /* [B, W] from spec_beam_select */
+  const int32_t *tok;             /* [B, W] */
+  const int32_t *seq_len;         /* [B] cache entries each beam holds */
+  const int32_t *prompt_blocks;   /* [B] */
+  const int32_t *owned;           /* [B, owned_ld] */
+  const int32_t *table_in;        /* [B * W, max_blocks] */
+  int32_t *table_out;             /* another buffer */
+  const int32_t *spare_in;        /* [B * W] each beam's spare block */
+  int32_t *spare_out;             /* another buffer */
+  int32_t *slots;                 /* [B * W] slot of the beam's next token */
+  const int32_t *hist_in;         /* [B * W, hist_ld] tokens so far, or NULL */
+  int32_t *hist_out;              /* another buffer (NULL with hist_in) */
+} spec_beam_state;
+
+/* Reorders the beams after a selection: beam j continues beam parent[j], and
+ * gets a private slot for its next token.  With n = seq_len[b], i = n /
+ * block_size, r = n % block_size and p = parent[b, j]:
+ *   table_out[j][0 .. i)  = table_in[p][0 .. i)          (full blocks are shared);
+ *   r = 0:            table_out[j][i] = owned[P + W + (i - P) * W + j];
+ *   r > 0, p = j:     table_out[j][i] = table_in[j][i];
+ *   r > 0, p != j:    table_out[j][i] = spare_in[j], its first r slots are copied
+ *                     from block table_in[p][i] in every layer, and spare_out[j] =
+ *                     table_in[j][i] (otherwise spare_out[j] = spare_in[j]);
+ *   table_out[j] past i is -1;  slots[j] = table_out[j][i] * block_size + r;
+ *   hist_out[j] = hist_in[p][0 .. n), tok[j], then -1.
+ * kv: n_layers descriptors (1 .. 64), host memory, of st->block_size;
+ * row_bytes: bytes of one slot of k (and of v) in each.  Block tables in kv are
+ * not read; ids are 0 <= id < the smallest num_slots / block_size.  Error word of ws (if not NULL): SPEC_ERR_DEVICE for a parent
+ * outside [0, W) (taken as j itself), a length or block id out of range (the
+ * entry becomes -1, no row is copied, the slot is -1), SPEC_ERR_CAPACITY for a
+ * table, owned or history row that is too short. */
+spec_status spec_beam_reorder(const spec_beam_state *st, int32_t n_layers, const spec_kv *kv, int32_t row_bytes,
+                              void *ws, spec_stream_t stream);
 
 /* Greedy verification without caller-provided scratch.  The paper has no
  * counterpart: this entry point exists for callers that cannot allocate device
