@@ -25,7 +25,8 @@ NAMES = [None, "tc_kernel (GEMMs, LM head)", "attn_ws_kernel", "attn_mma_kernel"
 # ids of the decoding kernels, which their own files declare
 DECODE_NAMES = {24: "block_tables_kernel", 25: "cache_append_kernel", 26: "paged_attention_kernel",
                 27: "beam_select_kernel", 28: "beam_reorder_kernel"}
-UNITS = ("beam", "layer", "lmhead", "metadata", "paged_attn", "prefill", "tables", "tc_gemm", "tree", "verify")
+UNITS = ("beam", "layer", "lmhead", "metadata", "paged_attn", "paged_attn_bf16",
+         "paged_attn_f16", "prefill", "tables", "tc_gemm", "tree", "verify")
 SLOTS = 1 << 20
 LOG_WORDS = 8 + 4 * SLOTS
 
