@@ -10,10 +10,10 @@
 namespace spec {
 namespace pa {
 
-Kernel kernel_f32(int hd, int) {
-  if (hd <= 64) return kernel_of<F32Math<64>>();
-  if (hd <= 128) return kernel_of<F32Math<128>>();
-  return kernel_of<F32Math<256>>();
+Kernel kernel_f32(int hd, int G) {
+  if (hd <= 64) return G <= 4 ? kernel_of<F32Math<64, 4>>() : kernel_of<F32Math<64, 8>>();
+  if (hd <= 128) return G <= 4 ? kernel_of<F32Math<128, 4>>() : kernel_of<F32Math<128, 8>>();
+  return G <= 4 ? kernel_of<F32Math<256, 4>>() : kernel_of<F32Math<256, 8>>();
 }
 
 constexpr size_t kSmemMax = 227 * 1024;
@@ -34,39 +34,93 @@ static int pow2_up(int x) {
 // query tiles and splits do not depend on the heads of a tile
 static void plan_queries(const Kernel& k, int G, Plan* p) {
   p->qtiles = (G + k.kq - 1) / k.kq;
-  p->qt = std::min(pow2_up(p->qtiles), k.warps);
+  p->qt = std::min(pow2_up(p->qtiles), k.warps / k.vs);
   p->qs = (p->qtiles + p->qt - 1) / p->qt;
 }
 
-static Plan make(const Kernel& k, const spec_attn_desc& d, int nh, int B) {
+static Plan make(const Kernel& k, const spec_attn_desc& d, int nh, int B, int block_size) {
   Plan p{};
   plan_queries(k, d.n_q_heads / d.n_kv_heads, &p);
   p.nh = nh;
-  p.kg = k.warps / (p.nh * p.qt);
+  p.kg = k.warps / k.vs / (p.nh * p.qt);
   p.kt = p.kg * k.sub;
   p.hgq = d.n_kv_heads / p.nh * p.qs;
-  p.row = p.nh * d.head_dim * k.es;
-  p.stride = p.row + ((p.row / 16) % 2 == 0 ? 16 : 0);
-  p.slots = (int)std::min<size_t>(kMaxSlots, (kSmemMax - 1024 - k.fixed(B)) / ((size_t)p.kt * p.stride));
+  const int head = d.head_dim * k.es;
+  const int chunks = (head + 127) / 128;
+  p.swz = block_size % 8 == 0;
+  if (p.swz) {
+    p.run_lg = block_size % 16 == 0 && p.kt >= 16 ? 4 : 3;
+    p.key_stride = 128;
+    p.copies = head % 128 == 0 ? 1 : chunks;
+    p.head_stride = (head % 128 == 0 ? chunks : 1) * (128 << p.run_lg);
+    p.chunk_stride = (head % 128 == 0 ? 1 : p.nh) * (128 << p.run_lg);
+    p.run_bytes = chunks * p.nh * (128 << p.run_lg);
+    p.slot_bytes = (p.kt >> p.run_lg) * p.run_bytes;
+  } else {
+    p.run_lg = 8;                      // all keys of a tile are one run
+    p.row = p.nh * head;
+    p.key_stride = p.row + ((p.row / 16) % 2 == 0 ? 16 : 0);
+    p.head_stride = head;
+    p.chunk_stride = 128;
+    p.slot_bytes = (int)align_up((size_t)p.kt * p.key_stride, 16);
+  }
+  p.slots = (int)std::min<size_t>(kMaxSlots, (kSmemMax - 1024 - k.fixed(B)) / p.slot_bytes);
   return p;
 }
 
-static Plan plan(const Kernel& k, const spec_attn_desc& d, int B, int max_len, int sms) {
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// The cache as [nkv][chunks][slots][128 bytes], boxes of one run of slots over the tile's heads and all chunks.  Where
+// a row is no multiple of 128 bytes a last chunk would run into the next head: there the view is [nkv][1][slots][row],
+// copied in 128-byte steps.  What is past a row's or the cache's end reads as zeros.
+static bool run_map(CUtensorMap* tm, const void* ptr, const spec_attn_desc& d, const spec_kv& kv, const Kernel& k,
+                    const Plan& p) {
+  static const EncodeTiledFn enc = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    const bool ok = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) ==
+                        cudaSuccess && q == cudaDriverEntryPointSuccess;
+    return ok ? reinterpret_cast<EncodeTiledFn>(f) : nullptr;
+  }();
+  if (!enc) return false;
+  const CUtensorMapDataType type = d.kv_dtype == SPEC_DTYPE_F32    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                   : d.kv_dtype == SPEC_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                   : d.kv_dtype == SPEC_DTYPE_F16  ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                                   : CU_TENSOR_MAP_DATA_TYPE_UINT8;
+  const cuuint64_t head = (cuuint64_t)d.head_dim * k.es;
+  const cuuint32_t whole = head % 128 == 0 ? (cuuint32_t)(head / 128) : 1;
+  cuuint64_t dims[4] = {head % 128 == 0 ? (cuuint64_t)(128 / k.es) : (cuuint64_t)d.head_dim, (cuuint64_t)kv.num_slots,
+                        whole, (cuuint64_t)d.n_kv_heads};
+  cuuint64_t strides[3] = {d.n_kv_heads * head, 128, head};
+  cuuint32_t box[4] = {(cuuint32_t)(128 / k.es), 1u << p.run_lg, whole, (cuuint32_t)p.nh};
+  cuuint32_t es[4] = {1, 1, 1, 1};
+  return enc(tm, type, 4, const_cast<void*>(ptr), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+static Plan plan(const Kernel& k, const spec_attn_desc& d, int B, int max_len, int block_size, int sms) {
   Plan q{};
   plan_queries(k, d.n_q_heads / d.n_kv_heads, &q);
+  // heads of a tile: as many as make a copy 16 KB (more do not stream faster: 64 requests of 4000 keys,
+  // 8 heads of 256 bytes: 1 / 2 / 4 / 8 heads 92.5 / 89.6 / 88.4 / 88.9 us; 8 heads of 128 bytes in 8 bits:
+  // 212 / 165 / 138 / 126), but fewer where that would cut a request's tiles into more than 6 pieces, each
+  // of which the joining CTA has to read (one request of 2000 keys: 13.0 / 13.5 / 15.2 / 22.1 us)
+  const int bytes = (block_size % 8 == 0 ? 16 : 1) * d.head_dim * k.es;
   int nh = 1;
-  while (d.n_kv_heads % (2 * nh) == 0 && 2 * nh * q.qt <= k.warps) nh *= 2;
+  while (d.n_kv_heads % (2 * nh) == 0 && 2 * nh * q.qt <= k.warps / k.vs && nh * bytes < 16384) nh *= 2;
   const int len = d.window > 0 ? std::min(d.window, max_len) : max_len;
-  // the last CTA of a group to finish reads every piece of it: few heads a tile where few requests
-  // are cut into many pieces
-  while (nh > 1) {
-    const Plan p = make(k, d, nh, B);
+  // as many as there are where the requests alone give every SM work: fewer, longer items (1000 requests of 20 keys:
+  // 4 / 8 heads 46.3 / 37.8 us; 200 of 1500: within 2 %)
+  while (d.n_kv_heads % (2 * nh) == 0 && 2 * nh * q.qt <= k.warps / k.vs && B * (d.n_kv_heads / (2 * nh)) >= sms) nh *= 2;
+  for (; nh > 1; nh /= 2) {
+    const Plan p = make(k, d, nh, B, block_size);
     const double tiles = (double)(len + p.kt - 1) / p.kt;
-    const double pieces = std::min(tiles, std::max(1.0, (double)sms / ((double)B * p.hgq)));
-    if (nh * pieces <= 40) break;
-    nh /= 2;
+    if (std::min(tiles, (double)sms / ((double)B * p.hgq)) <= 6) break;
   }
-  return make(k, d, nh, B);
+  return make(k, d, nh, B, block_size);
 }
 
 static bool check(const spec_attn_desc* d) {
@@ -84,6 +138,8 @@ static bool check_types(const spec_attn_desc& d) {
 // workspace and stay zero between calls.
 static size_t part_bytes(int sms) { return (size_t)sms * 2 * 8 * 72 * 32 * 4; }
 
+static int group_ints(int sms) { return (int)align_up((size_t)2 * sms, 64); }
+
 static size_t counter_bytes(const Kernel& k, const spec_attn_desc& d, int B) {
   Plan p{};
   plan_queries(k, d.n_q_heads / d.n_kv_heads, &p);
@@ -98,7 +154,8 @@ using namespace spec;
 extern "C" size_t spec_attention_workspace_bytes(const spec_attn_desc* desc, int32_t max_B) {
   if (!pa::check(desc) || !pa::check_types(*desc) || max_B <= 0) return 0;
   const pa::Kernel k = pa::kernel_for(*desc);
-  return kWsHeader + pa::part_bytes(sm_count()) + pa::counter_bytes(k, *desc, max_B);
+  return kWsHeader + pa::part_bytes(sm_count()) + (size_t)pa::group_ints(sm_count()) * 4 +
+          pa::counter_bytes(k, *desc, max_B);
 }
 
 extern "C" spec_status spec_paged_attention(const spec_attn_desc* desc, const void* q, int64_t q_ld, const spec_kv* kv,
@@ -131,17 +188,20 @@ extern "C" spec_status spec_paged_attention(const spec_attn_desc* desc, const vo
   g.scale2 = (d.scale > 0 ? d.scale : 1.f / sqrtf((float)d.head_dim)) * (e4m3 ? d.k_scale : 1.f) * pa::kLog2e;
   g.v_scale = e4m3 ? d.v_scale : 1.f;
   g.part = reinterpret_cast<float*>(static_cast<char*>(ws) + kWsHeader);
-  g.counters = reinterpret_cast<int*>(static_cast<char*>(ws) + kWsHeader + pa::part_bytes(sms));
+  g.group_counters = reinterpret_cast<int*>(static_cast<char*>(ws) + kWsHeader + pa::part_bytes(sms));
+  g.counters = g.group_counters + pa::group_ints(sms);
   g.ws = ws;
   for (int b0 = 0; b0 < B; b0 += pa::kMaxB) {
     g.b0 = b0;
     g.B = std::min(B - b0, pa::kMaxB);
-    g.p = pa::plan(k, d, g.B, longest, sms);
-    const size_t smem = (size_t)g.p.slots * g.p.kt * g.p.stride + k.fixed(g.B);
+    g.p = pa::plan(k, d, g.B, longest, kv->block_size, sms);
+    const size_t smem = (size_t)g.p.slots * g.p.slot_bytes + k.fixed(g.B);
     if (g.p.slots < 2) return SPEC_ERR_UNSUPPORTED;
+    if (g.p.swz && (!pa::run_map(&g.tmk, kv->k, d, *kv, k, g.p) || !pa::run_map(&g.tmv, kv->v, d, *kv, k, g.p)))
+      return SPEC_ERR_CUDA;
     if (cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
       return SPEC_ERR_CUDA;
-    launch_pdl(k.fn, dim3(sms), dim3(k.warps * 32 + 32), smem, stream, g);
+    launch_pdl(k.fn, dim3(sms), dim3(k.warps * 32 + 64), smem, stream, g);
   }
   return last_launch();
 }

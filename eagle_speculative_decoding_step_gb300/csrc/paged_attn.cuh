@@ -18,6 +18,7 @@ enum : unsigned { kTLPagedAttn = 26 };   // after common.cuh's ids
 
 constexpr int kMaxB = 2048;              // requests of one launch (their tile counts' prefix sums sit in shared memory)
 constexpr int kMaxSlots = 16;            // ring slots
+constexpr int kFlat = 8;                 // up to so many pieces are joined at once
 constexpr int kMaskWords = 8;            // validity words of a tile of at most 256 keys
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
@@ -30,12 +31,22 @@ struct Plan {
   int hgq;         // head groups x query splits of a request
   int qs;          // query splits (K/V is read once per split; 1 unless nq / nkv is large)
   int qtiles;      // query tiles of a kv head in all
-  int row;         // bytes of one key's nh heads
-  int stride;      // of rows in shared memory: an odd multiple of 16, so 8 rows hit 8 bank groups
-  int slots;       // ring slots of kt * stride bytes
+  int slots;       // ring slots of slot_bytes each: one K or V tile
+  int slot_bytes;
+  // A tile in shared memory: 16-byte unit u of key j of head h lies at
+  //   (j >> run_lg) * run_bytes + (j & (run - 1)) * key_stride + h * head_stride +
+  //   (u >> 3) * chunk_stride + (((u & 7) << 4) ^ swizzle(j)).
+  // Runs (block sizes that are multiples of 8): `run` consecutive slots of a block come as one tensor
+  // copy of all of the tile's heads, [head][128-byte chunk][slot] in TMA's 128-byte swizzle (rows that
+  // are no multiple of 128 bytes: one copy a chunk, [chunk][head][slot], zeros past the row's end).  Rows (other block sizes): one bulk copy a key, rows apart
+  // by an odd multiple of 16 bytes, no swizzle.  Either way 8 keys' units are in 8 bank groups.
+  int swz, run_lg, run_bytes, key_stride, head_stride, chunk_stride;
+  int copies;      // tensor copies of a run: 1, or the 128-byte chunks of a head's row
+  int row;         // rows: bytes of one key's nh heads
 };
 
 struct Args {
+  CUtensorMap tmk, tmv;   // runs: [nkv][chunks][slots][128 bytes] views of the cache
   spec_kv kv;
   Plan p;
   const void* q;
@@ -46,7 +57,8 @@ struct Args {
   int B, b0, nq, nkv, G, hd, window;
   float scale2;    // softmax scale (and k_scale) times log2(e)
   float v_scale;
-  int* counters;   // [B, hgq]
+  int* counters;         // [B, hgq]
+  int* group_counters;   // [grid, 2]
   float* part;     // [grid, 2, warps, entry]
   void* ws;
 };
@@ -74,6 +86,24 @@ SPEC_DEV void bulk_row(uint32_t dst, const void* src, uint32_t bytes, uint32_t m
       "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(mbar), "l"(policy)
       : "memory");
 }
+
+SPEC_DEV void tma_run(uint32_t dst, const CUtensorMap* tm, uint32_t mbar, int x, int slot, int head, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6], %7;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(slot), "r"(0), "r"(head), "r"(mbar), "l"(policy)
+      : "memory");
+}
+
+// Where a lane's key row is in a tile: offset, and the swizzle of its units.
+struct Row {
+  uint32_t off, x;
+  SPEC_DEV Row(const Plan& p, int key, int head)
+      : off((uint32_t)((key >> p.run_lg) * p.run_bytes + (key & ((1 << p.run_lg) - 1)) * p.key_stride +
+                       head * p.head_stride)),
+        x(p.swz ? (uint32_t)(key & 7) << 4 : 0u) {}
+  SPEC_DEV Row() {}
+};
 
 // ---------------------------------------------------------------- 16-bit products
 SPEC_DEV void ldsm4(uint32_t a, uint32_t* r) {
@@ -112,13 +142,11 @@ template <typename T> SPEC_DEV float2 unpack(uint32_t x) {
   if constexpr (std::is_same_v<T, __half>) return __half22float2(*reinterpret_cast<__half2*>(&x));
   else return __bfloat1622float2(*reinterpret_cast<__nv_bfloat162*>(&x));
 }
-// two 8-bit values (low 16 bits of x) as two T; exact (T has every 8-bit value)
-template <typename T> SPEC_DEV uint32_t widen(uint32_t x) {
+// two 8-bit values (low 16 bits of x) as two f16; exact
+SPEC_DEV uint32_t widen(uint32_t x) {
   const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(x & 0xffffu), __NV_E4M3);
   const __half2 f = h;
-  if constexpr (std::is_same_v<T, __half>) return *reinterpret_cast<const uint32_t*>(&f);
-  const float2 y = __half22float2(f);
-  return pack<T>(y.x, y.y);
+  return *reinterpret_cast<const uint32_t*>(&f);
 }
 
 // Scores and outputs of 16 keys x one kv head x 8 NT queries on warp-level matrix
@@ -126,23 +154,84 @@ template <typename T> SPEC_DEV uint32_t widen(uint32_t x) {
 // O^T += V^T P^T.  The instruction's 8-wide side is the queries, of which a decode
 // step has few; K rows and (transposed) V rows come out of shared memory as they
 // lie.  tcgen05 would want 128 rows of one operand per 16 keys' work.
+//
+// Where a head's row is 128 bytes or less (and 8-bit rows of 256) a step takes U = 2
+// tiles of 16 keys: the chain of dependent instructions is the same for twice the
+// bytes.  Wider rows fill a ring slot with one.
+//
+// 8-bit caches are multiplied in f16, which their values convert to in one
+// instruction (bf16 would take four).  bf16 queries are scaled by a power of two per
+// query, their largest component to [2^14, 2^15): exact but for components 2^28 times
+// smaller than that, and undone in the scores' scale.
 template <typename T, bool F8, int HD, int NT> struct MmaMath {
   using In = T;
-  static constexpr int kSub = 16, kQ = 8 * NT, kEs = F8 ? 1 : 2, kWarps = HD > 128 ? 4 : 8;
-  using S = State<HD / 16 * NT * 4, 2 * NT>;
+  using P = std::conditional_t<F8, __half, T>;      // operands of the products
+  static constexpr bool kScaled = F8 && std::is_same_v<T, __nv_bfloat16>;
+  float qs[2 * NT];        // kScaled: scores' scale by query
+  static constexpr int kEs = F8 ? 1 : 2, U = HD * kEs <= 128 || (F8 && HD == 256) ? 2 : 1;
+  static constexpr int kSub = 16 * U, kQ = 8 * NT;
+  // above 128 components two warps share keys and queries: both compute the scores, each half of the outputs
+  static constexpr int kWarps = 8, VS = HD > 128 ? 2 : 1, MT = HD / 16 / VS;
+  using S = State<MT * NT * 4, 2 * NT>;
+  // register r = (mt NT + nt) 4 + 2 i + j: query nt 8 + 2 (lane & 3) + j, component mt 16 + (lane >> 2) + 8 i
+  // (8-bit caches: mt 16 + 2 (lane >> 2) + i)
   SPEC_DEV static int st(int r) { return ((r >> 2) % NT) * 2 + (r & 1); }
-  // query and head-dim component of register r
-  SPEC_DEV static int query(int r, int lane) { return ((r >> 2) % NT) * 8 + 2 * (lane & 3) + (r & 1); }
-  SPEC_DEV static int comp(int r, int lane) {
-    const int mt = (r >> 2) / NT, hi = (r >> 1) & 1;
-    return mt * 16 + (F8 ? 2 * (lane >> 2) + hi : (lane >> 2) + 8 * hi);
+  // outputs two components at a time
+  SPEC_DEV static void write(const S& s, const float* inv, T* out, int hd, int nq, int lane, int vs) {
+    const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      if (nt * 8 >= nq) break;
+      if constexpr (F8) {
+        T* o = out + (long long)(nt * 8 + 2 * t) * hd + vs * MT * 16 + 2 * g;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+          if ((vs * MT + mt) * 16 < hd)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const float* x = &s.o[(mt * NT + nt) * 4 + j];
+              if (nt * 8 + 2 * t + j < nq)
+                *reinterpret_cast<uint32_t*>(o + j * hd + mt * 16) = pack<T>(x[0] * inv[nt * 2 + j], x[2] * inv[nt * 2 + j]);
+            }
+      } else {
+        // 8 components x 8 queries transposed: lane then has components 2 t, 2 t + 1 of query g
+        T* o = out + (long long)(nt * 8 + g) * hd + vs * MT * 16 + 2 * t;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+          if ((vs * MT + mt) * 16 < hd)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const float* x = &s.o[(mt * NT + nt) * 4 + 2 * i];
+              const uint32_t y = movm(pack<T>(x[0] * inv[nt * 2], x[1] * inv[nt * 2 + 1]));
+              if (nt * 8 + g < nq) *reinterpret_cast<uint32_t*>(o + mt * 16 + 8 * i) = y;
+            }
+      }
+    }
   }
   SPEC_DEV static int stat_query(int i, int lane) { return (i >> 1) * 8 + 2 * (lane & 3) + (i & 1); }
   SPEC_DEV static bool stat_owner(int lane) { return lane < 4; }
 
+  Row rk, rv;              // this lane's K row (units lane >> 4 and up) and V row
+  uint32_t next;           // from one tile of 16 keys to the next
+  SPEC_DEV void init(const Plan& p, int key0, int head, int lane) {
+    rk = Row(p, key0 + (lane & 15), head);
+    rk.x ^= (lane >> 4) << 4;
+    next = Row(p, key0 + (lane & 15) + 16 * (U - 1), head).off - rk.off;
+    rv = rk;
+    if constexpr (!F8) {
+      rv = Row(p, key0 + (lane & 7) + (lane >> 4) * 8, head);
+      rv.x ^= ((lane >> 3) & 1) << 4;
+    }
+  }
+  // address of units 2 i, 2 i + 1 (by lane) of a row
+  SPEC_DEV static uint32_t unit2(const Plan& p, uint32_t row, uint32_t x, int i) {
+    return row + (i >> 2) * p.chunk_stride + ((uint32_t)((i & 3) << 5) ^ x);
+  }
+
   uint32_t qf[HD / 16][NT][2];
-  uint32_t pf[NT][4];      // P^T operands: high parts of keys 0-7 and 8-15, low parts of both
-  uint32_t vm;             // valid keys (16 bits)
+  uint32_t pf[U][NT][4];   // P^T operands: high parts of keys 0-7 and 8-15, low parts of both
+  uint32_t vm;             // valid keys
+  static constexpr uint32_t kAll = U == 2 ? 0xffffffffu : 0xffffu;
 
   // queries of the tile: q points at the kv head's first query, n of them from q0 on exist
   SPEC_DEV void load_q(const Args& g, const T* q, int q0, int n, int lane, float*) {
@@ -166,50 +255,101 @@ template <typename T, bool F8, int HD, int NT> struct MmaMath {
         }
       }
   }
-
-  // scores of the 16 keys at shared address k (this warp's head), running statistics, weights
-  SPEC_DEV void scores(const Args& g, uint32_t k, uint32_t mask, int lane, S& s, float*) {
-    vm = mask & 0xffffu;
-    if (vm == 0) return;
-    float c[NT][4];
+  // after load_q, once its values are needed
+  SPEC_DEV void scale_q(const Args& g, int lane) {
+    if constexpr (kScaled) {
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) c[nt][0] = c[nt][1] = c[nt][2] = c[nt][3] = 0.f;
-    const uint32_t a0 = k + (uint32_t)((lane & 15) * g.p.stride) + (lane >> 4) * 16;
+      for (int nt = 0; nt < NT; ++nt) {
+        uint32_t big = 0;           // largest magnitude: as integers, bf16 magnitudes compare like numbers
+#pragma unroll
+        for (int ks = 0; ks < HD / 16; ++ks)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t x = qf[ks][nt][h] & 0x7fff7fffu;
+            big = max(big, max(x >> 16, x & 0xffffu));
+          }
+        big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
+        big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
+        // 2^(14 - exponent); 1 for a zero row or one that is not finite
+        const int e = big == 0 || big >= 0x7f80u ? 127 + 14 : max((int)(big >> 7), 15);
+        const float up = __uint_as_float((uint32_t)(127 + 14 + 127 - e) << 23), down = __uint_as_float((uint32_t)(e - 14) << 23);
+#pragma unroll
+        for (int ks = 0; ks < HD / 16; ++ks)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float2 f = unpack<T>(qf[ks][nt][h]);
+            qf[ks][nt][h] = pack<P>(f.x * up, f.y * up);
+          }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) qs[2 * nt + j] = __shfl_sync(0xffffffffu, down, (2 * (lane & 3) + j) * 4) * g.scale2;
+      }
+    }
+  }
+
+  // scores of this warp's keys in the K tile at shared address k, running statistics, weights
+  SPEC_DEV void scores(const Args& g, uint32_t k, uint32_t mask, int lane, S& s, float*) {
+    vm = mask & kAll;
+    if (vm == 0) return;
+    // one tile of 16 keys x 8 queries: two sums over alternate 16 components, so that two chains of
+    // products run side by side
+    constexpr int A = U * NT == 1 ? 2 : 1;
+    float ca[A][U][NT][4];
+#pragma unroll
+    for (int i = 0; i < A * U * NT * 4; ++i) (&ca[0][0][0][0])[i] = 0.f;
+    auto& c = ca[0];
+    const uint32_t a0 = k + rk.off;
     if constexpr (F8) {
 #pragma unroll
       for (int kp = 0; kp < HD / 32; ++kp)
         if (kp * 32 < g.hd) {
-          uint32_t r[4], a[4];
-          ldsm4(a0 + kp * 32, r);
+          uint32_t r[U][4], a[4];
+#pragma unroll
+          for (int u = 0; u < U; ++u) ldsm4(unit2(g.p, a0 + u * next, rk.x, kp), r[u]);
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             if (kp * 32 + j * 16 >= g.hd) break;
-            a[0] = widen<T>(r[2 * j]), a[1] = widen<T>(r[2 * j + 1]);
-            a[2] = widen<T>(r[2 * j] >> 16), a[3] = widen<T>(r[2 * j + 1] >> 16);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma<T>(c[nt], a, qf[kp * 2 + j][nt][0], qf[kp * 2 + j][nt][1]);
+            for (int u = 0; u < U; ++u) {
+              a[0] = widen(r[u][2 * j]), a[1] = widen(r[u][2 * j + 1]);
+              a[2] = widen(r[u][2 * j] >> 16), a[3] = widen(r[u][2 * j + 1] >> 16);
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+                mma<P>(ca[A == 2 ? j : 0][u][nt], a, qf[kp * 2 + j][nt][0], qf[kp * 2 + j][nt][1]);
+            }
           }
         }
     } else {
 #pragma unroll
       for (int ks = 0; ks < HD / 16; ++ks)
         if (ks * 16 < g.hd) {
-          uint32_t a[4];
-          ldsm4(a0 + ks * 32, a);
+          uint32_t a[U][4];
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) mma<T>(c[nt], a, qf[ks][nt][0], qf[ks][nt][1]);
+          for (int u = 0; u < U; ++u) ldsm4(unit2(g.p, a0 + u * next, rk.x, ks), a[u]);
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma<P>(ca[ks % A][u][nt], a[u], qf[ks][nt][0], qf[ks][nt][1]);
         }
     }
-    const bool k0 = vm >> (lane >> 2) & 1, k1 = vm >> ((lane >> 2) + 8) & 1;
+    if constexpr (A == 2) {
+#pragma unroll
+      for (int i = 0; i < U * NT * 4; ++i) (&ca[0][0][0][0])[i] += (&ca[A - 1][0][0][0])[i];
+    }
     bool grew = false;
     float mn[2 * NT];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        c[nt][j] = k0 ? c[nt][j] * g.scale2 : -INFINITY;
-        c[nt][2 + j] = k1 ? c[nt][2 + j] * g.scale2 : -INFINITY;
-        float x = fmaxf(c[nt][j], c[nt][2 + j]);
+        float x = -INFINITY;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const uint32_t v = vm >> (16 * u + (lane >> 2));
+          const float sc = kScaled ? qs[nt * 2 + j] : g.scale2;
+          c[u][nt][j] = v & 1 ? c[u][nt][j] * sc : -INFINITY;
+          c[u][nt][2 + j] = v >> 8 & 1 ? c[u][nt][2 + j] * sc : -INFINITY;
+          x = fmaxf(x, fmaxf(c[u][nt][j], c[u][nt][2 + j]));
+        }
         x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
         x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
         x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
@@ -228,67 +368,83 @@ template <typename T, bool F8, int HD, int NT> struct MmaMath {
       for (int r = 0; r < S::NR; ++r) s.o[r] *= al[st(r)];
     }
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
+    for (int u = 0; u < U; ++u)
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const float b = base_of(s.m[nt * 2 + j]);
-        c[nt][j] = exp2_fast(c[nt][j] - b);
-        c[nt][2 + j] = exp2_fast(c[nt][2 + j] - b);
-        s.l[nt * 2 + j] += c[nt][j] + c[nt][2 + j];
-      }
-      // a weight enters the second product as two 16-bit parts: one alone (2^-9 of it in bf16)
-      // would cost as much as the output's own rounding
+      for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint32_t hi = pack<T>(c[nt][2 * h], c[nt][2 * h + 1]);
-        const float2 f = unpack<T>(hi);
-        pf[nt][h] = movm(hi);
-        pf[nt][2 + h] = movm(pack<T>(c[nt][2 * h] - f.x, c[nt][2 * h + 1] - f.y));
+        for (int j = 0; j < 2; ++j) {
+          const float b = base_of(s.m[nt * 2 + j]);
+          c[u][nt][j] = exp2_fast(c[u][nt][j] - b);
+          c[u][nt][2 + j] = exp2_fast(c[u][nt][2 + j] - b);
+          s.l[nt * 2 + j] += c[u][nt][j] + c[u][nt][2 + j];
+        }
+        // a weight enters the second product as two 16-bit parts: one alone (2^-9 of it in bf16)
+        // would cost as much as the output's own rounding
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t hi = pack<P>(c[u][nt][2 * h], c[u][nt][2 * h + 1]);
+          const float2 f = unpack<P>(hi);
+          pf[u][nt][h] = movm(hi);
+          pf[u][nt][2 + h] = movm(pack<P>(c[u][nt][2 * h] - f.x, c[u][nt][2 * h + 1] - f.y));
+        }
       }
-    }
   }
 
-  SPEC_DEV void values(const Args& g, uint32_t v, int lane, S& s) {
+  SPEC_DEV void values(const Args& g, uint32_t v, int lane, S& s, int vs) {
     if (vm == 0) return;
     const int t2 = 2 * (lane & 3);
     // rows of keys that are not valid may hold anything: their bits are cleared
-    const bool some = vm != 0xffffu;
-    const uint32_t z0 = (vm >> t2 & 1 ? 0xffffu : 0) | (vm >> (t2 + 1) & 1 ? 0xffff0000u : 0);
-    const uint32_t z1 = (vm >> (t2 + 8) & 1 ? 0xffffu : 0) | (vm >> (t2 + 9) & 1 ? 0xffff0000u : 0);
-    auto step = [&](int mt, uint32_t* a) {
-      if (some) a[0] &= z0, a[1] &= z0, a[2] &= z1, a[3] &= z1;
+    const bool some = vm != kAll;
+    uint32_t z[U][2];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t b = vm >> (16 * u + 8 * h + t2);
+        z[u][h] = (b & 1 ? 0xffffu : 0) | (b & 2 ? 0xffff0000u : 0);
+      }
+    auto step = [&](int mt, int u, uint32_t* a) {
+      if (some) a[0] &= z[u][0], a[1] &= z[u][0], a[2] &= z[u][1], a[3] &= z[u][1];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         float* o = &s.o[(mt * NT + nt) * 4];
-        mma<T>(o, a, pf[nt][0], pf[nt][1]);
-        mma<T>(o, a, pf[nt][2], pf[nt][3]);
+        mma<P>(o, a, pf[u][nt][0], pf[u][nt][1]);
+        mma<P>(o, a, pf[u][nt][2], pf[u][nt][3]);
       }
     };
+    const uint32_t a0 = v + rv.off;
     if constexpr (F8) {
-      const uint32_t a0 = v + (uint32_t)((lane & 15) * g.p.stride) + (lane >> 4) * 16;
 #pragma unroll
-      for (int cp = 0; cp < HD / 32; ++cp)
+      for (int cl = 0; cl < MT / 2; ++cl) {
+        const int cp = vs * (MT / 2) + cl;
         if (cp * 32 < g.hd) {
-          uint32_t r[4], a[4];
-          ldsm4t(a0 + cp * 32, r);
+          uint32_t r[U][4], a[4];
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            if (cp * 32 + j * 16 >= g.hd) break;
-            // bytes (key, component): 00 01 10 11 -> component 0 of both keys, component 1 of both
-            const uint32_t x = __byte_perm(r[2 * j], 0, 0x3120), y = __byte_perm(r[2 * j + 1], 0, 0x3120);
-            a[0] = widen<T>(x), a[1] = widen<T>(x >> 16), a[2] = widen<T>(y), a[3] = widen<T>(y >> 16);
-            step(cp * 2 + j, a);
-          }
+          for (int u = 0; u < U; ++u) ldsm4t(unit2(g.p, a0 + u * next, rv.x, cp), r[u]);
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              if (cp * 32 + j * 16 >= g.hd) break;
+              // bytes (key, component): 00 01 10 11 -> component 0 of both keys, component 1 of both
+              const uint32_t x = __byte_perm(r[u][2 * j], 0, 0x3120), y = __byte_perm(r[u][2 * j + 1], 0, 0x3120);
+              a[0] = widen(x), a[1] = widen(x >> 16), a[2] = widen(y), a[3] = widen(y >> 16);
+              step(cl * 2 + j, u, a);
+            }
         }
+      }
     } else {
-      const uint32_t a0 = v + (uint32_t)(((lane & 7) + (lane >> 4) * 8) * g.p.stride) + ((lane >> 3) & 1) * 16;
 #pragma unroll
-      for (int mt = 0; mt < HD / 16; ++mt)
+      for (int ml = 0; ml < MT; ++ml) {
+        const int mt = vs * MT + ml;
         if (mt * 16 < g.hd) {
-          uint32_t a[4];
-          ldsm4t(a0 + mt * 32, a);
-          step(mt, a);
+          uint32_t a[U][4];
+#pragma unroll
+          for (int u = 0; u < U; ++u) ldsm4t(unit2(g.p, a0 + u * next, rv.x, mt), a[u]);
+#pragma unroll
+          for (int u = 0; u < U; ++u) step(ml, u, a[u]);
         }
+      }
     }
   }
   // sums over the lanes that hold other keys of the same query
@@ -302,48 +458,63 @@ template <typename T, bool F8, int HD, int NT> struct MmaMath {
   }
 };
 
-// The same for 32-bit caches on fp32 multiply-adds: 8 keys x 8 queries a step.
+// The same for 32-bit caches on fp32 multiply-adds: 8 keys x NQ (4 or 8) queries a step.
 // Scores: lane = (key, quarter of the components); outputs: a lane holds
 // components lane + 32 e (e < HD / 32) of every query.
-template <int HD> struct F32Math {
+template <int HD, int NQ> struct F32Math {
   using In = float;
-  static constexpr int kSub = 8, kQ = 8, kEs = 4, kWarps = HD > 128 ? 4 : 8;
-  using S = State<8 * (HD / 32), 8>;
+  static constexpr int kSub = 8, kQ = NQ, kEs = 4, kWarps = HD > 128 ? 4 : 8, VS = 1;
+  using S = State<NQ * (HD / 32), NQ>;
   SPEC_DEV static int st(int r) { return r / (HD / 32); }
-  SPEC_DEV static int query(int r, int) { return r / (HD / 32); }
-  SPEC_DEV static int comp(int r, int lane) { return lane + 32 * (r % (HD / 32)); }
+  SPEC_DEV static void write(const S& s, const float* inv, float* out, int hd, int nq, int lane, int) {
+#pragma unroll
+    for (int i = 0; i < NQ; ++i)
+#pragma unroll
+      for (int e = 0; e < HD / 32; ++e)
+        if (i < nq && lane + 32 * e < hd) out[(long long)i * hd + lane + 32 * e] = s.o[i * (HD / 32) + e] * inv[i];
+  }
   SPEC_DEV static int stat_query(int i, int) { return i; }
   SPEC_DEV static bool stat_owner(int lane) { return lane == 0; }
-  // a warp's shared scratch: its queries, then the 8 x 8 weights of a step
-  static constexpr int kScratch = 8 * HD + 64;
+  // a warp's shared scratch: its queries, then the NQ x 8 weights of a step
+  static constexpr int kScratch = NQ * HD + NQ * 8;
 
   uint32_t vm;
+  Row rk, rv;                                // lane's K row; the first V row (rv.x: whether units are swizzled)
+  SPEC_DEV void init(const Plan& p, int key0, int head, int lane) {
+    rk = Row(p, key0 + (lane & 7), head);
+    rv = Row(p, key0, head);
+    rv.x = p.swz;
+  }
   SPEC_DEV void load_q(const Args& g, const float* q, int q0, int n, int lane, float* w) {
     __syncwarp();
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < NQ; ++i)
       for (int c = lane; c < g.hd; c += 32) w[i * g.hd + c] = i < n ? q[(long long)(q0 + i) * g.hd + c] : 0.f;
     __syncwarp();
   }
+  SPEC_DEV void scale_q(const Args&, int) {}
   SPEC_DEV void scores(const Args& g, uint32_t k, uint32_t mask, int lane, S& s, float* w) {
     vm = mask & 0xffu;
     if (vm == 0) return;
     const int key = lane & 7, part = lane >> 3;
-    float c[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    const uint32_t row = k + (uint32_t)(key * g.p.stride);
+    float c[NQ];
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) c[i] = 0.f;
+    const uint32_t row = k + rk.off;
     for (int ch = part; ch < g.hd / 4; ch += 4) {
       float4 x;
-      asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w) : "r"(row + ch * 16) : "memory");
+      asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
+                   : "r"(row + (ch >> 3) * g.p.chunk_stride + ((uint32_t)((ch & 7) << 4) ^ rk.x)) : "memory");
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
+      for (int i = 0; i < NQ; ++i) {
         const float4 y = *reinterpret_cast<const float4*>(w + i * g.hd + ch * 4);
         c[i] = fmaf(x.x, y.x, fmaf(x.y, y.y, fmaf(x.z, y.z, fmaf(x.w, y.w, c[i]))));
       }
     }
     const bool ok = vm >> key & 1;
     bool grew = false;
-    float mn[8];
+    float mn[NQ];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < NQ; ++i) {
       c[i] += __shfl_xor_sync(0xffffffffu, c[i], 8);
       c[i] += __shfl_xor_sync(0xffffffffu, c[i], 16);
       c[i] = ok ? c[i] * g.scale2 : -INFINITY;
@@ -355,9 +526,9 @@ template <int HD> struct F32Math {
       grew |= x > s.m[i];
     }
     if (grew) {                               // the same in every lane
-      float al[8];
+      float al[NQ];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
+      for (int i = 0; i < NQ; ++i) {
         al[i] = exp2_fast(s.m[i] - base_of(mn[i]));
         s.m[i] = mn[i];
         s.l[i] *= al[i];
@@ -365,30 +536,41 @@ template <int HD> struct F32Math {
 #pragma unroll
       for (int r = 0; r < S::NR; ++r) s.o[r] *= al[st(r)];
     }
-    float* pw = w + 8 * g.hd;
+    float* pw = w + NQ * g.hd;
     __syncwarp();
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < NQ; ++i) {
       c[i] = exp2_fast(c[i] - base_of(s.m[i]));
       if (part == 0) s.l[i] += c[i];          // lanes 0-7 sum their own keys; finish() adds them up
-      if (part == (i >> 1)) pw[i * 8 + key] = c[i];
+      if (part == (i & 3)) pw[i * 8 + key] = c[i];
     }
     __syncwarp();
   }
   SPEC_DEV void values(const Args& g, uint32_t v, int lane, S& s, const float* w) {
     if (vm == 0) return;
-    const float* pw = w + 8 * g.hd;
+    const float* pw = w + NQ * g.hd;
+    const uint32_t unit = (uint32_t)(lane >> 2 << 4), word = (lane & 3) * 4;
 #pragma unroll
-    for (int key = 0; key < 8; ++key) {
-      if (!(vm >> key & 1)) continue;         // its row may hold anything
-      const uint32_t row = v + (uint32_t)(key * g.p.stride);
+    for (int k4 = 0; k4 < 8; k4 += 4) {
+      float4 pr[NQ];
+#pragma unroll
+      for (int i = 0; i < NQ; ++i) pr[i] = *reinterpret_cast<const float4*>(pw + i * 8 + k4);
 #pragma unroll
       for (int e = 0; e < HD / 32; ++e)
         if (lane + 32 * e < g.hd) {
-          float x;
-          asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x) : "r"(row + (lane + 32 * e) * 4) : "memory");
+          float x[4];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) s.o[i * (HD / 32) + e] = fmaf(pw[i * 8 + key], x, s.o[i * (HD / 32) + e]);
+          for (int j = 0; j < 4; ++j) {
+            const int key = k4 + j;
+            const uint32_t a = v + rv.off + key * g.p.key_stride + e * g.p.chunk_stride + (unit ^ (rv.x ? key << 4 : 0)) + word;
+            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x[j]) : "r"(a) : "memory");
+            x[j] = vm >> key & 1 ? x[j] : 0.f;           // the row of a key that is not valid may hold anything
+          }
+#pragma unroll
+          for (int i = 0; i < NQ; ++i) {
+            float& o = s.o[i * (HD / 32) + e];
+            o = fmaf(pr[i].x, x[0], fmaf(pr[i].y, x[1], fmaf(pr[i].z, x[2], fmaf(pr[i].w, x[3], o))));
+          }
         }
     }
   }
@@ -408,7 +590,7 @@ template <typename M> constexpr int entry_floats() { return (M::S::NR + 2 * M::S
 template <typename M> constexpr int exchange_floats() { return M::kWarps / 2 * entry_floats<M>(); }
 // shared memory besides the ring
 template <typename M> constexpr size_t fixed_smem(int B) {
-  return 1024 + (size_t)kMaxSlots * kMaskWords * 4 + (size_t)(B + 4) / 4 * 16 +
+  return 2048 + (size_t)kMaxSlots * kMaskWords * 4 + (size_t)(2 * B + 4) / 4 * 16 +
          4 * (size_t)(exchange_floats<M>() + M::kWarps * math_scratch<M>());
 }
 
@@ -418,7 +600,7 @@ template <typename S> SPEC_DEV void reset(S& s) {
 #pragma unroll
   for (int i = 0; i < S::NM; ++i) s.m[i] = -INFINITY, s.l[i] = 0.f;
 }
-// s and another state of the same queries, m and l of which are at x[NR ..) of the lane's column
+// s and another state of the same queries: get(r) is its o[r], then its m and l
 template <typename M, typename Get> SPEC_DEV void join(typename M::S& s, Get get) {
   using S = typename M::S;
   float a[S::NM], b[S::NM];
@@ -458,7 +640,7 @@ struct Walk {
     while ((long long)pre[b + 1] * hgq <= idx) ++b;
     nt = pre[b + 1] - pre[b];
     const long long off = idx - (long long)pre[b] * hgq;
-    hg = (int)(off / nt);
+    hg = off >> 32 ? (int)(off / nt) : (int)((uint32_t)off / (uint32_t)nt);
     t0 = (int)(off - (long long)hg * nt);
     const long long n = end - idx < nt - t0 ? end - idx : nt - t0;
     t1 = t0 + (int)n;
@@ -468,14 +650,13 @@ struct Walk {
 };
 
 // One CTA per SM walks its share of the tiles.  A producer warp copies the rows of
-// a tile's keys (kt keys x nh heads, whole rows of the cache: one bulk copy a key,
-// whatever the block size) into a ring of shared-memory slots, K and V tiles in
-// turn; each consumer warp takes 16 (8) keys of one head and one query tile of
+// a tile's keys (kt keys x nh heads) into a ring of shared-memory slots, K and V
+// tiles in turn; each consumer warp takes 16 (8) keys of one head and one query tile of
 // every tile.  Pieces of a (request, head group) that several CTAs share are left
 // as partial results; the last CTA of such a group to finish joins them in CTA
 // order, so results do not depend on timing.
 template <typename M>
-__global__ void __launch_bounds__(M::kWarps * 32 + 32, 1) paged_attention_kernel(const __grid_constant__ Args g) {
+__global__ void __launch_bounds__(M::kWarps * 32 + 64, 1) paged_attention_kernel(const __grid_constant__ Args g) {
   SPEC_TL(kTLPagedAttn);
   using T = typename M::In;
   using S = typename M::S;
@@ -483,19 +664,24 @@ __global__ void __launch_bounds__(M::kWarps * 32 + 32, 1) paged_attention_kernel
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const Plan& p = g.p;
-  uint8_t* ring = smem_raw;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(ring + (size_t)p.slots * p.kt * p.stride);   // full[kMaxSlots], empty[kMaxSlots]
+  uint8_t* ring = smem_raw + ((1024u - (tc::su32(smem_raw) & 1023u)) & 1023u);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(ring + (size_t)p.slots * p.slot_bytes);   // full[kMaxSlots], empty[kMaxSlots]
   volatile int* flags = reinterpret_cast<volatile int*>(bars + 2 * kMaxSlots);              // abort, last
   uint32_t* masks = reinterpret_cast<uint32_t*>(reinterpret_cast<uint8_t*>(bars) + 1024);
   float* exch = reinterpret_cast<float*>(masks + kMaxSlots * kMaskWords);
   float* mscr = exch + exchange_floats<M>();
   int* pre = reinterpret_cast<int*>(mscr + NW * math_scratch<M>());
-  __shared__ int wsum[NW + 1];
+  int* lens = pre + g.B + 1;
+  __shared__ int wsum[NW + 2];
   const uint32_t full0 = tc::su32(bars), empty0 = full0 + 8 * kMaxSlots;
   if (tid == 0) {
     for (int i = 0; i < p.slots; ++i) {
       tc::mbar_init(full0 + 8 * i, 1);
-      tc::mbar_init(empty0 + 8 * i, NW);
+      tc::mbar_init(empty0 + 8 * i, M::kWarps);
+    }
+    if (p.swz) {
+      asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&g.tmk)) : "memory");
+      asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&g.tmv)) : "memory");
     }
     flags[0] = 0;
     pre[0] = 0;
@@ -507,23 +693,21 @@ __global__ void __launch_bounds__(M::kWarps * 32 + 32, 1) paged_attention_kernel
   // every request is somebody's) and their prefix sums
   const long long most_l = (long long)g.kv.max_blocks * g.kv.block_size;
   const int most = (int)most_l;
-  auto range = [&](int b, int& lo, int& len) {
-    len = g.seq_len[g.b0 + b];
-    len = len < 0 ? 0 : (len > most ? most : len);
-    lo = g.window > 0 && len > g.window ? len - g.window : 0;
-  };
+  auto first_key = [&](int len) { return g.window > 0 && len > g.window ? len - g.window : 0; };
   int carry = 0;
-  for (int base = 0; base < g.B; base += NW * 32 + 32) {
+  for (int base = 0; base < g.B; base += NW * 32 + 64) {
     const int b = base + tid;
     int x = 0;
     if (b < g.B) {
-      int lo, len;
-      range(b, lo, len);
-      x = max(1, (len - lo + p.kt - 1) / p.kt);
-      if (blockIdx.x == 0) {
-        const int n = g.seq_len[g.b0 + b];
-        if (n < 0 || n > most) report(g.ws, SPEC_ERR_DEVICE, g.b0 + b, n);
+      int len = g.seq_len[g.b0 + b];
+      if (len < 0 || len > most) {
+        if (blockIdx.x == 0) report(g.ws, SPEC_ERR_DEVICE, g.b0 + b, len);
+        len = len < 0 ? 0 : most;
       }
+      lens[b] = len;
+      int lo = first_key(len);
+      if (p.swz) lo &= -1 << p.run_lg;       // tiles start with a run
+      x = max(1, (len - lo + p.kt - 1) / p.kt);
     }
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -533,7 +717,7 @@ __global__ void __launch_bounds__(M::kWarps * 32 + 32, 1) paged_attention_kernel
     if (lane == 31) wsum[warp] = x;
     __syncthreads();
     int before = carry;
-    for (int w = 0; w < NW + 1; ++w) {
+    for (int w = 0; w < NW + 2; ++w) {
       if (w < warp) before += wsum[w];
       carry += wsum[w];
     }
@@ -545,73 +729,114 @@ __global__ void __launch_bounds__(M::kWarps * 32 + 32, 1) paged_attention_kernel
   const int cta = blockIdx.x;
   if (cta >= C) return;
   Walk w(pre, g.B, p.hgq, cta * total / C, (cta + 1) * total / C);
-  const uint32_t ring0 = tc::su32(ring), slot_bytes = (uint32_t)(p.kt * p.stride);
+  const uint32_t ring0 = tc::su32(ring), slot_bytes = (uint32_t)p.slot_bytes;
 
-  if (warp == NW) {
-    // ------------------------------------------------------------ producer
+  if (warp >= NW) {
+    // ------------------------------------------------------------ producers: K, V
+    const int v = warp - NW;
     const uint64_t policy = tc::policy_evict_first();      // each K/V row is read once
     const long long row_all = (long long)g.nkv * g.hd * M::kEs;
-    const char* kp = static_cast<const char*>(g.kv.k);
-    const char* vp = static_cast<const char*>(g.kv.v);
     const int bs = g.kv.block_size, shift = (bs & (bs - 1)) == 0 ? __ffs(bs) - 1 : -1;
-    int slot = 0, phase = 0, issued = 0;
-    bool ok = true;
-    constexpr int kPer = kMaskWords;                       // keys of a tile a lane handles
-    while (ok && w.next()) {
-      int lo, len;
-      range(w.b, lo, len);
-      const int32_t* table = g.kv.block_table + (long long)(g.b0 + w.b) * g.kv.max_blocks;
-      const long long col = (long long)(w.hg / p.qs) * p.row;
-      for (int t = w.t0; ok && t < w.t1; ++t) {
-        const int key0 = lo + t * p.kt;
-        // this tile's cache slots (-1: no key), before waiting for room
-        int sl[kPer];
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-          sl[i] = -1;
-          const int j = i * 32 + lane, key = key0 + j;
-          if (j < p.kt && key < len) {
-            const int blk = shift >= 0 ? key >> shift : key / bs;
-            const int id = __ldcg(table + blk);
-            const long long s = (long long)id * bs + (key - blk * bs);
-            if (id >= 0 && s < g.kv.num_slots) sl[i] = (int)s;
-            else report(g.ws, SPEC_ERR_DEVICE, g.b0 + w.b, key);
-          }
-        }
-#pragma unroll
-        for (int v = 0; v < 2; ++v) {
-          ok = tc::mbar_wait(empty0 + 8 * slot, phase ^ 1, const_cast<volatile int*>(flags));
-          if (!__all_sync(0xffffffffu, ok)) {
-            ok = false;
-            break;
-          }
-          int n = 0;
-#pragma unroll
-          for (int i = 0; i < kPer; ++i)
-            if (i * 32 < p.kt) {
-              const uint32_t word = __ballot_sync(0xffffffffu, sl[i] >= 0);
-              if (lane == 0) masks[slot * kMaskWords + i] = word;
-              n += __popc(word);
-            }
-          if (lane == 0) tc::mbar_expect_tx(full0 + 8 * slot, (uint32_t)(n * p.row));
-          __syncwarp();
-          const char* src = (v ? vp : kp) + col;
-#pragma unroll
-          for (int i = 0; i < kPer; ++i)
-            if (sl[i] >= 0)
-              bulk_row(ring0 + slot * slot_bytes + (i * 32 + lane) * p.stride, src + sl[i] * row_all, p.row,
-                       full0 + 8 * slot, policy);
-          ++issued;
-          if (++slot == p.slots) slot = 0, phase ^= 1;
-        }
+    const int run = 1 << p.run_lg, runs = p.kt >> p.run_lg, copies = runs * p.copies;
+    int slot = v, phase = 0, issued = 0;                   // every second slot in turn is this warp's
+    constexpr int kPer = kMaskWords;                       // rows: keys of a tile a lane handles
+    // One tile ahead: its table entries are on their way while the tile before waits for room.
+    struct Tile {
+      int b, key0, lo, len, head0;
+      int id[kPer];          // runs: lane r has run r's block; rows: id[i] is the block of key 32 i + lane
+    };
+    bool in_piece = false;
+    int t = 0;
+    auto fetch = [&](Tile& x) {
+      if (!in_piece || ++t >= w.t1) {
+        if (!w.next()) return false;
+        in_piece = true;
+        t = w.t0;
       }
+      x.b = w.b;
+      x.len = lens[w.b];
+      x.lo = first_key(x.len);
+      x.key0 = (p.swz ? x.lo & -run : x.lo) + t * p.kt;
+      x.head0 = w.hg / p.qs * p.nh;
+      const int32_t* table = g.kv.block_table + (long long)(g.b0 + w.b) * g.kv.max_blocks;
+      auto entry = [&](int key) { return table[shift >= 0 ? key >> shift : key / bs]; };
+      if (p.swz) {
+        const int key = x.key0 + lane * run;
+        x.id[0] = lane < runs && key < x.len ? entry(key) : 0;
+      } else {
+#pragma unroll
+        for (int i = 0; i < kPer; ++i)
+          if (i * 32 < p.kt) {
+            const int key = x.key0 + i * 32 + lane;
+            x.id[i] = i * 32 + lane < p.kt && key < x.len ? entry(key) : 0;
+          }
+      }
+      return true;
+    };
+    Tile x;
+    bool ok = true, have = fetch(x);
+    while (ok && have) {
+      Tile y;
+      const bool more = fetch(y);
+      ok = __all_sync(0xffffffffu, tc::mbar_wait(empty0 + 8 * slot, phase ^ 1, const_cast<volatile int*>(flags)));
+      if (!ok) break;
+      const uint32_t full = full0 + 8 * slot, dst = ring0 + slot * slot_bytes;
+      // cache slot of a key (-1: none, or a block id out of range: the key is left out)
+      auto slot_of_key = [&](int key, int id) {
+        if (key >= x.len) return -1;
+        const long long s = (long long)id * bs + (shift >= 0 ? key & (bs - 1) : key % bs);
+        if (id >= 0 && s < g.kv.num_slots) return (int)s;
+        report(g.ws, SPEC_ERR_DEVICE, g.b0 + x.b, key);
+        return -1;
+      };
+      if (p.swz) {
+        const int sl = lane < runs ? slot_of_key(x.key0 + lane * run, x.id[0]) : -1;
+        const int in_run = sl < 0 ? 0 : min(run, g.kv.num_slots - sl);      // slots of the run that are in the cache
+        const int n = __popc(__ballot_sync(0xffffffffu, sl >= 0));
+        for (int i = 0; i * 32 < p.kt; ++i) {
+          const int j = i * 32 + lane, key = x.key0 + j;
+          const int have_r = __shfl_sync(0xffffffffu, in_run, (j >> p.run_lg) & 31);
+          const uint32_t word = __ballot_sync(0xffffffffu, j < p.kt && key >= x.lo && key < x.len && (j & (run - 1)) < have_r);
+          if (lane == 0) masks[slot * kMaskWords + i] = word;
+        }
+        if (lane == 0) tc::mbar_expect_tx(full, (uint32_t)(n * p.run_bytes));
+        __syncwarp();
+        for (int base = 0; base < copies; base += 32) {
+          const int i = base + lane, r = p.copies == 1 ? i : i / p.copies, c = i - r * p.copies;
+          const int s = __shfl_sync(0xffffffffu, sl, r & 31);
+          if (i < copies && s >= 0)
+            tma_run(dst + r * p.run_bytes + c * p.chunk_stride, v ? &g.tmv : &g.tmk, full, c * (128 / M::kEs), s, x.head0,
+                    policy);
+        }
+      } else {
+        int sl[kPer], n = 0;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i)
+          if (i * 32 < p.kt) {
+            sl[i] = i * 32 + lane < p.kt ? slot_of_key(x.key0 + i * 32 + lane, x.id[i]) : -1;
+            const uint32_t word = __ballot_sync(0xffffffffu, sl[i] >= 0);
+            if (lane == 0) masks[slot * kMaskWords + i] = word;
+            n += __popc(word);
+          }
+        if (lane == 0) tc::mbar_expect_tx(full, (uint32_t)(n * p.row));
+        __syncwarp();
+        const char* src = static_cast<const char*>(v ? g.kv.v : g.kv.k) + (long long)x.head0 * g.hd * M::kEs;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i)
+          if (i * 32 < p.kt && sl[i] >= 0)
+            bulk_row(dst + (i * 32 + lane) * p.key_stride, src + sl[i] * row_all, p.row, full, policy);
+      }
+      ++issued;
+      if ((slot += 2) >= p.slots) slot -= p.slots, phase ^= 1;
+      x = y;
+      have = more;
     }
     if (!ok) {
       // a wait ran out: let the copies in flight land before leaving
       if (lane == 0) report(g.ws, SPEC_ERR_TIMEOUT);
       int sl = slot, ph = phase;
-      for (int i = 0; i < (issued < p.slots ? issued : p.slots); ++i) {
-        if (--sl < 0) sl = p.slots - 1, ph ^= 1;
+      for (int i = 0; i < min(issued, (p.slots + 1) / 2); ++i) {
+        if ((sl -= 2) < 0) sl += p.slots, ph ^= 1;
         tc::mbar_wait(full0 + 8 * sl, ph, const_cast<volatile int*>(flags), false);
       }
     }
@@ -619,11 +844,13 @@ __global__ void __launch_bounds__(M::kWarps * 32 + 32, 1) paged_attention_kernel
   }
 
   // -------------------------------------------------------------- consumers
-  const int h = warp % p.nh, qi = warp / p.nh % p.qt, kgrp = warp / (p.nh * p.qt);
-  const uint32_t off = (uint32_t)(kgrp * M::kSub * p.stride + h * g.hd * M::kEs);
+  const int vs = warp % M::VS, unit = warp / M::VS;
+  const int h = unit % p.nh, qi = unit / p.nh % p.qt, kgrp = unit / (p.nh * p.qt);
   float* wscr = mscr + warp * math_scratch<M>();
   int slot = 0, phase = 0;
+  const int k0 = kgrp * M::kSub;
   M math;
+  math.init(p, k0, h, lane);
   S s;
   auto sync = [] { asm volatile("bar.sync 1, %0;" ::"n"(NW * 32) : "memory"); };
   auto advance = [&] {
@@ -634,7 +861,7 @@ __global__ void __launch_bounds__(M::kWarps * 32 + 32, 1) paged_attention_kernel
   // the key groups' states into group 0's
   auto merge_groups = [&] {
     for (int half = p.kg >> 1; half > 0; half >>= 1) {
-      const int pair = h + p.nh * (qi + p.qt * (kgrp & (half - 1)));     // < NW / 2
+      const int pair = (h + p.nh * (qi + p.qt * (kgrp & (half - 1)))) * M::VS + vs;     // < NW / 2
       float* x = exch + (size_t)pair * entry_floats<M>() + lane;
       if (kgrp >= half && kgrp < 2 * half) {
 #pragma unroll
@@ -647,70 +874,113 @@ __global__ void __launch_bounds__(M::kWarps * 32 + 32, 1) paged_attention_kernel
       sync();
     }
   };
-  while (w.next()) {
-    const int head = (w.hg / p.qs) * p.nh + h, qtile = (w.hg % p.qs) * p.qt + qi;
-    const int q0 = qtile * M::kQ, nq = min(M::kQ, g.G - q0);       // <= 0: this warp has no queries
+  // a piece's queries are loaded while the one before it is merged and written, where registers
+  // allow (16 queries: spills, and 64 requests of 4000 keys with 128 query heads 165 -> 190 us)
+  constexpr bool kEarly = S::NR <= 32;
+  auto queries = [&] { return min(M::kQ, g.G - ((w.hg % p.qs) * p.qt + qi) * M::kQ); };     // <= 0: none for this warp
+  auto head_of = [&] { return (w.hg / p.qs) * p.nh + h; };
+  auto load_q = [&] {
+    const int n = queries();
+    if (n > 0)
+      math.load_q(g, static_cast<const T*>(g.q) + (g.b0 + w.b) * g.q_ld + (long long)head_of() * g.G * g.hd,
+                  ((w.hg % p.qs) * p.qt + qi) * M::kQ, n, lane, wscr);
+  };
+  bool more = w.next();
+  if (kEarly && more) load_q();
+  while (more) {
+    const int head = head_of(), q0 = ((w.hg % p.qs) * p.qt + qi) * M::kQ, nq = queries();
     const long long b = g.b0 + w.b;
+    const int piece_b = w.b, hg = w.hg, nt = w.nt;
+    const bool whole = w.t1 - w.t0 == w.nt;
     reset(s);
-    if (nq > 0)
-      math.load_q(g, static_cast<const T*>(g.q) + b * g.q_ld + (long long)head * g.G * g.hd, q0, nq, lane, wscr);
+    if (!kEarly) load_q();
+    math.scale_q(g, lane);
     for (int t = w.t0; t < w.t1; ++t) {
       bool ok = tc::mbar_wait(full0 + 8 * slot, phase, const_cast<volatile int*>(flags));
       if (ok && nq > 0) {
-        const int k0 = kgrp * M::kSub;
-        math.scores(g, ring0 + slot * slot_bytes + off, masks[slot * kMaskWords + (k0 >> 5)] >> (k0 & 31), lane, s, wscr);
+        math.scores(g, ring0 + slot * slot_bytes, masks[slot * kMaskWords + (k0 >> 5)] >> (k0 & 31), lane, s, wscr);
       }
       advance();
       ok = tc::mbar_wait(full0 + 8 * slot, phase, const_cast<volatile int*>(flags)) && ok;
       if (ok && nq > 0) {
-        if constexpr (math_scratch<M>() > 0) math.values(g, ring0 + slot * slot_bytes + off, lane, s, wscr);
-        else math.values(g, ring0 + slot * slot_bytes + off, lane, s);
+        if constexpr (math_scratch<M>() > 0) math.values(g, ring0 + slot * slot_bytes, lane, s, wscr);
+        else math.values(g, ring0 + slot * slot_bytes, lane, s, vs);
       }
       advance();
     }
     math.finish(s);
+    more = w.next();
+    if (kEarly && more) load_q();
     merge_groups();
-    if (w.t1 - w.t0 < w.nt) {
+    if (!whole) {
       // one of several pieces: leave it, and join them all if it is the last to come
-      const long long i0 = (long long)pre[w.b] * p.hgq + (long long)w.hg * w.nt;
-      const int c0 = (int)(((i0 + 1) * C - 1) / total), c1 = (int)(((i0 + w.nt) * C - 1) / total);
-      auto entry = [&](int c) {                 // a CTA's first piece may have begun before it, its last may go on
-        return g.part + (((long long)c * 2 + (c == c0)) * NW + h + p.nh * qi) * entry_floats<M>() + lane * 4;
+      const long long i0 = (long long)pre[piece_b] * p.hgq + (long long)hg * nt;
+      const int c0 = (int)(((i0 + 1) * C - 1) / total), n = (int)(((i0 + nt) * C - 1) / total) - c0 + 1;
+      auto entry = [&](int i) {                 // piece i: a CTA's first piece may have begun before it, its last may go on
+        return g.part + (((long long)(c0 + i) * 2 + (i == 0)) * NW + (h + p.nh * qi) * M::VS + vs) * entry_floats<M>() + lane * 4;
       };
-      if (kgrp == 0) {
-        float* x = entry(cta);
+      auto leave = [&](int i) {                 // this warp's state as piece i
+        if (kgrp != 0) return;
+        float* x = entry(i);
 #pragma unroll
-        for (int r = 0; r < S::NR; r += 4) __stcg(reinterpret_cast<float4*>(x + r * 32), make_float4(s.o[r], s.o[r + 1], s.o[r + 2], s.o[r + 3]));
+        for (int r = 0; r < S::NR; r += 4)
+          __stcg(reinterpret_cast<float4*>(x + r * 32), make_float4(s.o[r], s.o[r + 1], s.o[r + 2], s.o[r + 3]));
         float ml[2 * S::NM];
 #pragma unroll
-        for (int i = 0; i < S::NM; ++i) ml[i] = s.m[i], ml[S::NM + i] = s.l[i];
+        for (int k = 0; k < S::NM; ++k) ml[k] = s.m[k], ml[S::NM + k] = s.l[k];
 #pragma unroll
         for (int r = 0; r < 2 * S::NM; r += 4)
           __stcg(reinterpret_cast<float4*>(x + (S::NR + r) * 32), make_float4(ml[r], ml[r + 1], ml[r + 2], ml[r + 3]));
-      }
-      __threadfence();
-      sync();
-      if (tid == 0) {
-        int* ctr = &g.counters[b * p.hgq + w.hg];
-        const bool last = atomicAdd(ctr, 1) == c1 - c0;
-        if (last) *ctr = 0;
-        flags[1] = last;
-      }
-      sync();
-      if (!flags[1]) continue;
-      __threadfence();
-      reset(s);
-      for (int c = c0 + kgrp; c <= c1; c += p.kg) {
-        const float* x = entry(c);
-        float y[S::NR + 2 * S::NM];
-#pragma unroll
-        for (int r = 0; r < S::NR + 2 * S::NM; r += 4) {
-          const float4 f = __ldcg(reinterpret_cast<const float4*>(x + r * 32));
-          y[r] = f.x, y[r + 1] = f.y, y[r + 2] = f.z, y[r + 3] = f.w;
+      };
+      auto last_of = [&](int* ctr, int count) { // whether this CTA is the last of `count` to come here
+        sync();                                 // its pieces are written; the atomic releases them and acquires the others'
+        if (tid == 0) {
+          int before;
+          asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;" : "=r"(before) : "l"(ctr) : "memory");
+          if (before == count - 1) *ctr = 0;
+          flags[1] = before == count - 1;
         }
-        join<M>(s, [&](int r) { return y[r]; });
+        sync();
+        return flags[1] != 0;
+      };
+      auto collect = [&](int i, int end, int step) {   // pieces i, i + step .. joined in order, key groups taking turns
+        reset(s);
+        for (i += kgrp * step; i < end; i += p.kg * step) {
+          const float* x = entry(i);
+          // which of the two forms spills less depends on the state's size; a spill of a few registers here
+          // costs the main loop 10 % (256 components: 160 -> 179 us, 16 queries: 165 -> 190 us)
+          if constexpr (S::NR > 32) {
+            float y[S::NR + 2 * S::NM];
+#pragma unroll
+            for (int r = 0; r < S::NR + 2 * S::NM; r += 4) {
+              const float4 f = __ldcg(reinterpret_cast<const float4*>(x + r * 32));
+              y[r] = f.x, y[r + 1] = f.y, y[r + 2] = f.z, y[r + 3] = f.w;
+            }
+            join<M>(s, [&](int r) { return y[r]; });
+          } else {
+            float4 f;
+            join<M>(s, [&](int r) {
+              if (r >= S::NR) return __ldcg(x + (r & ~3) * 32 + (r & 3));
+              if (r % 4 == 0) f = __ldcg(reinterpret_cast<const float4*>(x + r * 32));
+              return r % 4 == 0 ? f.x : r % 4 == 1 ? f.y : r % 4 == 2 ? f.z : f.w;
+            });
+          }
+        }
+        merge_groups();
+      };
+      const int i = cta - c0;
+      leave(i);
+      // many pieces are joined in two levels, about sqrt(n) at a time: one CTA reads a piece in ~0.5 us
+      int step = 1;
+      if (n > kFlat) {
+        while (step * step < n) ++step;
+        const int first = i / step * step, end = min(first + step, n);
+        if (!last_of(&g.group_counters[2 * (c0 + first) + (first == 0)], end - first)) continue;
+        collect(first, end, 1);
+        leave(first);
       }
-      merge_groups();
+      if (!last_of(&g.counters[b * p.hgq + hg], (n + step - 1) / step)) continue;
+      collect(0, n, step);
     }
     if (kgrp == 0 && nq > 0) {
       T* out = static_cast<T*>(g.out) + b * g.out_ld + ((long long)head * g.G + q0) * g.hd;
@@ -719,19 +989,10 @@ __global__ void __launch_bounds__(M::kWarps * 32 + 32, 1) paged_attention_kernel
       for (int i = 0; i < S::NM; ++i) {
         inv[i] = s.l[i] == 0.f ? 0.f : g.v_scale / s.l[i];
         const int q = M::stat_query(i, lane);
-        if (g.lse && M::stat_owner(lane) && q < nq)
+        if (g.lse && vs == 0 && M::stat_owner(lane) && q < nq)
           g.lse[b * g.nq + (long long)head * g.G + q0 + q] = s.l[i] == 0.f ? -INFINITY : (s.m[i] + log2f(s.l[i])) * kLn2;
       }
-#pragma unroll
-      for (int r = 0; r < S::NR; ++r) {
-        const int q = M::query(r, lane), c = M::comp(r, lane);
-        if (q < nq && c < g.hd) {
-          const float x = s.o[r] * inv[M::st(r)];
-          if constexpr (std::is_same_v<T, float>) out[(long long)q * g.hd + c] = x;
-          else if constexpr (std::is_same_v<T, __half>) out[(long long)q * g.hd + c] = __float2half_rn(x);
-          else out[(long long)q * g.hd + c] = __float2bfloat16_rn(x);
-        }
-      }
+      M::write(s, inv, out, g.hd, nq, lane, vs);
     }
   }
   if (tid == 0 && flags[0]) report(g.ws, SPEC_ERR_TIMEOUT);
@@ -740,12 +1001,12 @@ __global__ void __launch_bounds__(M::kWarps * 32 + 32, 1) paged_attention_kernel
 // What the planner needs to know of an instantiation, and its launch.
 struct Kernel {
   void (*fn)(Args);
-  int warps, sub, kq, es;
+  int warps, vs, sub, kq, es;
   size_t (*fixed)(int);
 };
 template <typename M> Kernel kernel_of() {
   static_assert(M::kWarps * entry_floats<M>() <= 8 * 72 * 32, "a CTA's piece fits the workspace");
-  return {paged_attention_kernel<M>, M::kWarps, M::kSub, M::kQ, M::kEs,
+  return {paged_attention_kernel<M>, M::kWarps, M::VS, M::kSub, M::kQ, M::kEs,
           [](int B) { return fixed_smem<M>(B); }};
 }
 
