@@ -8,6 +8,7 @@
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "common.cuh"
 #include "internal.h"
@@ -18,17 +19,34 @@ enum : unsigned { kTLBeamSelect = 27, kTLBeamReorder = 28 };   // after common.c
 
 // ---------------------------------------------------------------- selection
 // Within a beam the order of scores is the order of logits, so a row's chunk needs
-// only its W largest logits, its maximum and its sum of exponentials: one pass
-// over the logits, which stay in registers between the three uses.  The last
-// chunk of a request to finish (a counter, nobody waits) merges.
-constexpr int kSelThreads = 256, kSelWarps = kSelThreads / 32;
-constexpr int kSelElems = 32;                               // logits a thread holds
-constexpr int kSelChunk = kSelThreads * kSelElems;
-constexpr int kSelCap = 1024;                               // entries of a candidate list
+// only its W largest logits and its sum of exponentials: one pass over the logits,
+// bound by their bytes.  Each warp streams tiles of 1024 logits into registers, the
+// next tile's loads on their way while it works on one, with no barrier in the loop.
+// A lane's 32 logits of a tile are a group, whose maximum the running sum needs
+// anyway; it goes to shared memory.  The W largest logits lie in the W groups with
+// the largest maxima, so the search for them is over 1/32 of the chunk, and only the
+// few groups that are left are read again.  The last chunk of a request to finish (a
+// counter, nobody waits) merges the request.
+//
+// Which lane has which element of a tile does not depend on the row's alignment, and
+// rows are cut into equal chunks, so equal rows give equal sums and tie as they
+// should.
+constexpr int kSelWarps = 4, kSelThreads = kSelWarps * 32;
+constexpr int kSelElems = 32;                               // logits of a group
+constexpr int kSelTile = 32 * kSelElems;
+constexpr int kSelChunk = 128 * kSelTile;                   // at most in a chunk
+constexpr int kSelCap = 512;                                // entries of a candidate list
 constexpr float kLog2e = 1.4426950408889634f;
+#ifndef SELB
+#define SELB 2
+#endif
+
+// the requests' counters lie in the same place whatever a call's sizes (B W < 2^16), so that calls of
+// any sizes share a workspace
+constexpr size_t kSelCounterBytes = 65536 * 4;
 
 struct SelArgs {
-  int B, W, V, nch, eos;
+  int B, W, V, nch, chunk, eos;
   long long ld;
   const void* logits;
   const float* score;
@@ -36,280 +54,485 @@ struct SelArgs {
   int32_t *parent, *tok, *done_out;
   float* score_out;
   int* counters;      // [B]
-  float2* stats;      // [B * W, nch]  maximum, sum of exp(x - maximum)
+  float2* stats;      // [B * W, nch]  largest logit r, sum of exp(x - r)
   float2* cand;       // [B * W, nch, W]  logit, token id (bits)
 };
 
-SPEC_DEV float finite_or_mask(float x) { return fabsf(x) <= 3.402823466e38f ? x : -INFINITY; }
+SPEC_DEV bool finite(float x) { return fabsf(x) <= 3.402823466e38f; }
 SPEC_DEV float cvt(float x) { return x; }
 SPEC_DEV float cvt(__nv_bfloat16 x) { return __bfloat162float(x); }
 SPEC_DEV float cvt(__half x) { return __half2float(x); }
+SPEC_DEV float pow2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 
+// Values are ordered as unsigned integers (0 is below every number and stands for no
+// candidate): fp64 comparisons would go through the slow fp64 units.  -0 equals +0.
+SPEC_DEV uint32_t key_of(float x) {
+  const uint32_t u = __float_as_uint(x + 0.f);
+  return x == -INFINITY ? 0u : ((u >> 31) ? ~u : u | 0x80000000u);
+}
+SPEC_DEV float value_of(uint32_t k) { return k == 0 ? -INFINITY : __uint_as_float((k >> 31) ? k & 0x7fffffffu : ~k); }
+SPEC_DEV uint64_t key_of(double x) {
+  const uint64_t u = (uint64_t)__double_as_longlong(x + 0.0);
+  return (u >> 63) ? ~u : u | 0x8000000000000000ull;
+}
+SPEC_DEV double value_of(uint64_t k) {
+  return __longlong_as_double((long long)((k >> 63) ? k & 0x7fffffffffffffffull : ~k));
+}
 // a place in the order: larger value first, then smaller index
-template <typename F> SPEC_DEV bool ahead(F v, int i, F w, int j) { return v > w || (v == w && i < j); }
+template <typename K> SPEC_DEV bool ahead(K v, int i, K w, int j) { return v > w || (v == w && i < j); }
 
-// The k-th largest of the block's thread maxima by warps: each warp's k-th largest
-// lane value is reached by at least k values of the block, and so is the largest of
-// those over the warps: a lower bound of the block's k-th largest value.
-template <typename F> SPEC_DEV F block_bound(F v, int k, F* red) {
+struct SelShared {
+  uint64_t key[kSelCap], entry[kSelCap];
+  int idx[kSelCap];
+  uint64_t kred[kSelWarps];
+  int ired[kSelWarps];
+  float fred[2][kSelWarps];
+  int count, groups, last;
+  float border;
+  float score[32];    // of the request's beams; -infinity: none
+  int done[32];
+  double lse[32];
+};
+
+// A lower bound of the block's k-th largest value from the threads' maxima: a warp's
+// k-th largest is reached by k values, and so is the largest of those over the warps.
+template <typename K> SPEC_DEV K block_bound(K mine, int k, SelShared& sm) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int rank = 0;
 #pragma unroll
   for (int o = 1; o < 32; ++o) {
-    const F w = __shfl_sync(0xffffffffu, v, (lane + o) & 31);
-    rank += w > v || (w == v && ((lane + o) & 31) < lane);
+    const K w = __shfl_sync(0xffffffffu, mine, (lane + o) & 31);
+    rank += w > mine || (w == mine && ((lane + o) & 31) < lane);
   }
-  if (rank == k - 1) red[warp] = v;
+  if (rank == k - 1) sm.kred[warp] = mine;
   __syncthreads();
-  F b = red[0];
+  K b = (K)sm.kred[0];
 #pragma unroll
-  for (int w = 1; w < kSelWarps; ++w) b = red[w] > b ? red[w] : b;
+  for (int w = 1; w < kSelWarps; ++w) b = (K)sm.kred[w] > b ? (K)sm.kred[w] : b;
   __syncthreads();
   return b;
 }
 
-struct SelShared {
-  float fred[kSelWarps];
-  double dred[kSelWarps];
-  double val[kSelCap];
-  int idx[kSelCap];
-  int count, last;
-  double lse[32];
-};
-
-// Best (value, index) of the block strictly after (pv, pi); every thread gets it.
-template <typename F, typename Get> SPEC_DEV void block_next(F pv, int pi, int n, Get get, SelShared& sm, F& bv, int& bi) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  F v = (F)-INFINITY;
-  int at = 0x7fffffff;
-  for (int e = 0; e < n; ++e) {
-    F x;
-    int i;
-    get(e, x, i);
-    if (x > (F)-INFINITY && ahead(pv, pi, x, i) && ahead(x, i, v, at)) {
-      v = x;
-      at = i;
-    }
-  }
+// The block's k best of `lists` lists of up to k (key, index) entries, each in
+// descending order: get(list, place, index) is an entry's key, 0 past the list's end.
+// They go, in order, to the front of the shared list; sm.count is how many there are.
+// Entries at or above a bound are collected and ranked by counting; if those overflow
+// the list, k rounds of block-wide maxima.  The bound comes from the threads' maxima
+// over all entries where those can be held in registers between the two looks, else
+// over the lists' heads, so that only lists whose head reaches it are read (16 beams:
+// 512 entries 29.6 us against 35.7 by heads, 2560 entries 17.1 by heads against 35.8).
+template <typename Get> SPEC_DEV void block_best(int k, int lists, Get get, SelShared& sm) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  constexpr int kHeld = 8;
+  if (tid == 0) sm.count = sm.groups = 0;
+  auto keep = [&](uint64_t x, int i) {
+    const int at = atomicAdd(&sm.count, 1);
+    if (at < kSelCap) sm.key[at] = x, sm.idx[at] = i;
+  };
+  int open = 0;                                                // lists that were read
+  uint64_t mine = 0;
+  if (lists * k <= kHeld * kSelThreads) {
+    uint64_t held[kHeld];
+    int at_of[kHeld];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const F w = __shfl_xor_sync(0xffffffffu, v, o);
-    const int j = __shfl_xor_sync(0xffffffffu, at, o);
-    if (ahead(w, j, v, at)) {
-      v = w;
-      at = j;
+    for (int e = 0; e < kHeld; ++e) {
+      const int l = (tid + e * kSelThreads) / k;
+      held[e] = l < lists ? get(l, tid + e * kSelThreads - l * k, at_of[e]) : 0;
+      mine = held[e] > mine ? held[e] : mine;
+    }
+    uint64_t bound = block_bound<uint64_t>(mine, k, sm);       // has a barrier
+    if (bound == 0) bound = 1;
+#pragma unroll
+    for (int e = 0; e < kHeld; ++e)
+      if (held[e] >= bound) keep(held[e], at_of[e]);
+  } else {
+    for (int l = tid; l < lists; l += kSelThreads) {
+      int i;
+      const uint64_t x = get(l, 0, i);
+      mine = x > mine ? x : mine;
+    }
+    uint64_t bound = block_bound<uint64_t>(mine, k, sm);
+    if (bound == 0) bound = 1;
+    if (mine >= bound)
+      for (int l = tid; l < lists; l += kSelThreads) {
+        int i;
+        if (get(l, 0, i) < bound) continue;
+        const int at = atomicAdd(&sm.groups, 1);
+        if (at < kSelCap) sm.entry[at] = (uint64_t)l;
+      }
+    __syncthreads();
+    open = sm.groups;
+    for (int e = tid; e < min(open, kSelCap) * k; e += kSelThreads) {
+      int i;
+      const uint64_t x = get((int)sm.entry[e / k], e % k, i);
+      if (x >= bound) keep(x, i);
     }
   }
   __syncthreads();
-  if (lane == 0) {
-    sm.dred[warp] = (double)v;
-    sm.idx[warp] = at;
+  int count = sm.count;
+  if (count > kSelCap || open > kSelCap) {
+    uint64_t pv = ~0ull;
+    int pi = -1;
+    for (count = 0; count < k; ++count) {
+      uint64_t v = 0;
+      int at = 0x7fffffff;
+      for (int e = tid; e < lists * k; e += kSelThreads) {
+        int i;
+        const uint64_t x = get(e / k, e % k, i);
+        if (x > 0 && ahead(pv, pi, x, i) && ahead(x, i, v, at)) v = x, at = i;
+      }
+      for (int o = 16; o > 0; o >>= 1) {
+        const uint64_t w = __shfl_xor_sync(0xffffffffu, v, o);
+        const int j = __shfl_xor_sync(0xffffffffu, at, o);
+        if (ahead(w, j, v, at)) v = w, at = j;
+      }
+      __syncthreads();
+      if (lane == 0) sm.kred[warp] = v, sm.ired[warp] = at;
+      __syncthreads();
+      v = sm.kred[0], at = sm.ired[0];
+      for (int w = 1; w < kSelWarps; ++w)
+        if (ahead(sm.kred[w], sm.ired[w], v, at)) v = sm.kred[w], at = sm.ired[w];
+      if (v == 0) break;
+      if (tid == 0) sm.key[count] = v, sm.idx[count] = at;
+      pv = v;
+      pi = at;
+    }
+    __syncthreads();
+    if (tid == 0) sm.count = count;
+    __syncthreads();
+    return;
+  }
+  constexpr int kPer = kSelCap / kSelThreads;
+  uint64_t v[kPer];
+  int i[kPer], rank[kPer];
+#pragma unroll
+  for (int e = 0; e < kPer; ++e) {
+    const int a = tid + e * kSelThreads;
+    rank[e] = k;
+    if (a < count) {
+      v[e] = sm.key[a];
+      i[e] = sm.idx[a];
+      rank[e] = 0;
+#pragma unroll 4
+      for (int b = 0; b < count; ++b) rank[e] += ahead(sm.key[b], sm.idx[b], v[e], i[e]);
+    }
   }
   __syncthreads();
-  bv = (F)sm.dred[0];
-  bi = sm.idx[0];
 #pragma unroll
-  for (int w = 1; w < kSelWarps; ++w)
-    if (ahead((F)sm.dred[w], sm.idx[w], bv, bi)) {
-      bv = (F)sm.dred[w];
-      bi = sm.idx[w];
-    }
+  for (int e = 0; e < kPer; ++e)
+    if (rank[e] < k) sm.key[rank[e]] = v[e], sm.idx[rank[e]] = i[e];
+  if (tid == 0) sm.count = min(count, k);
   __syncthreads();
 }
 
-// The k best entries of the block's n-per-thread values, in order, each handed to
-// emit(rank, value, index) by one thread (ranks without an entry are not handed out).
-// Values at or above the bound are collected and ranked by counting; a list that
-// overflows (long runs of equal values) is replaced by k rounds of block-wide
-// maxima.  Returns the number of entries.
-template <typename F, typename Get, typename Emit>
-SPEC_DEV int block_top(int k, int n, Get get, Emit emit, SelShared& sm, F* red) {
-  F mine = (F)-INFINITY;
-  for (int e = 0; e < n; ++e) {
-    F x;
-    int i;
-    get(e, x, i);
-    mine = x > mine ? x : mine;
-  }
-  if (threadIdx.x == 0) sm.count = 0;
-  const F bound = block_bound<F>(mine, k, red);       // ends with a barrier
-  for (int e = 0; e < n; ++e) {
-    F x;
-    int i;
-    get(e, x, i);
-    if (x >= bound && x > (F)-INFINITY) {
-      const int at = atomicAdd(&sm.count, 1);
-      if (at < kSelCap) {
-        sm.val[at] = (double)x;
-        sm.idx[at] = i;
+// A tile's logits as a lane holds them: loads of 16 bytes (single elements where the
+// row is not aligned to that), consecutive lanes side by side.
+template <typename T> struct SelTile {
+  static constexpr int P = 16 / sizeof(T), N = kSelElems / P;
+  uint4 raw[N];
+  // element e of lane `lane`
+  SPEC_DEV static int pos(int e, int lane) { return (e / P) * 32 * P + lane * P + e % P; }
+  // n: elements of the tile that exist; the others become the type's -infinity.  A row off the 16-byte
+  // grid is read in words, a 16-bit one off the 4-byte grid in words that straddle its elements (not where
+  // that would reach over the row's ends: `inner`, an element before the tile and one after it are the row's)
+  SPEC_DEV void load(const T* p, int n, bool inner) {
+    const int lane = threadIdx.x & 31;
+    const uint32_t off = (uint32_t)reinterpret_cast<uintptr_t>(p);
+    if (n >= kSelTile && (off & 15) == 0) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) raw[i] = __ldcs(reinterpret_cast<const uint4*>(p + pos(i * P, lane)));
+    } else if (n >= kSelTile && (off & 3) == 0) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const uint32_t* q = reinterpret_cast<const uint32_t*>(p + pos(i * P, lane));
+        raw[i] = make_uint4(q[0], q[1], q[2], q[3]);
+      }
+    } else if (n >= kSelTile && inner) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const uint32_t* q = reinterpret_cast<const uint32_t*>(p + pos(i * P, lane) - 1);
+        uint32_t w[5];
+#pragma unroll
+        for (int j = 0; j < 5; ++j) w[j] = q[j];
+        raw[i] = make_uint4(__funnelshift_r(w[0], w[1], 16), __funnelshift_r(w[1], w[2], 16),
+                            __funnelshift_r(w[2], w[3], 16), __funnelshift_r(w[3], w[4], 16));
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        T v[P];
+#pragma unroll
+        for (int j = 0; j < P; ++j) v[j] = pos(i * P + j, lane) < n ? p[pos(i * P + j, lane)] : lowest();
+        raw[i] = *reinterpret_cast<const uint4*>(v);
       }
     }
   }
-  __syncthreads();
-  const int count = sm.count;
-  if (count <= kSelCap) {
-    for (int a = threadIdx.x; a < count; a += kSelThreads) {
-      const double v = sm.val[a];
-      const int i = sm.idx[a];
-      int rank = 0;
-      for (int b = 0; b < count; ++b) rank += ahead(sm.val[b], sm.idx[b], v, i);
-      if (rank < k) emit(rank, (F)v, i);
+  SPEC_DEV static T lowest() {
+    if constexpr (sizeof(T) == 4) return -INFINITY;
+    else if constexpr (std::is_same_v<T, __half>) return __ushort_as_half(0xfc00);
+    else return __ushort_as_bfloat16(0xff80);
+  }
+  SPEC_DEV void values(float* x) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const T* v = reinterpret_cast<const T*>(&raw[i]);
+#pragma unroll
+      for (int j = 0; j < P; ++j) x[i * P + j] = cvt(v[j]);
     }
-    __syncthreads();
-    return min(count, k);
   }
-  __syncthreads();
-  F pv = (F)INFINITY;
-  int pi = -1, r = 0;
-  for (; r < k; ++r) {
-    F v;
-    int i;
-    block_next<F>(pv, pi, n, get, sm, v, i);
-    if (!(v > (F)-INFINITY)) break;
-    if (threadIdx.x == 0) emit(r, v, i);
-    pv = v;
-    pi = i;
-  }
-  __syncthreads();
-  return r;
-}
+};
 
 template <typename T>
-__global__ void __launch_bounds__(kSelThreads) beam_select_kernel(const SelArgs g) {
+__global__ void __launch_bounds__(kSelThreads, 4) beam_select_kernel(const SelArgs g) {
   SPEC_TL(kTLBeamSelect);
   pdl_wait();
   pdl_trigger();
   __shared__ SelShared sm;
+  extern __shared__ float maxima[];         // [groups of a chunk]
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int ch = blockIdx.x, row = blockIdx.y, b = row / g.W, W = g.W;
-  const float my_score = g.score[row];
-  const bool live = fabsf(my_score) <= 3.402823466e38f && g.done[row] == 0;
+  if (tid < W) {
+    const float sc = g.score[b * W + tid];
+    sm.score[tid] = finite(sc) ? sc : -INFINITY;
+    sm.done[tid] = g.done[b * W + tid];
+  }
+  __syncthreads();
+  const int beam = row - b * W;
+  const bool live = sm.score[beam] > -INFINITY && sm.done[beam] == 0;
   if (live) {
-    // element e of thread t is logit base + (e / P) * (256 P) + t * P + e % P whatever the row's
-    // alignment (P elements are 16 bytes), so equal rows give equal sums
-    constexpr int P = 16 / sizeof(T);
     const T* src = static_cast<const T*>(g.logits) + (long long)row * g.ld;
-    const int base = ch * kSelChunk;
-    float x[kSelElems];
-    const bool vec = (reinterpret_cast<uintptr_t>(src) & 15) == 0;
+    const int c0 = ch * g.chunk, c1 = min(g.V, c0 + g.chunk);
+    float r = -INFINITY, s = 0.f;           // this lane's largest logit and sum of exp(x - r)
+    constexpr int kAhead = sizeof(T) == 4 ? 1 : 2;             // tiles on their way: 4 KB a warp
+    constexpr int kStep = kSelWarps * kSelTile;
+    SelTile<T> next[kAhead];
+    const int mine = c0 + warp * kSelTile;
+    auto fetch = [&](SelTile<T>& x, int at) { x.load(src + at, c1 - at, at > 0 && at + kSelTile < g.V); };
 #pragma unroll
-    for (int i = 0; i < kSelElems / P; ++i) {
-      const int v0 = base + (i * kSelThreads + tid) * P;
-      if (vec && v0 + P <= g.V) {
-        const uint4 raw = __ldcs(reinterpret_cast<const uint4*>(src + v0));
-        const T* p = reinterpret_cast<const T*>(&raw);
+    for (int a = 0; a < kAhead; ++a)
+      if (mine + a * kStep < c1) fetch(next[a], mine + a * kStep);
+    for (int base0 = mine; base0 < c1; base0 += kAhead * kStep) {
 #pragma unroll
-        for (int j = 0; j < P; ++j) x[i * P + j] = finite_or_mask(cvt(p[j]));
-      } else {
+      for (int a = 0; a < kAhead; ++a) {
+        const int base = base0 + a * kStep, then = base + kAhead * kStep;
+        if (base >= c1) break;
+        float x[kSelElems], m = -INFINITY;
+        next[a].values(x);
+        if (then < c1) fetch(next[a], then);
 #pragma unroll
-        for (int j = 0; j < P; ++j) x[i * P + j] = v0 + j < g.V ? finite_or_mask(cvt(src[v0 + j])) : -INFINITY;
+        for (int e = 0; e < kSelElems; ++e) m = fmaxf(m, x[e]);
+        auto total = [&](float ref) {
+          float a0 = 0.f, a1 = 0.f;
+#pragma unroll
+          for (int e = 0; e < kSelElems; e += 2) {
+            a0 += pow2((x[e] - ref) * kLog2e);
+            a1 += pow2((x[e + 1] - ref) * kLog2e);
+          }
+          return a0 + a1;
+        };
+        // a NaN or +infinity (not finite: masked) shows up in the sum
+        float rn = fmaxf(r, m), add = total(rn == -INFINITY ? 0.f : rn);
+        if (!(add <= 2.f * kSelElems)) {
+          m = -INFINITY;
+#pragma unroll
+          for (int e = 0; e < kSelElems; ++e) {
+            x[e] = finite(x[e]) ? x[e] : -INFINITY;
+            m = fmaxf(m, x[e]);
+          }
+          rn = fmaxf(r, m);
+          add = total(rn == -INFINITY ? 0.f : rn);
+        }
+        s = r == -INFINITY ? add : fmaf(s, pow2((r - rn) * kLog2e), add);
+        r = rn;
+        maxima[((base - c0) / kSelTile) * 32 + lane] = m;
       }
     }
-    float m = -INFINITY;
-#pragma unroll
-    for (int e = 0; e < kSelElems; ++e) m = fmaxf(m, x[e]);
-    m = warp_max(m);
-    if (lane == 0) sm.fred[warp] = m;
-    __syncthreads();
-    m = sm.fred[0];
-#pragma unroll
-    for (int w = 1; w < kSelWarps; ++w) m = fmaxf(m, sm.fred[w]);
-    // x - m first: at a type's lowest values m * log2(e) would overflow
-    const float ms = m > -INFINITY ? m : 0.f;
-    float s = 0.f;
-#pragma unroll
-    for (int e = 0; e < kSelElems; ++e) s += exp2f((x[e] - ms) * kLog2e);
-    s = warp_sum(s);
-    __syncthreads();
-    if (lane == 0) sm.fred[warp] = s;
+    // the chunk's sum, relative to its largest logit
+    const float rw = warp_max(r);
+    s = warp_sum(r == -INFINITY ? 0.f : s * pow2((r - rw) * kLog2e));
+    if (lane == 0) sm.fred[0][warp] = rw, sm.fred[1][warp] = s;
+    if (tid == 0) sm.count = sm.groups = 0;
     __syncthreads();
     if (tid == 0) {
-      s = 0.f;
-      for (int w = 0; w < kSelWarps; ++w) s += sm.fred[w];
-      g.stats[(long long)row * g.nch + ch] = make_float2(m, s);
+      float R = sm.fred[0][0], S = 0.f;
+      for (int w = 1; w < kSelWarps; ++w) R = fmaxf(R, sm.fred[0][w]);
+      for (int w = 0; w < kSelWarps; ++w)
+        if (sm.fred[0][w] > -INFINITY) S += sm.fred[1][w] * pow2((sm.fred[0][w] - R) * kLog2e);
+      g.stats[(long long)row * g.nch + ch] = make_float2(R, S);
+    }
+    // the W groups with the largest maxima (and those that equal the last of them)
+    const int groups = (c1 - c0 + kSelTile - 1) / kSelTile * 32;
+    float best = -INFINITY;
+    for (int i = tid; i < groups; i += kSelThreads) best = fmaxf(best, maxima[i]);
+    const float bound = value_of(block_bound<uint32_t>(key_of(best), W, sm));
+    if (best >= bound && best > -INFINITY)
+      for (int i = tid; i < groups; i += kSelThreads) {
+        const float m = maxima[i];
+        if (m >= bound && m > -INFINITY) {
+          const int at = atomicAdd(&sm.groups, 1);
+          if (at < kSelCap) sm.idx[at] = i, sm.key[at] = (uint64_t)key_of(m) << 32 | (uint32_t)at;
+        }
+      }
+    __syncthreads();
+    const int found = sm.groups;
+    if (tid == 0 && found < W) sm.border = -INFINITY;
+    if (found >= W && found <= kSelCap)
+      for (int a = tid; a < found; a += kSelThreads) {
+        const uint64_t v = sm.key[a];
+        int rank = 0;
+#pragma unroll 8
+        for (int i = 0; i < found; ++i) rank += sm.key[i] > v;
+        if (rank == W - 1) sm.border = value_of((uint32_t)(v >> 32));
+      }
+    if (tid == 0 && found > kSelCap) sm.border = bound;
+    __syncthreads();
+    const float border = sm.border;
+    // an entry: key and index (the smaller first) in one integer
+    auto entry = [&](int i) -> uint64_t {
+      const float x = cvt(src[i]);
+      return finite(x) && x >= border ? (uint64_t)key_of(x) << 32 | (uint32_t)~i : 0ull;
+    };
+    // their logits that reach the border: a warp takes every 8th group, the lanes its elements
+    int kept = 0;
+    if (found <= kSelCap) {
+      // places of the groups that are kept, in list order
+      for (int a = 0; a < found; a += 32) {
+        const bool in = a + lane < found && maxima[sm.idx[a + lane]] >= border;
+        unsigned who = __ballot_sync(0xffffffffu, in);
+        for (; who != 0; who &= who - 1, ++kept) {
+          if (kept % kSelWarps != warp) continue;
+          const int grp = sm.idx[a + __ffs(who) - 1], at = c0 + (grp >> 5) * kSelTile + SelTile<T>::pos(lane, grp & 31);
+          const uint64_t v = at < c1 ? entry(at) : 0ull;
+          const unsigned hit = __ballot_sync(0xffffffffu, v != 0);
+          int to = 0;
+          if (lane == 0) to = atomicAdd(&sm.count, __popc(hit));
+          to = __shfl_sync(0xffffffffu, to, 0) + __popc(hit & ((1u << lane) - 1));
+          if (v != 0 && to < kSelCap) sm.entry[to] = v;
+        }
+      }
     }
     __syncthreads();
+    int count = sm.count;
     float2* out = g.cand + ((long long)row * g.nch + ch) * W;
-    const int got = block_top<float>(
-        W, kSelElems,
-        [&](int e, float& v, int& i) {
-          v = x[e];
-          i = base + ((e / P) * kSelThreads + tid) * P + e % P;
-        },
-        [&](int r, float v, int i) { out[r] = make_float2(v, __int_as_float(i)); }, sm, sm.fred);
-    if (tid >= got && tid < W) out[tid] = make_float2(-INFINITY, __int_as_float(0x7fffffff));
+    auto put = [&](int rank, uint64_t v) { out[rank] = make_float2(value_of((uint32_t)(v >> 32)), __int_as_float(~(int)(uint32_t)v)); };
+    if (found <= kSelCap && count <= kSelCap) {
+      for (int a = tid; a < count; a += kSelThreads) {
+        const uint64_t v = sm.entry[a];
+        int rank = 0;
+#pragma unroll 8
+        for (int i = 0; i < count; ++i) rank += sm.entry[i] > v;
+        if (rank < W) put(rank, v);
+      }
+    } else {
+      // long runs of equal values: W rounds of block-wide maxima over the chunk
+      uint64_t last = ~0ull;
+      for (count = 0; count < W; ++count) {
+        uint64_t v = 0;
+        for (int i = c0 + tid; i < c1; i += kSelThreads) {
+          const uint64_t x = entry(i);
+          v = x < last && x > v ? x : v;
+        }
+        for (int o = 16; o > 0; o >>= 1) {
+          const uint64_t x = __shfl_xor_sync(0xffffffffu, v, o);
+          v = x > v ? x : v;
+        }
+        __syncthreads();
+        if (lane == 0) sm.kred[warp] = v;
+        __syncthreads();
+        for (int w = 0; w < kSelWarps; ++w) v = sm.kred[w] > v ? sm.kred[w] : v;
+        if (v == 0) break;
+        if (tid == 0) put(count, v);
+        last = v;
+      }
+    }
+    if (tid >= count && tid < W) out[tid] = make_float2(-INFINITY, __int_as_float(0x7fffffff));
   }
   // the request's last CTA merges
-  __threadfence();
   __syncthreads();
-  if (tid == 0) sm.last = atomicAdd(&g.counters[b], 1) == W * g.nch - 1;
-  __syncthreads();
-  if (!sm.last) return;
-  __threadfence();
-  if (tid == 0) g.counters[b] = 0;
-  // log-sum-exp of every live beam, in fp64
-  for (int j = warp; j < W; j += kSelWarps) {
-    const float2* st = g.stats + (long long)(b * W + j) * g.nch;
-    const float sc = g.score[b * W + j];
-    if (!(fabsf(sc) <= 3.402823466e38f) || g.done[b * W + j] != 0) continue;
-    float m = -INFINITY;
-    for (int c = lane; c < g.nch; c += 32) m = fmaxf(m, __ldcg(&st[c]).x);
-    m = warp_max(m);
-    double s = 0;
-    if (m > -INFINITY)
-      for (int c = lane; c < g.nch; c += 32) {
-        const float2 v = __ldcg(&st[c]);
-        if (v.x > -INFINITY) s += (double)v.y * exp((double)v.x - (double)m);
-      }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    if (lane == 0) sm.lse[j] = m > -INFINITY ? (double)m + log(s) : 0.0;
+  if (tid == 0) {
+    int before;
+    asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;" : "=r"(before) : "l"(&g.counters[b]) : "memory");
+    sm.last = before == W * g.nch - 1;
+    if (sm.last) g.counters[b] = 0;
   }
   __syncthreads();
-  // candidates of the request: W beams x nch chunks x W, scored in fp64
-  const int per = g.nch * W, all = W * per, n = (all + kSelThreads - 1) / kSelThreads;
-  auto get = [&](int e, double& v, int& i) {
-    const int k = e * kSelThreads + tid;
-    v = -INFINITY;
-    i = 0x7fffffff;
-    if (k >= all) return;
-    const int j = k / per, c = k - j * per;
-    const float sc = g.score[b * W + j];
-    if (!(fabsf(sc) <= 3.402823466e38f)) return;
-    if (g.done[b * W + j] != 0) {
-      if (c == 0) {
-        v = (double)sc;
-        i = j * g.V + max(g.eos, 0);
-      }
-      return;
+  if (!sm.last) return;
+  // log-sum-exp of every live beam: log2 of the sum with its exponent apart, so that fp32 is enough
+  for (int j = warp; j < W; j += kSelWarps) {
+    if (sm.score[j] == -INFINITY || sm.done[j] != 0) continue;
+    const float2* st = g.stats + (long long)(b * W + j) * g.nch;
+    float R = -INFINITY, s = 0.f;
+    for (int c = lane; c < g.nch; c += 32) {
+      const float2 v = __ldcg(&st[c]);
+      const float rn = fmaxf(R, v.x);
+      if (rn > -INFINITY) s = s * pow2((R - rn) * kLog2e) + v.y * pow2((v.x - rn) * kLog2e);
+      R = rn;
     }
-    const float2 x = __ldcg(&g.cand[(long long)(b * W + j) * per + c]);
-    if (!(x.x > -INFINITY)) return;
-    v = (double)sc + ((double)x.x - sm.lse[j]);
-    i = j * g.V + __float_as_int(x.y);
-  };
-  const int got = block_top<double>(
-      W, n, get,
-      [&](int r, double v, int i) {
-        const int j = i / g.V, o = b * W + r;
-        const bool fin = g.done[b * W + j] != 0;
-        const int t = fin ? g.eos : i - j * g.V;
-        g.parent[o] = j;
-        g.tok[o] = t;
-        g.score_out[o] = (float)v;
-        g.done_out[o] = fin || t == g.eos;
+    const float rw = warp_max(R);
+    s = warp_sum(R > -INFINITY ? s * pow2((R - rw) * kLog2e) : 0.f);
+    if (lane == 0) {
+      double l = 0;
+      if (s > 0.f) {
+        const int e = (int)(__float_as_uint(s) >> 23) - 127;
+        l = (double)rw + (double)((float)e) * 0.6931471805599453 +
+            (double)(log2f(__uint_as_float(__float_as_uint(s) - ((uint32_t)e << 23))) * 0.69314718f);
+      }
+      sm.lse[j] = l;
+    }
+  }
+  __syncthreads();
+  // candidates of the request: the lists of W beams x nch chunks, scored in fp64
+  block_best(
+      W, W * g.nch,
+      [&](int l, int c, int& i) -> uint64_t {
+        const int j = l / g.nch;
+        const float sc = sm.score[j];
+        if (sc == -INFINITY) return 0;
+        if (sm.done[j] != 0) {
+          i = j * g.V + max(g.eos, 0);
+          return c == 0 && l == j * g.nch ? key_of((double)sc) : 0;
+        }
+        const float2 x = __ldcg(&g.cand[((long long)b * W * g.nch + l) * W + c]);
+        if (!(x.x > -INFINITY)) return 0;
+        i = j * g.V + __float_as_int(x.y);
+        return key_of((double)sc + ((double)x.x - sm.lse[j]));
       },
-      sm, sm.dred);
-  if (tid >= got && tid < W) {
+      sm);
+  if (tid < W) {
     const int o = b * W + tid;
-    g.parent[o] = tid;
-    g.tok[o] = -1;
-    g.score_out[o] = -INFINITY;
-    g.done_out[o] = 1;
+    if (tid < sm.count) {
+      const int i = sm.idx[tid], j = i / g.V;
+      const bool fin = sm.done[j] != 0;
+      const int t = fin ? g.eos : i - j * g.V;
+      g.parent[o] = j;
+      g.tok[o] = t;
+      g.score_out[o] = (float)value_of(sm.key[tid]);
+      g.done_out[o] = fin || t == g.eos;
+    } else {
+      g.parent[o] = tid;
+      g.tok[o] = -1;
+      g.score_out[o] = -INFINITY;
+      g.done_out[o] = 1;
+    }
   }
 }
 
-static int sel_chunks(int V) { return (V + kSelChunk - 1) / kSelChunk; }
+// chunks of a row: the same for every row of a call
+static int sel_chunks(int B, int W, int V, int* chunk) {
+  constexpr int kStep = kSelWarps * kSelTile;
+  const int steps = (V + kStep - 1) / kStep;
+  // one chunk an SM (a chunk's end costs ~3 us: 32 x 8 rows of 151936, 2 / 4 / 8 chunks a row 33.9 / 38.4 /
+  // 45.4 us), of at least two steps (one row's worth of merging: 4 rows of 128256, 32 / 16 chunks 9.3 / 7.8 us)
+  int want = std::min((152 + B * W - 1) / (B * W), (steps + 1) / 2);
+  want = std::max(want, (steps + kSelChunk / kStep - 1) / (kSelChunk / kStep));
+  const int per = (steps + want - 1) / want;
+  *chunk = per * kStep;
+  return (steps + per - 1) / per;
+}
 
 // ---------------------------------------------------------------- reordering
 constexpr int kMaxLayers = 64;
@@ -433,8 +656,9 @@ using namespace spec;
 
 extern "C" size_t spec_beam_workspace_bytes(int32_t B, int32_t W, int32_t V) {
   if (B <= 0 || W <= 0 || W > 32 || V <= 0 || (long long)W * V >= (1ll << 30)) return 0;
-  const size_t n = (size_t)B * W * sel_chunks(V);
-  return kWsHeader + align_up((size_t)B * 4, 256) + align_up(n * 8, 256) + align_up(n * W * 8, 256);
+  int chunk;
+  const size_t n = (size_t)B * W * sel_chunks(B, W, V, &chunk);
+  return kWsHeader + kSelCounterBytes + align_up(n * 8, 256) + align_up(n * W * 8, 256);
 }
 
 extern "C" spec_status spec_beam_select(int32_t B, int32_t W, int32_t V, int32_t dtype, const void* logits, int64_t ld,
@@ -450,20 +674,21 @@ extern "C" spec_status spec_beam_select(int32_t B, int32_t W, int32_t V, int32_t
   if (ld < V) return SPEC_ERR_SHAPE;
   if (!aligned(logits, dtype == SPEC_DTYPE_F32 ? 4 : 2)) return SPEC_ERR_ALIGN;
   if (!ws || !aligned(ws, 256) || ws_bytes < need) return SPEC_ERR_WORKSPACE;
-  const int nch = sel_chunks(V);
+  int chunk;
+  const int nch = sel_chunks(B, W, V, &chunk);
   char* p = static_cast<char*>(ws) + kWsHeader;
   SelArgs g{};
-  g.B = B, g.W = W, g.V = V, g.nch = nch, g.eos = eos < 0 ? -1 : eos, g.ld = ld;
+  g.B = B, g.W = W, g.V = V, g.nch = nch, g.chunk = chunk, g.eos = eos < 0 ? -1 : eos, g.ld = ld;
   g.logits = logits, g.score = score, g.done = done;
   g.parent = parent, g.tok = tok, g.done_out = done_out, g.score_out = score_out;
   g.counters = reinterpret_cast<int*>(p);
-  p += align_up((size_t)B * 4, 256);
+  p += kSelCounterBytes;
   g.stats = reinterpret_cast<float2*>(p);
   p += align_up((size_t)B * W * nch * 8, 256);
   g.cand = reinterpret_cast<float2*>(p);
   auto* kern = dtype == SPEC_DTYPE_F32 ? beam_select_kernel<float>
                : dtype == SPEC_DTYPE_BF16 ? beam_select_kernel<__nv_bfloat16> : beam_select_kernel<__half>;
-  launch_pdl(kern, dim3(nch, B * W), dim3(kSelThreads), 0, stream, g);
+  launch_pdl(kern, dim3(nch, B * W), dim3(kSelThreads), (size_t)chunk / kSelElems * 4, stream, g);
   return last_launch();
 }
 

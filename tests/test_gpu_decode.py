@@ -391,6 +391,26 @@ def test_beam_select_ties_go_to_the_first(W):
         run_select(x, np.full((2, W), -1.5), np.zeros((2, W), dtype=int), 3, "bf16", V + 1)
 
 
+@pytest.mark.parametrize("W", [1, 5, 32])
+@pytest.mark.parametrize("t", ["f32", "f16"])
+def test_beam_select_rows_that_keep_rising(t, W):
+    """Every later logit beats the best so far: the running candidate list overflows again and again."""
+    V = 30011
+    up = torch.arange(V, device="cuda") / V * 20 - 10
+    x = torch.stack([up, up.flip(0), torch.where(torch.arange(V, device="cuda") % 5000 == 4999, up, -math.inf)])
+    x = x.repeat(1, W).view(3, W, V) + torch.arange(W, device="cuda")[:, None] * 0.25
+    run_select(x, -np.arange(3 * W).reshape(3, W) * 0.125, np.zeros((3, W), dtype=int), 7, t, V + 3)
+
+
+@pytest.mark.parametrize("t", ["f32", "bf16", "f16"])
+def test_beam_select_rows_of_the_lowest_value_are_uniform(t):
+    x = torch.full((2, 2, 9001), torch.finfo(TYPES[t]).min, device="cuda")
+    x[1, 0, 17] = 3.0
+    x[1, 1, 5] = -0.0
+    x[1, 1, 6] = 0.0
+    run_select(x, np.array([[-1.0, -2.0], [-1.0, -1.0]]), np.zeros((2, 2), dtype=int), 3, t)
+
+
 # ------------------------------------------------------------------ reordering
 @pytest.mark.parametrize("t", ["bf16", "f32", "e4m3"])
 @pytest.mark.parametrize("B,W,bs,layers,nkv,hd", [(1, 4, 16, 1, 8, 128), (5, 3, 4, 3, 1, 16), (3, 8, 1, 2, 2, 64), (9, 2, 24, 2, 1, 80),
