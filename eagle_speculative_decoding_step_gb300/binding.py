@@ -155,8 +155,14 @@ def _p(t):
     return t.data_ptr()
 
 
+# the raw handle of the current stream: building torch's Stream object around it costs 2.6 us a call
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream():
-    return torch.cuda.current_stream().cuda_stream
+    if _raw_stream is None:
+        return torch.cuda.current_stream().cuda_stream
+    return _raw_stream(torch.cuda.current_device())
 
 
 def _check(st, what):
