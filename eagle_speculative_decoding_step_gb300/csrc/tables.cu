@@ -7,6 +7,7 @@
 #include <cuda_fp8.h>
 
 #include <algorithm>
+#include <cmath>
 
 #include "common.cuh"
 #include "internal.h"
@@ -121,32 +122,16 @@ __global__ void __launch_bounds__(kTabThreads) block_tables_kernel(const TabArgs
   auto is_served = [&](int b) { return b < cut || (b > 0 && s_need[b] == s_need[b - 1]); };
   auto want_of = [&](int b) { return is_served(b) ? (s_new[b] + bs - 1) / bs : have_of(b); };
 
-  if (tid == 0) {
-    if (gridDim.x == 1) {
-      s_last = 1;
-    } else {
-      int* ctr = reinterpret_cast<int*>(static_cast<char*>(g.ws) + kWsHeader);
-      __threadfence();
-      s_last = atomicAdd(ctr, 1) == (int)gridDim.x - 1;
-      if (s_last) *ctr = 0;
-    }
-  }
-  __syncthreads();
-  if (s_last) {
-    if (tid == 0) {
-      *g.n_free_out = min(left, g.num_blocks);
-      if (carry[1] > avail || total > g.cap) report(g.ws, SPEC_ERR_CAPACITY, carry[1], avail);
-      if (left > g.num_blocks) report(g.ws, SPEC_ERR_DEVICE, left, g.num_blocks);
-      g.cu_new[0] = 0;
-    }
-    for (int b = tid; b < B; b += kTabThreads) {
-      g.cu_new[b + 1] = s_cnt[b];
-      g.len_out[b] = is_served(b) ? s_new[b] : s_old[b];
-    }
-  }
+  // this CTA has read what is replaced at the end; the answer is not looked at before that
+  int* ctr = reinterpret_cast<int*>(static_cast<char*>(g.ws) + kWsHeader);
+  int arrived = 0;
+  if (tid == 0) asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;" : "=r"(arrived) : "l"(ctr) : "memory");
 
   const int gt = blockIdx.x * kTabThreads + tid, gn = gridDim.x * kTabThreads;
   const bool out_of_place = g.table_out != g.table_in, pool_moves = g.free_out != g.free_in;
+  auto on16 = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; };
+  const bool vec_pool = on16(g.free_in) && on16(g.free_out);
+  const bool vec_table = mb % 4 == 0 && on16(g.table_in) && on16(g.table_out);
   // the j-th id of the pool with the released blocks on top
   auto pool_id = [&](int j) {
     int id;
@@ -166,47 +151,73 @@ __global__ void __launch_bounds__(kTabThreads) block_tables_kernel(const TabArgs
     return id;
   };
   // what stays in the pool (an entry of the free list that stays where it is is not
-  // written in place), and -1 past its end
-  for (int j = gt; j < g.num_blocks; j += gn) {
-    if (j < left) {
-      if (j >= n_free) g.free_out[j] = pool_id(j);
-      else if (pool_moves) g.free_out[j] = g.free_in[j];
-    } else if (pool_moves) {
-      g.free_out[j] = -1;
+  // written in place), and -1 past its end; four entries a thread
+  for (int j0 = 4 * gt; j0 < g.num_blocks; j0 += 4 * gn) {
+    const bool four = pool_moves && j0 + 4 <= g.num_blocks && vec_pool;
+    if (four && j0 + 4 <= min(left, n_free)) {
+      *reinterpret_cast<int4*>(g.free_out + j0) = *reinterpret_cast<const int4*>(g.free_in + j0);
+    } else if (four && j0 >= left) {
+      *reinterpret_cast<int4*>(g.free_out + j0) = make_int4(-1, -1, -1, -1);
+    } else {
+      for (int j = j0; j < min(j0 + 4, g.num_blocks); ++j) {
+        if (j < left) {
+          if (j >= n_free) g.free_out[j] = pool_id(j);
+          else if (pool_moves) g.free_out[j] = g.free_in[j];
+        } else if (pool_moves) {
+          g.free_out[j] = -1;
+        }
+      }
     }
   }
-  // deliveries: 2^lg lanes a block, so that a block's slots are written together
+  // deliveries: a lane takes a block and finds whose it is, then 2^lg lanes write a block's slots
   int lg = 0;
   while (lg < 5 && (1 << lg) < bs) ++lg;
-  const int part = lane & ((1 << lg) - 1), lead = lane & ~((1 << lg) - 1);
-  for (int base = (gt & ~31) >> lg; base < taken; base += gn >> lg) {
-    const int i = base + (lane >> lg);               // the i-th block taken
-    int id = -1;
-    if (i < taken && part == 0) {
+  const int part = lane & ((1 << lg) - 1);
+  constexpr int kTake = 8;                           // blocks of a warp: few, so that many warps share them
+  for (int base = (gt >> 5) * kTake; base < taken; base += (gn >> 5) * kTake) {
+    const int i = lane < kTake ? base + lane : taken;  // the i-th block taken
+    int id = -1, first = 0, end = 0, to = 0;         // tokens [first, end) of the block, slot entry of token 0
+    int e = 0;
+    if (i < taken) {
       const int j = avail - 1 - i;
       id = pool_id(j);
       if (!pool_moves && j < n_free) g.free_out[j] = -1;
+      const int b = first_above(s_need, B, i);
+      e = have_of(b) + i - (b > 0 ? s_need[b - 1] : 0);
+      g.table_out[(long long)b * mb + e] = id;
+      to = (b > 0 ? s_cnt[b - 1] : 0) - s_old[b];
+      first = max(s_old[b], e * bs);
+      end = min(s_new[b], (e + 1) * bs);
     }
-    id = __shfl_sync(0xffffffffu, id, lead);
-    if (i >= taken) continue;
-    const int b = first_above(s_need, B, i);
-    const int e = have_of(b) + i - (b > 0 ? s_need[b - 1] : 0);
-    if (part == 0) g.table_out[(long long)b * mb + e] = id;
-    const int off = (b > 0 ? s_cnt[b - 1] : 0) - s_old[b];
-    const int end = min(s_new[b], (e + 1) * bs);
-    for (int t = max(s_old[b], e * bs) + part; t < end; t += 1 << lg)
-      if (off + t < g.cap) {
-        g.slots[off + t] = id < 0 ? -1 : id * bs + (t - e * bs);
-        if (g.pos) g.pos[off + t] = t;
-      }
+    const int valid = min(kTake, taken - base);
+    for (int from0 = 0; from0 < valid; from0 += 32 >> lg) {
+      const int from = (from0 + (lane >> lg)) & 31;
+      const int id_ = __shfl_sync(0xffffffffu, id, from), end_ = __shfl_sync(0xffffffffu, end, from);
+      const int to_ = __shfl_sync(0xffffffffu, to, from), e0 = __shfl_sync(0xffffffffu, e, from) * bs;
+      for (int t = __shfl_sync(0xffffffffu, first, from) + part; t < end_; t += 1 << lg)
+        if (to_ + t < g.cap) {
+          g.slots[to_ + t] = id_ < 0 ? -1 : id_ * bs + (t - e0);
+          if (g.pos) g.pos[to_ + t] = t;
+        }
+    }
   }
-  // kept entries, and -1 past a request's blocks
+  // kept entries, and -1 past a request's blocks: a warp takes 128 entries of a row
   if (out_of_place) {
-    const int entries = B * mb;
-    for (int k = gt; k < entries; k += gn) {
-      const int b = k / mb, i = k - b * mb, want = want_of(b);
-      if (i < min(have_of(b), want)) g.table_out[k] = g.table_in[k];
-      else if (i >= want) g.table_out[k] = -1;
+    const int segs = (mb + 127) >> 7;
+    for (int task = gt >> 5; task < B * segs; task += gn >> 5) {
+      const int b = task / segs, i0 = (task - b * segs) * 128 + 4 * lane, want = want_of(b), keep = min(have_of(b), want);
+      const int32_t* in = g.table_in + (long long)b * mb + i0;
+      int32_t* out = g.table_out + (long long)b * mb + i0;
+      if (vec_table && i0 + 4 <= keep) {
+        *reinterpret_cast<int4*>(out) = *reinterpret_cast<const int4*>(in);
+      } else if (vec_table && i0 >= want && i0 + 4 <= mb) {
+        *reinterpret_cast<int4*>(out) = make_int4(-1, -1, -1, -1);
+      } else {
+        for (int i = 0; i < 4 && i0 + i < mb; ++i) {
+          if (i0 + i < keep) out[i] = in[i];
+          else if (i0 + i >= want) out[i] = -1;
+        }
+      }
     }
   }
   // tokens of blocks that were there before, a warp a request; all tokens of a request
@@ -234,6 +245,23 @@ __global__ void __launch_bounds__(kTabThreads) block_tables_kernel(const TabArgs
     g.slots[k] = -1;
     if (g.pos) g.pos[k] = 0;
   }
+  // by the last CTA to have read them: the lengths, the pool's size, the prefix sums
+  if (tid == 0) {
+    s_last = arrived == (int)gridDim.x - 1;
+    if (s_last) *ctr = 0;
+  }
+  __syncthreads();
+  if (!s_last) return;
+  if (tid == 0) {
+    *g.n_free_out = min(left, g.num_blocks);
+    if (carry[1] > avail || total > g.cap) report(g.ws, SPEC_ERR_CAPACITY, carry[1], avail);
+    if (left > g.num_blocks) report(g.ws, SPEC_ERR_DEVICE, left, g.num_blocks);
+    g.cu_new[0] = 0;
+  }
+  for (int b = tid; b < B; b += kTabThreads) {
+    g.cu_new[b + 1] = s_cnt[b];
+    g.len_out[b] = is_served(b) ? s_new[b] : s_old[b];
+  }
 }
 
 // ---------------------------------------------------------------- K/V append
@@ -243,20 +271,33 @@ SPEC_DEV float to_f(float x) { return x; }
 SPEC_DEV float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
 SPEC_DEV float to_f(__half x) { return __half2float(x); }
 
-// value in the cache's type.  E4M3: x / scale in fp32 (the quotient, not a product
-// with the reciprocal, so that values next to a rounding border go the way the
-// definition says), then one rounding to nearest even, saturating
-template <typename T, typename C> SPEC_DEV C stored(T x, float scale) {
+// Value in the cache's type.  E4M3: the fp32 quotient x / scale, then one rounding to
+// nearest even, saturating.  The quotient itself takes more instructions than the
+// copy can hide, so it is only taken where it matters: with a power of two for scale
+// the product with its reciprocal is the quotient; otherwise the product is within 2
+// steps of it, and rounds the same way unless it lies next to a border between two
+// 8-bit values (a middle of the 20 bits that are dropped, or a number too small for
+// the type's normal ones).
+template <typename T, typename C, bool EXACT> SPEC_DEV C stored(T x, float scale, float inv) {
   if constexpr (sizeof(C) == 1) {
-    return __nv_cvt_float_to_fp8(__fdiv_rn(to_f(x), scale), __NV_SATFINITE, __NV_E4M3);
+    float y = to_f(x) * inv;
+    if constexpr (!EXACT) {
+      const uint32_t past = (__float_as_uint(y) + 4u - 0x80000u) & 0xfffffu;
+      if (past < 8u || fabsf(y) < 0.015625f) y = __fdiv_rn(to_f(x), scale);
+    }
+    return __nv_cvt_float_to_fp8(y, __NV_SATFINITE, __NV_E4M3);
   } else {
     return x;
   }
 }
+static bool power_of_two(float s) {
+  int e;
+  return frexpf(s, &e) == 0.5f && e > -120 && e < 120;
+}
 
 // Rows to slots, bound by the bytes moved.  2^lg lanes share a row (as many as it
 // has vectors of eight elements, at most a warp), blockIdx.y picks K or V.
-template <typename T, typename C, bool VEC>
+template <typename T, typename C, bool VEC, bool EXACT>
 __global__ void __launch_bounds__(256) cache_append_kernel(const T* __restrict__ k, const T* __restrict__ v,
                                                            long long ld, const int32_t* __restrict__ slots, int n,
                                                            C* __restrict__ ck, C* __restrict__ cv, int width,
@@ -267,42 +308,57 @@ __global__ void __launch_bounds__(256) cache_append_kernel(const T* __restrict__
   pdl_trigger();
   const T* __restrict__ src = blockIdx.y ? v : k;
   C* __restrict__ dst = blockIdx.y ? cv : ck;
-  const float scale = blockIdx.y ? v_scale : k_scale;
+  const float scale = blockIdx.y ? v_scale : k_scale, inv = 1.f / scale;
   const int per = 1 << lg, part = threadIdx.x & (per - 1);
   const long long row = (long long)blockIdx.x * (256 >> lg) + (threadIdx.x >> lg);
   if (row >= n) return;
-  const int slot = slots[row];
-  if (slot < 0 || slot >= num_slots) {
-    if (slot != -1 && part == 0) report(ws, SPEC_ERR_DEVICE, (int)row, slot);
-    return;
-  }
   const T* s = src + row * ld;
-  C* d = dst + (long long)slot * width;
   if constexpr (VEC) {
+    // four vectors on their way before the slot is looked at
+    constexpr int kBatch = 4;
     const int nv = width >> 3;
-#pragma unroll 4
-    for (int i = part; i < nv; i += per) {
-      const Vec8<T> x = [&] {
-        Vec8<T> y;
-        const uint4* p = reinterpret_cast<const uint4*>(s + 8 * i);
-        uint4* q = reinterpret_cast<uint4*>(&y);
-        q[0] = __ldcs(p);
-        if constexpr (sizeof(T) == 4) q[1] = __ldcs(p + 1);
-        return y;
-      }();
-      Vec8<C> o;
+    int slot = 0;
+    for (int i0 = part; i0 < nv; i0 += kBatch * per) {
+      Vec8<T> x[kBatch];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) o.v[j] = stored<T, C>(x.v[j], scale);
-      if constexpr (sizeof(C) == 1) {
-        *reinterpret_cast<uint2*>(d + 8 * i) = *reinterpret_cast<uint2*>(&o);
-      } else {
-        uint4* q = reinterpret_cast<uint4*>(d + 8 * i);
-        q[0] = reinterpret_cast<uint4*>(&o)[0];
-        if constexpr (sizeof(C) == 4) q[1] = reinterpret_cast<uint4*>(&o)[1];
+      for (int j = 0; j < kBatch; ++j)
+        if (i0 + j * per < nv) {
+          const uint4* p = reinterpret_cast<const uint4*>(s + 8 * (i0 + j * per));
+          uint4* q = reinterpret_cast<uint4*>(&x[j]);
+          q[0] = __ldcs(p);
+          if constexpr (sizeof(T) == 4) q[1] = __ldcs(p + 1);
+        }
+      if (i0 == part) {
+        slot = slots[row];
+        if (slot < 0 || slot >= num_slots) {
+          if (slot != -1 && part == 0) report(ws, SPEC_ERR_DEVICE, (int)row, slot);
+          return;
+        }
       }
+      C* d = dst + (long long)slot * width;
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j)
+        if (i0 + j * per < nv) {
+          Vec8<C> o;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) o.v[e] = stored<T, C, EXACT>(x[j].v[e], scale, inv);
+          C* w = d + 8 * (i0 + j * per);
+          if constexpr (sizeof(C) == 1) {
+            *reinterpret_cast<uint2*>(w) = *reinterpret_cast<uint2*>(&o);
+          } else {
+            reinterpret_cast<uint4*>(w)[0] = reinterpret_cast<uint4*>(&o)[0];
+            if constexpr (sizeof(C) == 4) reinterpret_cast<uint4*>(w)[1] = reinterpret_cast<uint4*>(&o)[1];
+          }
+        }
     }
   } else {
-    for (int i = part; i < width; i += per) d[i] = stored<T, C>(s[i], scale);
+    const int slot = slots[row];
+    if (slot < 0 || slot >= num_slots) {
+      if (slot != -1 && part == 0) report(ws, SPEC_ERR_DEVICE, (int)row, slot);
+      return;
+    }
+    C* d = dst + (long long)slot * width;
+    for (int i = part; i < width; i += per) d[i] = stored<T, C, EXACT>(s[i], scale, inv);
   }
 }
 
@@ -316,7 +372,10 @@ static void launch_append(const spec_attn_desc& d, const void* k, const void* v,
                    aligned(kv.v, 16);
   const int rows = 256 >> lg;
   const dim3 grid((n + rows - 1) / rows, 2);
-  auto* kern = vec ? cache_append_kernel<T, C, true> : cache_append_kernel<T, C, false>;
+  auto* kern = vec ? cache_append_kernel<T, C, true, true> : cache_append_kernel<T, C, false, true>;
+  if constexpr (sizeof(C) == 1)
+    if (!power_of_two(d.k_scale) || !power_of_two(d.v_scale))
+      kern = vec ? cache_append_kernel<T, C, true, false> : cache_append_kernel<T, C, false, false>;
   launch_pdl(kern, grid, dim3(256), 0, st, (const T*)k, (const T*)v, ld, slots, n, (C*)kv.k, (C*)kv.v, width,
              (int)kv.num_slots, d.k_scale, d.v_scale, lg, ws);
 }
@@ -347,9 +406,11 @@ extern "C" spec_status spec_block_tables(int32_t B, int32_t block_size, int32_t 
   if (!ws || !aligned(ws, 256) || ws_bytes < spec_block_tables_workspace_bytes(B)) return SPEC_ERR_WORKSPACE;
   TabArgs a{B, block_size, max_blocks, num_blocks, slots_cap, len_old, len_new, table_in, free_in, n_free_in,
             table_out, free_out, n_free_out, len_out, cu_new, slots, pos, ws};
-  // a CTA per 8192 items it may have to touch: below that a second CTA's scan costs more than its share saves
+  // a CTA per 1024 items it may have to touch, up to three an SM: every CTA scans the requests for itself
+  // (64 requests of 8000 tokens 5.6 us from 512 to 2048 items a CTA; 512 requests, 1 million new tokens,
+  // 1 / 2 / 3 / 4 CTAs an SM 22.1 / 15.5 / 14.7 / 15.9 us)
   const long long items = (table_out != table_in ? (long long)B * max_blocks : 0) + num_blocks + slots_cap;
-  const int grid = (int)std::min<long long>(std::max<long long>(1, items / 8192), sm_count());
+  const int grid = (int)std::min<long long>(std::max<long long>(1, items / 1024), 3 * sm_count());
   const size_t smem = (size_t)5 * B * 4;
   if (smem > 48 * 1024 &&
       cudaFuncSetAttribute(block_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
