@@ -101,26 +101,25 @@ static bool run_map(CUtensorMap* tm, const void* ptr, const spec_attn_desc& d, c
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Heads of a tile: the cheapest by share_out() with every request as long as the longest.  Copies of less than 16 KB
+// cost more where a request's heads are not all under way at once (64 requests of up to 8190 keys, 8 heads of 256
+// bytes, 4 / 2 / 1 heads a tile, copies of 16 / 8 / 4 KB: 166 / 179 / 212 us; 16 requests of 4000: 48.1 / 47.8 / 47.0), and always in 8 bits (64 requests, 8 / 4 heads 101 /
+// 110 us).
 static Plan plan(const Kernel& k, const spec_attn_desc& d, int B, int max_len, int block_size, int sms) {
-  Plan q{};
+  Plan q{}, best{};
   plan_queries(k, d.n_q_heads / d.n_kv_heads, &q);
-  // heads of a tile: as many as make a copy 16 KB (more do not stream faster: 64 requests of 4000 keys,
-  // 8 heads of 256 bytes: 1 / 2 / 4 / 8 heads 92.5 / 89.6 / 88.4 / 88.9 us; 8 heads of 128 bytes in 8 bits:
-  // 212 / 165 / 138 / 126), but fewer where that would cut a request's tiles into more than 6 pieces, each
-  // of which the joining CTA has to read (one request of 2000 keys: 13.0 / 13.5 / 15.2 / 22.1 us)
-  const int bytes = (block_size % 8 == 0 ? 16 : 1) * d.head_dim * k.es;
-  int nh = 1;
-  while (d.n_kv_heads % (2 * nh) == 0 && 2 * nh * q.qt <= k.warps / k.vs && nh * bytes < 16384) nh *= 2;
   const int len = d.window > 0 ? std::min(d.window, max_len) : max_len;
-  // as many as there are where the requests alone give every SM work: fewer, longer items (1000 requests of 20 keys:
-  // 4 / 8 heads 46.3 / 37.8 us; 200 of 1500: within 2 %)
-  while (d.n_kv_heads % (2 * nh) == 0 && 2 * nh * q.qt <= k.warps / k.vs && B * (d.n_kv_heads / (2 * nh)) >= sms) nh *= 2;
-  for (; nh > 1; nh /= 2) {
+  float least = 0.f;
+  for (int nh = 1; d.n_kv_heads % nh == 0 && nh * q.qt <= k.warps / k.vs; nh *= 2) {
     const Plan p = make(k, d, nh, B, block_size);
-    const double tiles = (double)(len + p.kt - 1) / p.kt;
-    if (std::min(tiles, (double)sms / ((double)B * p.hgq)) <= 6) break;
+    const int tiles = std::max(1, (len + p.kt - 1) / p.kt);
+    const long long items = (long long)B * p.hgq, copy = (long long)(p.swz ? 1 << p.run_lg : 1) * nh * d.head_dim * k.es;
+    int cuts;
+    const float cost = share_out(items * tiles, items, tiles, p.kg, sms, &cuts) *
+                       (copy >= 16384 || (items <= sms && k.es > 1) ? 1.f : copy >= 8192 ? 1.08f : 1.25f);
+    if (nh == 1 || cost < least) least = cost, best = p;
   }
-  return make(k, d, nh, B, block_size);
+  return best;
 }
 
 static bool check(const spec_attn_desc* d) {

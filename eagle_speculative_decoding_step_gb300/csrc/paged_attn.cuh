@@ -63,6 +63,46 @@ struct Args {
   void* ws;
 };
 
+// What it costs, in tiles (64 KB, ~1.35 us), to leave n pieces of an item and join
+// them: the exchange itself, a second level beyond kFlat pieces, and the pieces that
+// the joining CTA reads one after another, its kg key groups taking turns.
+__host__ __device__ inline float join_cost(int n, float per_kg) {
+  if (n <= 1) return 0.f;
+  const float reads = n > kFlat ? 2.f * sqrtf((float)n) + 1.f : (float)n;
+  return (n > kFlat ? 2.5f : 1.5f) + 0.37f * fmaxf(reads * per_kg, 1.f);
+}
+
+// How `total` tiles of `items` (request, head group)s, the longest of `most` tiles, are
+// shared out: in `cuts` equal pieces an item, a CTA each, or (cuts = 0) in equal
+// shares of the tiles in a row, which begin and end inside items.  Returns the cost
+// in tiles.  Measured: 16 requests of 1000 keys, 128 items of 8 tiles, 15.8 us whole,
+// 19.7 in shares; 32 items of 8 tiles 10.4 us in 4 pieces each, 13.0 in shares; 64
+// requests of 8190 keys, 128 items of 256 tiles, in shares.
+//
+// In fp32 throughout: every CTA works it out for itself before it can start (integer
+// divisions made a call of one key 0.6 us longer).
+__host__ __device__ inline float share_out(long long total_, long long items_, int most, int kg, int ctas, int* cuts) {
+  const float total = (float)total_, items = (float)items_, used = fminf(total, (float)ctas), per_kg = 1.f / (float)kg;
+  // merging the key groups; ~0.8 tiles for every further item that a share touches
+  const float base = kg == 1 ? 0.f : kg == 2 ? 0.1f : kg == 4 ? 0.2f : 0.3f;
+  float best = total / used + 2.f + 0.8f * items / used;
+  const int pieces = (int)((used + 0.5f) / items) + 1;
+  best += join_cost(pieces > 2 ? pieces : 2, per_kg);
+  *cuts = 0;
+  if (items <= (float)ctas) {
+    const int room = (int)(((float)ctas + 0.5f) / items), all = room < most ? room : most;
+    const int few = all < kFlat ? all : kFlat;
+    if ((float)most <= best) best = (float)most, *cuts = 1;
+    const float c8 = ceilf(((float)most - 0.5f) / (float)few) + join_cost(few, per_kg);
+    if (c8 < best) best = c8, *cuts = few;
+    if (all > few) {
+      const float ca = ceilf(((float)most - 0.5f) / (float)all) + join_cost(all, per_kg);
+      if (ca < best) best = ca, *cuts = all;
+    }
+  }
+  return best + base;
+}
+
 // A consumer warp's running state for one (kv head, query tile): unnormalised
 // outputs o, running maxima m (log2 units) and sums l, in the layout of its math.
 // Register r of o belongs to statistics index st(r).
@@ -616,9 +656,9 @@ template <typename M, typename Get> SPEC_DEV void join(typename M::S& s, Get get
   for (int r = 0; r < S::NR; ++r) s.o[r] = s.o[r] * a[M::st(r)] + get(r) * b[M::st(r)];
 }
 
-// The linear order of a launch's tiles: (request, head group, tile); CTA c owns
-// tiles [c T / C, (c + 1) T / C).  Every CTA finds its range by bisection of the
-// prefix sums of the requests' tile counts.
+// The linear order of a launch's tiles: (request, head group, tile).  CTA c owns tiles
+// [c T / C, (c + 1) T / C), or a piece of one item.  Every CTA finds its range by
+// bisection of the prefix sums of the requests' tile counts.
 struct Walk {
   const int* pre;       // [B + 1] exclusive prefix sums of tile counts
   int hgq;
@@ -672,7 +712,7 @@ __global__ void __launch_bounds__(M::kWarps * 32 + 64, 1) paged_attention_kernel
   float* mscr = exch + exchange_floats<M>();
   int* pre = reinterpret_cast<int*>(mscr + NW * math_scratch<M>());
   int* lens = pre + g.B + 1;
-  __shared__ int wsum[NW + 2];
+  __shared__ int wsum[NW + 2], wmax[NW + 2];
   const uint32_t full0 = tc::su32(bars), empty0 = full0 + 8 * kMaxSlots;
   if (tid == 0) {
     for (int i = 0; i < p.slots; ++i) {
@@ -694,7 +734,7 @@ __global__ void __launch_bounds__(M::kWarps * 32 + 64, 1) paged_attention_kernel
   const long long most_l = (long long)g.kv.max_blocks * g.kv.block_size;
   const int most = (int)most_l;
   auto first_key = [&](int len) { return g.window > 0 && len > g.window ? len - g.window : 0; };
-  int carry = 0;
+  int carry = 0, most_tiles = 0;
   for (int base = 0; base < g.B; base += NW * 32 + 64) {
     const int b = base + tid;
     int x = 0;
@@ -709,26 +749,53 @@ __global__ void __launch_bounds__(M::kWarps * 32 + 64, 1) paged_attention_kernel
       if (p.swz) lo &= -1 << p.run_lg;       // tiles start with a run
       x = max(1, (len - lo + p.kt - 1) / p.kt);
     }
+    const int largest = __reduce_max_sync(0xffffffffu, x);
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int y = __shfl_up_sync(0xffffffffu, x, o);
       if (lane >= o) x += y;
     }
-    if (lane == 31) wsum[warp] = x;
+    if (lane == 31) wsum[warp] = x, wmax[warp] = largest;
     __syncthreads();
     int before = carry;
     for (int w = 0; w < NW + 2; ++w) {
       if (w < warp) before += wsum[w];
       carry += wsum[w];
+      most_tiles = max(most_tiles, wmax[w]);
     }
     if (b < g.B) pre[b + 1] = before + x;
     __syncthreads();
   }
   const long long total = (long long)pre[g.B] * p.hgq;
-  const long long C = total < (long long)gridDim.x ? total : (long long)gridDim.x;
   const int cta = blockIdx.x;
-  if (cta >= C) return;
-  Walk w(pre, g.B, p.hgq, cta * total / C, (cta + 1) * total / C);
+  int cuts;
+  share_out(total, (long long)g.B * p.hgq, most_tiles, p.kg, gridDim.x, &cuts);
+  const long long C = total < (long long)gridDim.x ? total : (long long)gridDim.x;
+  long long beg, end;
+  if (cuts > 0) {
+    const int item = cta / cuts, piece = cta - item * cuts, b = item / p.hgq;
+    if (b >= g.B) return;
+    const int nt = pre[b + 1] - pre[b], n = min(cuts, nt);
+    if (piece >= n) return;
+    const long long i0 = (long long)pre[b] * p.hgq + (long long)(item - b * p.hgq) * nt;
+    beg = i0 + (long long)nt * piece / n;
+    end = i0 + (long long)nt * (piece + 1) / n;
+  } else {
+    if (cta >= C) return;
+    beg = cta * total / C;
+    end = (cta + 1) * total / C;
+  }
+  // the CTAs that have pieces of an item: the first, and how many
+  auto owners = [&](int b, int hg, int nt, int* first) {
+    if (cuts > 0) {
+      *first = (b * p.hgq + hg) * cuts;
+      return min(cuts, nt);
+    }
+    const long long i0 = (long long)pre[b] * p.hgq + (long long)hg * nt;
+    *first = (int)(((i0 + 1) * C - 1) / total);
+    return (int)(((i0 + nt) * C - 1) / total) - *first + 1;
+  };
+  Walk w(pre, g.B, p.hgq, beg, end);
   const uint32_t ring0 = tc::su32(ring), slot_bytes = (uint32_t)p.slot_bytes;
 
   if (warp >= NW) {
@@ -914,8 +981,8 @@ __global__ void __launch_bounds__(M::kWarps * 32 + 64, 1) paged_attention_kernel
     merge_groups();
     if (!whole) {
       // one of several pieces: leave it, and join them all if it is the last to come
-      const long long i0 = (long long)pre[piece_b] * p.hgq + (long long)hg * nt;
-      const int c0 = (int)(((i0 + 1) * C - 1) / total), n = (int)(((i0 + nt) * C - 1) / total) - c0 + 1;
+      int c0;
+      const int n = owners(piece_b, hg, nt, &c0);
       auto entry = [&](int i) {                 // piece i: a CTA's first piece may have begun before it, its last may go on
         return g.part + (((long long)(c0 + i) * 2 + (i == 0)) * NW + (h + p.nh * qi) * M::VS + vs) * entry_floats<M>() + lane * 4;
       };
