@@ -42,7 +42,8 @@ static Plan make(const Kernel& k, const spec_attn_desc& d, int nh, int B, int bl
   Plan p{};
   plan_queries(k, d.n_q_heads / d.n_kv_heads, &p);
   p.nh = nh;
-  p.kg = k.warps / k.vs / (p.nh * p.qt);
+  p.kg = 1;
+  while (2 * p.kg * p.nh * p.qt <= k.warps / k.vs) p.kg *= 2;
   p.kt = p.kg * k.sub;
   p.hgq = d.n_kv_heads / p.nh * p.qs;
   const int head = d.head_dim * k.es;
@@ -110,13 +111,17 @@ static Plan plan(const Kernel& k, const spec_attn_desc& d, int B, int max_len, i
   plan_queries(k, d.n_q_heads / d.n_kv_heads, &q);
   const int len = d.window > 0 ? std::min(d.window, max_len) : max_len;
   float least = 0.f;
-  for (int nh = 1; d.n_kv_heads % nh == 0 && nh * q.qt <= k.warps / k.vs; nh *= 2) {
+  for (int nh = 1; nh * q.qt <= k.warps / k.vs; ++nh) {
+    if (d.n_kv_heads % nh != 0) continue;
     const Plan p = make(k, d, nh, B, block_size);
     const int tiles = std::max(1, (len + p.kt - 1) / p.kt);
     const long long items = (long long)B * p.hgq, copy = (long long)(p.swz ? 1 << p.run_lg : 1) * nh * d.head_dim * k.es;
     int cuts;
-    const float cost = share_out(items * tiles, items, tiles, p.kg, sms, &cuts) *
-                       (copy >= 16384 || (items <= sms && k.es > 1) ? 1.f : copy >= 8192 ? 1.08f : 1.25f);
+    // tiles are smaller where warps are left over (3 or 5 heads); a single key's copy wants 2 KB
+    const float cost = share_out(items * tiles, items, tiles, p.kg, sms, &cuts) * (float)(p.nh * p.qt * p.kg) /
+                       (float)(k.warps / k.vs) *
+                       (!p.swz ? (copy >= 2048 ? 1.1f : copy >= 1024 ? 1.4f : copy >= 512 ? 2.1f : 3.5f)
+                        : copy >= 16384 || (items <= sms && k.es > 1) ? 1.f : copy >= 8192 ? 1.08f : 1.25f);
     if (nh == 1 || cost < least) least = cost, best = p;
   }
   return best;
@@ -164,7 +169,7 @@ extern "C" spec_status spec_paged_attention(const spec_attn_desc* desc, const vo
   if (!desc || !q || !kv || !kv->k || !kv->v || !kv->block_table || !seq_len || !out) return SPEC_ERR_ARG;
   const spec_attn_desc& d = *desc;
   if (!pa::check(desc) || B <= 0 || max_len < 0 || kv->block_size <= 0 || kv->max_blocks <= 0 ||
-      kv->num_slots <= 0 || (long long)kv->max_blocks * kv->block_size >= (1ll << 31))
+      kv->num_slots <= 0 || (long long)kv->max_blocks * kv->block_size >= (1ll << 30))
     return SPEC_ERR_SHAPE;
   if (!pa::check_types(d)) return SPEC_ERR_UNSUPPORTED;
   const bool e4m3 = d.kv_dtype == SPEC_DTYPE_E4M3;
@@ -198,9 +203,10 @@ extern "C" spec_status spec_paged_attention(const spec_attn_desc* desc, const vo
     if (g.p.slots < 2) return SPEC_ERR_UNSUPPORTED;
     if (g.p.swz && (!pa::run_map(&g.tmk, kv->k, d, *kv, k, g.p) || !pa::run_map(&g.tmv, kv->v, d, *kv, k, g.p)))
       return SPEC_ERR_CUDA;
-    if (cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+    // always the same limit: another thread may be launching the same kernel with another plan
+    if (cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(pa::kSmemMax - 1024)) != cudaSuccess)
       return SPEC_ERR_CUDA;
-    launch_pdl(k.fn, dim3(sms), dim3(k.warps * 32 + 64), smem, stream, g);
+    launch_pdl(k.fn, dim3(sms), dim3(k.warps * 32 + 128), smem, stream, g);
   }
   return last_launch();
 }

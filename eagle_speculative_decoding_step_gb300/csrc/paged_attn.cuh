@@ -26,7 +26,7 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 struct Plan {
   int nh;          // kv heads of a tile
   int qt;          // query tiles of a kv head (warps over the same keys)
-  int kg;          // key groups: nh * qt * kg consumer warps
+  int kg;          // key groups, a power of two: nh * qt * kg units of consumer warps, at most all of them
   int kt;          // keys of a tile
   int hgq;         // head groups x query splits of a request
   int qs;          // query splits (K/V is read once per split; 1 unless nq / nkv is large)
@@ -108,7 +108,8 @@ __host__ __device__ inline float share_out(long long total_, long long items_, i
 // Register r of o belongs to statistics index st(r).
 template <int NR_, int NM_> struct State {
   static constexpr int NR = NR_, NM = NM_;
-  float o[NR], m[NM], l[NM];
+  alignas(8) float o[NR];
+  float m[NM], l[NM];
 };
 
 SPEC_DEV float exp2_fast(float x) {
@@ -499,124 +500,181 @@ template <typename T, bool F8, int HD, int NT> struct MmaMath {
 };
 
 // The same for 32-bit caches on fp32 multiply-adds: 8 keys x NQ (4 or 8) queries a step.
-// Scores: lane = (key, quarter of the components); outputs: a lane holds
-// components lane + 32 e (e < HD / 32) of every query.
+// A lane holds HD / 32 components of the queries and outputs and reads those of every
+// key, so a row is read from shared memory once for all queries; the 8 NQ partial
+// sums are added up over the lanes in a butterfly that halves their number at every
+// step and leaves a lane with one key's NQ / 4 scores.  (Queries in shared memory and a
+// lane a key were bound by shared-memory reads: 64 queries on 8 heads, 32 requests of
+// 2000 keys, 127 us; three tf32 products per product 122.)
 template <int HD, int NQ> struct F32Math {
   using In = float;
   static constexpr int kSub = 8, kQ = NQ, kEs = 4, kWarps = HD > 128 ? 4 : 8, VS = 1;
-  using S = State<NQ * (HD / 32), NQ>;
-  SPEC_DEV static int st(int r) { return r / (HD / 32); }
+  static constexpr int E = HD / 32, V = E < 4 ? E : 4, J = NQ / 4;      // components, of one load; own scores
+  using S = State<NQ * E, NQ>;
+  SPEC_DEV static int st(int r) { return r / E; }
+  SPEC_DEV static int stat_query(int i, int) { return i; }
+  SPEC_DEV static bool stat_owner(int lane) { return lane == 0; }
+  // component e of a lane
+  SPEC_DEV static int comp(int e, int lane) { return e / V * (32 * V) + lane * V + e % V; }
   SPEC_DEV static void write(const S& s, const float* inv, float* out, int hd, int nq, int lane, int) {
 #pragma unroll
     for (int i = 0; i < NQ; ++i)
 #pragma unroll
-      for (int e = 0; e < HD / 32; ++e)
-        if (i < nq && lane + 32 * e < hd) out[(long long)i * hd + lane + 32 * e] = s.o[i * (HD / 32) + e] * inv[i];
+      for (int e = 0; e < E; ++e)
+        if (i < nq && comp(e, lane) < hd) out[(long long)i * hd + comp(e, lane)] = s.o[i * E + e] * inv[i];
   }
-  SPEC_DEV static int stat_query(int i, int) { return i; }
-  SPEC_DEV static bool stat_owner(int lane) { return lane == 0; }
-  // a warp's shared scratch: its queries, then the NQ x 8 weights of a step
-  static constexpr int kScratch = NQ * HD + NQ * 8;
+  static constexpr int kScratch = NQ * 8;    // a step's weights
 
-  uint32_t vm;
-  Row rk, rv;                                // lane's K row; the first V row (rv.x: whether units are swizzled)
+  float qf[NQ][E];
+  float mo[J], lo[J];      // running maxima and this lane's sums of its own queries
+  uint32_t vm, row0, stride, at[E / V];      // first key's row, from row to row, offsets in a row
+  uint32_t x0[E / V];
+  bool swz, in[E / V];
+
   SPEC_DEV void init(const Plan& p, int key0, int head, int lane) {
-    rk = Row(p, key0 + (lane & 7), head);
-    rv = Row(p, key0, head);
-    rv.x = p.swz;
+    row0 = Row(p, key0, head).off;
+    stride = p.key_stride;
+    swz = p.swz;
+#pragma unroll
+    for (int u = 0; u < E / V; ++u) {
+      const int byte = comp(u * V, lane) * 4;
+      at[u] = (byte >> 7) * p.chunk_stride + (byte & 15);
+      x0[u] = byte & 112;
+    }
   }
-  SPEC_DEV void load_q(const Args& g, const float* q, int q0, int n, int lane, float* w) {
-    __syncwarp();
+  SPEC_DEV void load_q(const Args& g, const float* q, int q0, int n, int lane, float*) {
+#pragma unroll
+    for (int u = 0; u < E / V; ++u) in[u] = comp(u * V, lane) < g.hd;
+#pragma unroll
     for (int i = 0; i < NQ; ++i)
-      for (int c = lane; c < g.hd; c += 32) w[i * g.hd + c] = i < n ? q[(long long)(q0 + i) * g.hd + c] : 0.f;
-    __syncwarp();
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+        qf[i][e] = i < n && in[e / V] ? q[(long long)(q0 + i) * g.hd + comp(e, lane)] : 0.f;
   }
-  SPEC_DEV void scale_q(const Args&, int) {}
+  SPEC_DEV void scale_q(const Args&, int) {
+#pragma unroll
+    for (int j = 0; j < J; ++j) mo[j] = -INFINITY, lo[j] = 0.f;
+  }
+  // a lane's components of a key's row (zeros past the head's end)
+  SPEC_DEV void read(uint32_t tile, int key, float* x) const {
+#pragma unroll
+    for (int u = 0; u < E / V; ++u) {
+      const uint32_t a = tile + row0 + key * stride + at[u] + (x0[u] ^ (swz ? key << 4 : 0));
+      if constexpr (V == 4)
+        asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
+                     : "=f"(x[u * V]), "=f"(x[u * V + 1]), "=f"(x[u * V + 2]), "=f"(x[u * V + 3]) : "r"(a) : "memory");
+      else
+        asm volatile("ld.shared.v2.f32 {%0,%1}, [%2];" : "=f"(x[u * V]), "=f"(x[u * V + 1]) : "r"(a) : "memory");
+#pragma unroll
+      for (int e = 0; e < V; ++e) x[u * V + e] = in[u] ? x[u * V + e] : 0.f;
+    }
+  }
+  // adds the halves of v over lanes that differ in bit `o`: a lane keeps the half that its bit names
+  template <int N> SPEC_DEV static void fold(float* v, int o, int lane) {
+    const bool up = lane & o;
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+      const float keep = up ? v[i + N / 2] : v[i], give = up ? v[i] : v[i + N / 2];
+      v[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+    }
+  }
   SPEC_DEV void scores(const Args& g, uint32_t k, uint32_t mask, int lane, S& s, float* w) {
     vm = mask & 0xffu;
     if (vm == 0) return;
-    const int key = lane & 7, part = lane >> 3;
-    float c[NQ];
+    float c[4 * NQ];                          // [key & 3][query], key's highest bit folded at once
 #pragma unroll
-    for (int i = 0; i < NQ; ++i) c[i] = 0.f;
-    const uint32_t row = k + rk.off;
-    for (int ch = part; ch < g.hd / 4; ch += 4) {
-      float4 x;
-      asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
-                   : "r"(row + (ch >> 3) * g.p.chunk_stride + ((uint32_t)((ch & 7) << 4) ^ rk.x)) : "memory");
+    for (int k4 = 0; k4 < 4; ++k4) {
+      float v[2 * NQ];
 #pragma unroll
-      for (int i = 0; i < NQ; ++i) {
-        const float4 y = *reinterpret_cast<const float4*>(w + i * g.hd + ch * 4);
-        c[i] = fmaf(x.x, y.x, fmaf(x.y, y.y, fmaf(x.z, y.z, fmaf(x.w, y.w, c[i]))));
+      for (int h = 0; h < 2; ++h) {
+        float x[E];
+        read(k, k4 + 4 * h, x);
+#pragma unroll
+        for (int i = 0; i < NQ; ++i) {
+          float2 d = make_float2(x[0] * qf[i][0], x[1] * qf[i][1]);
+#pragma unroll
+          for (int e = 2; e < E; e += 2) d = __ffma2_rn(make_float2(x[e], x[e + 1]), make_float2(qf[i][e], qf[i][e + 1]), d);
+          v[h * NQ + i] = d.x + d.y;
+        }
       }
+      fold<2 * NQ>(v, 16, lane);
+#pragma unroll
+      for (int i = 0; i < NQ; ++i) c[k4 * NQ + i] = v[i];
     }
-    const bool ok = vm >> key & 1;
+    fold<4 * NQ>(c, 8, lane);
+    fold<2 * NQ>(c, 4, lane);
+    fold<NQ>(c, 2, lane);
+    fold<NQ / 2>(c, 1, lane);
+    // c[j]: key lane >> 2, query J (lane & 3) + j
+    const bool ok = vm >> (lane >> 2) & 1;
     bool grew = false;
-    float mn[NQ];
+    float mn[J];
 #pragma unroll
-    for (int i = 0; i < NQ; ++i) {
-      c[i] += __shfl_xor_sync(0xffffffffu, c[i], 8);
-      c[i] += __shfl_xor_sync(0xffffffffu, c[i], 16);
-      c[i] = ok ? c[i] * g.scale2 : -INFINITY;
-      float x = c[i];
-      x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-      x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+    for (int j = 0; j < J; ++j) {
+      c[j] = ok ? c[j] * g.scale2 : -INFINITY;
+      float x = c[j];
       x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
-      mn[i] = fmaxf(s.m[i], x);
-      grew |= x > s.m[i];
+      x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+      x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+      mn[j] = fmaxf(mo[j], x);
+      grew |= x > mo[j];
     }
-    if (grew) {                               // the same in every lane
-      float al[NQ];
+    if (__any_sync(0xffffffffu, grew)) {
 #pragma unroll
-      for (int i = 0; i < NQ; ++i) {
-        al[i] = exp2_fast(s.m[i] - base_of(mn[i]));
-        s.m[i] = mn[i];
-        s.l[i] *= al[i];
+      for (int j = 0; j < J; ++j) {
+        lo[j] *= exp2_fast(mo[j] - base_of(mn[j]));
+        mo[j] = mn[j];
       }
 #pragma unroll
-      for (int r = 0; r < S::NR; ++r) s.o[r] *= al[st(r)];
+      for (int i = 0; i < NQ; ++i) {
+        const float m = __shfl_sync(0xffffffffu, mn[i % J], i / J), al = exp2_fast(s.m[i] - base_of(m));
+        s.m[i] = m;
+#pragma unroll
+        for (int e = 0; e < E; ++e) s.o[i * E + e] *= al;
+      }
     }
-    float* pw = w + NQ * g.hd;
     __syncwarp();
 #pragma unroll
-    for (int i = 0; i < NQ; ++i) {
-      c[i] = exp2_fast(c[i] - base_of(s.m[i]));
-      if (part == 0) s.l[i] += c[i];          // lanes 0-7 sum their own keys; finish() adds them up
-      if (part == (i & 3)) pw[i * 8 + key] = c[i];
+    for (int j = 0; j < J; ++j) {
+      c[j] = exp2_fast(c[j] - base_of(mo[j]));
+      lo[j] += c[j];
+      w[(J * (lane & 3) + j) * 8 + (lane >> 2)] = c[j];
     }
     __syncwarp();
   }
   SPEC_DEV void values(const Args& g, uint32_t v, int lane, S& s, const float* w) {
     if (vm == 0) return;
-    const float* pw = w + NQ * g.hd;
-    const uint32_t unit = (uint32_t)(lane >> 2 << 4), word = (lane & 3) * 4;
 #pragma unroll
     for (int k4 = 0; k4 < 8; k4 += 4) {
       float4 pr[NQ];
 #pragma unroll
-      for (int i = 0; i < NQ; ++i) pr[i] = *reinterpret_cast<const float4*>(pw + i * 8 + k4);
+      for (int i = 0; i < NQ; ++i) pr[i] = *reinterpret_cast<const float4*>(w + i * 8 + k4);
 #pragma unroll
-      for (int e = 0; e < HD / 32; ++e)
-        if (lane + 32 * e < g.hd) {
-          float x[4];
+      for (int j = 0; j < 4; ++j) {
+        if (!(vm >> (k4 + j) & 1)) continue;                  // its row may hold anything
+        float x[E];
+        read(v, k4 + j, x);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int key = k4 + j;
-            const uint32_t a = v + rv.off + key * g.p.key_stride + e * g.p.chunk_stride + (unit ^ (rv.x ? key << 4 : 0)) + word;
-            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x[j]) : "r"(a) : "memory");
-            x[j] = vm >> key & 1 ? x[j] : 0.f;           // the row of a key that is not valid may hold anything
-          }
+        for (int i = 0; i < NQ; ++i) {
+          const float p = j == 0 ? pr[i].x : j == 1 ? pr[i].y : j == 2 ? pr[i].z : pr[i].w;
 #pragma unroll
-          for (int i = 0; i < NQ; ++i) {
-            float& o = s.o[i * (HD / 32) + e];
-            o = fmaf(pr[i].x, x[0], fmaf(pr[i].y, x[1], fmaf(pr[i].z, x[2], fmaf(pr[i].w, x[3], o))));
+          for (int e = 0; e < E; e += 2) {
+            float2* o = reinterpret_cast<float2*>(&s.o[i * E + e]);
+            *o = __ffma2_rn(make_float2(p, p), make_float2(x[e], x[e + 1]), *o);
           }
         }
+      }
     }
   }
   SPEC_DEV void finish(S& s) {
 #pragma unroll
-    for (int i = 0; i < S::NM; ++i) s.l[i] = warp_sum(s.l[i]);
+    for (int j = 0; j < J; ++j) {
+      lo[j] += __shfl_xor_sync(0xffffffffu, lo[j], 4);
+      lo[j] += __shfl_xor_sync(0xffffffffu, lo[j], 8);
+      lo[j] += __shfl_xor_sync(0xffffffffu, lo[j], 16);
+    }
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) s.l[i] = __shfl_sync(0xffffffffu, lo[i % J], i / J);
   }
 };
 
@@ -696,7 +754,7 @@ struct Walk {
 // as partial results; the last CTA of such a group to finish joins them in CTA
 // order, so results do not depend on timing.
 template <typename M>
-__global__ void __launch_bounds__(M::kWarps * 32 + 64, 1) paged_attention_kernel(const __grid_constant__ Args g) {
+__global__ void __launch_bounds__(M::kWarps * 32 + 128, 1) paged_attention_kernel(const __grid_constant__ Args g) {
   SPEC_TL(kTLPagedAttn);
   using T = typename M::In;
   using S = typename M::S;
@@ -712,7 +770,7 @@ __global__ void __launch_bounds__(M::kWarps * 32 + 64, 1) paged_attention_kernel
   float* mscr = exch + exchange_floats<M>();
   int* pre = reinterpret_cast<int*>(mscr + NW * math_scratch<M>());
   int* lens = pre + g.B + 1;
-  __shared__ int wsum[NW + 2], wmax[NW + 2];
+  __shared__ int wsum[NW + 4], wmax[NW + 4];
   const uint32_t full0 = tc::su32(bars), empty0 = full0 + 8 * kMaxSlots;
   if (tid == 0) {
     for (int i = 0; i < p.slots; ++i) {
@@ -735,7 +793,7 @@ __global__ void __launch_bounds__(M::kWarps * 32 + 64, 1) paged_attention_kernel
   const int most = (int)most_l;
   auto first_key = [&](int len) { return g.window > 0 && len > g.window ? len - g.window : 0; };
   int carry = 0, most_tiles = 0;
-  for (int base = 0; base < g.B; base += NW * 32 + 64) {
+  for (int base = 0; base < g.B; base += NW * 32 + 128) {
     const int b = base + tid;
     int x = 0;
     if (b < g.B) {
@@ -758,7 +816,7 @@ __global__ void __launch_bounds__(M::kWarps * 32 + 64, 1) paged_attention_kernel
     if (lane == 31) wsum[warp] = x, wmax[warp] = largest;
     __syncthreads();
     int before = carry;
-    for (int w = 0; w < NW + 2; ++w) {
+    for (int w = 0; w < NW + 4; ++w) {
       if (w < warp) before += wsum[w];
       carry += wsum[w];
       most_tiles = max(most_tiles, wmax[w]);
@@ -800,7 +858,10 @@ __global__ void __launch_bounds__(M::kWarps * 32 + 64, 1) paged_attention_kernel
 
   if (warp >= NW) {
     // ------------------------------------------------------------ producers: K, V
-    const int v = warp - NW;
+    // Rows have many small copies, which two warps issue in turn (a copy takes a warp ~80 cycles): the
+    // second one waits and looks up like the first, which alone writes the masks and arrives.
+    const int v = (warp - NW) & 1, second = (warp - NW) >> 1;
+    if (second && p.swz) return;
     const uint64_t policy = tc::policy_evict_first();      // each K/V row is read once
     const long long row_all = (long long)g.nkv * g.hd * M::kEs;
     const int bs = g.kv.block_size, shift = (bs & (bs - 1)) == 0 ? __ffs(bs) - 1 : -1;
@@ -882,15 +943,15 @@ __global__ void __launch_bounds__(M::kWarps * 32 + 64, 1) paged_attention_kernel
           if (i * 32 < p.kt) {
             sl[i] = i * 32 + lane < p.kt ? slot_of_key(x.key0 + i * 32 + lane, x.id[i]) : -1;
             const uint32_t word = __ballot_sync(0xffffffffu, sl[i] >= 0);
-            if (lane == 0) masks[slot * kMaskWords + i] = word;
+            if (lane == 0 && !second) masks[slot * kMaskWords + i] = word;
             n += __popc(word);
           }
-        if (lane == 0) tc::mbar_expect_tx(full, (uint32_t)(n * p.row));
+        if (lane == 0 && !second) tc::mbar_expect_tx(full, (uint32_t)(n * p.row));
         __syncwarp();
         const char* src = static_cast<const char*>(v ? g.kv.v : g.kv.k) + (long long)x.head0 * g.hd * M::kEs;
 #pragma unroll
         for (int i = 0; i < kPer; ++i)
-          if (i * 32 < p.kt && sl[i] >= 0)
+          if (i * 32 < p.kt && sl[i] >= 0 && (lane & 1) == second)
             bulk_row(dst + (i * 32 + lane) * p.key_stride, src + sl[i] * row_all, p.row, full, policy);
       }
       ++issued;
@@ -944,7 +1005,9 @@ __global__ void __launch_bounds__(M::kWarps * 32 + 64, 1) paged_attention_kernel
   // a piece's queries are loaded while the one before it is merged and written, where registers
   // allow (16 queries: spills, and 64 requests of 4000 keys with 128 query heads 165 -> 190 us)
   constexpr bool kEarly = S::NR <= 32;
-  auto queries = [&] { return min(M::kQ, g.G - ((w.hg % p.qs) * p.qt + qi) * M::kQ); };     // <= 0: none for this warp
+  auto queries = [&] {                       // <= 0: none for this warp
+    return kgrp < p.kg ? min(M::kQ, g.G - ((w.hg % p.qs) * p.qt + qi) * M::kQ) : 0;
+  };
   auto head_of = [&] { return (w.hg / p.qs) * p.nh + h; };
   auto load_q = [&] {
     const int n = queries();

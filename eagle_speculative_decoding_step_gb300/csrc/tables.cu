@@ -412,8 +412,8 @@ extern "C" spec_status spec_block_tables(int32_t B, int32_t block_size, int32_t 
   const long long items = (table_out != table_in ? (long long)B * max_blocks : 0) + num_blocks + slots_cap;
   const int grid = (int)std::min<long long>(std::max<long long>(1, items / 1024), 3 * sm_count());
   const size_t smem = (size_t)5 * B * 4;
-  if (smem > 48 * 1024 &&
-      cudaFuncSetAttribute(block_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+  if (smem > 47 * 1024 && cudaFuncSetAttribute(block_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               5 * kTabMaxB * 4) != cudaSuccess)
     return SPEC_ERR_CUDA;
   launch_pdl(block_tables_kernel, dim3(grid), dim3(kTabThreads), smem, stream, a);
   return last_launch();
