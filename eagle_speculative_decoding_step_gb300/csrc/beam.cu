@@ -538,7 +538,7 @@ static int sel_chunks(int B, int W, int V, int* chunk) {
 constexpr int kMaxLayers = 64;
 struct ReorderArgs {
   spec_beam_state s;
-  int n_layers, row_bytes, num_blocks;
+  int n_layers, row_bytes, num_blocks, lanes;      // lanes: threads of a copy
   void* k[kMaxLayers];
   void* v[kMaxLayers];
   void* ws;
@@ -605,10 +605,10 @@ SPEC_DEV Tail beam_tail(const ReorderArgs& g, int row, bool tell) {
   return t;
 }
 
-// Grid (part, row): part 0 writes the row's integers, part 1 + 2 * layer + (0 or
-// 1) copies the partial block's K or V rows, which are contiguous (slots of a
-// block follow one another).  A copy's source is some beam's current block and its
-// target a spare block, and no block is both.
+// Grid (part, row): part 0 writes the row's integers, the others copy the partial
+// block's K or V rows, 256 / lanes (layer, K or V)s each; the rows are contiguous
+// (slots of a block follow one another).  A copy's source is some beam's current block
+// and its target a spare block, and no block is both.
 __global__ void __launch_bounds__(256) beam_reorder_kernel(const __grid_constant__ ReorderArgs g) {
   SPEC_TL(kTLBeamReorder);
   pdl_wait();
@@ -633,9 +633,9 @@ __global__ void __launch_bounds__(256) beam_reorder_kernel(const __grid_constant
     }
     return;
   }
-  if (t.from < 0) return;
-  const int layer = (part - 1) >> 1;
-  char* base = static_cast<char*>((part - 1) & 1 ? g.v[layer] : g.k[layer]);
+  const int copy = (part - 1) * (256 / g.lanes) + tid / g.lanes, me = tid % g.lanes;
+  if (t.from < 0 || copy >= 2 * g.n_layers) return;
+  char* base = static_cast<char*>(copy & 1 ? g.v[copy >> 1] : g.k[copy >> 1]);
   const long long block_bytes = (long long)s.block_size * g.row_bytes;
   const char* from = base + t.from * block_bytes;
   char* to = base + t.block * block_bytes;
@@ -643,10 +643,18 @@ __global__ void __launch_bounds__(256) beam_reorder_kernel(const __grid_constant
   if (((reinterpret_cast<uintptr_t>(base) | g.row_bytes) & 15) == 0) {
     const uint4* f = reinterpret_cast<const uint4*>(from);
     uint4* o = reinterpret_cast<uint4*>(to);
-#pragma unroll 4
-    for (int i = tid; i < bytes >> 4; i += 256) o[i] = __ldcs(f + i);
+    const int n = bytes >> 4;
+    for (int i0 = me; i0 < n; i0 += 4 * g.lanes) {
+      uint4 x[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (i0 + j * g.lanes < n) x[j] = __ldcs(f + i0 + j * g.lanes);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (i0 + j * g.lanes < n) o[i0 + j * g.lanes] = x[j];
+    }
   } else {
-    for (int i = tid; i < bytes; i += 256) to[i] = from[i];
+    for (int i = me; i < bytes; i += g.lanes) to[i] = from[i];
   }
 }
 
@@ -719,7 +727,13 @@ extern "C" spec_status spec_beam_reorder(const spec_beam_state* st, int32_t n_la
     g.k[i] = kv[i].k;
     g.v[i] = kv[i].v;
   }
-  launch_pdl(beam_reorder_kernel, dim3(1 + 2 * n_layers, s.B * s.W), dim3(256), 0, stream, g);
+  const long long block_bytes = (long long)s.block_size * row_bytes;
+  // few lanes for small blocks, whose copies would leave most of a CTA idle (384 beams, 36 layers, 6 KB blocks, 32 / 64 /
+  // 128 / 256 lanes 12.0 / 16.1 / 27.9 / 51.0 us; 144 beams, 24 layers, 16 KB 14.1 / 10.2 / 10.6 / 15.7; 128 beams, 32
+  // layers, 32 KB 26.6 / 23.3 / 22.3 / 25.5), all of them where there are few copies (4 beams, 1 layer 4.6 / 3.5 / 3.2 / 2.9)
+  g.lanes = 2ll * n_layers * s.B * s.W <= 4 * sm_count() ? 256 : block_bytes <= 8192 ? 32 : block_bytes <= 16384 ? 64 : 128;
+  const int per = 256 / g.lanes;
+  launch_pdl(beam_reorder_kernel, dim3(1 + (2 * n_layers + per - 1) / per, s.B * s.W), dim3(256), 0, stream, g);
   return last_launch();
 }
 
