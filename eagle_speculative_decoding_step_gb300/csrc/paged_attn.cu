@@ -117,11 +117,13 @@ static Plan plan(const Kernel& k, const spec_attn_desc& d, int B, int max_len, i
     const int tiles = std::max(1, (len + p.kt - 1) / p.kt);
     const long long items = (long long)B * p.hgq, copy = (long long)(p.swz ? 1 << p.run_lg : 1) * nh * d.head_dim * k.es;
     int cuts;
-    // tiles are smaller where warps are left over (3 or 5 heads); a single key's copy wants 2 KB
-    const float cost = share_out(items * tiles, items, tiles, p.kg, sms, &cuts) * (float)(p.nh * p.qt * p.kg) /
-                       (float)(k.warps / k.vs) *
-                       (!p.swz ? (copy >= 2048 ? 1.1f : copy >= 1024 ? 1.4f : copy >= 512 ? 2.1f : 3.5f)
-                        : copy >= 16384 || (items <= sms && k.es > 1) ? 1.f : copy >= 8192 ? 1.08f : 1.25f);
+    // Rows: tiles are smaller where warps are left over (3 or 5 heads), and a single key's copy wants 2 KB (64 requests
+    // of 4000 keys, blocks of one slot, copies of 2048 / 1024 / 512 / 256 bytes: 97 / 82 / 58 / 35 % of the copy
+    // bandwidth).  Runs: a smaller tile takes a warp as long as a whole one.
+    const float form = p.swz ? (copy >= 16384 || (items <= sms && k.es > 1) ? 1.f : copy >= 8192 ? 1.08f : 1.25f)
+                             : (copy >= 2048 ? 1.f : copy >= 1024 ? 1.2f : copy >= 512 ? 1.7f : 2.8f) *
+                                   (float)(p.nh * p.qt * p.kg * k.vs) / (float)k.warps;
+    const float cost = share_out(items * tiles, items, tiles, p.kg, sms, &cuts) * form;
     if (nh == 1 || cost < least) least = cost, best = p;
   }
   return best;
