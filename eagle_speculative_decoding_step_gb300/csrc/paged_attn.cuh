@@ -254,7 +254,7 @@ template <typename T, bool F8, int HD, int NT> struct MmaMath {
 
   Row rk, rv;              // this lane's K row (units lane >> 4 and up) and V row
   uint32_t next;           // from one tile of 16 keys to the next
-  SPEC_DEV void init(const Plan& p, int key0, int head, int lane) {
+  SPEC_DEV void init(const Plan& p, int key0, int head, int lane, uint32_t) {
     rk = Row(p, key0 + (lane & 15), head);
     rk.x ^= (lane >> 4) << 4;
     next = Row(p, key0 + (lane & 15) + 16 * (U - 1), head).off - rk.off;
@@ -500,112 +500,129 @@ template <typename T, bool F8, int HD, int NT> struct MmaMath {
 };
 
 // The same for 32-bit caches on fp32 multiply-adds: 8 keys x NQ (4 or 8) queries a step.
-// A lane holds HD / 32 components of the queries and outputs and reads those of every
-// key, so a row is read from shared memory once for all queries; the 8 NQ partial
-// sums are added up over the lanes in a butterfly that halves their number at every
-// step and leaves a lane with one key's NQ / 4 scores.  (Queries in shared memory and a
-// lane a key were bound by shared-memory reads: 64 queries on 8 heads, 32 requests of
-// 2000 keys, 127 us; three tf32 products per product 122.)
+// A row's components are spread over R lanes (16 up to 64 components, where each half of
+// the warp takes 4 of the keys; else 32), so that a row is read from shared memory once for
+// all queries.  The partial sums are added up over the lanes in a butterfly that halves
+// their number at every step and leaves a lane with one key's NQ / 4 scores; a lane
+// takes keys and queries in an order of its own (its number's bits flipped), so that what it
+// keeps is always the first half.  Queries go in pairs through packed multiply-adds.
+// Measured: 32 requests of 2000 keys on 8 heads of 128, 32 / 64 / 128 queries 84 / 102 / 184
+// us (77 at the copy bandwidth): by the latency of a step, its multiply-adds, shuffles
+// and shared-memory reads each ~60 us of the 184.  (Lanes with a key each and queries in
+// shared memory: 64 queries 127 us; three tf32 products per product 122.)
 template <int HD, int NQ> struct F32Math {
   using In = float;
   static constexpr int kSub = 8, kQ = NQ, kEs = 4, kWarps = HD > 128 ? 4 : 8, VS = 1;
-  static constexpr int E = HD / 32, V = E < 4 ? E : 4, J = NQ / 4;      // components, of one load; own scores
+  static constexpr int R = HD <= 64 ? 16 : 32, E = HD / R, NP = NQ / 2, J = NQ / 4;   // a lane's components and own scores
+  static constexpr int KK = 8 * R / 32;      // keys a lane looks at
   using S = State<NQ * E, NQ>;
-  SPEC_DEV static int st(int r) { return r / E; }
+  // register r of o: pair of queries, component, query of the pair
+  SPEC_DEV static int reg(int i, int e) { return (i >> 1) * 2 * E + e * 2 + (i & 1); }
+  SPEC_DEV static int st(int r) { return r / (2 * E) * 2 + (r & 1); }
   SPEC_DEV static int stat_query(int i, int) { return i; }
   SPEC_DEV static bool stat_owner(int lane) { return lane == 0; }
-  // component e of a lane
-  SPEC_DEV static int comp(int e, int lane) { return e / V * (32 * V) + lane * V + e % V; }
+  // the first of components 4 u .. 4 u + 3 of a lane
+  SPEC_DEV static int comp(int u, int lane) { return 4 * (u * R + (lane & (R - 1))); }
   SPEC_DEV static void write(const S& s, const float* inv, float* out, int hd, int nq, int lane, int) {
 #pragma unroll
     for (int i = 0; i < NQ; ++i)
 #pragma unroll
-      for (int e = 0; e < E; ++e)
-        if (i < nq && comp(e, lane) < hd) out[(long long)i * hd + comp(e, lane)] = s.o[i * E + e] * inv[i];
+      for (int u = 0; u < E / 4; ++u)
+        if (i < nq && comp(u, lane) < hd && lane < R)
+          *reinterpret_cast<float4*>(out + (long long)i * hd + comp(u, lane)) =
+              make_float4(s.o[reg(i, 4 * u)] * inv[i], s.o[reg(i, 4 * u + 1)] * inv[i], s.o[reg(i, 4 * u + 2)] * inv[i],
+                          s.o[reg(i, 4 * u + 3)] * inv[i]);
   }
   static constexpr int kScratch = NQ * 8;    // a step's weights
 
-  float qf[NQ][E];
+  float2 qf[NP][E];        // place i: query i ^ flip(lane)
   float mo[J], lo[J];      // running maxima and this lane's sums of its own queries
-  uint32_t vm, row0, stride, at[E / V];      // first key's row, from row to row, offsets in a row
-  uint32_t x0[E / V];
-  bool swz, in[E / V];
+  uint32_t vm, zero;       // valid keys; 16 bytes of zeros
+  uint32_t koff[KK], voff[KK], upper;        // offsets of a lane's K and V rows; from u to u + 1
+  bool in[E / 4];
 
-  SPEC_DEV void init(const Plan& p, int key0, int head, int lane) {
-    row0 = Row(p, key0, head).off;
-    stride = p.key_stride;
-    swz = p.swz;
+  SPEC_DEV static int flip(int lane) { return (lane & 2 ? NQ / 2 : 0) | (lane & 1 ? NQ / 4 : 0); }
+  SPEC_DEV void init(const Plan& p, int key0, int head, int lane, uint32_t zero_) {
+    zero = zero_;
+    const uint32_t byte = comp(0, lane) * 4, unit = (byte >> 7) * p.chunk_stride, x = byte & 127;
+    upper = (R * 16 >> 7) * p.chunk_stride;
 #pragma unroll
-    for (int u = 0; u < E / V; ++u) {
-      const int byte = comp(u * V, lane) * 4;
-      at[u] = (byte >> 7) * p.chunk_stride + (byte & 15);
-      x0[u] = byte & 112;
+    for (int k = 0; k < KK; ++k) {
+      const Row rk(p, key0 + (k ^ (lane >> 2)), head), rv(p, key0 + (R == 16 ? (lane >> 4) * 4 + k : k), head);
+      koff[k] = rk.off + unit + (x ^ rk.x);
+      voff[k] = rv.off + unit + (x ^ rv.x);
     }
   }
   SPEC_DEV void load_q(const Args& g, const float* q, int q0, int n, int lane, float*) {
 #pragma unroll
-    for (int u = 0; u < E / V; ++u) in[u] = comp(u * V, lane) < g.hd;
+    for (int u = 0; u < E / 4; ++u) {
+      in[u] = comp(u, lane) < g.hd;
 #pragma unroll
-    for (int i = 0; i < NQ; ++i)
-#pragma unroll
-      for (int e = 0; e < E; ++e)
-        qf[i][e] = i < n && in[e / V] ? q[(long long)(q0 + i) * g.hd + comp(e, lane)] : 0.f;
+      for (int i = 0; i < NQ; ++i) {
+        const int j = i ^ flip(lane);
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (j < n && in[u]) x = *reinterpret_cast<const float4*>(q + (long long)(q0 + j) * g.hd + comp(u, lane));
+        float* o = reinterpret_cast<float*>(&qf[i >> 1][4 * u]) + (i & 1);
+        o[0] = x.x, o[2] = x.y, o[4] = x.z, o[6] = x.w;
+      }
+    }
   }
   SPEC_DEV void scale_q(const Args&, int) {
 #pragma unroll
     for (int j = 0; j < J; ++j) mo[j] = -INFINITY, lo[j] = 0.f;
   }
-  // a lane's components of a key's row (zeros past the head's end)
-  SPEC_DEV void read(uint32_t tile, int key, float* x) const {
+  // a lane's components of a row (zeros past the head's end, or if the row is not wanted)
+  SPEC_DEV void read(uint32_t row, bool wanted, float* x) const {
 #pragma unroll
-    for (int u = 0; u < E / V; ++u) {
-      const uint32_t a = tile + row0 + key * stride + at[u] + (x0[u] ^ (swz ? key << 4 : 0));
-      if constexpr (V == 4)
-        asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
-                     : "=f"(x[u * V]), "=f"(x[u * V + 1]), "=f"(x[u * V + 2]), "=f"(x[u * V + 3]) : "r"(a) : "memory");
-      else
-        asm volatile("ld.shared.v2.f32 {%0,%1}, [%2];" : "=f"(x[u * V]), "=f"(x[u * V + 1]) : "r"(a) : "memory");
-#pragma unroll
-      for (int e = 0; e < V; ++e) x[u * V + e] = in[u] ? x[u * V + e] : 0.f;
+    for (int u = 0; u < E / 4; ++u) {
+      const uint32_t a = in[u] && wanted ? row + u * upper : zero;
+      asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
+                   : "=f"(x[4 * u]), "=f"(x[4 * u + 1]), "=f"(x[4 * u + 2]), "=f"(x[4 * u + 3]) : "r"(a) : "memory");
     }
   }
-  // adds the halves of v over lanes that differ in bit `o`: a lane keeps the half that its bit names
-  template <int N> SPEC_DEV static void fold(float* v, int o, int lane) {
-    const bool up = lane & o;
+  SPEC_DEV static float2 plus_other(float2 keep, float2 give, int o) {
+    return __fadd2_rn(keep, make_float2(__shfl_xor_sync(0xffffffffu, give.x, o), __shfl_xor_sync(0xffffffffu, give.y, o)));
+  }
+  // dot products of a lane's components of key k
+  SPEC_DEV void dots(uint32_t tile, int k, float2* d) const {
+    float x[E];
+    read(tile + koff[k], true, x);
 #pragma unroll
-    for (int i = 0; i < N / 2; ++i) {
-      const float keep = up ? v[i + N / 2] : v[i], give = up ? v[i] : v[i + N / 2];
-      v[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
-    }
+    for (int i = 0; i < NP; ++i) d[i] = __fmul2_rn(make_float2(x[0], x[0]), qf[i][0]);
+#pragma unroll
+    for (int e = 1; e < E; ++e)
+#pragma unroll
+      for (int i = 0; i < NP; ++i) d[i] = __ffma2_rn(make_float2(x[e], x[e]), qf[i][e], d[i]);
   }
   SPEC_DEV void scores(const Args& g, uint32_t k, uint32_t mask, int lane, S& s, float* w) {
     vm = mask & 0xffu;
     if (vm == 0) return;
-    float c[4 * NQ];                          // [key & 3][query], key's highest bit folded at once
+    float2 d[4][NP];
 #pragma unroll
-    for (int k4 = 0; k4 < 4; ++k4) {
-      float v[2 * NQ];
+    for (int i = 0; i < 4; ++i) {
+      dots(k, i, d[i]);
+      if constexpr (R == 32) {
+        float2 e[NP];
+        dots(k, i + 4, e);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        float x[E];
-        read(k, k4 + 4 * h, x);
-#pragma unroll
-        for (int i = 0; i < NQ; ++i) {
-          float2 d = make_float2(x[0] * qf[i][0], x[1] * qf[i][1]);
-#pragma unroll
-          for (int e = 2; e < E; e += 2) d = __ffma2_rn(make_float2(x[e], x[e + 1]), make_float2(qf[i][e], qf[i][e + 1]), d);
-          v[h * NQ + i] = d.x + d.y;
-        }
+        for (int j = 0; j < NP; ++j) d[i][j] = plus_other(d[i][j], e[j], 16);
       }
-      fold<2 * NQ>(v, 16, lane);
-#pragma unroll
-      for (int i = 0; i < NQ; ++i) c[k4 * NQ + i] = v[i];
     }
-    fold<4 * NQ>(c, 8, lane);
-    fold<2 * NQ>(c, 4, lane);
-    fold<NQ>(c, 2, lane);
-    fold<NQ / 2>(c, 1, lane);
-    // c[j]: key lane >> 2, query J (lane & 3) + j
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < NP; ++j) d[i][j] = plus_other(d[i][j], d[i + 2][j], 8);
+#pragma unroll
+    for (int j = 0; j < NP; ++j) d[0][j] = plus_other(d[0][j], d[1][j], 4);
+#pragma unroll
+    for (int j = 0; j < NP / 2; ++j) d[0][j] = plus_other(d[0][j], d[0][j + NP / 2], 2);
+    float c[J];                    // key lane >> 2, query J (lane & 3) + j
+    if constexpr (J == 2) {
+      const float2 x = plus_other(d[0][0], d[0][1], 1);
+      c[0] = x.x, c[J - 1] = x.y;
+    } else {
+      c[0] = d[0][0].x + __shfl_xor_sync(0xffffffffu, d[0][0].y, 1);
+    }
     const bool ok = vm >> (lane >> 2) & 1;
     bool grew = false;
     float mn[J];
@@ -625,43 +642,43 @@ template <int HD, int NQ> struct F32Math {
         lo[j] *= exp2_fast(mo[j] - base_of(mn[j]));
         mo[j] = mn[j];
       }
+      float al[NQ];
 #pragma unroll
       for (int i = 0; i < NQ; ++i) {
-        const float m = __shfl_sync(0xffffffffu, mn[i % J], i / J), al = exp2_fast(s.m[i] - base_of(m));
+        const float m = __shfl_sync(0xffffffffu, mn[i % J], i / J);
+        al[i] = exp2_fast(s.m[i] - base_of(m));
         s.m[i] = m;
-#pragma unroll
-        for (int e = 0; e < E; ++e) s.o[i * E + e] *= al;
       }
+#pragma unroll
+      for (int r = 0; r < S::NR; ++r) s.o[r] *= al[st(r)];
     }
     __syncwarp();
 #pragma unroll
     for (int j = 0; j < J; ++j) {
       c[j] = exp2_fast(c[j] - base_of(mo[j]));
       lo[j] += c[j];
-      w[(J * (lane & 3) + j) * 8 + (lane >> 2)] = c[j];
+      w[J * lane + j] = c[j];      // [key][query]
     }
     __syncwarp();
   }
   SPEC_DEV void values(const Args& g, uint32_t v, int lane, S& s, const float* w) {
     if (vm == 0) return;
+    const int key0 = R == 16 ? (lane >> 4) * 4 : 0;
+    const uint32_t ok = vm >> key0;
 #pragma unroll
-    for (int k4 = 0; k4 < 8; k4 += 4) {
-      float4 pr[NQ];
+    for (int k = 0; k < KK; ++k) {
+      float x[E];
+      float4 pr[NQ / 4];
+      read(v + voff[k], ok >> k & 1, x);               // the row of a key that is not valid may hold anything
 #pragma unroll
-      for (int i = 0; i < NQ; ++i) pr[i] = *reinterpret_cast<const float4*>(w + i * 8 + k4);
+      for (int i = 0; i < NQ / 4; ++i) pr[i] = *reinterpret_cast<const float4*>(w + (key0 + k) * NQ + 4 * i);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if (!(vm >> (k4 + j) & 1)) continue;                  // its row may hold anything
-        float x[E];
-        read(v, k4 + j, x);
+      for (int i = 0; i < NP; ++i) {
+        const float2 p2 = i & 1 ? make_float2(pr[i / 2].z, pr[i / 2].w) : make_float2(pr[i / 2].x, pr[i / 2].y);
 #pragma unroll
-        for (int i = 0; i < NQ; ++i) {
-          const float p = j == 0 ? pr[i].x : j == 1 ? pr[i].y : j == 2 ? pr[i].z : pr[i].w;
-#pragma unroll
-          for (int e = 0; e < E; e += 2) {
-            float2* o = reinterpret_cast<float2*>(&s.o[i * E + e]);
-            *o = __ffma2_rn(make_float2(p, p), make_float2(x[e], x[e + 1]), *o);
-          }
+        for (int e = 0; e < E; ++e) {
+          float2* o = reinterpret_cast<float2*>(&s.o[reg(2 * i, e)]);
+          *o = __ffma2_rn(p2, make_float2(x[e], x[e]), *o);
         }
       }
     }
@@ -675,6 +692,10 @@ template <int HD, int NQ> struct F32Math {
     }
 #pragma unroll
     for (int i = 0; i < NQ; ++i) s.l[i] = __shfl_sync(0xffffffffu, lo[i % J], i / J);
+    if constexpr (R == 16) {
+#pragma unroll
+      for (int r = 0; r < S::NR; ++r) s.o[r] += __shfl_xor_sync(0xffffffffu, s.o[r], 16);
+    }
   }
 };
 
@@ -765,13 +786,14 @@ __global__ void __launch_bounds__(M::kWarps * 32 + 128, 1) paged_attention_kerne
   uint8_t* ring = smem_raw + ((1024u - (tc::su32(smem_raw) & 1023u)) & 1023u);
   uint64_t* bars = reinterpret_cast<uint64_t*>(ring + (size_t)p.slots * p.slot_bytes);   // full[kMaxSlots], empty[kMaxSlots]
   volatile int* flags = reinterpret_cast<volatile int*>(bars + 2 * kMaxSlots);              // abort, last
+  float* zeros = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(bars) + 512);
   uint32_t* masks = reinterpret_cast<uint32_t*>(reinterpret_cast<uint8_t*>(bars) + 1024);
   float* exch = reinterpret_cast<float*>(masks + kMaxSlots * kMaskWords);
   float* mscr = exch + exchange_floats<M>();
   int* pre = reinterpret_cast<int*>(mscr + NW * math_scratch<M>());
   int* lens = pre + g.B + 1;
   __shared__ int wsum[NW + 4], wmax[NW + 4];
-  const uint32_t full0 = tc::su32(bars), empty0 = full0 + 8 * kMaxSlots;
+  const uint32_t full0 = tc::su32(bars), empty0 = full0 + 8 * kMaxSlots, zero0 = tc::su32(zeros);
   if (tid == 0) {
     for (int i = 0; i < p.slots; ++i) {
       tc::mbar_init(full0 + 8 * i, 1);
@@ -781,6 +803,7 @@ __global__ void __launch_bounds__(M::kWarps * 32 + 128, 1) paged_attention_kerne
       asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&g.tmk)) : "memory");
       asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&g.tmv)) : "memory");
     }
+    for (int i = 0; i < 4; ++i) zeros[i] = 0.f;
     flags[0] = 0;
     pre[0] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -978,7 +1001,7 @@ __global__ void __launch_bounds__(M::kWarps * 32 + 128, 1) paged_attention_kerne
   int slot = 0, phase = 0;
   const int k0 = kgrp * M::kSub;
   M math;
-  math.init(p, k0, h, lane);
+  math.init(p, k0, h, lane, zero0);
   S s;
   auto sync = [] { asm volatile("bar.sync 1, %0;" ::"n"(NW * 32) : "memory"); };
   auto advance = [&] {
