@@ -65,6 +65,7 @@ static Plan make(const Kernel& k, const spec_attn_desc& d, int nh, int B, int bl
     p.chunk_stride = 128;
     p.slot_bytes = (int)align_up((size_t)p.kt * p.key_stride, 16);
   }
+  p.full = d.head_dim == k.hd || (p.swz && chunks == (k.hd * k.es + 127) / 128);
   p.slots = (int)std::min<size_t>(kMaxSlots, (kSmemMax - 1024 - k.fixed(B)) / p.slot_bytes);
   return p;
 }
@@ -186,6 +187,7 @@ extern "C" spec_status spec_paged_attention(const spec_attn_desc* desc, const vo
     return SPEC_ERR_ALIGN;
   if (!ws || !aligned(ws, 256) || ws_bytes < spec_attention_workspace_bytes(desc, B)) return SPEC_ERR_WORKSPACE;
   const pa::Kernel k = pa::kernel_for(d);
+  if (!k.fits()) return SPEC_ERR_CUDA;
   const int sms = sm_count();
   const int longest = max_len > 0 ? max_len : kv->max_blocks * kv->block_size;
   pa::Args g{};

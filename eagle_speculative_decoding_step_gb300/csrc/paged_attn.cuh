@@ -20,6 +20,10 @@ constexpr int kMaxB = 2048;              // requests of one launch (their tile c
 constexpr int kMaxSlots = 16;            // ring slots
 constexpr int kFlat = 8;                 // up to so many pieces are joined at once
 constexpr int kMaskWords = 8;            // validity words of a tile of at most 256 keys
+// Registers a thread of 8 + 4 warps is launched with, and those after the two kinds of warps have
+// shared them out (kMoreRegs): 4 x 88 + 8 x 208 = 12 x 168.
+constexpr int kLaunchRegs = 168, kProducerRegs = 88, kConsumerRegs = 208;
+static_assert(4 * kProducerRegs + 8 * kConsumerRegs <= 12 * kLaunchRegs, "");
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // How a call's work is cut (host, paged_attn.cu).
@@ -43,6 +47,7 @@ struct Plan {
   int swz, run_lg, run_bytes, key_stride, head_stride, chunk_stride;
   int copies;      // tensor copies of a run: 1, or the 128-byte chunks of a head's row
   int row;         // rows: bytes of one key's nh heads
+  int full;        // rows in shared memory have all the components that the kernel handles (zeros past the head's)
 };
 
 struct Args {
@@ -206,13 +211,15 @@ SPEC_DEV uint32_t widen(uint32_t x) {
 // smaller than that, and undone in the scores' scale.
 template <typename T, bool F8, int HD, int NT> struct MmaMath {
   using In = T;
+  static constexpr int kHd = HD;
   using P = std::conditional_t<F8, __half, T>;      // operands of the products
   static constexpr bool kScaled = F8 && std::is_same_v<T, __nv_bfloat16>;
   float qs[2 * NT];        // kScaled: scores' scale by query
-  static constexpr int kEs = F8 ? 1 : 2, U = HD * kEs <= 128 || (F8 && HD == 256) ? 2 : 1;
+  static constexpr int kEs = F8 ? 1 : 2, U = HD * kEs <= 128 || (F8 && HD > 128) ? 2 : 1;
   static constexpr int kSub = 16 * U, kQ = 8 * NT;
   // above 128 components two warps share keys and queries: both compute the scores, each half of the outputs
   static constexpr int kWarps = 8, VS = HD > 128 ? 2 : 1, MT = HD / 16 / VS;
+  static constexpr bool kMoreRegs = NT == 2 && HD == 128;
   using S = State<MT * NT * 4, 2 * NT>;
   // register r = (mt NT + nt) 4 + 2 i + j: query nt 8 + 2 (lane & 3) + j, component mt 16 + (lane >> 2) + 8 i
   // (8-bit caches: mt 16 + 2 (lane >> 2) + i)
@@ -327,51 +334,97 @@ template <typename T, bool F8, int HD, int NT> struct MmaMath {
     }
   }
 
-  // scores of this warp's keys in the K tile at shared address k, running statistics, weights
-  SPEC_DEV void scores(const Args& g, uint32_t k, uint32_t mask, int lane, S& s, float*) {
-    vm = mask & kAll;
-    if (vm == 0) return;
-    // one tile of 16 keys x 8 queries: two sums over alternate 16 components, so that two chains of
-    // products run side by side
-    constexpr int A = U * NT == 1 ? 2 : 1;
-    float ca[A][U][NT][4];
+  // one tile of 16 keys x 8 queries: two sums over alternate 16 components, so that two chains of
+  // products run side by side
+  static constexpr int A = U * NT == 1 ? 2 : 1;
+  static constexpr int KS = F8 ? HD / 32 : HD / 16, VSTEPS = KS / VS;     // steps of 32 bytes of a row
+  float ca[A][U][NT][4];   // scores of the tile whose keys were read last
+  SPEC_DEV void clear() {
 #pragma unroll
     for (int i = 0; i < A * U * NT * 4; ++i) (&ca[0][0][0][0])[i] = 0.f;
-    auto& c = ca[0];
+  }
+  // FULL: rows have all HD components (no branches between the instructions of several steps)
+  template <bool FULL> SPEC_DEV void dot_step(const Args& g, uint32_t k, int i) {
+    if (!FULL && i * (HD / KS) >= g.hd) return;
     const uint32_t a0 = k + rk.off;
+    uint32_t r[U][4];
+#pragma unroll
+    for (int u = 0; u < U; ++u) ldsm4(unit2(g.p, a0 + u * next, rk.x, i), r[u]);
     if constexpr (F8) {
 #pragma unroll
-      for (int kp = 0; kp < HD / 32; ++kp)
-        if (kp * 32 < g.hd) {
-          uint32_t r[U][4], a[4];
+      for (int j = 0; j < 2; ++j) {
+        if (!FULL && i * 32 + j * 16 >= g.hd) break;
 #pragma unroll
-          for (int u = 0; u < U; ++u) ldsm4(unit2(g.p, a0 + u * next, rk.x, kp), r[u]);
+        for (int u = 0; u < U; ++u) {
+          uint32_t a[4];
+          a[0] = widen(r[u][2 * j]), a[1] = widen(r[u][2 * j + 1]);
+          a[2] = widen(r[u][2 * j] >> 16), a[3] = widen(r[u][2 * j + 1] >> 16);
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            if (kp * 32 + j * 16 >= g.hd) break;
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-              a[0] = widen(r[u][2 * j]), a[1] = widen(r[u][2 * j + 1]);
-              a[2] = widen(r[u][2 * j] >> 16), a[3] = widen(r[u][2 * j + 1] >> 16);
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
-                mma<P>(ca[A == 2 ? j : 0][u][nt], a, qf[kp * 2 + j][nt][0], qf[kp * 2 + j][nt][1]);
-            }
-          }
+          for (int nt = 0; nt < NT; ++nt) mma<P>(ca[A == 2 ? j : 0][u][nt], a, qf[i * 2 + j][nt][0], qf[i * 2 + j][nt][1]);
         }
+      }
     } else {
 #pragma unroll
-      for (int ks = 0; ks < HD / 16; ++ks)
-        if (ks * 16 < g.hd) {
-          uint32_t a[U][4];
+      for (int u = 0; u < U; ++u)
 #pragma unroll
-          for (int u = 0; u < U; ++u) ldsm4(unit2(g.p, a0 + u * next, rk.x, ks), a[u]);
-#pragma unroll
-          for (int u = 0; u < U; ++u)
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma<P>(ca[ks % A][u][nt], a[u], qf[ks][nt][0], qf[ks][nt][1]);
-        }
+        for (int nt = 0; nt < NT; ++nt) mma<P>(ca[i % A][u][nt], r[u], qf[i][nt][0], qf[i][nt][1]);
     }
+  }
+  // ALL: every key is valid
+  template <bool FULL, bool ALL> SPEC_DEV void value_step(const Args& g, uint32_t v, S& s, int vs, int il, const uint32_t (*z)[2]) {
+    const int i = vs * VSTEPS + il;
+    if (!FULL && i * (HD / KS) >= g.hd) return;
+    const uint32_t a0 = v + rv.off;
+    uint32_t r[U][4];
+#pragma unroll
+    for (int u = 0; u < U; ++u) ldsm4t(unit2(g.p, a0 + u * next, rv.x, i), r[u]);
+    auto step = [&](int mt, int u, uint32_t* a) {
+      if (!ALL) a[0] &= z[u][0], a[1] &= z[u][0], a[2] &= z[u][1], a[3] &= z[u][1];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float* o = &s.o[(mt * NT + nt) * 4];
+        mma<P>(o, a, pf[u][nt][0], pf[u][nt][1]);
+        mma<P>(o, a, pf[u][nt][2], pf[u][nt][3]);
+      }
+    };
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if constexpr (F8) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          if (!FULL && i * 32 + j * 16 >= g.hd) break;
+          // bytes (key, component): 00 01 10 11 -> component 0 of both keys, component 1 of both
+          const uint32_t x = __byte_perm(r[u][2 * j], 0, 0x3120), y = __byte_perm(r[u][2 * j + 1], 0, 0x3120);
+          uint32_t a[4] = {widen(x), widen(x >> 16), widen(y), widen(y >> 16)};
+          step(il * 2 + j, u, a);
+        }
+      } else {
+        step(il, u, r[u]);
+      }
+    }
+  }
+  // scores of this warp's keys in the K tile at shared address k
+  SPEC_DEV void dots(const Args& g, uint32_t k, uint32_t mask) {
+    if ((mask & kAll) == 0) return;
+    clear();
+#pragma unroll
+    for (int i = 0; i < KS; ++i) dot_step<false>(g, k, i);
+  }
+  // that and values() of the tile before: two independent chains of instructions in one run without a branch
+  SPEC_DEV bool can_run_both(const Args& g, uint32_t mask) const { return vm == kAll && (mask & kAll) == kAll && g.p.full; }
+  SPEC_DEV void both(const Args& g, uint32_t k, uint32_t v, S& s, int vs) {
+    clear();
+#pragma unroll
+    for (int i = 0; i < KS; ++i) {
+      dot_step<true>(g, k, i);
+      if (i % VS == 0) value_step<true, true>(g, v, s, vs, i / VS, nullptr);
+    }
+  }
+  // scores become weights: running statistics
+  SPEC_DEV void weights(const Args& g, uint32_t mask, int lane, S& s) {
+    vm = mask & kAll;
+    if (vm == 0) return;
+    auto& c = ca[0];
     if constexpr (A == 2) {
 #pragma unroll
       for (int i = 0; i < U * NT * 4; ++i) (&ca[0][0][0][0])[i] += (&ca[A - 1][0][0][0])[i];
@@ -435,7 +488,6 @@ template <typename T, bool F8, int HD, int NT> struct MmaMath {
     if (vm == 0) return;
     const int t2 = 2 * (lane & 3);
     // rows of keys that are not valid may hold anything: their bits are cleared
-    const bool some = vm != kAll;
     uint32_t z[U][2];
 #pragma unroll
     for (int u = 0; u < U; ++u)
@@ -444,49 +496,8 @@ template <typename T, bool F8, int HD, int NT> struct MmaMath {
         const uint32_t b = vm >> (16 * u + 8 * h + t2);
         z[u][h] = (b & 1 ? 0xffffu : 0) | (b & 2 ? 0xffff0000u : 0);
       }
-    auto step = [&](int mt, int u, uint32_t* a) {
-      if (some) a[0] &= z[u][0], a[1] &= z[u][0], a[2] &= z[u][1], a[3] &= z[u][1];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        float* o = &s.o[(mt * NT + nt) * 4];
-        mma<P>(o, a, pf[u][nt][0], pf[u][nt][1]);
-        mma<P>(o, a, pf[u][nt][2], pf[u][nt][3]);
-      }
-    };
-    const uint32_t a0 = v + rv.off;
-    if constexpr (F8) {
-#pragma unroll
-      for (int cl = 0; cl < MT / 2; ++cl) {
-        const int cp = vs * (MT / 2) + cl;
-        if (cp * 32 < g.hd) {
-          uint32_t r[U][4], a[4];
-#pragma unroll
-          for (int u = 0; u < U; ++u) ldsm4t(unit2(g.p, a0 + u * next, rv.x, cp), r[u]);
-#pragma unroll
-          for (int u = 0; u < U; ++u)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              if (cp * 32 + j * 16 >= g.hd) break;
-              // bytes (key, component): 00 01 10 11 -> component 0 of both keys, component 1 of both
-              const uint32_t x = __byte_perm(r[u][2 * j], 0, 0x3120), y = __byte_perm(r[u][2 * j + 1], 0, 0x3120);
-              a[0] = widen(x), a[1] = widen(x >> 16), a[2] = widen(y), a[3] = widen(y >> 16);
-              step(cl * 2 + j, u, a);
-            }
-        }
-      }
-    } else {
-#pragma unroll
-      for (int ml = 0; ml < MT; ++ml) {
-        const int mt = vs * MT + ml;
-        if (mt * 16 < g.hd) {
-          uint32_t a[U][4];
-#pragma unroll
-          for (int u = 0; u < U; ++u) ldsm4t(unit2(g.p, a0 + u * next, rv.x, mt), a[u]);
-#pragma unroll
-          for (int u = 0; u < U; ++u) step(ml, u, a[u]);
-        }
-      }
-    }
+    for (int i = 0; i < VSTEPS; ++i) value_step<false, false>(g, v, s, vs, i, z);
   }
   // sums over the lanes that hold other keys of the same query
   SPEC_DEV void finish(S& s) {
@@ -512,7 +523,8 @@ template <typename T, bool F8, int HD, int NT> struct MmaMath {
 // shared memory: 64 queries 127 us; three tf32 products per product 122.)
 template <int HD, int NQ> struct F32Math {
   using In = float;
-  static constexpr int kSub = 8, kQ = NQ, kEs = 4, kWarps = HD > 128 ? 4 : 8, VS = 1;
+  static constexpr bool kMoreRegs = false;
+  static constexpr int kHd = HD, kSub = 8, kQ = NQ, kEs = 4, kWarps = HD > 128 ? 4 : 8, VS = 1;
   static constexpr int R = HD <= 64 ? 16 : 32, E = HD / R, NP = NQ / 2, J = NQ / 4;   // a lane's components and own scores
   static constexpr int KK = 8 * R / 32;      // keys a lane looks at
   using S = State<NQ * E, NQ>;
@@ -881,6 +893,7 @@ __global__ void __launch_bounds__(M::kWarps * 32 + 128, 1) paged_attention_kerne
 
   if (warp >= NW) {
     // ------------------------------------------------------------ producers: K, V
+    if constexpr (M::kMoreRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kProducerRegs));
     // Rows have many small copies, which two warps issue in turn (a copy takes a warp ~80 cycles): the
     // second one waits and looks up like the first, which alone writes the masks and arrives.
     const int v = (warp - NW) & 1, second = (warp - NW) >> 1;
@@ -995,6 +1008,7 @@ __global__ void __launch_bounds__(M::kWarps * 32 + 128, 1) paged_attention_kerne
   }
 
   // -------------------------------------------------------------- consumers
+  if constexpr (M::kMoreRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kConsumerRegs));
   const int vs = warp % M::VS, unit = warp / M::VS;
   const int h = unit % p.nh, qi = unit / p.nh % p.qt, kgrp = unit / (p.nh * p.qt);
   float* wscr = mscr + warp * math_scratch<M>();
@@ -1048,18 +1062,46 @@ __global__ void __launch_bounds__(M::kWarps * 32 + 128, 1) paged_attention_kerne
     reset(s);
     if (!kEarly) load_q();
     math.scale_q(g, lane);
-    for (int t = w.t0; t < w.t1; ++t) {
-      bool ok = tc::mbar_wait(full0 + 8 * slot, phase, const_cast<volatile int*>(flags));
-      if (ok && nq > 0) {
-        math.scores(g, ring0 + slot * slot_bytes, masks[slot * kMaskWords + (k0 >> 5)] >> (k0 & 31), lane, s, wscr);
+    auto wait = [&](int sl, int ph) { return tc::mbar_wait(full0 + 8 * sl, ph, const_cast<volatile int*>(flags)); };
+    auto mask_of = [&](int sl) { return masks[sl * kMaskWords + (k0 >> 5)] >> (k0 & 31); };
+    if constexpr (std::is_same_v<T, float>) {
+      for (int t = w.t0; t < w.t1; ++t) {
+        bool ok = wait(slot, phase);
+        if (ok && nq > 0) math.scores(g, ring0 + slot * slot_bytes, mask_of(slot), lane, s, wscr);
+        advance();
+        ok = wait(slot, phase) && ok;
+        if (ok && nq > 0) math.values(g, ring0 + slot * slot_bytes, lane, s, wscr);
+        advance();
       }
+    } else {
+      // a tile's values together with the next one's scores
+      bool ok = wait(slot, phase);
+      uint32_t mask = mask_of(slot);
+      if (ok && nq > 0) math.dots(g, ring0 + slot * slot_bytes, mask);
       advance();
-      ok = tc::mbar_wait(full0 + 8 * slot, phase, const_cast<volatile int*>(flags)) && ok;
-      if (ok && nq > 0) {
-        if constexpr (math_scratch<M>() > 0) math.values(g, ring0 + slot * slot_bytes, lane, s, wscr);
-        else math.values(g, ring0 + slot * slot_bytes, lane, s, vs);
+      for (int t = w.t0; t < w.t1; ++t) {
+        if (ok && nq > 0) math.weights(g, mask, lane, s);
+        ok = wait(slot, phase) && ok;
+        const uint32_t v = ring0 + slot * slot_bytes;
+        if (t + 1 == w.t1) {
+          if (ok && nq > 0) math.values(g, v, lane, s, vs);
+        } else {
+          const int ks = slot + 1 == p.slots ? 0 : slot + 1;
+          ok = wait(ks, ks == 0 ? phase ^ 1 : phase) && ok;
+          mask = mask_of(ks);
+          const uint32_t k = ring0 + ks * slot_bytes;
+          if (ok && nq > 0) {
+            if (math.can_run_both(g, mask)) {
+              math.both(g, k, v, s, vs);
+            } else {
+              math.dots(g, k, mask);
+              math.values(g, v, lane, s, vs);
+            }
+          }
+          advance();
+        }
+        advance();
       }
-      advance();
     }
     math.finish(s);
     more = w.next();
@@ -1154,13 +1196,22 @@ __global__ void __launch_bounds__(M::kWarps * 32 + 128, 1) paged_attention_kerne
 // What the planner needs to know of an instantiation, and its launch.
 struct Kernel {
   void (*fn)(Args);
-  int warps, vs, sub, kq, es;
+  int warps, vs, sub, kq, es, hd;
   size_t (*fixed)(int);
+  bool (*fits)();      // launched with the registers that its warps share out
 };
 template <typename M> Kernel kernel_of() {
   static_assert(M::kWarps * entry_floats<M>() <= 8 * 72 * 32, "a CTA's piece fits the workspace");
-  return {paged_attention_kernel<M>, M::kWarps, M::VS, M::kSub, M::kQ, M::kEs,
-          [](int B) { return fixed_smem<M>(B); }};
+  return {paged_attention_kernel<M>, M::kWarps, M::VS, M::kSub, M::kQ, M::kEs, M::kHd,
+          [](int B) { return fixed_smem<M>(B); },
+          [] {
+            static const bool ok = [] {      // a share above the launch's registers would be waited for without end
+              cudaFuncAttributes a;
+              return !M::kMoreRegs || (cudaFuncGetAttributes(&a, paged_attention_kernel<M>) == cudaSuccess &&
+                                       M::kWarps == 8 && a.numRegs == kLaunchRegs);
+            }();
+            return ok;
+          }};
 }
 
 Kernel kernel_bf16(bool e4m3, int hd, int G);
@@ -1172,7 +1223,7 @@ Kernel kernel_f32(int hd, int G);
 template <typename T, bool F8> Kernel pick16(int hd, int G) {
   if (hd <= 64) return G <= 8 ? kernel_of<MmaMath<T, F8, 64, 1>>() : kernel_of<MmaMath<T, F8, 64, 2>>();
   if (hd <= 128) return G <= 8 ? kernel_of<MmaMath<T, F8, 128, 1>>() : kernel_of<MmaMath<T, F8, 128, 2>>();
-  return kernel_of<MmaMath<T, F8, 256, 1>>();
+  return hd <= 192 ? kernel_of<MmaMath<T, F8, 192, 1>>() : kernel_of<MmaMath<T, F8, 256, 1>>();
 }
 
 }  // namespace pa
