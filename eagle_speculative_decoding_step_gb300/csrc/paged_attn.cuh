@@ -219,7 +219,7 @@ template <typename T, bool F8, int HD, int NT> struct MmaMath {
   static constexpr int kSub = 16 * U, kQ = 8 * NT;
   // above 128 components two warps share keys and queries: both compute the scores, each half of the outputs
   static constexpr int kWarps = 8, VS = HD > 128 ? 2 : 1, MT = HD / 16 / VS;
-  static constexpr bool kMoreRegs = NT == 2 && HD == 128;
+  static constexpr bool kMoreRegs = NT == 2 && HD >= 128;
   using S = State<MT * NT * 4, 2 * NT>;
   // register r = (mt NT + nt) 4 + 2 i + j: query nt 8 + 2 (lane & 3) + j, component mt 16 + (lane >> 2) + 8 i
   // (8-bit caches: mt 16 + 2 (lane >> 2) + i)
@@ -1218,12 +1218,14 @@ Kernel kernel_bf16(bool e4m3, int hd, int G);
 Kernel kernel_f16(bool e4m3, int hd, int G);
 Kernel kernel_f32(int hd, int G);
 
-// 8 queries a warp, 16 where a kv head has more than 8 (not above 128 components, where the state
-// of 16 queries would not fit in registers)
+// 8 queries a warp, 16 where a kv head has more than 8: keys are then read from shared memory once for
+// all of them (32 requests of 4000 keys, 8 heads of 256, 128 queries, by 8 / by 16: 196 / 168 us, in 8
+// bits 158 / 139; 192 components 191 / 127)
 template <typename T, bool F8> Kernel pick16(int hd, int G) {
   if (hd <= 64) return G <= 8 ? kernel_of<MmaMath<T, F8, 64, 1>>() : kernel_of<MmaMath<T, F8, 64, 2>>();
   if (hd <= 128) return G <= 8 ? kernel_of<MmaMath<T, F8, 128, 1>>() : kernel_of<MmaMath<T, F8, 128, 2>>();
-  return hd <= 192 ? kernel_of<MmaMath<T, F8, 192, 1>>() : kernel_of<MmaMath<T, F8, 256, 1>>();
+  if (hd <= 192) return G <= 8 ? kernel_of<MmaMath<T, F8, 192, 1>>() : kernel_of<MmaMath<T, F8, 192, 2>>();
+  return G <= 8 ? kernel_of<MmaMath<T, F8, 256, 1>>() : kernel_of<MmaMath<T, F8, 256, 2>>();
 }
 
 }  // namespace pa
