@@ -68,12 +68,30 @@ struct Args {
   void* ws;
 };
 
+// quotient and root of the cost model: the device's need only be the same in every CTA
+__host__ __device__ inline float cost_div(float a, float b) {
+#ifdef __CUDA_ARCH__
+  return __fdividef(a, b);
+#else
+  return a / b;
+#endif
+}
+__host__ __device__ inline float cost_sqrt(float x) {
+#ifdef __CUDA_ARCH__
+  float y;
+  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+#else
+  return sqrtf(x);
+#endif
+}
+
 // What it costs, in tiles (64 KB, ~1.35 us), to leave n pieces of an item and join
 // them: the exchange itself, a second level beyond kFlat pieces, and the pieces that
 // the joining CTA reads one after another, its kg key groups taking turns.
 __host__ __device__ inline float join_cost(int n, float per_kg) {
   if (n <= 1) return 0.f;
-  const float reads = n > kFlat ? 2.f * sqrtf((float)n) + 1.f : (float)n;
+  const float reads = n > kFlat ? 2.f * cost_sqrt((float)n) + 1.f : (float)n;
   return (n > kFlat ? 2.5f : 1.5f) + 0.37f * fmaxf(reads * per_kg, 1.f);
 }
 
@@ -84,24 +102,23 @@ __host__ __device__ inline float join_cost(int n, float per_kg) {
 // 19.7 in shares; 32 items of 8 tiles 10.4 us in 4 pieces each, 13.0 in shares; 64
 // requests of 8190 keys, 128 items of 256 tiles, in shares.
 //
-// In fp32 throughout: every CTA works it out for itself before it can start (integer
-// divisions made a call of one key 0.6 us longer).
+// In fp32 throughout: every CTA works it out for itself before it can start.
 __host__ __device__ inline float share_out(long long total_, long long items_, int most, int kg, int ctas, int* cuts) {
-  const float total = (float)total_, items = (float)items_, used = fminf(total, (float)ctas), per_kg = 1.f / (float)kg;
+  const float total = (float)total_, items = (float)items_, used = fminf(total, (float)ctas), per_kg = cost_div(1.f, (float)kg);
   // merging the key groups; ~0.8 tiles for every further item that a share touches
   const float base = kg == 1 ? 0.f : kg == 2 ? 0.1f : kg == 4 ? 0.2f : 0.3f;
-  float best = total / used + 2.f + 0.8f * items / used;
-  const int pieces = (int)((used + 0.5f) / items) + 1;
+  float best = cost_div(total + 0.8f * items, used) + 2.f;
+  const int pieces = (int)cost_div(used + 0.5f, items) + 1;
   best += join_cost(pieces > 2 ? pieces : 2, per_kg);
   *cuts = 0;
   if (items <= (float)ctas) {
-    const int room = (int)(((float)ctas + 0.5f) / items), all = room < most ? room : most;
+    const int room = (int)cost_div((float)ctas + 0.5f, items), all = room < most ? room : most;
     const int few = all < kFlat ? all : kFlat;
     if ((float)most <= best) best = (float)most, *cuts = 1;
-    const float c8 = ceilf(((float)most - 0.5f) / (float)few) + join_cost(few, per_kg);
+    const float c8 = ceilf(cost_div((float)most - 0.5f, (float)few)) + join_cost(few, per_kg);
     if (c8 < best) best = c8, *cuts = few;
     if (all > few) {
-      const float ca = ceilf(((float)most - 0.5f) / (float)all) + join_cost(all, per_kg);
+      const float ca = ceilf(cost_div((float)most - 0.5f, (float)all)) + join_cost(all, per_kg);
       if (ca < best) best = ca, *cuts = all;
     }
   }
@@ -226,6 +243,10 @@ template <typename T, bool F8, int HD, int NT> struct MmaMath {
   SPEC_DEV static int st(int r) { return ((r >> 2) % NT) * 2 + (r & 1); }
   // outputs two components at a time
   SPEC_DEV static void write(const S& s, const float* inv, T* out, int hd, int nq, int lane, int vs) {
+    if (hd == HD) write_as<true>(s, inv, out, HD, nq, lane, vs);
+    else write_as<false>(s, inv, out, hd, nq, lane, vs);
+  }
+  template <bool FULL> SPEC_DEV static void write_as(const S& s, const float* inv, T* out, int hd, int nq, int lane, int vs) {
     const int g = lane >> 2, t = lane & 3;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -234,7 +255,7 @@ template <typename T, bool F8, int HD, int NT> struct MmaMath {
         T* o = out + (long long)(nt * 8 + 2 * t) * hd + vs * MT * 16 + 2 * g;
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
-          if ((vs * MT + mt) * 16 < hd)
+          if (FULL || (vs * MT + mt) * 16 < hd)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
               const float* x = &s.o[(mt * NT + nt) * 4 + j];
@@ -246,7 +267,7 @@ template <typename T, bool F8, int HD, int NT> struct MmaMath {
         T* o = out + (long long)(nt * 8 + g) * hd + vs * MT * 16 + 2 * t;
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
-          if ((vs * MT + mt) * 16 < hd)
+          if (FULL || (vs * MT + mt) * 16 < hd)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
               const float* x = &s.o[(mt * NT + nt) * 4 + 2 * i];
@@ -282,7 +303,11 @@ template <typename T, bool F8, int HD, int NT> struct MmaMath {
   static constexpr uint32_t kAll = U == 2 ? 0xffffffffu : 0xffffu;
 
   // queries of the tile: q points at the kv head's first query, n of them from q0 on exist
-  SPEC_DEV void load_q(const Args& g, const T* q, int q0, int n, int lane, float*) {
+  SPEC_DEV void load_q(const Args& g, const T* q, int q0, int n, int lane) {
+    if (g.hd == HD) load_q_as<true>(q + (long long)q0 * HD, HD, n, lane);
+    else load_q_as<false>(q + (long long)q0 * g.hd, g.hd, n, lane);
+  }
+  template <bool FULL> SPEC_DEV void load_q_as(const T* q, int hd, int n, int lane) {
     const int gq = lane >> 2, t = lane & 3;
 #pragma unroll
     for (int ks = 0; ks < HD / 16; ++ks)
@@ -290,8 +315,8 @@ template <typename T, bool F8, int HD, int NT> struct MmaMath {
       for (int nt = 0; nt < NT; ++nt) {
         const int i = nt * 8 + gq;
         qf[ks][nt][0] = qf[ks][nt][1] = 0;
-        if (i < n && ks * 16 < g.hd) {
-          const T* p = q + (long long)(q0 + i) * g.hd + ks * 16;
+        if (i < n && (FULL || ks * 16 < hd)) {
+          const T* p = q + (long long)i * hd + ks * 16;
           if constexpr (F8) {       // component order of an 8-bit K row's words
             const uint2 x = *reinterpret_cast<const uint2*>(p + 4 * t);
             qf[ks][nt][0] = x.x;
@@ -407,8 +432,13 @@ template <typename T, bool F8, int HD, int NT> struct MmaMath {
   SPEC_DEV void dots(const Args& g, uint32_t k, uint32_t mask) {
     if ((mask & kAll) == 0) return;
     clear();
+    if (g.p.full) {
 #pragma unroll
-    for (int i = 0; i < KS; ++i) dot_step<false>(g, k, i);
+      for (int i = 0; i < KS; ++i) dot_step<true>(g, k, i);
+    } else {
+#pragma unroll
+      for (int i = 0; i < KS; ++i) dot_step<false>(g, k, i);
+    }
   }
   // that and values() of the tile before: two independent chains of instructions in one run without a branch
   SPEC_DEV bool can_run_both(const Args& g, uint32_t mask) const { return vm == kAll && (mask & kAll) == kAll && g.p.full; }
@@ -496,8 +526,13 @@ template <typename T, bool F8, int HD, int NT> struct MmaMath {
         const uint32_t b = vm >> (16 * u + 8 * h + t2);
         z[u][h] = (b & 1 ? 0xffffu : 0) | (b & 2 ? 0xffff0000u : 0);
       }
+    if (g.p.full) {
 #pragma unroll
-    for (int i = 0; i < VSTEPS; ++i) value_step<false, false>(g, v, s, vs, i, z);
+      for (int i = 0; i < VSTEPS; ++i) value_step<true, false>(g, v, s, vs, i, z);
+    } else {
+#pragma unroll
+      for (int i = 0; i < VSTEPS; ++i) value_step<false, false>(g, v, s, vs, i, z);
+    }
   }
   // sums over the lanes that hold other keys of the same query
   SPEC_DEV void finish(S& s) {
@@ -565,7 +600,7 @@ template <int HD, int NQ> struct F32Math {
       voff[k] = rv.off + unit + (x ^ rv.x);
     }
   }
-  SPEC_DEV void load_q(const Args& g, const float* q, int q0, int n, int lane, float*) {
+  SPEC_DEV void load_q(const Args& g, const float* q, int q0, int n, int lane) {
 #pragma unroll
     for (int u = 0; u < E / 4; ++u) {
       in[u] = comp(u, lane) < g.hd;
@@ -747,35 +782,36 @@ template <typename M, typename Get> SPEC_DEV void join(typename M::S& s, Get get
   for (int r = 0; r < S::NR; ++r) s.o[r] = s.o[r] * a[M::st(r)] + get(r) * b[M::st(r)];
 }
 
+// a / b for 0 <= a, 0 < b: in fp32 where that is exact (a < 2^20: the quotient of a + 0.5 is at least 0.5 / b
+// from an integer, and within 2^-21 of its value), which is quicker than the integer division
+SPEC_DEV int quot(int a, int b) { return a < (1 << 20) ? (int)__fdividef((float)a + 0.5f, (float)b) : a / b; }
+
 // The linear order of a launch's tiles: (request, head group, tile).  CTA c owns tiles
-// [c T / C, (c + 1) T / C), or a piece of one item.  Every CTA finds its range by
-// bisection of the prefix sums of the requests' tile counts.
+// [c T / C, (c + 1) T / C), or a piece of one item; pre [B + 1]: exclusive prefix sums of the
+// requests' tile counts.  A Walk goes through the pieces that a CTA owns.
 struct Walk {
-  const int* pre;       // [B + 1] exclusive prefix sums of tile counts
+  const int* pre;
   int hgq;
-  long long idx, end;
-  int b;
+  long long left;       // tiles after the current piece
+  bool first;
   // current piece: tiles [t0, t1) of head group hg of request b, which has nt
-  int hg, t0, t1, nt;
-  SPEC_DEV Walk(const int* pre_, int B, int hgq_, long long beg, long long end_) : pre(pre_), hgq(hgq_), idx(beg), end(end_) {
-    int lo = 0, hi = B;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if ((long long)pre[mid] * hgq <= beg) lo = mid;
-      else hi = mid;
-    }
-    b = lo;
-  }
+  int b, hg, t0, t1, nt;
+  // from tile t of (b, hg)
+  SPEC_DEV Walk(const int* pre_, int hgq_, int b_, int hg_, int t, long long tiles)
+      : pre(pre_), hgq(hgq_), left(tiles), first(true), b(b_), hg(hg_), t0(t), t1(0), nt(pre_[b_ + 1] - pre_[b_]) {}
   SPEC_DEV bool next() {
-    if (idx >= end) return false;
-    while ((long long)pre[b + 1] * hgq <= idx) ++b;
-    nt = pre[b + 1] - pre[b];
-    const long long off = idx - (long long)pre[b] * hgq;
-    hg = off >> 32 ? (int)(off / nt) : (int)((uint32_t)off / (uint32_t)nt);
-    t0 = (int)(off - (long long)hg * nt);
-    const long long n = end - idx < nt - t0 ? end - idx : nt - t0;
-    t1 = t0 + (int)n;
-    idx += n;
+    if (left <= 0) return false;
+    if (!first) {
+      t0 = 0;
+      if (++hg == hgq) {
+        hg = 0;
+        ++b;
+        nt = pre[b + 1] - pre[b];
+      }
+    }
+    first = false;
+    t1 = left < nt - t0 ? t0 + (int)left : nt;
+    left -= t1 - t0;
     return true;
   }
 };
@@ -820,6 +856,12 @@ __global__ void __launch_bounds__(M::kWarps * 32 + 128, 1) paged_attention_kerne
     pre[0] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  // consumers: the keys, head and queries of a warp
+  const int vs = warp % M::VS, unit = warp / M::VS;
+  const int kq = quot(unit, p.nh), h = unit - kq * p.nh, kgrp = quot(kq, p.qt), qi = kq - kgrp * p.qt;
+  const int k0 = kgrp * M::kSub;
+  M math;
+  if (warp < NW) math.init(p, k0, h, lane, zero0);
   pdl_wait();
   pdl_trigger();
   // tile counts of the requests (one empty tile where there is nothing to attend to, so that
@@ -827,12 +869,19 @@ __global__ void __launch_bounds__(M::kWarps * 32 + 128, 1) paged_attention_kerne
   const long long most_l = (long long)g.kv.max_blocks * g.kv.block_size;
   const int most = (int)most_l;
   auto first_key = [&](int len) { return g.window > 0 && len > g.window ? len - g.window : 0; };
-  int carry = 0, most_tiles = 0;
-  for (int base = 0; base < g.B; base += NW * 32 + 128) {
-    const int b = base + tid;
-    int x = 0;
-    if (b < g.B) {
-      int len = g.seq_len[g.b0 + b];
+  constexpr int kThreads = NW * 32 + 128, kPerThread = (kMaxB + kThreads - 1) / kThreads;
+  const int per = (g.B + kThreads - 1) / kThreads;
+  int most_tiles = 0, mine = 0, own_tiles[kPerThread];
+#pragma unroll
+  for (int j = 0; j < kPerThread; ++j) {
+    const int b = tid * per + j;
+    own_tiles[j] = j < per && b < g.B ? g.seq_len[g.b0 + b] : 0;
+  }
+#pragma unroll
+  for (int j = 0; j < kPerThread; ++j) {
+    const int b = tid * per + j;
+    if (j < per && b < g.B) {
+      int len = own_tiles[j];
       if (len < 0 || len > most) {
         if (blockIdx.x == 0) report(g.ws, SPEC_ERR_DEVICE, g.b0 + b, len);
         len = len < 0 ? 0 : most;
@@ -840,23 +889,30 @@ __global__ void __launch_bounds__(M::kWarps * 32 + 128, 1) paged_attention_kerne
       lens[b] = len;
       int lo = first_key(len);
       if (p.swz) lo &= -1 << p.run_lg;       // tiles start with a run
-      x = max(1, (len - lo + p.kt - 1) / p.kt);
+      own_tiles[j] = max(1, quot(len - lo + p.kt - 1, p.kt));
+      mine += own_tiles[j];
+      most_tiles = max(most_tiles, own_tiles[j]);
     }
-    const int largest = __reduce_max_sync(0xffffffffu, x);
+  }
+  {
+    int sum = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
+      const int y = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += y;
     }
-    if (lane == 31) wsum[warp] = x, wmax[warp] = largest;
+    most_tiles = __reduce_max_sync(0xffffffffu, most_tiles);
+    if (lane == 31) wsum[warp] = sum, wmax[warp] = most_tiles;
     __syncthreads();
-    int before = carry;
+    sum -= mine;
+#pragma unroll
     for (int w = 0; w < NW + 4; ++w) {
-      if (w < warp) before += wsum[w];
-      carry += wsum[w];
+      if (w < warp) sum += wsum[w];
       most_tiles = max(most_tiles, wmax[w]);
     }
-    if (b < g.B) pre[b + 1] = before + x;
+#pragma unroll
+    for (int j = 0; j < kPerThread; ++j)
+      if (j < per && tid * per + j < g.B) pre[tid * per + j + 1] = sum += own_tiles[j];
     __syncthreads();
   }
   const long long total = (long long)pre[g.B] * p.hgq;
@@ -864,19 +920,33 @@ __global__ void __launch_bounds__(M::kWarps * 32 + 128, 1) paged_attention_kerne
   int cuts;
   share_out(total, (long long)g.B * p.hgq, most_tiles, p.kg, gridDim.x, &cuts);
   const long long C = total < (long long)gridDim.x ? total : (long long)gridDim.x;
-  long long beg, end;
+  int b_at, hg_at = 0, t_at;
+  long long tiles;
   if (cuts > 0) {
-    const int item = cta / cuts, piece = cta - item * cuts, b = item / p.hgq;
-    if (b >= g.B) return;
-    const int nt = pre[b + 1] - pre[b], n = min(cuts, nt);
+    const int item = quot(cta, cuts), piece = cta - item * cuts;
+    b_at = quot(item, p.hgq);
+    if (b_at >= g.B) return;
+    hg_at = item - b_at * p.hgq;
+    const int nt = pre[b_at + 1] - pre[b_at], n = min(cuts, nt);
     if (piece >= n) return;
-    const long long i0 = (long long)pre[b] * p.hgq + (long long)(item - b * p.hgq) * nt;
-    beg = i0 + (long long)nt * piece / n;
-    end = i0 + (long long)nt * (piece + 1) / n;
+    auto cut = [&](int i) { return nt < 4096 ? quot(nt * i, n) : (int)((long long)nt * i / n); };
+    t_at = cut(piece);
+    tiles = cut(piece + 1) - t_at;
   } else {
     if (cta >= C) return;
-    beg = cta * total / C;
-    end = (cta + 1) * total / C;
+    const long long beg = cta * total / C;
+    tiles = (cta + 1) * total / C - beg;
+    int hi = g.B;
+    b_at = 0;
+    while (hi - b_at > 1) {
+      const int mid = (b_at + hi) >> 1;
+      if ((long long)pre[mid] * p.hgq <= beg) b_at = mid;
+      else hi = mid;
+    }
+    const long long off = beg - (long long)pre[b_at] * p.hgq;
+    const int nt = pre[b_at + 1] - pre[b_at];
+    hg_at = off >> 31 ? (int)(off / nt) : quot((int)off, nt);
+    t_at = (int)(off - (long long)hg_at * nt);
   }
   // the CTAs that have pieces of an item: the first, and how many
   auto owners = [&](int b, int hg, int nt, int* first) {
@@ -888,7 +958,7 @@ __global__ void __launch_bounds__(M::kWarps * 32 + 128, 1) paged_attention_kerne
     *first = (int)(((i0 + 1) * C - 1) / total);
     return (int)(((i0 + nt) * C - 1) / total) - *first + 1;
   };
-  Walk w(pre, g.B, p.hgq, beg, end);
+  Walk w(pre, p.hgq, b_at, hg_at, t_at, tiles);
   const uint32_t ring0 = tc::su32(ring), slot_bytes = (uint32_t)p.slot_bytes;
 
   if (warp >= NW) {
@@ -921,7 +991,7 @@ __global__ void __launch_bounds__(M::kWarps * 32 + 128, 1) paged_attention_kerne
       x.len = lens[w.b];
       x.lo = first_key(x.len);
       x.key0 = (p.swz ? x.lo & -run : x.lo) + t * p.kt;
-      x.head0 = w.hg / p.qs * p.nh;
+      x.head0 = (p.qs == 1 ? w.hg : w.hg / p.qs) * p.nh;
       const int32_t* table = g.kv.block_table + (long long)(g.b0 + w.b) * g.kv.max_blocks;
       auto entry = [&](int key) { return table[shift >= 0 ? key >> shift : key / bs]; };
       if (p.swz) {
@@ -1009,13 +1079,8 @@ __global__ void __launch_bounds__(M::kWarps * 32 + 128, 1) paged_attention_kerne
 
   // -------------------------------------------------------------- consumers
   if constexpr (M::kMoreRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kConsumerRegs));
-  const int vs = warp % M::VS, unit = warp / M::VS;
-  const int h = unit % p.nh, qi = unit / p.nh % p.qt, kgrp = unit / (p.nh * p.qt);
   float* wscr = mscr + warp * math_scratch<M>();
   int slot = 0, phase = 0;
-  const int k0 = kgrp * M::kSub;
-  M math;
-  math.init(p, k0, h, lane, zero0);
   S s;
   auto sync = [] { asm volatile("bar.sync 1, %0;" ::"n"(NW * 32) : "memory"); };
   auto advance = [&] {
@@ -1042,20 +1107,20 @@ __global__ void __launch_bounds__(M::kWarps * 32 + 128, 1) paged_attention_kerne
   // a piece's queries are loaded while the one before it is merged and written, where registers
   // allow (16 queries: spills, and 64 requests of 4000 keys with 128 query heads 165 -> 190 us)
   constexpr bool kEarly = S::NR <= 32;
-  auto queries = [&] {                       // <= 0: none for this warp
-    return kgrp < p.kg ? min(M::kQ, g.G - ((w.hg % p.qs) * p.qt + qi) * M::kQ) : 0;
-  };
-  auto head_of = [&] { return (w.hg / p.qs) * p.nh + h; };
+  auto group = [&] { return p.qs == 1 ? w.hg : w.hg / p.qs; };
+  auto query0 = [&] { return ((w.hg - group() * p.qs) * p.qt + qi) * M::kQ; };
+  auto queries = [&] { return kgrp < p.kg ? min(M::kQ, g.G - query0()) : 0; };     // <= 0: none for this warp
+  auto head_of = [&] { return group() * p.nh + h; };
   auto load_q = [&] {
     const int n = queries();
     if (n > 0)
       math.load_q(g, static_cast<const T*>(g.q) + (g.b0 + w.b) * g.q_ld + (long long)head_of() * g.G * g.hd,
-                  ((w.hg % p.qs) * p.qt + qi) * M::kQ, n, lane, wscr);
+                  query0(), n, lane);
   };
   bool more = w.next();
   if (kEarly && more) load_q();
   while (more) {
-    const int head = head_of(), q0 = ((w.hg % p.qs) * p.qt + qi) * M::kQ, nq = queries();
+    const int head = head_of(), q0 = query0(), nq = queries();
     const long long b = g.b0 + w.b;
     const int piece_b = w.b, hg = w.hg, nt = w.nt;
     const bool whole = w.t1 - w.t0 == w.nt;
