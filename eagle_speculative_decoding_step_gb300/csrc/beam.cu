@@ -37,9 +37,6 @@ constexpr int kSelTile = 32 * kSelElems;
 constexpr int kSelChunk = 128 * kSelTile;                   // at most in a chunk
 constexpr int kSelCap = 512;                                // entries of a candidate list
 constexpr float kLog2e = 1.4426950408889634f;
-#ifndef SELB
-#define SELB 2
-#endif
 
 // the requests' counters lie in the same place whatever a call's sizes (B W < 2^16), so that calls of
 // any sizes share a workspace

@@ -128,6 +128,16 @@ __global__ void __launch_bounds__(kTabThreads) block_tables_kernel(const TabArgs
   if (tid == 0) asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;" : "=r"(arrived) : "l"(ctr) : "memory");
 
   const int gt = blockIdx.x * kTabThreads + tid, gn = gridDim.x * kTabThreads;
+  // The warps take the four kinds of work below one after another, a kind beginning with the warp at which the
+  // one before it ended: a warp has one or two pieces of one kind rather than the latencies of all four
+  // (512 requests, 0.8 million new tokens: then 3 CTAs an SM: 13.8 -> 11.8 us).
+  const int warps = gn >> 5;
+  int begun = 0;
+  auto first_piece = [&](long long pieces) {
+    const int at = (gt >> 5) - begun;
+    begun = (int)((begun + pieces) % warps);
+    return at < 0 ? at + warps : at;
+  };
   const bool out_of_place = g.table_out != g.table_in, pool_moves = g.free_out != g.free_in;
   auto on16 = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; };
   const bool vec_pool = on16(g.free_in) && on16(g.free_out);
@@ -152,7 +162,7 @@ __global__ void __launch_bounds__(kTabThreads) block_tables_kernel(const TabArgs
   };
   // what stays in the pool (an entry of the free list that stays where it is is not
   // written in place), and -1 past its end; four entries a thread
-  for (int j0 = 4 * gt; j0 < g.num_blocks; j0 += 4 * gn) {
+  for (int j0 = 128 * first_piece((g.num_blocks + 127) >> 7) + 4 * lane; j0 < g.num_blocks; j0 += 4 * gn) {
     const bool four = pool_moves && j0 + 4 <= g.num_blocks && vec_pool;
     if (four && j0 + 4 <= min(left, n_free)) {
       *reinterpret_cast<int4*>(g.free_out + j0) = *reinterpret_cast<const int4*>(g.free_in + j0);
@@ -173,8 +183,8 @@ __global__ void __launch_bounds__(kTabThreads) block_tables_kernel(const TabArgs
   int lg = 0;
   while (lg < 5 && (1 << lg) < bs) ++lg;
   const int part = lane & ((1 << lg) - 1);
-  constexpr int kTake = 8;                           // blocks of a warp: few, so that many warps share them
-  for (int base = (gt >> 5) * kTake; base < taken; base += (gn >> 5) * kTake) {
+  constexpr int kTake = 16;                          // blocks of a warp (8 / 16 / 32: 9.9 / 8.7 / 9.0 us for 512 requests as below)
+  for (int base = first_piece((taken + kTake - 1) / kTake) * kTake; base < taken; base += warps * kTake) {
     const int i = lane < kTake ? base + lane : taken;  // the i-th block taken
     int id = -1, first = 0, end = 0, to = 0;         // tokens [first, end) of the block, slot entry of token 0
     int e = 0;
@@ -204,7 +214,7 @@ __global__ void __launch_bounds__(kTabThreads) block_tables_kernel(const TabArgs
   // kept entries, and -1 past a request's blocks: a warp takes 128 entries of a row
   if (out_of_place) {
     const int segs = (mb + 127) >> 7;
-    for (int task = gt >> 5; task < B * segs; task += gn >> 5) {
+    for (int task = first_piece((long long)B * segs); task < B * segs; task += warps) {
       const int b = task / segs, i0 = (task - b * segs) * 128 + 4 * lane, want = want_of(b), keep = min(have_of(b), want);
       const int32_t* in = g.table_in + (long long)b * mb + i0;
       int32_t* out = g.table_out + (long long)b * mb + i0;
@@ -222,7 +232,7 @@ __global__ void __launch_bounds__(kTabThreads) block_tables_kernel(const TabArgs
   }
   // tokens of blocks that were there before, a warp a request; all tokens of a request
   // that is not served
-  for (int b = gt >> 5; b < B; b += gn >> 5) {
+  for (int b = first_piece(B); b < B; b += warps) {
     const int o = s_old[b], off = (b > 0 ? s_cnt[b - 1] : 0) - o;
     const bool ok = is_served(b);
     const int end = ok ? min(s_new[b], have_of(b) * bs) : s_new[b];
@@ -406,11 +416,11 @@ extern "C" spec_status spec_block_tables(int32_t B, int32_t block_size, int32_t 
   if (!ws || !aligned(ws, 256) || ws_bytes < spec_block_tables_workspace_bytes(B)) return SPEC_ERR_WORKSPACE;
   TabArgs a{B, block_size, max_blocks, num_blocks, slots_cap, len_old, len_new, table_in, free_in, n_free_in,
             table_out, free_out, n_free_out, len_out, cu_new, slots, pos, ws};
-  // a CTA per 1024 items it may have to touch, up to three an SM: every CTA scans the requests for itself
-  // (64 requests of 8000 tokens 5.6 us from 512 to 2048 items a CTA; 512 requests, 1 million new tokens,
-  // 1 / 2 / 3 / 4 CTAs an SM 22.1 / 15.5 / 14.7 / 15.9 us)
+  // a CTA per 1024 items it may have to touch, up to two an SM: every CTA scans the requests for itself
+  // (64 requests of 8000 tokens 4.1 / 4.0 / 4.6 us with 512 / 1024 / 2048 items a CTA; 512 requests, 0.8 million new
+  // tokens, 1 / 2 / 3 CTAs an SM 10.2 / 8.7 / 10.7 us)
   const long long items = (table_out != table_in ? (long long)B * max_blocks : 0) + num_blocks + slots_cap;
-  const int grid = (int)std::min<long long>(std::max<long long>(1, items / 1024), 3 * sm_count());
+  const int grid = (int)std::min<long long>(std::max<long long>(1, items / 1024), 2 * sm_count());
   const size_t smem = (size_t)5 * B * 4;
   if (smem > 47 * 1024 && cudaFuncSetAttribute(block_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                5 * kTabMaxB * 4) != cudaSuccess)
