@@ -86,6 +86,7 @@ struct SelShared {
   uint64_t key[kSelCap], entry[kSelCap];
   int idx[kSelCap];
   uint64_t kred[kSelWarps];
+  uint32_t bound[kSelWarps];
   int ired[kSelWarps];
   float fred[2][kSelWarps];
   int count, groups, last;
@@ -97,67 +98,75 @@ struct SelShared {
 
 // A lower bound of the block's k-th largest value from the threads' maxima: a warp's
 // k-th largest is reached by k values, and so is the largest of those over the warps.
-template <typename K> SPEC_DEV K block_bound(K mine, int k, SelShared& sm) {
+// In two steps, the caller's barrier between them.
+SPEC_DEV void leave_bound(uint32_t mine, int k, SelShared& sm) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int rank = 0;
 #pragma unroll
   for (int o = 1; o < 32; ++o) {
-    const K w = __shfl_sync(0xffffffffu, mine, (lane + o) & 31);
+    const uint32_t w = __shfl_sync(0xffffffffu, mine, (lane + o) & 31);
     rank += w > mine || (w == mine && ((lane + o) & 31) < lane);
   }
-  if (rank == k - 1) sm.kred[warp] = mine;
-  __syncthreads();
-  K b = (K)sm.kred[0];
+  if (rank == k - 1) sm.bound[warp] = mine;
+}
+SPEC_DEV uint32_t block_bound(const SelShared& sm) {
+  uint32_t b = sm.bound[0];
 #pragma unroll
-  for (int w = 1; w < kSelWarps; ++w) b = (K)sm.kred[w] > b ? (K)sm.kred[w] : b;
-  __syncthreads();
+  for (int w = 1; w < kSelWarps; ++w) b = max(b, sm.bound[w]);
   return b;
 }
 
 // The block's k best of `lists` lists of up to k (key, index) entries, each in
-// descending order: get(list, place, index) is an entry's key, 0 past the list's end.
+// descending order: get(place, index) is the key of an entry, lists one after another, 0 past a list's end;
+// first(e, place, index) the same of the e-th that a thread can hold.
 // They go, in order, to the front of the shared list; sm.count is how many there are.
 // Entries at or above a bound are collected and ranked by counting; if those overflow
 // the list, k rounds of block-wide maxima.  The bound comes from the threads' maxima
 // over all entries where those can be held in registers between the two looks, else
 // over the lists' heads, so that only lists whose head reaches it are read (16 beams:
 // 512 entries 29.6 us against 35.7 by heads, 2560 entries 17.1 by heads against 35.8).
-template <typename Get> SPEC_DEV void block_best(int k, int lists, Get get, SelShared& sm) {
+constexpr int kHeld = 8;
+SPEC_DEV bool can_hold(int k, int lists) { return lists * k <= kHeld * kSelThreads; }
+template <typename First, typename Get> SPEC_DEV void block_best(int k, int lists, First first, Get get, SelShared& sm) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  constexpr int kHeld = 8;
   if (tid == 0) sm.count = sm.groups = 0;
   auto keep = [&](uint64_t x, int i) {
     const int at = atomicAdd(&sm.count, 1);
     if (at < kSelCap) sm.key[at] = x, sm.idx[at] = i;
   };
+  auto shared_bound = [&](uint64_t mine) {
+    leave_bound((uint32_t)(mine >> 32), k, sm);                // of the keys' upper halves
+    __syncthreads();
+    const uint64_t bound = (uint64_t)block_bound(sm) << 32;
+    return bound == 0 ? (uint64_t)1 : bound;
+  };
   int open = 0;                                                // lists that were read
   uint64_t mine = 0;
-  if (lists * k <= kHeld * kSelThreads) {
+  if (can_hold(k, lists)) {
     uint64_t held[kHeld];
     int at_of[kHeld];
 #pragma unroll
     for (int e = 0; e < kHeld; ++e) {
-      const int l = (tid + e * kSelThreads) / k;
-      held[e] = l < lists ? get(l, tid + e * kSelThreads - l * k, at_of[e]) : 0;
+      const int at = tid + e * kSelThreads;
+      held[e] = 0;
+      if (at < lists * k) held[e] = first(e, at, at_of[e]);
       mine = held[e] > mine ? held[e] : mine;
     }
-    uint64_t bound = block_bound<uint64_t>(mine, k, sm);       // has a barrier
-    if (bound == 0) bound = 1;
+    const uint64_t bound = shared_bound(mine);
 #pragma unroll
     for (int e = 0; e < kHeld; ++e)
       if (held[e] >= bound) keep(held[e], at_of[e]);
   } else {
     for (int l = tid; l < lists; l += kSelThreads) {
       int i;
-      const uint64_t x = get(l, 0, i);
+      const uint64_t x = get(l * k, i);
       mine = x > mine ? x : mine;
     }
-    uint64_t bound = block_bound<uint64_t>(mine, k, sm);
-    if (bound == 0) bound = 1;
+    const uint64_t bound = shared_bound(mine);
     if (mine >= bound)
       for (int l = tid; l < lists; l += kSelThreads) {
         int i;
-        if (get(l, 0, i) < bound) continue;
+        if (get(l * k, i) < bound) continue;
         const int at = atomicAdd(&sm.groups, 1);
         if (at < kSelCap) sm.entry[at] = (uint64_t)l;
       }
@@ -165,7 +174,7 @@ template <typename Get> SPEC_DEV void block_best(int k, int lists, Get get, SelS
     open = sm.groups;
     for (int e = tid; e < min(open, kSelCap) * k; e += kSelThreads) {
       int i;
-      const uint64_t x = get((int)sm.entry[e / k], e % k, i);
+      const uint64_t x = get((int)sm.entry[e / k] * k + e % k, i);
       if (x >= bound) keep(x, i);
     }
   }
@@ -179,7 +188,7 @@ template <typename Get> SPEC_DEV void block_best(int k, int lists, Get get, SelS
       int at = 0x7fffffff;
       for (int e = tid; e < lists * k; e += kSelThreads) {
         int i;
-        const uint64_t x = get(e / k, e % k, i);
+        const uint64_t x = get(e, i);
         if (x > 0 && ahead(pv, pi, x, i) && ahead(x, i, v, at)) v = x, at = i;
       }
       for (int o = 16; o > 0; o >>= 1) {
@@ -348,11 +357,13 @@ __global__ void __launch_bounds__(kSelThreads, 4) beam_select_kernel(const SelAr
         maxima[((base - c0) / kSelTile) * 32 + lane] = m;
       }
     }
-    // the chunk's sum, relative to its largest logit
+    // the chunk's sum, relative to its largest logit; a bound of its W-th largest group maximum
+    // from the lanes' largest
     const float rw = warp_max(r);
     s = warp_sum(r == -INFINITY ? 0.f : s * pow2((r - rw) * kLog2e));
     if (lane == 0) sm.fred[0][warp] = rw, sm.fred[1][warp] = s;
     if (tid == 0) sm.count = sm.groups = 0;
+    leave_bound(key_of(r), W, sm);
     __syncthreads();
     if (tid == 0) {
       float R = sm.fred[0][0], S = 0.f;
@@ -361,12 +372,11 @@ __global__ void __launch_bounds__(kSelThreads, 4) beam_select_kernel(const SelAr
         if (sm.fred[0][w] > -INFINITY) S += sm.fred[1][w] * pow2((sm.fred[0][w] - R) * kLog2e);
       g.stats[(long long)row * g.nch + ch] = make_float2(R, S);
     }
-    // the W groups with the largest maxima (and those that equal the last of them)
-    const int groups = (c1 - c0 + kSelTile - 1) / kSelTile * 32;
-    float best = -INFINITY;
-    for (int i = tid; i < groups; i += kSelThreads) best = fmaxf(best, maxima[i]);
-    const float bound = value_of(block_bound<uint32_t>(key_of(best), W, sm));
-    if (best >= bound && best > -INFINITY)
+    // the W groups with the largest maxima (and those that equal the last of them), each lane among its own
+    const float bound = value_of(block_bound(sm));
+    if (r >= bound && r > -INFINITY) {
+      const int groups = (c1 - c0 + kSelTile - 1) / kSelTile * 32;
+#pragma unroll 4
       for (int i = tid; i < groups; i += kSelThreads) {
         const float m = maxima[i];
         if (m >= bound && m > -INFINITY) {
@@ -374,6 +384,7 @@ __global__ void __launch_bounds__(kSelThreads, 4) beam_select_kernel(const SelAr
           if (at < kSelCap) sm.idx[at] = i, sm.key[at] = (uint64_t)key_of(m) << 32 | (uint32_t)at;
         }
       }
+    }
     __syncthreads();
     const int found = sm.groups;
     if (tid == 0 && found < W) sm.border = -INFINITY;
@@ -396,19 +407,35 @@ __global__ void __launch_bounds__(kSelThreads, 4) beam_select_kernel(const SelAr
     // their logits that reach the border: a warp takes every 8th group, the lanes its elements
     int kept = 0;
     if (found <= kSelCap) {
-      // places of the groups that are kept, in list order
+      // places of the groups that are kept, in list order; a warp's are read kBatch at a time
+      constexpr int kBatch = 4;
       for (int a = 0; a < found; a += 32) {
         const bool in = a + lane < found && maxima[sm.idx[a + lane]] >= border;
         unsigned who = __ballot_sync(0xffffffffu, in);
-        for (; who != 0; who &= who - 1, ++kept) {
-          if (kept % kSelWarps != warp) continue;
-          const int grp = sm.idx[a + __ffs(who) - 1], at = c0 + (grp >> 5) * kSelTile + SelTile<T>::pos(lane, grp & 31);
-          const uint64_t v = at < c1 ? entry(at) : 0ull;
-          const unsigned hit = __ballot_sync(0xffffffffu, v != 0);
-          int to = 0;
-          if (lane == 0) to = atomicAdd(&sm.count, __popc(hit));
-          to = __shfl_sync(0xffffffffu, to, 0) + __popc(hit & ((1u << lane) - 1));
-          if (v != 0 && to < kSelCap) sm.entry[to] = v;
+        while (who != 0) {
+          int at[kBatch];
+          uint64_t v[kBatch];
+#pragma unroll
+          for (int e = 0; e < kBatch; ++e) {
+            at[e] = c1;
+            for (; who != 0 && kept % kSelWarps != warp; who &= who - 1) ++kept;
+            if (who == 0) continue;
+            const int grp = sm.idx[a + __ffs(who) - 1];
+            at[e] = c0 + (grp >> 5) * kSelTile + SelTile<T>::pos(lane, grp & 31);
+            who &= who - 1;
+            ++kept;
+          }
+#pragma unroll
+          for (int e = 0; e < kBatch; ++e) v[e] = at[e] < c1 ? entry(at[e]) : 0ull;
+#pragma unroll
+          for (int e = 0; e < kBatch; ++e) {
+            const unsigned hit = __ballot_sync(0xffffffffu, v[e] != 0);
+            if (hit == 0) continue;
+            int to = 0;
+            if (lane == 0) to = atomicAdd(&sm.count, __popc(hit));
+            to = __shfl_sync(0xffffffffu, to, 0) + __popc(hit & ((1u << lane) - 1));
+            if (v[e] != 0 && to < kSelCap) sm.entry[to] = v[e];
+          }
         }
       }
     }
@@ -458,6 +485,17 @@ __global__ void __launch_bounds__(kSelThreads, 4) beam_select_kernel(const SelAr
   }
   __syncthreads();
   if (!sm.last) return;
+  // the candidates: W lists of each chunk of each beam; on their way while the sums are added up
+  const float2* cand = g.cand + (long long)b * W * g.nch * W;
+  const int lists = W * g.nch;
+  float2 early[kHeld];
+  if (can_hold(W, lists)) {
+#pragma unroll
+    for (int e = 0; e < kHeld; ++e) {
+      early[e] = make_float2(-INFINITY, 0.f);
+      if (tid + e * kSelThreads < lists * W) early[e] = __ldcg(&cand[tid + e * kSelThreads]);
+    }
+  }
   // log-sum-exp of every live beam: log2 of the sum with its exponent apart, so that fp32 is enough
   for (int j = warp; j < W; j += kSelWarps) {
     if (sm.score[j] == -INFINITY || sm.done[j] != 0) continue;
@@ -482,23 +520,24 @@ __global__ void __launch_bounds__(kSelThreads, 4) beam_select_kernel(const SelAr
     }
   }
   __syncthreads();
-  // candidates of the request: the lists of W beams x nch chunks, scored in fp64
+  // scored in fp64
+  const float per_beam = (float)(g.nch * W);
+  auto scored = [&](int at, float2 x, int& i) -> uint64_t {
+    // at / (nch W) in fp32: exact below 2^20
+    const int j = at < (1 << 20) ? (int)__fdividef((float)at + 0.5f, per_beam) : at / (g.nch * W);
+    const float sc = sm.score[j];
+    if (sc == -INFINITY) return 0;
+    if (sm.done[j] != 0) {
+      i = j * g.V + max(g.eos, 0);
+      return at == j * g.nch * W ? key_of((double)sc) : 0;
+    }
+    if (!(x.x > -INFINITY)) return 0;
+    i = j * g.V + __float_as_int(x.y);
+    return key_of((double)sc + ((double)x.x - sm.lse[j]));
+  };
   block_best(
-      W, W * g.nch,
-      [&](int l, int c, int& i) -> uint64_t {
-        const int j = l / g.nch;
-        const float sc = sm.score[j];
-        if (sc == -INFINITY) return 0;
-        if (sm.done[j] != 0) {
-          i = j * g.V + max(g.eos, 0);
-          return c == 0 && l == j * g.nch ? key_of((double)sc) : 0;
-        }
-        const float2 x = __ldcg(&g.cand[((long long)b * W * g.nch + l) * W + c]);
-        if (!(x.x > -INFINITY)) return 0;
-        i = j * g.V + __float_as_int(x.y);
-        return key_of((double)sc + ((double)x.x - sm.lse[j]));
-      },
-      sm);
+      W, lists, [&](int e, int at, int& i) { return scored(at, early[e], i); },
+      [&](int at, int& i) { return scored(at, __ldcg(&cand[at]), i); }, sm);
   if (tid < W) {
     const int o = b * W + tid;
     if (tid < sm.count) {
