@@ -973,76 +973,117 @@ __global__ void __launch_bounds__(M::kWarps * 32 + 128, 1) paged_attention_kerne
     const int bs = g.kv.block_size, shift = (bs & (bs - 1)) == 0 ? __ffs(bs) - 1 : -1;
     const int run = 1 << p.run_lg, runs = p.kt >> p.run_lg, copies = runs * p.copies;
     int slot = v, phase = 0, issued = 0;                   // every second slot in turn is this warp's
-    constexpr int kPer = kMaskWords;                       // rows: keys of a tile a lane handles
-    // One tile ahead: its table entries are on their way while the tile before waits for room.
-    struct Tile {
-      int b, key0, lo, len, head0;
-      int id[kPer];          // runs: lane r has run r's block; rows: id[i] is the block of key 32 i + lane
+    auto room = [&] { return __all_sync(0xffffffffu, tc::mbar_wait(empty0 + 8 * slot, phase ^ 1, const_cast<volatile int*>(flags))); };
+    auto passed = [&] {
+      ++issued;
+      if ((slot += 2) >= p.slots) slot -= p.slots, phase ^= 1;
     };
-    bool in_piece = false;
-    int t = 0;
-    auto fetch = [&](Tile& x) {
-      if (!in_piece || ++t >= w.t1) {
-        if (!w.next()) return false;
-        in_piece = true;
-        t = w.t0;
+    auto head_of_group = [&] { return (p.qs == 1 ? w.hg : w.hg / p.qs) * p.nh; };
+    bool ok = true, have = w.next();
+    int t = w.t0;
+    // The table entries of the next tile are on their way while this one waits for room.
+    if (p.swz) {
+      // lane r has run r's block
+      int len = 0, lo = 0, key = 0, head0 = 0, id = 0;
+      const int32_t* table = nullptr;
+      const int last_id = (g.kv.num_slots - 1) / bs;
+      auto piece = [&] {
+        len = lens[w.b];
+        lo = first_key(len);
+        key = (lo & -run) + t * p.kt + lane * run;         // of the lane's run
+        head0 = head_of_group();
+        table = g.kv.block_table + (long long)(g.b0 + w.b) * g.kv.max_blocks;
+      };
+      auto look = [&] { id = lane < runs && key < len ? table[shift >= 0 ? key >> shift : key / bs] : -1; };
+      if (have) {
+        piece();
+        look();
       }
-      x.b = w.b;
-      x.len = lens[w.b];
-      x.lo = first_key(x.len);
-      x.key0 = (p.swz ? x.lo & -run : x.lo) + t * p.kt;
-      x.head0 = (p.qs == 1 ? w.hg : w.hg / p.qs) * p.nh;
-      const int32_t* table = g.kv.block_table + (long long)(g.b0 + w.b) * g.kv.max_blocks;
-      auto entry = [&](int key) { return table[shift >= 0 ? key >> shift : key / bs]; };
-      if (p.swz) {
-        const int key = x.key0 + lane * run;
-        x.id[0] = lane < runs && key < x.len ? entry(key) : 0;
-      } else {
+      const uint32_t whole_word = p.kt >= 32 ? 0xffffffffu : (1u << p.kt) - 1;
+      const unsigned whole_runs = 0xffffffffu >> (32 - runs);
+      while (have) {
+        const int key_ = key, len_ = len, lo_ = lo, head_ = head0, id_ = id, b_ = w.b;
+        if (++t < w.t1) {
+          key += p.kt;
+        } else if ((have = w.next())) {
+          t = w.t0;
+          piece();
+        }
+        if (have) look();
+        if (!(ok = room())) break;
+        const uint32_t full = full0 + 8 * slot, dst = ring0 + slot * slot_bytes;
+        // the run's first cache slot (-1: none, or a block id out of range: its keys are left out), and how
+        // many slots from there are in the cache
+        int sl = -1, in_run = 0;
+        if (lane < runs && key_ < len_) {
+          const uint32_t s = (uint32_t)id_ * bs + (shift >= 0 ? key_ & (bs - 1) : key_ % bs);   // < 2^32 up to last_id
+          if (id_ >= 0 && id_ <= last_id && s < (uint32_t)g.kv.num_slots)
+            sl = (int)s, in_run = min(run, g.kv.num_slots - sl);
+          else
+            report(g.ws, SPEC_ERR_DEVICE, g.b0 + b_, key_);
+        }
+        const int key0 = key_ - lane * run;
+        const unsigned there = __ballot_sync(0xffffffffu, sl >= 0);
+        if (key0 >= lo_ && key0 + p.kt <= len_ && __all_sync(0xffffffffu, lane >= runs || in_run == run) && there == whole_runs) {
+          if (lane * 32 < p.kt) masks[slot * kMaskWords + lane] = whole_word;
+        } else {
+          for (int i = 0; i * 32 < p.kt; ++i) {
+            const int j = i * 32 + lane, k = key0 + j;
+            const int have_r = __shfl_sync(0xffffffffu, in_run, (j >> p.run_lg) & 31);
+            const uint32_t word = __ballot_sync(0xffffffffu, j < p.kt && k >= lo_ && k < len_ && (j & (run - 1)) < have_r);
+            if (lane == 0) masks[slot * kMaskWords + i] = word;
+          }
+        }
+        __syncwarp();
+        if (lane == 0) tc::mbar_expect_tx(full, (uint32_t)(__popc(there) * p.run_bytes));
+        __syncwarp();
+        const CUtensorMap* tm = v ? &g.tmv : &g.tmk;
+        if (p.copies == 1) {
+          if (sl >= 0) tma_run(dst + lane * p.run_bytes, tm, full, 0, sl, head_, policy);
+        } else {
+          for (int base = 0; base < copies; base += 32) {
+            const int i = base + lane, r = quot(i, p.copies), c = i - r * p.copies;
+            const int s = __shfl_sync(0xffffffffu, sl, r & 31);
+            if (i < copies && s >= 0) tma_run(dst + r * p.run_bytes + c * p.chunk_stride, tm, full, c * (128 / M::kEs), s, head_, policy);
+          }
+        }
+        passed();
+      }
+    } else {
+      constexpr int kPer = kMaskWords;                     // keys of a tile a lane handles
+      struct Tile {
+        int b, key0, len, head0;
+        int id[kPer];        // id[i] is the block of key 32 i + lane
+      };
+      auto fetch = [&](Tile& x) {
+        x.b = w.b;
+        x.len = lens[w.b];
+        x.key0 = first_key(x.len) + t * p.kt;
+        x.head0 = head_of_group();
+        const int32_t* table = g.kv.block_table + (long long)(g.b0 + w.b) * g.kv.max_blocks;
 #pragma unroll
         for (int i = 0; i < kPer; ++i)
           if (i * 32 < p.kt) {
             const int key = x.key0 + i * 32 + lane;
-            x.id[i] = i * 32 + lane < p.kt && key < x.len ? entry(key) : 0;
+            x.id[i] = i * 32 + lane < p.kt && key < x.len ? table[shift >= 0 ? key >> shift : key / bs] : 0;
           }
-      }
-      return true;
-    };
-    Tile x;
-    bool ok = true, have = fetch(x);
-    while (ok && have) {
-      Tile y;
-      const bool more = fetch(y);
-      ok = __all_sync(0xffffffffu, tc::mbar_wait(empty0 + 8 * slot, phase ^ 1, const_cast<volatile int*>(flags)));
-      if (!ok) break;
-      const uint32_t full = full0 + 8 * slot, dst = ring0 + slot * slot_bytes;
-      // cache slot of a key (-1: none, or a block id out of range: the key is left out)
-      auto slot_of_key = [&](int key, int id) {
-        if (key >= x.len) return -1;
-        const long long s = (long long)id * bs + (shift >= 0 ? key & (bs - 1) : key % bs);
-        if (id >= 0 && s < g.kv.num_slots) return (int)s;
-        report(g.ws, SPEC_ERR_DEVICE, g.b0 + x.b, key);
-        return -1;
       };
-      if (p.swz) {
-        const int sl = lane < runs ? slot_of_key(x.key0 + lane * run, x.id[0]) : -1;
-        const int in_run = sl < 0 ? 0 : min(run, g.kv.num_slots - sl);      // slots of the run that are in the cache
-        const int n = __popc(__ballot_sync(0xffffffffu, sl >= 0));
-        for (int i = 0; i * 32 < p.kt; ++i) {
-          const int j = i * 32 + lane, key = x.key0 + j;
-          const int have_r = __shfl_sync(0xffffffffu, in_run, (j >> p.run_lg) & 31);
-          const uint32_t word = __ballot_sync(0xffffffffu, j < p.kt && key >= x.lo && key < x.len && (j & (run - 1)) < have_r);
-          if (lane == 0) masks[slot * kMaskWords + i] = word;
-        }
-        if (lane == 0) tc::mbar_expect_tx(full, (uint32_t)(n * p.run_bytes));
-        __syncwarp();
-        for (int base = 0; base < copies; base += 32) {
-          const int i = base + lane, r = p.copies == 1 ? i : i / p.copies, c = i - r * p.copies;
-          const int s = __shfl_sync(0xffffffffu, sl, r & 31);
-          if (i < copies && s >= 0)
-            tma_run(dst + r * p.run_bytes + c * p.chunk_stride, v ? &g.tmv : &g.tmk, full, c * (128 / M::kEs), s, x.head0,
-                    policy);
-        }
-      } else {
+      Tile x;
+      if (have) fetch(x);
+      while (have) {
+        Tile y;
+        if (++t >= w.t1 && (have = w.next())) t = w.t0;
+        if (have) fetch(y);
+        if (!(ok = room())) break;
+        const uint32_t full = full0 + 8 * slot, dst = ring0 + slot * slot_bytes;
+        // cache slot of a key (-1: none, or a block id out of range: the key is left out)
+        auto slot_of_key = [&](int key, int id) {
+          if (key >= x.len) return -1;
+          const long long s = (long long)id * bs + (shift >= 0 ? key & (bs - 1) : key % bs);
+          if (id >= 0 && s < g.kv.num_slots) return (int)s;
+          report(g.ws, SPEC_ERR_DEVICE, g.b0 + x.b, key);
+          return -1;
+        };
         int sl[kPer], n = 0;
 #pragma unroll
         for (int i = 0; i < kPer; ++i)
@@ -1059,11 +1100,9 @@ __global__ void __launch_bounds__(M::kWarps * 32 + 128, 1) paged_attention_kerne
         for (int i = 0; i < kPer; ++i)
           if (i * 32 < p.kt && sl[i] >= 0 && (lane & 1) == second)
             bulk_row(dst + (i * 32 + lane) * p.key_stride, src + sl[i] * row_all, p.row, full, policy);
+        passed();
+        x = y;
       }
-      ++issued;
-      if ((slot += 2) >= p.slots) slot -= p.slots, phase ^= 1;
-      x = y;
-      have = more;
     }
     if (!ok) {
       // a wait ran out: let the copies in flight land before leaving

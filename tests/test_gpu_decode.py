@@ -232,6 +232,15 @@ def test_attention_shapes(t, ct, nq, nkv, hd, bs):
 
 
 @pytest.mark.parametrize("t,ct", PAIRS)
+@pytest.mark.parametrize("nkv,hd,bs", [(8, 16, 16), (8, 32, 8), (4, 32, 16), (2, 64, 32), (6, 64, 16), (16, 48, 16), (3, 64, 8),
+                                       (2, 144, 16), (2, 160, 24), (4, 192, 16), (1, 208, 1), (2, 224, 16)])
+def test_attention_head_sizes(t, ct, nkv, hd, bs):
+    """Heads that share 128 bytes, heads that fill no whole 128 bytes, and those above 128 components."""
+    for group in (1, 5, 12):
+        attend(hd + group, t, ct, [0, 1, 31, 33, 260, 700], group * nkv, nkv, hd, bs)
+
+
+@pytest.mark.parametrize("t,ct", PAIRS)
 @pytest.mark.parametrize("lens", [[1], [0], [0, 0, 0], [4097], [33, 0, 5000, 1, 64, 65, 127, 128], [2] * 300])
 def test_attention_lengths(t, ct, lens):
     attend(len(lens) + sum(lens), t, ct, lens, 8, 2, 64, 16)
