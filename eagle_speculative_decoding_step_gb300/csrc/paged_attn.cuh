@@ -1071,7 +1071,7 @@ __global__ void __launch_bounds__(M::kWarps * 32 + 128, 1) paged_attention_kerne
       Tile x;
       if (have) fetch(x);
       while (have) {
-        Tile y;
+        Tile y = x;          // (not initialised: 167 us in place of 160 for 64 requests of 4000 keys)
         if (++t >= w.t1 && (have = w.next())) t = w.t0;
         if (have) fetch(y);
         if (!(ok = room())) break;
