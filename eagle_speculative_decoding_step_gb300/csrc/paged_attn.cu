@@ -108,10 +108,10 @@ static bool run_map(CUtensorMap* tm, const void* ptr, const spec_attn_desc& d, c
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Heads of a tile: the cheapest by share_out() with every request as long as the longest.  Copies of less than 16 KB
-// cost more where a request's heads are not all under way at once (64 requests of up to 8190 keys, 8 heads of 256
-// bytes, 4 / 2 / 1 heads a tile, copies of 16 / 8 / 4 KB: 166 / 179 / 212 us; 16 requests of 4000: 48.1 / 47.8 / 47.0), and always in 8 bits (64 requests, 8 / 4 heads 101 /
-// 110 us).
+// Heads of a tile: the cheapest by share_out() with every request as long as the longest.  Small copies cost
+// more where a request's heads are not all under way at once: 64 requests of up to 8190 keys, 8 heads of 256 bytes,
+// 8 / 4 / 2 / 1 heads a tile, copies of 32 / 16 / 8 / 4 KB: 162 / 162 / 166 / 185 us (16 requests of 4000:
+// 46.7 / 46.2 / 46.0 / 45.3); and always in 8 bits: 64 requests of 4000, copies of 16 / 8 / 4 / 2 KB 86 / 86 / 87 / 125 us.
 static Plan plan(const Kernel& k, const spec_attn_desc& d, int B, int max_len, int block_size, int sms) {
   Plan q{}, best{};
   plan_queries(k, d.n_q_heads / d.n_kv_heads, &q);
@@ -124,8 +124,8 @@ static Plan plan(const Kernel& k, const spec_attn_desc& d, int B, int max_len, i
     const long long items = (long long)B * p.hgq, copy = (long long)(p.swz ? 1 << p.run_lg : 1) * nh * d.head_dim * k.es;
     int cuts;
     // Rows: tiles are smaller where warps are left over (3 or 5 heads), and a single key's copy wants 2 KB (64 requests
-    // of 4000 keys, blocks of one slot, copies of 2048 / 1024 / 512 / 256 bytes: 97 / 82 / 58 / 35 % of the copy
-    // bandwidth).  Runs: a smaller tile takes a warp as long as a whole one.
+    // of 4000 keys, blocks of one slot, 8 heads of 256 bytes, copies of 2048 / 1024 / 512 / 256 bytes: 159 / 166 / 232 /
+    // 361 us).  Runs: a smaller tile takes a warp as long as a whole one.
     const float form = p.swz ? (copy >= 16384 || (items <= sms && k.es > 1) ? 1.f : copy >= 8192 ? 1.08f : 1.25f)
                              : (copy >= 2048 ? 1.f : copy >= 1024 ? 1.2f : copy >= 512 ? 1.7f : 2.8f) *
                                    (float)(p.nh * p.qt * p.kg * k.vs) / (float)k.warps;

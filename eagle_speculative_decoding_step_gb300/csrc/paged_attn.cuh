@@ -98,9 +98,9 @@ __host__ __device__ inline float join_cost(int n, float per_kg) {
 // How `total` tiles of `items` (request, head group)s, the longest of `most` tiles, are
 // shared out: in `cuts` equal pieces an item, a CTA each, or (cuts = 0) in equal
 // shares of the tiles in a row, which begin and end inside items.  Returns the cost
-// in tiles.  Measured: 16 requests of 1000 keys, 128 items of 8 tiles, 15.8 us whole,
-// 19.7 in shares; 32 items of 8 tiles 10.4 us in 4 pieces each, 13.0 in shares; 64
-// requests of 8190 keys, 128 items of 256 tiles, in shares.
+// in tiles.  Measured: 16 requests of 1000 keys, 128 items of 8 tiles, 12.7 us whole,
+// 17.5 in shares; 4 requests, 32 items of 8 tiles, 11.9 whole, 9.8 in 4 pieces each, 12.7
+// in shares; 64 requests of up to 8190 keys, 128 items of 256 tiles, 160 us in shares.
 //
 // In fp32 throughout: every CTA works it out for itself before it can start.
 __host__ __device__ inline float share_out(long long total_, long long items_, int most, int kg, int ctas, int* cuts) {
@@ -218,7 +218,7 @@ SPEC_DEV uint32_t widen(uint32_t x) {
 // step has few; K rows and (transposed) V rows come out of shared memory as they
 // lie.  tcgen05 would want 128 rows of one operand per 16 keys' work.
 //
-// Where a head's row is 128 bytes or less (and 8-bit rows of 256) a step takes U = 2
+// Where a head's row is 128 bytes or less (and 8-bit rows of up to 256) a step takes U = 2
 // tiles of 16 keys: the chain of dependent instructions is the same for twice the
 // bytes.  Wider rows fill a ring slot with one.
 //
@@ -816,12 +816,21 @@ struct Walk {
   }
 };
 
-// One CTA per SM walks its share of the tiles.  A producer warp copies the rows of
-// a tile's keys (kt keys x nh heads) into a ring of shared-memory slots, K and V
-// tiles in turn; each consumer warp takes 16 (8) keys of one head and one query tile of
+// One CTA per SM walks its share of the tiles.  A producer warp each for K and V copies the
+// rows of a tile's keys (kt keys x nh heads) into a ring of shared-memory slots, K and V
+// tiles in turn; each consumer warp takes 16 or 32 (fp32: 8) keys of one head and one query tile of
 // every tile.  Pieces of a (request, head group) that several CTAs share are left
 // as partial results; the last CTA of such a group to finish joins them in CTA
 // order, so results do not depend on timing.
+//
+// One pass over K and V with running maxima m and sums l (log2 units): o <- o 2^(m - m') + sum p v,
+// p = 2^(s - m').  Bound by the bytes of K and V, which the ring (up to 220 KB an SM) keeps in
+// flight.  Measured, 64 requests on 8 K/V heads of 128, 4 queries each: bf16, 4000 keys 155 us (6.75
+// TB/s, the copy bandwidth), e4m3 85 (6.1 TB/s: the warps' chain from shared memory through the conversion
+// and two products); one request of 131071 keys 84 (152 pieces and their join); 4 of 256 keys 7.1 (launch and
+// ~10 dependent steps).  A tile's values and the next tile's scores run as one stretch of
+// instructions without a branch, so that two independent chains fill each other's gaps (one after the other:
+// e4m3 98 us; 256 components 224 -> 162).
 template <typename M>
 __global__ void __launch_bounds__(M::kWarps * 32 + 128, 1) paged_attention_kernel(const __grid_constant__ Args g) {
   SPEC_TL(kTLPagedAttn);
@@ -1143,9 +1152,6 @@ __global__ void __launch_bounds__(M::kWarps * 32 + 128, 1) paged_attention_kerne
       sync();
     }
   };
-  // a piece's queries are loaded while the one before it is merged and written, where registers
-  // allow (16 queries: spills, and 64 requests of 4000 keys with 128 query heads 165 -> 190 us)
-  constexpr bool kEarly = S::NR <= 32;
   auto group = [&] { return p.qs == 1 ? w.hg : w.hg / p.qs; };
   auto query0 = [&] { return ((w.hg - group() * p.qs) * p.qt + qi) * M::kQ; };
   auto queries = [&] { return kgrp < p.kg ? min(M::kQ, g.G - query0()) : 0; };     // <= 0: none for this warp
@@ -1156,15 +1162,15 @@ __global__ void __launch_bounds__(M::kWarps * 32 + 128, 1) paged_attention_kerne
       math.load_q(g, static_cast<const T*>(g.q) + (g.b0 + w.b) * g.q_ld + (long long)head_of() * g.G * g.hd,
                   query0(), n, lane);
   };
+  // a piece's queries are loaded while the one before it is merged and written
   bool more = w.next();
-  if (kEarly && more) load_q();
+  if (more) load_q();
   while (more) {
     const int head = head_of(), q0 = query0(), nq = queries();
     const long long b = g.b0 + w.b;
     const int piece_b = w.b, hg = w.hg, nt = w.nt;
     const bool whole = w.t1 - w.t0 == w.nt;
     reset(s);
-    if (!kEarly) load_q();
     math.scale_q(g, lane);
     auto wait = [&](int sl, int ph) { return tc::mbar_wait(full0 + 8 * sl, ph, const_cast<volatile int*>(flags)); };
     auto mask_of = [&](int sl) { return masks[sl * kMaskWords + (k0 >> 5)] >> (k0 & 31); };
@@ -1209,7 +1215,7 @@ __global__ void __launch_bounds__(M::kWarps * 32 + 128, 1) paged_attention_kerne
     }
     math.finish(s);
     more = w.next();
-    if (kEarly && more) load_q();
+    if (more) load_q();
     merge_groups();
     if (!whole) {
       // one of several pieces: leave it, and join them all if it is the last to come
@@ -1246,24 +1252,12 @@ __global__ void __launch_bounds__(M::kWarps * 32 + 128, 1) paged_attention_kerne
         reset(s);
         for (i += kgrp * step; i < end; i += p.kg * step) {
           const float* x = entry(i);
-          // which of the two forms spills less depends on the state's size; a spill of a few registers here
-          // costs the main loop 10 % (256 components: 160 -> 179 us, 16 queries: 165 -> 190 us)
-          if constexpr (S::NR > 32) {
-            float y[S::NR + 2 * S::NM];
-#pragma unroll
-            for (int r = 0; r < S::NR + 2 * S::NM; r += 4) {
-              const float4 f = __ldcg(reinterpret_cast<const float4*>(x + r * 32));
-              y[r] = f.x, y[r + 1] = f.y, y[r + 2] = f.z, y[r + 3] = f.w;
-            }
-            join<M>(s, [&](int r) { return y[r]; });
-          } else {
-            float4 f;
-            join<M>(s, [&](int r) {
-              if (r >= S::NR) return __ldcg(x + (r & ~3) * 32 + (r & 3));
-              if (r % 4 == 0) f = __ldcg(reinterpret_cast<const float4*>(x + r * 32));
-              return r % 4 == 0 ? f.x : r % 4 == 1 ? f.y : r % 4 == 2 ? f.z : f.w;
-            });
-          }
+          float4 f;
+          join<M>(s, [&](int r) {
+            if (r >= S::NR) return __ldcg(x + (r & ~3) * 32 + (r & 3));
+            if (r % 4 == 0) f = __ldcg(reinterpret_cast<const float4*>(x + r * 32));
+            return r % 4 == 0 ? f.x : r % 4 == 1 ? f.y : r % 4 == 2 ? f.z : f.w;
+          });
         }
         merge_groups();
       };
