@@ -28,6 +28,11 @@ enum : unsigned { kTLBeamSelect = 27, kTLBeamReorder = 28 };   // after common.c
 // few groups that are left are read again.  The last chunk of a request to finish (a
 // counter, nobody waits) merges the request.
 //
+// log sum exp = m + log(sum of e^(x - m)), m the running maximum.  Measured: 32 x 8 rows of 151936 of random
+// logits, fp32 33.6 us (4.6 TB/s; the stream ~23, a chunk's end ~5 under load: bound, second look at the kept
+// groups, counter; the request's merge ~3), bf16 23; 4 rows of 128256 8.5 us, all latency: the first loads,
+// the chunk's end, counter and merge are ~12 dependent trips to memory or across the block.
+//
 // Which lane has which element of a tile does not depend on the row's alignment, and
 // rows are cut into equal chunks, so equal rows give equal sums and tie as they
 // should.
@@ -124,7 +129,7 @@ SPEC_DEV uint32_t block_bound(const SelShared& sm) {
 // the list, k rounds of block-wide maxima.  The bound comes from the threads' maxima
 // over all entries where those can be held in registers between the two looks, else
 // over the lists' heads, so that only lists whose head reaches it are read (16 beams:
-// 512 entries 29.6 us against 35.7 by heads, 2560 entries 17.1 by heads against 35.8).
+// 512 entries 28.8 us against 35.7 by heads; 2560 entries 17.1 by heads against 35.8 by all entries).
 constexpr int kHeld = 8;
 SPEC_DEV bool can_hold(int k, int lists) { return lists * k <= kHeld * kSelThreads; }
 template <typename First, typename Get> SPEC_DEV void block_best(int k, int lists, First first, Get get, SelShared& sm) {
@@ -561,8 +566,8 @@ __global__ void __launch_bounds__(kSelThreads, 4) beam_select_kernel(const SelAr
 static int sel_chunks(int B, int W, int V, int* chunk) {
   constexpr int kStep = kSelWarps * kSelTile;
   const int steps = (V + kStep - 1) / kStep;
-  // one chunk an SM (a chunk's end costs ~3 us: 32 x 8 rows of 151936, 2 / 4 / 8 chunks a row 33.9 / 38.4 /
-  // 45.4 us), of at least two steps (one row's worth of merging: 4 rows of 128256, 32 / 16 chunks 9.3 / 7.8 us)
+  // one chunk an SM (a chunk's end costs ~3 us: 32 x 8 rows of 151936 in fp32, 2 / 4 chunks a row 33.6 / 37.5 us), of
+  // at least two steps (merging: 4 rows of 128256 in fp32, 16 / 32 / 64 chunks 8.5 / 9.0 / 9.2 us)
   int want = std::min((152 + B * W - 1) / (B * W), (steps + 1) / 2);
   want = std::max(want, (steps + kSelChunk / kStep - 1) / (kSelChunk / kStep));
   const int per = (steps + want - 1) / want;
@@ -644,7 +649,8 @@ SPEC_DEV Tail beam_tail(const ReorderArgs& g, int row, bool tell) {
 // Grid (part, row): part 0 writes the row's integers, the others copy the partial
 // block's K or V rows, 256 / lanes (layer, K or V)s each; the rows are contiguous
 // (slots of a block follow one another).  A copy's source is some beam's current block
-// and its target a spare block, and no block is both.
+// and its target a spare block, and no block is both.  Bound by the copies' bytes where they are many
+// (128 beams, 32 layers, up to 32 KB each of K and V: 22.5 us), else by three dependent reads (4 beams: 2.9 us).
 __global__ void __launch_bounds__(256) beam_reorder_kernel(const __grid_constant__ ReorderArgs g) {
   SPEC_TL(kTLBeamReorder);
   pdl_wait();
