@@ -131,6 +131,23 @@ def test_cache_append(t, c, nkv, hd, n, ld, off):
         np.testing.assert_array_equal(cache.float().cpu().numpy().reshape(slots, w), ref.astype(np.float32))
 
 
+@pytest.mark.parametrize("t", ["bf16", "f16"])
+@pytest.mark.parametrize("ks,vs", [(0.0625, 1.0), (0.3, 1.7e-3), (7.1, 3e4)])
+def test_cache_append_every_value_to_eight_bits(t, ks, vs):
+    """All 65536 bit patterns: the quotient in fp32, then one rounding to nearest even, whatever the scale."""
+    x = torch.arange(65536, dtype=torch.int32, device="cuda").to(torch.int16).view(TYPES[t]).reshape(64, 1024)
+    ck, cv = torch.zeros(2, 64, 8, 128, device="cuda").to(TYPES["e4m3"]).unbind(0)
+    ws = zeros(256)
+    kv = lib.make_kv(dict(k=ck, v=cv, block_table=None, block_size=1, max_blocks=0, num_slots=64))
+    lib.spec_cache_append(lib.make_attn_desc(8, 8, 128, t, "e4m3", k_scale=ks, v_scale=vs), x, x, 0, i32(np.arange(64)), 64, kv,
+                          ws)
+    assert error(ws) == 0
+    with np.errstate(over="ignore"):
+        for cache, s in ((ck, ks), (cv, vs)):
+            ref = oracle.e4m3_round(x.float().cpu().numpy() / np.float32(s))
+            np.testing.assert_array_equal(cache.float().cpu().numpy().reshape(64, 1024), ref.astype(np.float32))
+
+
 def test_cache_append_skips_slots_out_of_range():
     ck, cv = torch.zeros(2, 8, 1, 16, device="cuda").unbind(0)
     x = torch.ones(4, 16, device="cuda")
@@ -281,6 +298,30 @@ def test_attention_is_deterministic():
         lib.spec_paged_attention(desc, q, c.kv(), i32(c.lens), 3, o, None, ws)
         outs.append(o)
     assert all(torch.equal(o, outs[0]) for o in outs)
+
+
+def test_attention_calls_of_all_shapes_share_a_workspace():
+    """One workspace, calls of other shapes in between: the same bits as with a workspace of its own."""
+    cases = [("bf16", "bf16", [30000], 32, 8, 128, 16), ("f32", "f32", [900, 0, 77], 16, 2, 64, 8),
+             ("f16", "e4m3", [3000, 5, 2500, 1], 32, 2, 256, 16), ("bf16", "bf16", [40] * 200, 4, 4, 80, 24),
+             ("bf16", "e4m3", [12345], 6, 3, 128, 32), ("f32", "f32", [5000, 4000], 8, 1, 256, 1)]
+    calls, size = [], 0
+    for i, (t, ct, lens, nq, nkv, hd, bs) in enumerate(cases):
+        c = Cache(i, lens, nkv, hd, bs, ct, 0, 0.05, 0.02) if ct == "e4m3" else Cache(i, lens, nkv, hd, bs, ct)
+        desc = lib.make_attn_desc(nq, nkv, hd, t, ct, k_scale=0.05, v_scale=0.02)
+        q = torch.randn(len(lens), nq, hd, device="cuda").to(TYPES[t])
+        own = zeros(lib.spec_attention_workspace_bytes(desc, len(lens)))
+        size = max(size, own.numel())
+        ref, lse = torch.empty_like(q), torch.empty(len(lens), nq, device="cuda")
+        lib.spec_paged_attention(desc, q, c.kv(), i32(lens), len(lens), ref, lse, own)
+        calls.append((desc, q, c, lens, ref, lse))
+    shared = zeros(size)
+    for _ in range(2):
+        for desc, q, c, lens, ref, ref_lse in calls:
+            out, lse = torch.empty_like(q), torch.empty_like(ref_lse)
+            lib.spec_paged_attention(desc, q, c.kv(), i32(lens), len(lens), out, lse, shared)
+            assert torch.equal(out, ref) and torch.equal(lse, ref_lse)
+    assert error(shared) == 0
 
 
 def test_attention_leaves_out_bad_blocks_and_clamps_lengths():
