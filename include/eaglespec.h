@@ -501,9 +501,11 @@ size_t spec_attention_workspace_bytes(const spec_attn_desc *desc, int32_t max_B)
  * one request to the next (0 = n_q_heads * head_dim); lse [B, n_q_heads] fp32 or
  * NULL.  max_len: an upper bound of seq_len over the batch, or 0 if unknown; it
  * only chooses how work is laid out.  Any block_size; max_blocks * block_size
- * < 2^30.  q, the cache and, with
- * ld's, every row of q 16-byte aligned (SPEC_ERR_ALIGN).
- * Sums and softmax statistics are fp32.  Error word: SPEC_ERR_DEVICE for a
+ * < 2^30.  q, out, the cache and, with
+ * ld's, every row of q and out 16-byte aligned (SPEC_ERR_ALIGN).
+ * Sums and softmax statistics are fp32.  A K or V value that is not finite in a
+ * row that is attended to makes outputs of its head that are not finite; rows that are
+ * not attended to may hold anything.  Error word: SPEC_ERR_DEVICE for a
  * seq_len outside [0, max_blocks * block_size] (clamped) or a block id out of
  * range (its keys are left out). */
 spec_status spec_paged_attention(const spec_attn_desc *desc, const void *q, int64_t q_ld, const spec_kv *kv,
