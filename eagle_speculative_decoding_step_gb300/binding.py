@@ -115,6 +115,8 @@ EXPORTS = {
                                   c_vp, c_vp, c_vp, c_i32, c_vp, c_size, c_vp]),
     "spec_cache_append": (c_i32, [ctypes.POINTER(AttnDesc), c_vp, c_vp, c_i64, c_vp, c_i32, ctypes.POINTER(KV), c_vp,
                                   c_vp]),
+    "spec_cache_append_strided": (c_i32, [ctypes.POINTER(AttnDesc), c_vp, c_i64, c_vp, c_i64, c_vp, c_i32,
+                                          ctypes.POINTER(KV), c_vp, c_vp]),
     "spec_attention_workspace_bytes": (c_size, [ctypes.POINTER(AttnDesc), c_i32]),
     "spec_paged_attention": (c_i32, [ctypes.POINTER(AttnDesc), c_vp, c_i64, ctypes.POINTER(KV), c_vp, c_i32, c_i32,
                                      c_vp, c_i64, c_vp, c_vp, c_size, c_vp]),
@@ -356,7 +358,12 @@ def spec_block_tables(B, block_size, max_blocks, num_blocks, len_old, len_new, t
                                     ws.numel() * ws.element_size(), _stream()), "spec_block_tables")
 
 
-def spec_cache_append(desc, k, v, ld, slots, n, kv, ws=None):
+def spec_cache_append(desc, k, v, ld, slots, n, kv, ws=None, v_ld=None):
+    """v_ld: the row stride of v where it is not k's (spec_cache_append_strided)."""
+    if v_ld is not None:
+        _check(_lib().spec_cache_append_strided(ctypes.byref(desc), _p(k), ld, _p(v), v_ld, _p(slots), n, ctypes.byref(kv),
+                                                _p(ws), _stream()), "spec_cache_append_strided")
+        return
     _check(_lib().spec_cache_append(ctypes.byref(desc), _p(k), _p(v), ld, _p(slots), n, ctypes.byref(kv), _p(ws),
                                     _stream()), "spec_cache_append")
 

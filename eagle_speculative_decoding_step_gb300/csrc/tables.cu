@@ -312,7 +312,8 @@ static bool power_of_two(float s) {
 // slices of a fused product, into 8 bits 27.9 us (7.2 TB/s: the last writes stay in L2), 256 rows 1.9 us.
 template <typename T, typename C, bool VEC, bool EXACT>
 __global__ void __launch_bounds__(256) cache_append_kernel(const T* __restrict__ k, const T* __restrict__ v,
-                                                           long long ld, const int32_t* __restrict__ slots, int n,
+                                                           long long k_ld, long long v_ld,
+                                                           const int32_t* __restrict__ slots, int n,
                                                            C* __restrict__ ck, C* __restrict__ cv, int width,
                                                            int num_slots, float k_scale, float v_scale, int lg,
                                                            void* ws) {
@@ -325,7 +326,7 @@ __global__ void __launch_bounds__(256) cache_append_kernel(const T* __restrict__
   const int per = 1 << lg, part = threadIdx.x & (per - 1);
   const long long row = (long long)blockIdx.x * (256 >> lg) + (threadIdx.x >> lg);
   if (row >= n) return;
-  const T* s = src + row * ld;
+  const T* s = src + row * (blockIdx.y ? v_ld : k_ld);
   if constexpr (VEC) {
     // four vectors on their way before the slot is looked at
     constexpr int kBatch = 4;
@@ -376,20 +377,20 @@ __global__ void __launch_bounds__(256) cache_append_kernel(const T* __restrict__
 }
 
 template <typename T, typename C>
-static void launch_append(const spec_attn_desc& d, const void* k, const void* v, long long ld, const int32_t* slots,
-                          int n, const spec_kv& kv, void* ws, cudaStream_t st) {
+static void launch_append(const spec_attn_desc& d, const void* k, long long k_ld, const void* v, long long v_ld,
+                          const int32_t* slots, int n, const spec_kv& kv, void* ws, cudaStream_t st) {
   const int width = d.n_kv_heads * d.head_dim;
   int lg = 0;
   while (lg < 5 && (8 << lg) < width) ++lg;
-  const bool vec = (ld * (long long)sizeof(T)) % 16 == 0 && aligned(k, 16) && aligned(v, 16) && aligned(kv.k, 16) &&
-                   aligned(kv.v, 16);
+  const bool vec = (k_ld * (long long)sizeof(T)) % 16 == 0 && (v_ld * (long long)sizeof(T)) % 16 == 0 && aligned(k, 16) &&
+                   aligned(v, 16) && aligned(kv.k, 16) && aligned(kv.v, 16);
   const int rows = 256 >> lg;
   const dim3 grid((n + rows - 1) / rows, 2);
   auto* kern = vec ? cache_append_kernel<T, C, true, true> : cache_append_kernel<T, C, false, true>;
   if constexpr (sizeof(C) == 1)
     if (!power_of_two(d.k_scale) || !power_of_two(d.v_scale))
       kern = vec ? cache_append_kernel<T, C, true, false> : cache_append_kernel<T, C, false, false>;
-  launch_pdl(kern, grid, dim3(256), 0, st, (const T*)k, (const T*)v, ld, slots, n, (C*)kv.k, (C*)kv.v, width,
+  launch_pdl(kern, grid, dim3(256), 0, st, (const T*)k, (const T*)v, k_ld, v_ld, slots, n, (C*)kv.k, (C*)kv.v, width,
              (int)kv.num_slots, d.k_scale, d.v_scale, lg, ws);
 }
 
@@ -435,6 +436,12 @@ extern "C" spec_status spec_block_tables(int32_t B, int32_t block_size, int32_t 
 extern "C" spec_status spec_cache_append(const spec_attn_desc* desc, const void* k, const void* v, int64_t ld,
                                          const int32_t* slots, int32_t n, const spec_kv* kv, void* ws,
                                          spec_stream_t stream) {
+  return spec_cache_append_strided(desc, k, ld, v, ld, slots, n, kv, ws, stream);
+}
+
+extern "C" spec_status spec_cache_append_strided(const spec_attn_desc* desc, const void* k, int64_t k_ld, const void* v,
+                                                 int64_t v_ld, const int32_t* slots, int32_t n, const spec_kv* kv,
+                                                 void* ws, spec_stream_t stream) {
   if (!desc || !k || !v || !slots || !kv || !kv->k || !kv->v) return SPEC_ERR_ARG;
   const spec_attn_desc& d = *desc;
   if (d.n_kv_heads <= 0 || d.head_dim <= 0 || d.head_dim % 16 || d.head_dim > 256 || n <= 0 || kv->num_slots <= 0)
@@ -445,19 +452,20 @@ extern "C" spec_status spec_cache_append(const spec_attn_desc* desc, const void*
   if (e4m3 && !(d.k_scale > 0 && d.v_scale > 0)) return SPEC_ERR_ARG;
   const long long width = (long long)d.n_kv_heads * d.head_dim;
   if (width >= (1ll << 30)) return SPEC_ERR_SHAPE;
-  if (ld == 0) ld = width;
-  if (ld < width) return SPEC_ERR_SHAPE;
+  if (k_ld == 0) k_ld = width;
+  if (v_ld == 0) v_ld = width;
+  if (k_ld < width || v_ld < width) return SPEC_ERR_SHAPE;
   const size_t es = d.dtype == SPEC_DTYPE_F32 ? 4 : 2;
   if (!aligned(k, es) || !aligned(v, es) || (!e4m3 && (!aligned(kv->k, es) || !aligned(kv->v, es))))
     return SPEC_ERR_ALIGN;
   if (ws && !aligned(ws, 256)) return SPEC_ERR_WORKSPACE;
-  if (d.dtype == SPEC_DTYPE_F32) launch_append<float, float>(d, k, v, ld, slots, n, *kv, ws, stream);
+  if (d.dtype == SPEC_DTYPE_F32) launch_append<float, float>(d, k, k_ld, v, v_ld, slots, n, *kv, ws, stream);
   else if (d.dtype == SPEC_DTYPE_BF16 && !e4m3)
-    launch_append<__nv_bfloat16, __nv_bfloat16>(d, k, v, ld, slots, n, *kv, ws, stream);
+    launch_append<__nv_bfloat16, __nv_bfloat16>(d, k, k_ld, v, v_ld, slots, n, *kv, ws, stream);
   else if (d.dtype == SPEC_DTYPE_BF16)
-    launch_append<__nv_bfloat16, uint8_t>(d, k, v, ld, slots, n, *kv, ws, stream);
-  else if (!e4m3) launch_append<__half, __half>(d, k, v, ld, slots, n, *kv, ws, stream);
-  else launch_append<__half, uint8_t>(d, k, v, ld, slots, n, *kv, ws, stream);
+    launch_append<__nv_bfloat16, uint8_t>(d, k, k_ld, v, v_ld, slots, n, *kv, ws, stream);
+  else if (!e4m3) launch_append<__half, __half>(d, k, k_ld, v, v_ld, slots, n, *kv, ws, stream);
+  else launch_append<__half, uint8_t>(d, k, k_ld, v, v_ld, slots, n, *kv, ws, stream);
   return last_launch();
 }
 

@@ -31,6 +31,21 @@ def _ints(*shape, device, fill=0):
     return torch.full(shape, fill, dtype=torch.int32, device=device)
 
 
+def _rows(x, n, heads, hd, dtype, name):
+    """x [n, heads, hd] or [n, heads * hd] as rows (copied if a row is not in one piece), and the
+    elements from one to the next."""
+    at, step = x.shape, x.stride()
+    if at == (n, heads, hd) and x.dtype == dtype and step[2] == 1 and step[1] == hd and step[0] >= heads * hd:
+        return x, step[0]
+    whole = x.numel() == n * heads * hd and x.shape[0] == n
+    if not whole or x.dtype != dtype or tuple(x.shape[-2:]) not in ((heads, hd), (n, heads * hd)):
+        raise ValueError("%s is %s %s, the cache takes %s %s" % (name, x.dtype, tuple(x.shape), dtype, (n, heads, hd)))
+    x = x.reshape(n, heads * hd)
+    if x.stride(1) != 1 or (n > 1 and x.stride(0) < heads * hd):
+        x = x.contiguous()
+    return x, x.stride(0) if n > 1 else heads * hd
+
+
 class PagedCache:
     """K/V of ``layers`` layers in ``num_blocks`` blocks of ``block_size`` slots, and the
     pool of free blocks."""
@@ -38,6 +53,7 @@ class PagedCache:
     def __init__(self, layers, num_blocks, block_size, n_q_heads, n_kv_heads, head_dim, dtype="bf16", kv_dtype=None,
                  k_scale=1.0, v_scale=1.0, window=0, max_rows=64, device="cuda"):
         self.layers, self.num_blocks, self.block_size, self.device = layers, num_blocks, block_size, device
+        self.n_q_heads, self.n_kv_heads, self.head_dim, self.dtype = n_q_heads, n_kv_heads, head_dim, _TORCH[dtype]
         self.desc = lib.make_attn_desc(n_q_heads, n_kv_heads, head_dim, dtype, kv_dtype, window=window, k_scale=k_scale,
                                        v_scale=v_scale)
         stored = _TORCH[kv_dtype or dtype]
@@ -58,16 +74,19 @@ class PagedCache:
 
     def attend(self, kvs, slots, seq_len, max_len=0):
         """The ``attend`` of a model whose row i writes slot slots[i] and then attends to its
-        request's first seq_len[i] cache entries."""
+        request's first seq_len[i] cache entries.  q, k and v are of the cache's row type, each with
+        strides of its own."""
         n = slots.numel()
         if n > self.max_rows:
             raise ValueError("%d rows, the cache was made for %d" % (n, self.max_rows))
 
         def call(layer, q, k, v):
-            lib.spec_cache_append(self.desc, k, v, k.stride(0), slots, n, kvs[layer], self.ws)
             out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-            lib.spec_paged_attention(self.desc, q, kvs[layer], seq_len, n, out, None, self.ws, max_len=max_len,
-                                     q_ld=q.stride(0))
+            q, q_ld = _rows(q, n, self.n_q_heads, self.head_dim, self.dtype, "q")
+            k, k_ld = _rows(k, n, self.n_kv_heads, self.head_dim, self.dtype, "k")
+            v, v_ld = _rows(v, n, self.n_kv_heads, self.head_dim, self.dtype, "v")
+            lib.spec_cache_append(self.desc, k, v, k_ld, slots, n, kvs[layer], self.ws, v_ld=v_ld)
+            lib.spec_paged_attention(self.desc, q, kvs[layer], seq_len, n, out, None, self.ws, max_len=max_len, q_ld=q_ld)
             return out
         return call
 

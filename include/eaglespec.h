@@ -483,6 +483,13 @@ typedef struct {
 spec_status spec_cache_append(const spec_attn_desc *desc, const void *k, const void *v, int64_t ld,
                               const int32_t *slots, int32_t n, const spec_kv *kv, void *ws, spec_stream_t stream);
 
+/* The same with a row stride each for k and v (0 = n_kv_heads * head_dim): a
+ * model that rotates its keys has them in a tensor of their own, and the values
+ * still as a slice of the fused product. */
+spec_status spec_cache_append_strided(const spec_attn_desc *desc, const void *k, int64_t k_ld, const void *v,
+                                      int64_t v_ld, const int32_t *slots, int32_t n, const spec_kv *kv, void *ws,
+                                      spec_stream_t stream);
+
 /* Workspace of spec_paged_attention for at most max_B requests: header,
  * counters, partial results.  Zero-filled before its first use; every call
  * leaves the counters at zero.  Calls that share a workspace must not overlap

@@ -66,6 +66,13 @@ def test_cache_append_refusals():
     assert append(ws=F + 16) == WS
 
 
+def test_cache_append_strided_refusals():
+    def strided(k_ld=0, v_ld=0, k=F, v=F, n=4):
+        return call("spec_cache_append_strided", ctypes.byref(desc()), k, k_ld, v, v_ld, F, n, ctypes.byref(kv()), F, None)
+    assert strided(k_ld=127) == SHAPE and strided(v_ld=127) == SHAPE and strided(k_ld=-128, v_ld=128) == SHAPE
+    assert strided(k=None) == ARG and strided(v=None) == ARG and strided(v=F + 1) == ALIGN and strided(n=0) == SHAPE
+
+
 def attend(d=None, q=F, q_ld=0, cache=None, lens=F, B=4, max_len=0, out=F, out_ld=0, lse=F, ws=F, wsb=BIG):
     return call("spec_paged_attention", ctypes.byref(d or desc()), q, q_ld, ctypes.byref(cache or kv()), lens, B, max_len,
                 out, out_ld, lse, ws, wsb, None)

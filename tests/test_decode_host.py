@@ -1,0 +1,85 @@
+"""What decode.py hands to the library and makes of its answers, on CPU tensors (cpu_library): layouts of a model's rows,
+requests that cannot go on, runs one after another."""
+import numpy as np
+import pytest
+import torch
+
+import cpu_library
+from eagle_speculative_decoding_step_gb300 import decode
+
+
+@pytest.fixture(autouse=True)
+def on_cpu(monkeypatch):
+    cpu_library.use(monkeypatch)
+
+
+class Layouts(decode.RandomModel):
+    """RandomModel whose rows reach ``attend`` in another layout (lay: of q, k, v), their values the same."""
+
+    def __init__(self, lay=None, **kw):
+        super().__init__(layers=2, hidden=64, nq=4, nkv=2, hd=16, inter=96, vocab=203, max_len=256, dtype="f32", device="cpu",
+                         **kw)
+        self.lay = lay or (lambda q, k, v: (q, k, v))
+
+    def __call__(self, tok, pos, attend):
+        return super().__call__(tok, pos, lambda i, q, k, v: attend(i, *self.lay(q, k, v)))
+
+
+def cache_of(m, blocks=60, bs=4, rows=8):
+    return decode.PagedCache(2, blocks, bs, m.nq, m.nkv, m.hd, dtype="f32", max_rows=rows, device="cpu")
+
+
+def ids(*a):
+    return torch.tensor(a, dtype=torch.int32)
+
+
+def heads_first(x):
+    """The same values, heads outermost in memory."""
+    return x.transpose(0, 1).contiguous().transpose(0, 1)
+
+
+def components_first(x):
+    return x.transpose(1, 2).contiguous().transpose(1, 2)
+
+
+LAYOUTS = dict(k_its_own=lambda q, k, v: (q, k.contiguous(), v), v_its_own=lambda q, k, v: (q, k, v.contiguous()),
+               all_their_own=lambda q, k, v: (q.contiguous(), k.contiguous(), v.contiguous()),
+               q_by_heads=lambda q, k, v: (heads_first(q), k, v), k_by_heads=lambda q, k, v: (q, heads_first(k), v),
+               v_by_components=lambda q, k, v: (q, k, components_first(v)),
+               flat=lambda q, k, v: (q.flatten(1), k.flatten(1), v.flatten(1)))
+
+
+@pytest.mark.parametrize("beams", [False, True])
+@pytest.mark.parametrize("name", LAYOUTS)
+def test_rows_of_any_layout_give_the_same(name, beams):
+    """K that was rotated is a tensor of its own while V is a slice of the fused product, and so on."""
+    got = []
+    for lay in (None, LAYOUTS[name]):
+        m = Layouts(lay, seed=3)
+        c = cache_of(m)
+        if beams:
+            b = decode.BeamBatch(m, c, [[5, 9, 7, 2, 1], [11]], 2, 6, m.vocab)
+            for _ in range(6):
+                b.step()
+            got.append(b.tokens.clone())
+        else:
+            b = decode.Batch(m, c, 3, 16, m.vocab)
+            got.append(b.decode(ids(5, 17, 100), 9))
+        assert b.error() == 0
+    assert torch.equal(*got)
+
+
+def test_a_single_row_whose_first_stride_means_nothing():
+    m = Layouts(lambda q, k, v: tuple(x.as_strided(x.shape, (1, x.stride(1), 1)) for x in (q, k, v)), seed=3)
+    b, ref = (decode.Batch(x, cache_of(x), 1, 16, x.vocab) for x in (m, Layouts(seed=3)))
+    assert torch.equal(b.decode(ids(5), 5), ref.decode(ids(5), 5))
+
+
+def test_rows_of_another_type_or_shape_are_refused():
+    for lay in (lambda q, k, v: (q.double(), k, v), lambda q, k, v: (q, k.bfloat16(), v), lambda q, k, v: (q, k, v.half()),
+                lambda q, k, v: (q[:, :2], k, v), lambda q, k, v: (q, k[..., :8], v), lambda q, k, v: (q, k, v[:1]),
+                lambda q, k, v: (q.transpose(1, 2), k, v)):
+        m = Layouts(lay)
+        b = decode.Batch(m, cache_of(m), 2, 16, m.vocab)
+        with pytest.raises(ValueError):
+            b.feed(ids(5, 6))

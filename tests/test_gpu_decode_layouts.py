@@ -1,0 +1,67 @@
+"""GPU parity of the decoding calls at layouts and shapes that a model's rows can have, against the fp64 oracle."""
+import numpy as np
+import pytest
+import torch
+
+from eagle_speculative_decoding_step_gb300 import binding as lib
+from eagle_speculative_decoding_step_gb300 import decode
+
+pytestmark = pytest.mark.gpu
+TYPES = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16, "e4m3": torch.float8_e4m3fn}
+
+
+def i32(a):
+    return torch.as_tensor(np.asarray(a), dtype=torch.int32).cuda()
+
+
+# ------------------------------------------------------------------ strides of K and V
+@pytest.mark.parametrize("t,c", [("bf16", "bf16"), ("f32", "f32"), ("f16", "e4m3")])
+@pytest.mark.parametrize("nkv,hd,k_ld,v_ld,off", [(2, 64, 0, 512, 256), (2, 64, 512, 0, 256), (3, 80, 240, 777, 3), (3, 80, 777, 0, 3),
+                                                  (8, 128, 1024, 6144, 5120)])
+def test_cache_append_takes_k_and_v_of_other_strides(t, c, nkv, hd, k_ld, v_ld, off):
+    """Values are small integers, which every type holds."""
+    n, w = 37, nkv * hd
+    g = torch.Generator(device="cuda").manual_seed(w + k_ld)
+
+    def rows(ld, off):
+        x = torch.randint(-8, 9, (n, ld or w), generator=g, device="cuda").to(TYPES[t])
+        return x[:, off:off + w] if ld > w else x
+    k, v = rows(k_ld, off), rows(v_ld, off)
+    at = np.random.default_rng(n).permutation(n + 9)[:n]
+    ck = torch.zeros(n + 9, nkv, hd, device="cuda").to(TYPES[c])
+    cv = torch.zeros(n + 9, nkv, hd, device="cuda").to(TYPES[c])
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    kv = lib.make_kv(dict(k=ck, v=cv, block_table=None, block_size=1, max_blocks=0, num_slots=n + 9))
+    lib.spec_cache_append(lib.make_attn_desc(nkv, nkv, hd, t, c), k, v, k_ld, i32(at), n, kv, ws, v_ld=v_ld)
+    assert lib.spec_get_device_error(ws) == 0
+    for cache, x in ((ck, k), (cv, v)):
+        ref = torch.zeros(n + 9, w)
+        ref[torch.from_numpy(at)] = x.float().cpu()
+        assert torch.equal(cache.float().cpu().view(n + 9, w), ref)
+
+
+class Layouts(decode.RandomModel):
+    def __init__(self, lay, **kw):
+        super().__init__(**kw)
+        self.lay = lay
+
+    def __call__(self, tok, pos, attend):
+        return super().__call__(tok, pos, lambda i, q, k, v: attend(i, *self.lay(q, k, v)))
+
+
+def by_heads(x):
+    return x.transpose(0, 1).contiguous().transpose(0, 1)
+
+
+@pytest.mark.parametrize("kv_dtype", [None, "e4m3"])
+def test_decoding_does_not_depend_on_the_layout_of_the_rows(kv_dtype):
+    got = []
+    for lay in (lambda q, k, v: (q, k, v), lambda q, k, v: (q, k.contiguous(), v), lambda q, k, v: (q, k, v.contiguous()),
+                lambda q, k, v: (by_heads(q), by_heads(k), by_heads(v))):
+        m = Layouts(lay, seed=1)
+        c = decode.PagedCache(2, 64, 16, m.nq, m.nkv, m.hd, kv_dtype=kv_dtype, k_scale=0.02, v_scale=0.02)
+        b = decode.Batch(m, c, 5, 64, m.vocab)
+        logits = [b.feed(i32([3, 50, 7, 9, 1000 + t])) for t in range(20)]
+        assert b.error() == 0
+        got.append(torch.stack(logits))
+    assert all(torch.equal(x, got[0]) for x in got[1:])
