@@ -140,9 +140,9 @@ class Batch:
                               self.B, self.tws)
 
     def feed(self, tok):
-        """One more token of every request, tok [B]; its logits [B, V]."""
+        """One more token of every request, tok [B] (of a row that has none: below 0); its logits [B, V]."""
         self.resize(self.length + 1)
-        return self.model(tok, self.pos, self.cache.attend(self.kvs, self.slots, self.length, self.max_len))
+        return self.model(tok.clamp(min=0), self.pos, self.cache.attend(self.kvs, self.slots, self.length, self.max_len))
 
     def decode(self, tok, steps):
         """Feeds tok [B] and then each step's best token: tokens [B, steps]."""

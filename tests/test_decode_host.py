@@ -83,3 +83,12 @@ def test_rows_of_another_type_or_shape_are_refused():
         b = decode.Batch(m, cache_of(m), 2, 16, m.vocab)
         with pytest.raises(ValueError):
             b.feed(ids(5, 6))
+
+
+def test_a_row_without_a_token_is_not_looked_up():
+    """Token ids that reach the model are ids: a row with no candidate, or that has ended without an end token, has -1."""
+    m = Layouts(seed=3)
+    seen = []
+    b = decode.Batch(lambda tok, pos, attend: seen.append(tok) or m(tok, pos, attend) * float("nan"), cache_of(m), 2, 16, m.vocab)
+    assert (b.decode(ids(5, 6), 4) == -1).all()
+    assert all((t >= 0).all() for t in seen)
