@@ -112,13 +112,21 @@ class _Select:
                              self.tok, self.score[b], self.done[b], self.ws, ld=logits.stride(0))
         self.at = b
 
+    def finish(self, which):
+        """The beams of which [B, W] select nothing more."""
+        self.done[self.at] |= which
+
 
 def _dtype_name(t):
     return next(k for k, v in _TORCH.items() if v == t.dtype)
 
 
 class Batch:
-    """One continuation a request (a batch of up to B requests of up to max_len tokens)."""
+    """One continuation a request (a batch of up to B requests of up to max_len tokens).
+
+    A request that cannot take another token, because its table is full or the pool has no block for
+    it, is ``stopped`` [B]: it keeps its blocks and length, its tokens are -1 from there on, and
+    ``error`` says what was missing.  The others go on."""
 
     def __init__(self, model, cache, B, max_len, vocab, eos=-1):
         self.model, self.cache, self.B = model, cache, B
@@ -129,33 +137,45 @@ class Batch:
         self.kvs = cache.views(self.table)
         self.slots, self.pos, self.cu = _ints(B, device=dev), _ints(B, device=dev), _ints(B + 1, device=dev)
         self.tws = torch.zeros(lib.spec_block_tables_workspace_bytes(B), dtype=torch.uint8, device=dev)
+        self.stopped = torch.zeros(B, dtype=torch.bool, device=dev)
         self.select = _Select(B, 1, vocab, eos, dev)
 
     def resize(self, want):
         """Grow to (or give back down to) want [B] tokens by at most B new ones in all: their slots and
-        positions, in request order, are in ``slots`` and ``pos``."""
+        positions are in ``slots`` and ``pos``, those of request b from ``cu``[b] on (a request that is
+        refused for its length has none there)."""
         c = self.cache
         lib.spec_block_tables(self.B, c.block_size, self.table.shape[1], c.num_blocks, self.length, want, self.table,
                               self.table, c.free, c.n_free, c.free, c.n_free, self.length, self.cu, self.slots, self.pos,
                               self.B, self.tws)
 
     def feed(self, tok):
-        """One more token of every request, tok [B] (of a row that has none: below 0); its logits [B, V]."""
-        self.resize(self.length + 1)
-        return self.model(tok.clamp(min=0), self.pos, self.cache.attend(self.kvs, self.slots, self.length, self.max_len))
+        """One more token of every request that can take one, tok [B] (of a row that has none: below 0);
+        logits [B, V], which mean nothing in the other rows."""
+        want = torch.where(self.stopped, self.length, self.length + 1)
+        self.resize(want)
+        self.stopped = self.stopped | (self.length != want)
+        fed = ~self.stopped
+        slots = torch.where(fed, self.slots[self.cu[:-1].clamp(max=self.B - 1).long()], -1)
+        length = torch.where(fed, self.length, 0)
+        return self.model(tok.clamp(min=0), (length - 1).clamp(min=0),
+                          self.cache.attend(self.kvs, slots, length, self.max_len))
 
     def decode(self, tok, steps):
         """Feeds tok [B] and then each step's best token: tokens [B, steps]."""
         out = []
         for _ in range(steps):
             logits = self.feed(tok)
+            self.select.finish(self.stopped[:, None])
             self.select(logits, _dtype_name(logits))
-            tok = self.select.tok[:, 0].clone()
+            tok = torch.where(self.stopped, -1, self.select.tok[:, 0])
             out.append(tok)
         return torch.stack(out, 1)
 
     def release(self):
+        """Gives all blocks back; the batch can take other requests."""
         self.resize(torch.zeros_like(self.length))
+        self.stopped = torch.zeros_like(self.stopped)
 
     def error(self):
         return lib.spec_get_device_error(self.tws) or self.cache.error()

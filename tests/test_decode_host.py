@@ -92,3 +92,50 @@ def test_a_row_without_a_token_is_not_looked_up():
     b = decode.Batch(lambda tok, pos, attend: seen.append(tok) or m(tok, pos, attend) * float("nan"), cache_of(m), 2, 16, m.vocab)
     assert (b.decode(ids(5, 6), 4) == -1).all()
     assert all((t >= 0).all() for t in seen)
+
+
+# ------------------------------------------------------------------ requests that cannot go on
+def alone(first, steps, seed=3, eos=-1):
+    """What a request decodes by itself."""
+    m = Layouts(seed=seed)
+    return decode.Batch(m, cache_of(m), 1, 64, m.vocab, eos).decode(ids(first), steps)[0].tolist()
+
+
+def feed_one(b, i, tok):
+    """One token of request i only."""
+    one = torch.zeros(b.B, dtype=torch.int32)
+    one[i] = 1
+    b.resize(b.length + one)
+    slots = torch.where(one == 1, b.slots[0], -1).int()
+    return b.model(torch.full((b.B,), tok, dtype=torch.int32), (b.length - 1).clamp(min=0),
+                   b.cache.attend(b.kvs, slots, b.length * one, b.max_len))[i]
+
+
+def test_a_request_at_its_tables_end_leaves_the_others_right():
+    m = Layouts(seed=5)
+    toks = [[7, 8, 9, 10, 11, 12, 13, 14, 15, 16], [20, 21, 22, 23, 24], [30, 31, 32, 33, 34, 35, 36]]
+    b = decode.Batch(m, cache_of(m), 3, 8, m.vocab)
+    for i, n in enumerate((8, 3, 5)):
+        for t in range(n):
+            feed_one(b, i, toks[i][t])
+    got = [b.feed(ids(toks[0][8 + s], toks[1][3 + s], toks[2][5 + s])) for s in range(2)]
+    assert b.length.tolist() == [8, 5, 7] and b.error() == cpu_library.ERR_DEVICE and b.stopped.tolist() == [True, False, False]
+    for i in (1, 2):
+        one = decode.Batch(m, cache_of(m), 1, 8, m.vocab)
+        ref = [one.feed(ids(t)) for t in toks[i]][-2:]
+        for x, y in zip(got, ref):
+            assert torch.allclose(x[i], y[0], atol=1e-5)
+
+
+def test_a_request_that_the_pool_cannot_serve_stops_and_the_others_go_on():
+    m = Layouts(seed=3)
+    b = decode.Batch(m, cache_of(m, blocks=4, bs=4), 3, 16, m.vocab)      # a block each, and one more for request 0
+    got = b.decode(ids(5, 17, 100), 8).tolist()
+    assert got[0] == alone(5, 8)
+    for row, first in ((1, 17), (2, 100)):
+        assert got[row] == alone(first, 4) + [-1] * 4
+    assert b.length.tolist() == [8, 4, 4] and b.stopped.tolist() == [False, True, True]
+    assert b.error() == cpu_library.ERR_CAPACITY
+    b.release()
+    assert int(b.cache.n_free[0]) == 4 and not b.stopped.any()
+    assert [int(x) for x in b.feed(ids(5, 17, 100)).argmax(1)] == [alone(f, 1)[0] for f in (5, 17, 100)]

@@ -1,0 +1,54 @@
+"""Plain batches on the GPU whose requests end at different steps: each request decodes what it decodes by itself."""
+import numpy as np
+import pytest
+import torch
+
+from eagle_speculative_decoding_step_gb300 import decode
+
+pytestmark = pytest.mark.gpu
+ERR_CAPACITY = -4
+FIRST = (5, 17, 400, 33)
+
+
+@pytest.fixture(autouse=True)
+def full_fp32():
+    before = torch.backends.cuda.matmul.allow_tf32
+    torch.backends.cuda.matmul.allow_tf32 = False
+    yield
+    torch.backends.cuda.matmul.allow_tf32 = before
+
+
+def small(seed=3):
+    return decode.RandomModel(layers=2, hidden=64, nq=4, nkv=2, hd=32, inter=96, vocab=503, max_len=256, dtype="f32", seed=seed)
+
+
+def batch(m, n, blocks=200, bs=8, max_len=64, eos=-1):
+    return decode.Batch(m, decode.PagedCache(2, blocks, bs, m.nq, m.nkv, m.hd, dtype="f32", max_rows=4), n, max_len, m.vocab, eos)
+
+
+def ids(*a):
+    return torch.tensor(a, dtype=torch.int32, device="cuda")
+
+
+def alone(steps, eos=-1):
+    """Each of FIRST decoded by itself; the best logits lie far enough apart for the batch size not to matter."""
+    m = small()
+    return [batch(m, 1, eos=eos).decode(ids(f), steps)[0].tolist() for f in FIRST]
+
+
+def test_requests_that_the_pool_cannot_serve_stop_and_the_others_go_on():
+    want = alone(20)
+    b = batch(small(), 4, blocks=6)                       # 8 tokens a block: two of the four get a second one
+    got = b.decode(ids(*FIRST), 20).tolist()
+    assert got[:2] == [w[:16] + [-1] * 4 for w in want[:2]]
+    assert got[2:] == [w[:8] + [-1] * 12 for w in want[2:]]
+    assert b.error() == ERR_CAPACITY and b.length.tolist() == [16, 16, 8, 8] and b.stopped.all()
+    b.release()
+    assert int(b.cache.n_free[0]) == 6 and b.length.tolist() == [0] * 4
+
+
+def test_requests_at_the_end_of_their_tables_stop():
+    want = alone(20)
+    b = batch(small(), 4, max_len=16)
+    got = b.decode(ids(*FIRST), 20).tolist()
+    assert got == [w[:16] + [-1] * 4 for w in want] and b.error() != 0 and b.length.tolist() == [16] * 4
