@@ -112,6 +112,11 @@ class _Select:
                              self.tok, self.score[b], self.done[b], self.ws, ld=logits.stride(0))
         self.at = b
 
+    def begin(self):
+        """Every beam live, with score 0."""
+        self.score[self.at].zero_()
+        self.done[self.at].zero_()
+
     def finish(self, which):
         """The beams of which [B, W] select nothing more."""
         self.done[self.at] |= which
@@ -126,7 +131,8 @@ class Batch:
 
     A request that cannot take another token, because its table is full or the pool has no block for
     it, is ``stopped`` [B]: it keeps its blocks and length, its tokens are -1 from there on, and
-    ``error`` says what was missing.  The others go on."""
+    ``error`` says what was missing.  The others go on.  A request that has selected the end token gives
+    its blocks back with the next ``feed`` and goes on selecting that token; ``release`` ends all of them."""
 
     def __init__(self, model, cache, B, max_len, vocab, eos=-1):
         self.model, self.cache, self.B = model, cache, B
@@ -152,10 +158,11 @@ class Batch:
     def feed(self, tok):
         """One more token of every request that can take one, tok [B] (of a row that has none: below 0);
         logits [B, V], which mean nothing in the other rows."""
-        want = torch.where(self.stopped, self.length, self.length + 1)
+        done = self.select.done[self.select.at][:, 0] != 0
+        want = torch.where(self.stopped, self.length, torch.where(done, 0, self.length + 1))
         self.resize(want)
         self.stopped = self.stopped | (self.length != want)
-        fed = ~self.stopped
+        fed = ~(self.stopped | done)
         slots = torch.where(fed, self.slots[self.cu[:-1].clamp(max=self.B - 1).long()], -1)
         length = torch.where(fed, self.length, 0)
         return self.model(tok.clamp(min=0), (length - 1).clamp(min=0),
@@ -176,6 +183,7 @@ class Batch:
         """Gives all blocks back; the batch can take other requests."""
         self.resize(torch.zeros_like(self.length))
         self.stopped = torch.zeros_like(self.stopped)
+        self.select.begin()
 
     def error(self):
         return lib.spec_get_device_error(self.tws) or self.cache.error()

@@ -139,3 +139,36 @@ def test_a_request_that_the_pool_cannot_serve_stops_and_the_others_go_on():
     b.release()
     assert int(b.cache.n_free[0]) == 4 and not b.stopped.any()
     assert [int(x) for x in b.feed(ids(5, 17, 100)).argmax(1)] == [alone(f, 1)[0] for f in (5, 17, 100)]
+
+
+def test_finished_requests_give_their_blocks_back():
+    eos = alone(17, 3)[-1]
+    want = [alone(f, 12, eos=eos) for f in (5, 17, 100)]
+    assert want[1][2:] == [eos] * 10 and eos not in want[0]
+    m = Layouts(seed=3)
+    c = cache_of(m, blocks=20, bs=4)
+    b = decode.Batch(m, c, 3, 16, m.vocab, eos)
+    got = b.decode(ids(5, 17, 100), 12).tolist()
+    assert got == want and b.error() == 0
+    assert b.length[1] == 0 and int(c.n_free[0]) == 20 - sum(-(-int(n) // 4) for n in b.length)
+    assert sorted(c.free[:int(c.n_free[0])].tolist() + b.table[b.table >= 0].tolist()) == list(range(20))
+
+
+def test_a_batch_starts_anew_after_release():
+    eos = alone(17, 3)[-1]
+    m = Layouts(seed=3)
+    b = decode.Batch(m, cache_of(m), 2, 16, m.vocab, eos)
+    first = b.decode(ids(17, 5), 12).tolist()
+    assert first == [alone(17, 12, eos=eos), alone(5, 12)]
+    score = b.select.score[b.select.at].clone()
+    b.release()
+    assert b.decode(ids(5, 17), 12).tolist() == first[::-1] and b.error() == 0
+    assert torch.allclose(b.select.score[b.select.at].flip(0), score)
+
+
+def test_finished_requests_make_room_for_the_others():
+    """Four blocks, all of which one request needs: the other one ends after three tokens."""
+    eos = alone(17, 3)[-1]
+    m = Layouts(seed=3)
+    b = decode.Batch(m, cache_of(m, blocks=4, bs=4), 2, 16, m.vocab, eos)
+    assert b.decode(ids(5, 17), 16).tolist() == [alone(5, 16), alone(17, 16, eos=eos)] and b.error() == 0

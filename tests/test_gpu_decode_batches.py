@@ -52,3 +52,17 @@ def test_requests_at_the_end_of_their_tables_stop():
     b = batch(small(), 4, max_len=16)
     got = b.decode(ids(*FIRST), 20).tolist()
     assert got == [w[:16] + [-1] * 4 for w in want] and b.error() != 0 and b.length.tolist() == [16] * 4
+
+
+def test_finished_requests_give_their_blocks_back_and_a_batch_is_used_again():
+    eos = alone(5)[1][-1]
+    want = alone(20, eos)
+    b = batch(small(), 4, eos=eos)
+    got = b.decode(ids(*FIRST), 20).tolist()
+    assert got == want and b.error() == 0
+    ended = [i for i, w in enumerate(want) if eos in w[:-1]]
+    assert 1 in ended and len(ended) < 4
+    assert [int(n) == 0 for n in b.length] == [i in ended for i in range(4)]
+    assert int(b.cache.n_free[0]) == 200 - 3 * (4 - len(ended))
+    b.release()
+    assert b.decode(ids(*FIRST[::-1]), 20).tolist() == want[::-1] and b.error() == 0
