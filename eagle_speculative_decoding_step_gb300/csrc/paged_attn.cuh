@@ -126,7 +126,7 @@ __host__ __device__ inline float share_out(long long total_, long long items_, i
 }
 
 // A consumer warp's running state for one (kv head, query tile): unnormalised
-// outputs o, running maxima m (log2 units) and sums l, in the layout of its math.
+// outputs o, references m (running maxima, or a constant below; log2 units) and sums l, in the layout of its math.
 // Register r of o belongs to statistics index st(r).
 template <int NR_, int NM_> struct State {
   static constexpr int NR = NR_, NM = NM_;
@@ -238,6 +238,10 @@ template <typename T, bool F8, int HD, int NT> struct MmaMath {
   static constexpr int kWarps = 8, VS = HD > 128 ? 2 : 1, MT = HD / 16 / VS;
   static constexpr bool kMoreRegs = NT == 2 && HD >= 128;
   using S = State<MT * NT * 4, 2 * NT>;
+  // m is the largest score less kBelow: weights are up to 2^kBelow.  f16 has no exponents for small ones: with weights up
+  // to 1, those under 2^-25 would be lost and those under 2^-14 held in steps of 2^-24 (a first key 14 above 1000 others,
+  // its value zero: the output 8e-3 off).  2^15 is the largest power of two below f16's largest number.
+  static constexpr float kBelow = std::is_same_v<P, __half> ? 15.f : 0.f;
   // register r = (mt NT + nt) 4 + 2 i + j: query nt 8 + 2 (lane & 3) + j, component mt 16 + (lane >> 2) + 8 i
   // (8-bit caches: mt 16 + 2 (lane >> 2) + i)
   SPEC_DEV static int st(int r) { return ((r >> 2) % NT) * 2 + (r & 1); }
@@ -476,7 +480,7 @@ template <typename T, bool F8, int HD, int NT> struct MmaMath {
         }
         x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
         x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16)) - kBelow;
         mn[nt * 2 + j] = fmaxf(s.m[nt * 2 + j], x);
         grew |= x > s.m[nt * 2 + j];
       }
@@ -503,7 +507,8 @@ template <typename T, bool F8, int HD, int NT> struct MmaMath {
           s.l[nt * 2 + j] += c[u][nt][j] + c[u][nt][2 + j];
         }
         // a weight enters the second product as two 16-bit parts: one alone (2^-9 of it in bf16)
-        // would cost as much as the output's own rounding
+        // would cost as much as the output's own rounding.  Two bf16 parts lose 2^-18 of it; two f16 parts 2^-22, or
+        // where the lower one is subnormal 2^-25, 2^-40 of the largest weight (kBelow)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const uint32_t hi = pack<P>(c[u][nt][2 * h], c[u][nt][2 * h + 1]);

@@ -510,7 +510,10 @@ size_t spec_attention_workspace_bytes(const spec_attn_desc *desc, int32_t max_B)
  * only chooses how work is laid out.  Any block_size; max_blocks * block_size
  * < 2^30.  q, out, the cache and, with
  * ld's, every row of q and out 16-byte aligned (SPEC_ERR_ALIGN).
- * Sums and softmax statistics are fp32.  A K or V value that is not finite in a
+ * Sums and softmax statistics are fp32.  A softmax weight enters the product with
+ * v in fp32 (F32 cache), as two bf16 parts (BF16 cache: 2^-18 of it lost) or as two
+ * f16 parts (F16 and E4M3 caches: 2^-22 of it lost, or 2^-40 of the largest weight
+ * where that is more).  A K or V value that is not finite in a
  * row that is attended to makes outputs of its head that are not finite; rows that are
  * not attended to may hold anything.  Error word: SPEC_ERR_DEVICE for a
  * seq_len outside [0, max_blocks * block_size] (clamped) or a block id out of
