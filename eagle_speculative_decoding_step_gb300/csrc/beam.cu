@@ -409,7 +409,7 @@ __global__ void __launch_bounds__(kSelThreads, 4) beam_select_kernel(const SelAr
       const float x = cvt(src[i]);
       return finite(x) && x >= border ? (uint64_t)key_of(x) << 32 | (uint32_t)~i : 0ull;
     };
-    // their logits that reach the border: a warp takes every 8th group, the lanes its elements
+    // their logits that reach the border: the warps take a group each in turn, the lanes its elements
     int kept = 0;
     if (found <= kSelCap) {
       // places of the groups that are kept, in list order; a warp's are read kBatch at a time
@@ -562,17 +562,27 @@ __global__ void __launch_bounds__(kSelThreads, 4) beam_select_kernel(const SelAr
   }
 }
 
+constexpr int kSelSms = 152;
 // chunks of a row: the same for every row of a call
 static int sel_chunks(int B, int W, int V, int* chunk) {
   constexpr int kStep = kSelWarps * kSelTile;
   const int steps = (V + kStep - 1) / kStep;
   // one chunk an SM (a chunk's end costs ~3 us: 32 x 8 rows of 151936 in fp32, 2 / 4 chunks a row 33.6 / 37.5 us), of
   // at least two steps (merging: 4 rows of 128256 in fp32, 16 / 32 / 64 chunks 8.5 / 9.0 / 9.2 us)
-  int want = std::min((152 + B * W - 1) / (B * W), (steps + 1) / 2);
+  int want = std::min((kSelSms + B * W - 1) / (B * W), (steps + 1) / 2);
   want = std::max(want, (steps + kSelChunk / kStep - 1) / (kSelChunk / kStep));
   const int per = (steps + want - 1) / want;
   *chunk = per * kStep;
   return (steps + per - 1) / per;
+}
+
+// Chunks of all rows, at most, of any batch up to B: fewer rows are cut into more chunks each.  It grows with each of
+// the three sizes.
+static size_t sel_most_chunks(int B, int W, int V) {
+  constexpr int kStep = kSelWarps * kSelTile;
+  const long long rows = (long long)B * W, steps = (V + kStep - 1) / kStep;
+  return (size_t)std::max(std::min(kSelSms + rows - 1, rows * ((steps + 1) / 2)),
+                          rows * ((steps + kSelChunk / kStep - 1) / (kSelChunk / kStep)));
 }
 
 // ---------------------------------------------------------------- reordering
@@ -704,11 +714,13 @@ __global__ void __launch_bounds__(256) beam_reorder_kernel(const __grid_constant
 
 using namespace spec;
 
+static size_t sel_bytes(size_t chunks, int W) {
+  return kWsHeader + kSelCounterBytes + align_up(chunks * 8, 256) + align_up(chunks * W * 8, 256);
+}
+
 extern "C" size_t spec_beam_workspace_bytes(int32_t B, int32_t W, int32_t V) {
   if (B <= 0 || W <= 0 || W > 32 || V <= 0 || (long long)W * V >= (1ll << 30)) return 0;
-  int chunk;
-  const size_t n = (size_t)B * W * sel_chunks(B, W, V, &chunk);
-  return kWsHeader + kSelCounterBytes + align_up(n * 8, 256) + align_up(n * W * 8, 256);
+  return sel_bytes(sel_most_chunks(B, W, V), W);
 }
 
 extern "C" spec_status spec_beam_select(int32_t B, int32_t W, int32_t V, int32_t dtype, const void* logits, int64_t ld,
@@ -718,14 +730,13 @@ extern "C" spec_status spec_beam_select(int32_t B, int32_t W, int32_t V, int32_t
   if (!logits || !score || !done || !parent || !tok || !score_out || !done_out) return SPEC_ERR_ARG;
   if (score == score_out || done == done_out) return SPEC_ERR_ARG;
   if (dtype < SPEC_DTYPE_F32 || dtype > SPEC_DTYPE_F16) return SPEC_ERR_UNSUPPORTED;
-  const size_t need = spec_beam_workspace_bytes(B, W, V);
-  if (need == 0 || eos >= V || (long long)B * W > 65535) return SPEC_ERR_SHAPE;
+  if (spec_beam_workspace_bytes(B, W, V) == 0 || eos >= V || (long long)B * W > 65535) return SPEC_ERR_SHAPE;
   if (ld == 0) ld = V;
   if (ld < V) return SPEC_ERR_SHAPE;
   if (!aligned(logits, dtype == SPEC_DTYPE_F32 ? 4 : 2)) return SPEC_ERR_ALIGN;
-  if (!ws || !aligned(ws, 256) || ws_bytes < need) return SPEC_ERR_WORKSPACE;
   int chunk;
   const int nch = sel_chunks(B, W, V, &chunk);
+  if (!ws || !aligned(ws, 256) || ws_bytes < sel_bytes((size_t)B * W * nch, W)) return SPEC_ERR_WORKSPACE;
   char* p = static_cast<char*>(ws) + kWsHeader;
   SelArgs g{};
   g.B = B, g.W = W, g.V = V, g.nch = nch, g.chunk = chunk, g.eos = eos < 0 ? -1 : eos, g.ld = ld;

@@ -522,9 +522,10 @@ spec_status spec_paged_attention(const spec_attn_desc *desc, const void *q, int6
                                  const int32_t *seq_len, int32_t B, int32_t max_len, void *out, int64_t out_ld,
                                  float *lse, void *ws, size_t ws_bytes, spec_stream_t stream);
 
-/* Workspace of spec_beam_select: header, counters, per-chunk records.
- * Zero-filled before its first use; every call leaves the counters at zero.
- * Calls that share a workspace must not overlap on the GPU. */
+/* Workspace of spec_beam_select for at most B requests (W beams and V tokens, or
+ * fewer): header, counters, per-chunk records.  Zero-filled before its first use;
+ * every call leaves the counters at zero.  Calls that share a workspace must not
+ * overlap on the GPU. */
 size_t spec_beam_workspace_bytes(int32_t B, int32_t W, int32_t V);
 
 /* One selection step of beam search: the W best continuations of the W beams of

@@ -110,6 +110,18 @@ def test_beam_select_refusals():
     assert lib.spec_beam_workspace_bytes(2, 4, 100) > 0 and lib.spec_beam_workspace_bytes(2, 33, 100) == 0
 
 
+def test_a_beam_workspace_serves_every_smaller_batch():
+    """A smaller batch cuts its rows into more chunks; the size is that of the largest need up to B."""
+    for W, V in ((1, 128256), (4, 128256), (8, 151936), (8, 40000), (5, 33), (32, 262144), (3, 8193)):
+        n = [lib.spec_beam_workspace_bytes(B, W, V) for B in range(1, 400)]
+        assert n == sorted(n), (W, V)
+    for B, V in ((1, 5000), (3, 128256), (40, 128256)):
+        n = [lib.spec_beam_workspace_bytes(B, W, V) for W in range(1, 33)]
+        assert n == sorted(n)
+        n = [lib.spec_beam_workspace_bytes(B, 4, v) for v in range(1, V, 997)]
+        assert n == sorted(n)
+
+
 def reorder(kvs=None, n=None, row_bytes=256, ws=F, **over):
     f = dict(B=2, W=4, block_size=16, max_blocks=8, owned_ld=40, hist_ld=100)
     f.update({n: F + 256 * i for i, n in enumerate(["parent", "tok", "seq_len", "prompt_blocks", "owned", "table_in",
