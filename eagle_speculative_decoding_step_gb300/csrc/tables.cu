@@ -412,10 +412,11 @@ extern "C" spec_status spec_block_tables(int32_t B, int32_t block_size, int32_t 
   if (!len_old || !len_new || !table_in || !table_out || !free_in || !n_free_in || !free_out || !n_free_out ||
       !len_out || !cu_new || !slots)
     return SPEC_ERR_ARG;
-  // token indices, slots and pool positions (free and released ids together) are 32-bit integers
+  // token indices, slots, places in the slot map and pool positions (free and released ids together) are 32-bit integers
   const long long limit = 1ll << 30;
   if (B > kTabMaxB || (long long)max_blocks * block_size >= limit ||
-      (long long)B * ((long long)max_blocks * block_size) >= limit || (long long)num_blocks * block_size >= limit)
+      (long long)B * ((long long)max_blocks * block_size) >= limit || (long long)num_blocks * block_size >= limit ||
+      slots_cap >= limit)
     return SPEC_ERR_CAPACITY;
   if (!ws || !aligned(ws, 256) || ws_bytes < spec_block_tables_workspace_bytes(B)) return SPEC_ERR_WORKSPACE;
   TabArgs a{B, block_size, max_blocks, num_blocks, slots_cap, len_old, len_new, table_in, free_in, n_free_in,

@@ -451,8 +451,8 @@ size_t spec_block_tables_workspace_bytes(int32_t B);
  * less than cu_new[B]; SPEC_ERR_DEVICE for a length outside
  * [0, max_blocks * block_size] (the request is left as it is), an n_free_in
  * outside [0, num_blocks], or an id out of range.
- * B <= 8192; B * max_blocks * block_size and num_blocks * block_size < 2^30
- * (SPEC_ERR_CAPACITY). */
+ * B <= 8192; B * max_blocks * block_size, num_blocks * block_size and slots_cap
+ * < 2^30 (SPEC_ERR_CAPACITY). */
 spec_status spec_block_tables(int32_t B, int32_t block_size, int32_t max_blocks, int32_t num_blocks,
                               const int32_t *len_old, const int32_t *len_new, const int32_t *table_in,
                               int32_t *table_out, const int32_t *free_in, const int32_t *n_free_in,

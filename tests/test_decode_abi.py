@@ -43,6 +43,11 @@ def test_block_tables_refusals():
     assert lib.spec_block_tables_workspace_bytes(4) > 0 and lib.spec_block_tables_workspace_bytes(0) == 0
 
 
+def test_block_tables_refuses_a_slot_map_past_its_32_bit_counts():
+    for cap in (1 << 30, 2 ** 31 - 100000, 2 ** 31 - 1):
+        assert tables(cap=cap, ws=None) == CAPACITY
+
+
 def desc(nq=8, nkv=2, hd=64, t="bf16", c=None, **kw):
     return lib.make_attn_desc(nq, nkv, hd, t, c, **kw)
 
