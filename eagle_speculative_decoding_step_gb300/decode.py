@@ -58,8 +58,8 @@ class PagedCache:
                                        v_scale=v_scale)
         stored = _TORCH[kv_dtype or dtype]
         shape = (layers, num_blocks * block_size, n_kv_heads, head_dim)
-        self.k = torch.zeros(shape, device=device).to(stored)
-        self.v = torch.zeros(shape, device=device).to(stored)
+        same = torch.uint8 if stored == torch.float8_e4m3fn else stored        # zero bits are zeros in every type
+        self.k, self.v = (torch.zeros(shape, dtype=same, device=device).view(stored) for _ in range(2))
         self.row_bytes = n_kv_heads * head_dim * self.k.element_size()
         self.free = torch.arange(num_blocks - 1, -1, -1, dtype=torch.int32, device=device)
         self.n_free = _ints(1, device=device, fill=num_blocks)

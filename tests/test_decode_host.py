@@ -172,3 +172,18 @@ def test_finished_requests_make_room_for_the_others():
     m = Layouts(seed=3)
     b = decode.Batch(m, cache_of(m, blocks=4, bs=4), 2, 16, m.vocab, eos)
     assert b.decode(ids(5, 17), 16).tolist() == [alone(5, 16), alone(17, 16, eos=eos)] and b.error() == 0
+
+
+# ------------------------------------------------------------------ the cache's memory
+@pytest.mark.parametrize("dtype,kv_dtype,es", [("f32", None, 4), ("bf16", None, 2), ("f16", "e4m3", 1)])
+def test_a_cache_is_made_in_its_own_type(monkeypatch, dtype, kv_dtype, es):
+    """Nothing larger than K or V is made on the way."""
+    made = []
+    for name in ("zeros", "empty", "full"):
+        f = getattr(torch, name)
+        monkeypatch.setattr(torch, name, lambda *a, _f=f, **kw: made.append(_f(*a, **kw)) or made[-1])
+    c = decode.PagedCache(3, 50, 8, 4, 2, 16, dtype=dtype, kv_dtype=kv_dtype, device="cpu")
+    size = 3 * 50 * 8 * 2 * 16 * es
+    assert c.k.numel() * c.k.element_size() == size == c.v.numel() * c.v.element_size()
+    assert max(x.numel() * x.element_size() for x in made) == size
+    assert c.k.shape == (3, 400, 2, 16) and (c.k.float() == 0).all() and (c.v.float() == 0).all()

@@ -65,3 +65,15 @@ def test_decoding_does_not_depend_on_the_layout_of_the_rows(kv_dtype):
         assert b.error() == 0
         got.append(torch.stack(logits))
     assert all(torch.equal(x, got[0]) for x in got[1:])
+
+
+# ------------------------------------------------------------------ memory
+@pytest.mark.parametrize("dtype,kv_dtype,es", [("bf16", None, 2), ("bf16", "e4m3", 1)])
+def test_making_a_cache_takes_no_more_than_the_cache(dtype, kv_dtype, es):
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    before = torch.cuda.memory_allocated()
+    torch.cuda.reset_peak_memory_stats()
+    c = decode.PagedCache(4, 4096, 16, 32, 8, 128, dtype=dtype, kv_dtype=kv_dtype)
+    size = 2 * 4 * 4096 * 16 * 8 * 128 * es
+    assert torch.cuda.max_memory_allocated() - before < size + c.ws.numel() + (1 << 22)
