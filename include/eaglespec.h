@@ -508,16 +508,20 @@ size_t spec_attention_workspace_bytes(const spec_attn_desc *desc, int32_t max_B)
  * one request to the next (0 = n_q_heads * head_dim); lse [B, n_q_heads] fp32 or
  * NULL.  max_len: an upper bound of seq_len over the batch, or 0 if unknown; it
  * only chooses how work is laid out.  Any block_size; max_blocks * block_size
- * < 2^30.  q, out, the cache and, with
- * ld's, every row of q and out 16-byte aligned (SPEC_ERR_ALIGN).
+ * < 2^30.  q, out, the cache and, with ld's, every row of q and out 16-byte
+ * aligned (SPEC_ERR_ALIGN).
  * Sums and softmax statistics are fp32.  A softmax weight enters the product with
  * v in fp32 (F32 cache), as two bf16 parts (BF16 cache: 2^-18 of it lost) or as two
  * f16 parts (F16 and E4M3 caches: 2^-22 of it lost, or 2^-40 of the largest weight
- * where that is more).  A K or V value that is not finite in a
- * row that is attended to makes outputs of its head that are not finite; rows that are
- * not attended to may hold anything.  Error word: SPEC_ERR_DEVICE for a
- * seq_len outside [0, max_blocks * block_size] (clamped) or a block id out of
- * range (its keys are left out). */
+ * where that is more).  BF16 queries on an E4M3 cache: components 2^-28 times a
+ * query's largest lose bits.
+ * A score of +infinity or NaN (a K or q value that is not finite) makes its head's
+ * outputs and lse not finite; one of -infinity is a weight of 0, and a row that has
+ * no other score is like one without keys.  A V value that is not finite in a row
+ * that is attended to makes that component of its head's outputs not finite; rows
+ * that are not attended to may hold anything.
+ * Error word: SPEC_ERR_DEVICE for a seq_len outside [0, max_blocks * block_size]
+ * (clamped) or a block id out of range (its keys are left out). */
 spec_status spec_paged_attention(const spec_attn_desc *desc, const void *q, int64_t q_ld, const spec_kv *kv,
                                  const int32_t *seq_len, int32_t B, int32_t max_len, void *out, int64_t out_ld,
                                  float *lse, void *ws, size_t ws_bytes, spec_stream_t stream);

@@ -91,3 +91,40 @@ def test_a_key_without_value_that_holds_nearly_all_of_the_weight(t, ct, nq, nkv,
         ks.append(k if first else k[::-1])
         vs.append((v if first else v[::-1]) * 64)
     check(t, ct, bs, q, ks, vs, *((0.5, 2.0) if ct == "e4m3" else (1.0, 1.0)))
+
+
+# ------------------------------------------------------------------ values that are not finite
+def plain_call(t, q, k, v, bs=16):
+    """One request of len(k) keys, blocks in order."""
+    nq, hd = q.shape
+    n, nkv = k.shape[:2]
+    table = torch.arange(-(-n // bs), dtype=torch.int32, device="cuda")[None]
+    pad = torch.zeros(table.numel() * bs - n, nkv, hd)
+    k, v = (torch.cat([x, pad]).to(TYPES[t]).cuda() for x in (k, v))
+    kv = lib.make_kv(dict(k=k, v=v, block_table=table, block_size=bs, max_blocks=table.numel(), num_slots=k.shape[0]))
+    desc = lib.make_attn_desc(nq, nkv, hd, t)
+    ws = torch.zeros(lib.spec_attention_workspace_bytes(desc, 1), dtype=torch.uint8, device="cuda")
+    out, lse = torch.empty(1, nq, hd, dtype=TYPES[t], device="cuda"), torch.empty(1, nq, device="cuda")
+    lib.spec_paged_attention(desc, q.to(TYPES[t]).cuda(), kv, torch.tensor([n], dtype=torch.int32, device="cuda"), 1, out, lse, ws)
+    return out[0].float().cpu(), lse[0].cpu()
+
+
+@pytest.mark.parametrize("t", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("n", [1, 40, 700])
+def test_scores_that_are_not_finite(t, n):
+    g = torch.Generator().manual_seed(n)
+    q, k, v = torch.randn(4, 64, generator=g), torch.randn(n, 2, 64, generator=g), torch.randn(n, 2, 64, generator=g)
+    q[0, 3], q[1, 3], q[2:, 3] = 1.0, -1.0, 0.0               # of head 0: scores of +infinity, -infinity; of head 1: NaN
+    i = n // 2
+    k[i, :, 3] = float("inf")
+    out, lse = plain_call(t, q, k, v)
+    assert not torch.isfinite(out[0]).any() and not torch.isfinite(lse[0])
+    assert not torch.isfinite(out[2:]).any() and not torch.isfinite(lse[2:]).any()
+    if n == 1:                                                # no score but -infinity: as without keys
+        assert (out[1] == 0).all() and lse[1] == -float("inf")
+        return
+    keep = torch.arange(n) != i
+    rest, rest_lse = plain_call(t, q, k[keep], v[keep])
+    assert torch.isfinite(out[1]).all()
+    eps = torch.finfo(TYPES[t]).eps                           # the same sum in another order, rounded once each
+    assert (out[1] - rest[1]).abs().max() <= eps * rest[1].abs().max() + 1e-5 and abs(lse[1] - rest_lse[1]) < 1e-5
