@@ -289,18 +289,22 @@ SPEC_DEV float to_f(__half x) { return __half2float(x); }
 // the product with its reciprocal is the quotient; otherwise the product is within 2
 // steps of it, and rounds the same way unless it lies next to a border between two
 // 8-bit values (a middle of the 20 bits that are dropped, or a number too small for
-// the type's normal ones).
+// the type's normal ones).  A scale whose reciprocal fp32 holds in fewer bits or not at all
+// has NaN for it (reciprocal()), and the quotient is taken every time.
 template <typename T, typename C, bool EXACT> SPEC_DEV C stored(T x, float scale, float inv) {
   if constexpr (sizeof(C) == 1) {
     float y = to_f(x) * inv;
     if constexpr (!EXACT) {
       const uint32_t past = (__float_as_uint(y) + 4u - 0x80000u) & 0xfffffu;
-      if (past < 8u || fabsf(y) < 0.015625f) y = __fdiv_rn(to_f(x), scale);
+      if (past < 8u || !(fabsf(y) >= 0.015625f)) y = __fdiv_rn(to_f(x), scale);
     }
     return __nv_cvt_float_to_fp8(y, __NV_SATFINITE, __NV_E4M3);
   } else {
     return x;
   }
+}
+SPEC_DEV float reciprocal(float s) {
+  return s >= 1.17549435e-38f && s <= 8.50705917e37f ? 1.f / s : NAN;      // 2^-126 .. 2^126
 }
 static bool power_of_two(float s) {
   int e;
@@ -322,7 +326,7 @@ __global__ void __launch_bounds__(256) cache_append_kernel(const T* __restrict__
   pdl_trigger();
   const T* __restrict__ src = blockIdx.y ? v : k;
   C* __restrict__ dst = blockIdx.y ? cv : ck;
-  const float scale = blockIdx.y ? v_scale : k_scale, inv = 1.f / scale;
+  const float scale = blockIdx.y ? v_scale : k_scale, inv = reciprocal(scale);
   const int per = 1 << lg, part = threadIdx.x & (per - 1);
   const long long row = (long long)blockIdx.x * (256 >> lg) + (threadIdx.x >> lg);
   if (row >= n) return;

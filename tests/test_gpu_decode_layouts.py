@@ -5,6 +5,7 @@ import torch
 
 from eagle_speculative_decoding_step_gb300 import binding as lib
 from eagle_speculative_decoding_step_gb300 import decode
+from oracle import decode as oracle
 
 pytestmark = pytest.mark.gpu
 TYPES = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16, "e4m3": torch.float8_e4m3fn}
@@ -77,3 +78,21 @@ def test_making_a_cache_takes_no_more_than_the_cache(dtype, kv_dtype, es):
     c = decode.PagedCache(4, 4096, 16, 32, 8, 128, dtype=dtype, kv_dtype=kv_dtype)
     size = 2 * 4 * 4096 * 16 * 8 * 128 * es
     assert torch.cuda.max_memory_allocated() - before < size + c.ws.numel() + (1 << 22)
+
+
+# ------------------------------------------------------------------ scales
+@pytest.mark.parametrize("t", ["bf16", "f16"])
+@pytest.mark.parametrize("ks,vs", [(1e-39, 3e38), (2.9e-39, 1.1e38), (1.2e-38, 8.4e37), (1e-45, 1.9e38), (2.0 ** -127, 2.0 ** 127)])
+def test_cache_append_to_eight_bits_with_scales_at_the_ends_of_their_type(t, ks, vs):
+    """All 65536 bit patterns: the quotient in fp32, whatever the reciprocal of the scale is in that type."""
+    x = torch.arange(65536, dtype=torch.int32, device="cuda").to(torch.int16).view(TYPES[t]).reshape(64, 1024)
+    ck, cv = torch.zeros(2, 64, 8, 128, device="cuda").to(TYPES["e4m3"]).unbind(0)
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    kv = lib.make_kv(dict(k=ck, v=cv, block_table=None, block_size=1, max_blocks=0, num_slots=64))
+    lib.spec_cache_append(lib.make_attn_desc(8, 8, 128, t, "e4m3", k_scale=ks, v_scale=vs), x, x, 0, i32(np.arange(64)), 64, kv,
+                          ws)
+    assert lib.spec_get_device_error(ws) == 0
+    with np.errstate(all="ignore"):
+        for cache, s in ((ck, ks), (cv, vs)):
+            ref = oracle.e4m3_round(x.float().cpu().numpy() / np.float32(s))
+            np.testing.assert_array_equal(cache.float().cpu().numpy().reshape(64, 1024), ref.astype(np.float32))
