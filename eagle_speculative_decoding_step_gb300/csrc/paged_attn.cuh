@@ -1041,6 +1041,8 @@ __global__ void __launch_bounds__(M::kWarps * 32 + 128, 1) paged_attention_kerne
         if (key0 >= lo_ && key0 + p.kt <= len_ && __all_sync(0xffffffffu, lane >= runs || in_run == run) && there == whole_runs) {
           if (lane * 32 < p.kt) masks[slot * kMaskWords + lane] = whole_word;
         } else {
+          // a block that the cache's end cuts: its keys past the end are left out as well
+          if (sl >= 0 && max(key_ + in_run, lo_) < min(key_ + run, len_)) report(g.ws, SPEC_ERR_DEVICE, g.b0 + b_, key_ + in_run);
           for (int i = 0; i * 32 < p.kt; ++i) {
             const int j = i * 32 + lane, k = key0 + j;
             const int have_r = __shfl_sync(0xffffffffu, in_run, (j >> p.run_lg) & 31);

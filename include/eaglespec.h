@@ -521,7 +521,8 @@ size_t spec_attention_workspace_bytes(const spec_attn_desc *desc, int32_t max_B)
  * that is attended to makes that component of its head's outputs not finite; rows
  * that are not attended to may hold anything.
  * Error word: SPEC_ERR_DEVICE for a seq_len outside [0, max_blocks * block_size]
- * (clamped) or a block id out of range (its keys are left out). */
+ * (clamped) or a slot out of range, of a block id outside the cache or of a block
+ * that its end cuts (such keys are left out). */
 spec_status spec_paged_attention(const spec_attn_desc *desc, const void *q, int64_t q_ld, const spec_kv *kv,
                                  const int32_t *seq_len, int32_t B, int32_t max_len, void *out, int64_t out_ld,
                                  float *lse, void *ws, size_t ws_bytes, spec_stream_t stream);

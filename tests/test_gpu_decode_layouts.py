@@ -96,3 +96,27 @@ def test_cache_append_to_eight_bits_with_scales_at_the_ends_of_their_type(t, ks,
         for cache, s in ((ck, ks), (cv, vs)):
             ref = oracle.e4m3_round(x.float().cpu().numpy() / np.float32(s))
             np.testing.assert_array_equal(cache.float().cpu().numpy().reshape(64, 1024), ref.astype(np.float32))
+
+
+# ------------------------------------------------------------------ a cache that ends inside a block
+@pytest.mark.parametrize("bs", [16, 8, 24, 12, 1])
+@pytest.mark.parametrize("t,ct", [("bf16", "bf16"), ("f32", "f32"), ("f16", "e4m3")])
+def test_keys_past_the_caches_end_are_left_out_and_told(bs, t, ct):
+    """Block 3 lies partly in the cache; its other slots are out of range as a block id past the end is."""
+    there = bs // 2
+    slots = 3 * bs + there
+    g = torch.Generator(device="cuda").manual_seed(bs)
+    k, v = (torch.randn(slots, 2, 64, generator=g, device="cuda").to(TYPES[ct]) for _ in range(2))
+    q = torch.randn(2, 4, 64, generator=g, device="cuda").to(TYPES[t])
+    table = i32([[0, 1, 3, -1], [2, 0, 1, -1]])
+    desc = lib.make_attn_desc(4, 2, 64, t, ct)
+    ws = torch.zeros(lib.spec_attention_workspace_bytes(desc, 2), dtype=torch.uint8, device="cuda")
+    kv = lib.make_kv(dict(k=k, v=v, block_table=table, block_size=bs, max_blocks=4, num_slots=slots))
+    for lens, code in (([2 * bs + there, 3 * bs], 0), ([3 * bs, 3 * bs], -6), ([2 * bs + there + 1, 1], -6)):
+        ws.zero_()
+        out = torch.empty_like(q)
+        lib.spec_paged_attention(desc, q, kv, i32(lens), 2, out, None, ws)
+        assert lib.spec_get_device_error(ws) == code, lens
+        ref, _ = oracle.paged_attention(q.double().cpu().numpy(), k.double().cpu().numpy(), v.double().cpu().numpy(),
+                                        table.cpu().numpy(), bs, lens)
+        assert np.abs(out.double().cpu().numpy() - ref).max() <= torch.finfo(TYPES[t]).eps * np.abs(ref).max() + 1e-5
