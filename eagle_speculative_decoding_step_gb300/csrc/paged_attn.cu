@@ -204,9 +204,13 @@ extern "C" spec_status spec_paged_attention(const spec_attn_desc* desc, const vo
   g.group_counters = reinterpret_cast<int*>(static_cast<char*>(ws) + kWsHeader + pa::part_bytes(sms));
   g.counters = g.group_counters + pa::group_ints(sms);
   g.ws = ws;
-  for (int b0 = 0; b0 < B; b0 += pa::kMaxB) {
+  // a launch's tiles are counted in 32 bits: fewer requests of one where every table could be full of small tiles
+  // (tables of over 2^23 tokens)
+  const long long most_tiles = (long long)kv->max_blocks * kv->block_size / k.sub + 2;
+  const int per = (int)std::min<long long>(pa::kMaxB, 0x7fffffff / most_tiles);
+  for (int b0 = 0; b0 < B; b0 += per) {
     g.b0 = b0;
-    g.B = std::min(B - b0, pa::kMaxB);
+    g.B = std::min(B - b0, per);
     g.p = pa::plan(k, d, g.B, longest, kv->block_size, sms);
     const size_t smem = (size_t)g.p.slots * g.p.slot_bytes + k.fixed(g.B);
     if (g.p.slots < 2) return SPEC_ERR_UNSUPPORTED;

@@ -120,3 +120,28 @@ def test_keys_past_the_caches_end_are_left_out_and_told(bs, t, ct):
         ref, _ = oracle.paged_attention(q.double().cpu().numpy(), k.double().cpu().numpy(), v.double().cpu().numpy(),
                                         table.cpu().numpy(), bs, lens)
         assert np.abs(out.double().cpu().numpy() - ref).max() <= torch.finfo(TYPES[t]).eps * np.abs(ref).max() + 1e-5
+
+
+def test_tables_of_half_a_billion_tokens_a_request():
+    """Blocks of 2^20 slots: a call's requests go in launches of 31 or 127, whose tiles 32 bits count at any lengths."""
+    B, bs, mb, slots = 200, 1 << 20, 512, 5000
+    g = torch.Generator(device="cuda").manual_seed(0)
+    for t in ("bf16", "f32"):
+        k, v = (torch.randn(slots, 2, 64, generator=g, device="cuda").to(TYPES[t]) for _ in range(2))
+        q = torch.randn(B, 4, 64, generator=g, device="cuda").to(TYPES[t])
+        lens = i32((np.arange(B) * 37) % slots)
+        desc = lib.make_attn_desc(4, 2, 64, t)
+        ws = torch.zeros(lib.spec_attention_workspace_bytes(desc, B), dtype=torch.uint8, device="cuda")
+        got = []
+        for size, n in ((bs, mb), (8192, 1)):
+            table = torch.full((B, n), -1, dtype=torch.int32, device="cuda")
+            table[:, 0] = 0
+            kv = lib.make_kv(dict(k=k, v=v, block_table=table, block_size=size, max_blocks=n, num_slots=slots))
+            out, lse = torch.empty_like(q), torch.empty(B, 4, device="cuda")
+            lib.spec_paged_attention(desc, q, kv, lens, B, out, lse, ws, max_len=slots)
+            assert lib.spec_get_device_error(ws) == 0
+            got.append((out, lse))
+        (a, x), (b, y) = got                                  # cut in other places: the same but for the order of the sums
+        eps = torch.finfo(TYPES[t]).eps
+        assert (a.float() - b.float()).abs().max() <= 2 * eps * b.abs().max().float() + 1e-5
+        assert torch.equal(torch.isfinite(x), torch.isfinite(y)) and (x - y).nan_to_num(0.0).abs().max() < 1e-5
