@@ -128,3 +128,33 @@ def test_scores_that_are_not_finite(t, n):
     assert torch.isfinite(out[1]).all()
     eps = torch.finfo(TYPES[t]).eps                           # the same sum in another order, rounded once each
     assert (out[1] - rest[1]).abs().max() <= eps * rest[1].abs().max() + 1e-5 and abs(lse[1] - rest_lse[1]) < 1e-5
+
+
+# ------------------------------------------------------------------ forms that few calls take
+def run_lens(t, ct, nq, nkv, hd, bs, lens, window=0):
+    g = np.random.default_rng(nq + hd + bs + window)
+    q = g.standard_normal((len(lens), nq, hd))
+    check(t, ct, bs, q, *([g.standard_normal((n, nkv, hd)) for n in lens] for _ in range(2)), *scales(ct), window=window)
+
+
+@pytest.mark.parametrize("t,ct", PAIRS)
+@pytest.mark.parametrize("nq,nkv,hd,bs", [(128, 1, 256, 16), (80, 1, 192, 16), (136, 2, 256, 1), (100, 1, 144, 24), (128, 1, 128, 16)])
+def test_more_query_tiles_than_warps(t, ct, nq, nkv, hd, bs):
+    """Over 64 queries a K/V head above 128 components (fp32: over 32, and over 64 below that): K and V are read once for
+    each split."""
+    run_lens(t, ct, nq, nkv, hd, bs, [1, 17, 40, 200])
+
+
+@pytest.mark.parametrize("t,ct", PAIRS)
+@pytest.mark.parametrize("bs", [1, 2, 3, 4, 12, 20, 100])
+def test_blocks_that_are_no_multiple_of_eight(t, ct, bs):
+    """A key a copy; block and slot of a key by shifts or by divisions."""
+    run_lens(t, ct, 8, 2, 64, bs, [1, 2, 13, 64, 129, 700])
+    run_lens(t, ct, 4, 4, 128, bs, [5, 33, 300])
+
+
+@pytest.mark.parametrize("t,ct", PAIRS)
+@pytest.mark.parametrize("bs", [1, 2, 4, 12, 8, 24, 16])
+@pytest.mark.parametrize("window", [1, 7, 50, 300])
+def test_windows_on_any_block_size(t, ct, bs, window):
+    run_lens(t, ct, 8, 2, 64, bs, [1, 6, 7, 8, 51, 299, 301, 900], window)
