@@ -24,6 +24,7 @@ import torch
 
 from . import binding as lib
 
+_LOGITS = {torch.float32: "f32", torch.bfloat16: "bf16", torch.float16: "f16"}
 _TORCH = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16, "e4m3": torch.float8_e4m3fn}
 
 
@@ -106,10 +107,17 @@ class _Select:
         self.parent, self.tok = _ints(B, W, device=device), _ints(B, W, device=device)
         self.at = 0
 
-    def __call__(self, logits, dtype):
-        a, b = self.at, 1 - self.at
-        lib.spec_beam_select(self.B, self.W, self.V, dtype, logits, self.score[a], self.done[a], self.eos, self.parent,
-                             self.tok, self.score[b], self.done[b], self.ws, ld=logits.stride(0))
+    def __call__(self, logits):
+        """logits [B * W, V] in fp32, bf16 or fp16 (copied if a row is not in one piece)."""
+        n, V, a, b = self.B * self.W, self.V, self.at, 1 - self.at
+        name = _LOGITS.get(logits.dtype)
+        if name is None or logits.numel() != n * V or logits.shape[-1] != V:
+            raise ValueError("logits are %s %s, not %s of floats" % (logits.dtype, tuple(logits.shape), (n, V)))
+        x = logits.reshape(n, V)
+        if x.stride(1) != 1 or (n > 1 and x.stride(0) < V):
+            x = x.contiguous()
+        lib.spec_beam_select(self.B, self.W, V, name, x, self.score[a], self.done[a], self.eos, self.parent, self.tok,
+                             self.score[b], self.done[b], self.ws, ld=x.stride(0) if n > 1 else V)
         self.at = b
 
     def begin(self):
@@ -120,10 +128,6 @@ class _Select:
     def finish(self, which):
         """The beams of which [B, W] select nothing more."""
         self.done[self.at] |= which
-
-
-def _dtype_name(t):
-    return next(k for k, v in _TORCH.items() if v == t.dtype)
 
 
 class Batch:
@@ -174,7 +178,7 @@ class Batch:
         for _ in range(steps):
             logits = self.feed(tok)
             self.select.finish(self.stopped[:, None])
-            self.select(logits, _dtype_name(logits))
+            self.select(logits)
             tok = torch.where(self.stopped, -1, self.select.tok[:, 0])
             out.append(tok)
         return torch.stack(out, 1)
@@ -277,7 +281,7 @@ class BeamBatch:
         pos = self.length.repeat_interleave(W)
         kvs = self.kvs[self.at]
         logits = self.model(self.tok, pos, self.cache.attend(kvs, self.slots, pos + 1, self.max_len))
-        self.select(logits, _dtype_name(logits))
+        self.select(logits)
         self.length = self.length + 1
         # a request that comes to a block border needs W more blocks
         border = self.length % bs == 0

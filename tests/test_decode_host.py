@@ -187,3 +187,36 @@ def test_a_cache_is_made_in_its_own_type(monkeypatch, dtype, kv_dtype, es):
     assert c.k.numel() * c.k.element_size() == size == c.v.numel() * c.v.element_size()
     assert max(x.numel() * x.element_size() for x in made) == size
     assert c.k.shape == (3, 400, 2, 16) and (c.k.float() == 0).all() and (c.v.float() == 0).all()
+
+
+# ------------------------------------------------------------------ layouts of the logits
+def columns(x):
+    """The same values, every second column of a wider tensor."""
+    return x.repeat_interleave(2, 1)[:, ::2]
+
+
+@pytest.mark.parametrize("name,lay", [("by_columns", lambda x: x.T.contiguous().T), ("every_second", columns),
+                                      ("part", lambda x: torch.nn.functional.pad(x, (3, 5))[:, 3:-5]),
+                                      ("one_more_axis", lambda x: x[:, None])])
+@pytest.mark.parametrize("rows", [1, 3])
+def test_logits_of_any_layout_select_the_same(name, lay, rows):
+    m = Layouts(seed=3)
+    got = [decode.Batch(f, cache_of(m), rows, 16, m.vocab).decode(ids(5, 17, 100)[:rows], 9)
+           for f in (m, lambda *a: lay(m(*a)))]
+    assert torch.equal(*got)
+
+
+def test_logits_that_all_rows_share():
+    """One row in memory for all of the batch."""
+    m = Layouts(seed=3)
+    got = [decode.Batch(lambda *a: f(m(*a)[:1]), cache_of(m), 3, 16, m.vocab).decode(ids(5, 17, 100), 4)
+           for f in (lambda x: x.expand(3, -1), lambda x: x.repeat(3, 1))]
+    assert torch.equal(*got) and (got[0] == got[0][:1]).all()
+
+
+def test_logits_of_another_shape_or_type_are_refused():
+    m = Layouts(seed=3)
+    for lay in (lambda x: x[:, :-1], lambda x: x[:1], lambda x: x.double(), lambda x: x.long()):
+        b = decode.Batch(lambda *a: lay(m(*a)), cache_of(m), 2, 16, m.vocab)
+        with pytest.raises(ValueError):
+            b.decode(ids(5, 6), 1)
