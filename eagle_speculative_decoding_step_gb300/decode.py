@@ -195,7 +195,10 @@ class Batch:
 
 class BeamBatch:
     """Beam search: W beams of each of the given prompts (host lists of token ids, not empty), up to
-    max_new new tokens."""
+    max_new new tokens.
+
+    A request that the pool has no blocks for is ``stopped`` [B]: its beams keep their scores, their
+    tokens are -1 from there on, and ``error`` says what was missing.  The others go on."""
 
     def __init__(self, model, cache, prompts, W, max_new, vocab, eos=-1):
         self.model, self.cache, self.W, self.B = model, cache, W, len(prompts)
@@ -208,6 +211,7 @@ class BeamBatch:
         owned_ld = int(whole.max()) + W + groups * W
         self.owned = _ints(B, owned_ld, device=dev, fill=-1)
         self.held = _ints(B, device=dev)                    # tokens the owned blocks have room for
+        self.stopped = torch.zeros(B, dtype=torch.bool, device=dev)
         self.want = ((self.whole + 2 * W) * bs).int()       # shared blocks, spares, the first private ones
         self.cap = int(whole.sum() + 2 * W * B) * bs
         self.slot_map, self.cu = _ints(self.cap, device=dev), _ints(B + 1, device=dev)
@@ -244,6 +248,7 @@ class BeamBatch:
         lib.spec_block_tables(self.B, c.block_size, self.owned.shape[1], c.num_blocks, self.held, self.want, self.owned,
                               self.owned, c.free, c.n_free, c.free, c.n_free, self.held, self.cu, self.slot_map, None,
                               self.cap, self.tws)
+        self.stopped = self.stopped | (self.held != self.want)
 
     def _prompts(self, prompts, n):
         """All but the last prompt token, one a step, by beam 0 of each request."""
@@ -280,16 +285,20 @@ class BeamBatch:
         W, bs = self.W, self.cache.block_size
         pos = self.length.repeat_interleave(W)
         kvs = self.kvs[self.at]
-        logits = self.model(self.tok, pos, self.cache.attend(kvs, self.slots, pos + 1, self.max_len))
+        seen = torch.where(self.stopped, 0, self.length + 1).repeat_interleave(W)
+        logits = self.model(self.tok, pos, self.cache.attend(kvs, self.slots, seen, self.max_len))
+        stopped = self.stopped[:, None]
+        self.select.finish(stopped)
         self.select(logits)
+        tok = torch.where(stopped, -1, self.select.tok)
         self.length = self.length + 1
         # a request that comes to a block border needs W more blocks
-        border = self.length % bs == 0
+        border = (self.length % bs == 0) & ~self.stopped
         need = (self.length // bs - self.whole + 1) * W + W + self.whole
         self.want = torch.where(border, torch.maximum(self.held, need * bs), self.held).int()
         self._own()
-        self._reorder(self.select.parent, self.select.tok)
-        self.tok = self.select.tok.reshape(-1).clamp(min=0)
+        self._reorder(self.select.parent, tok)
+        self.tok = tok.reshape(-1).clamp(min=0)
         self.new += 1
 
     @property

@@ -87,13 +87,22 @@ def beam_reorder(state, kv_layers, row_bytes, ws=None):
     r = oracle.beam_reorder(bs, parent.view(B, W).numpy(), tok.view(B, W).numpy(), seq_len.numpy(), prompt_blocks.numpy(),
                             owned.numpy(), table_in.view(B, W, -1).numpy(), spare_in.view(B, W).numpy(),
                             None if hist_in is None else hist_in.view(B, W, -1).numpy())
+    # a block that is missing stays missing, and nothing is copied
+    at = np.minimum(seq_len.numpy() // bs, state.max_blocks - 1)
+    for b in range(B):
+        for j in range(W):
+            src, here = table_in.view(B, W, -1)[b, int(parent.view(B, W)[b, j]), at[b]], r["table"][b, j]
+            if here[at[b]] >= 0 and seq_len[b] % bs and int(parent.view(B, W)[b, j]) != j and src < 0:
+                here[at[b]] = -1
+            if here[at[b]] < 0:
+                r["slots"][b, j] = -1
     for t, name in ((table_out, "table"), (spare_out, "spare"), (slots, "slots"), (hist_out, "hist")):
         if t is not None:
             t.copy_(torch.from_numpy(np.asarray(r[name])).view(t.shape))
     for kv in kv_layers:
         for address in (kv.k, kv.v):
             cache = _at(address, np.uint8, kv.num_slots, row_bytes)
-            for f, d, n in r["copies"]:
+            for f, d, n in (c for c in r["copies"] if min(c[:2]) >= 0):
                 cache[d * bs:d * bs + n] = cache[f * bs:f * bs + n]
 
 

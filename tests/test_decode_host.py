@@ -174,6 +174,30 @@ def test_finished_requests_make_room_for_the_others():
     assert b.decode(ids(5, 17), 16).tolist() == [alone(5, 16), alone(17, 16, eos=eos)] and b.error() == 0
 
 
+def beams_of(prompts, W, steps, blocks=200, bs=4, new=12, seed=3, eos=-1):
+    m = Layouts(seed=seed)
+    b = decode.BeamBatch(m, cache_of(m, blocks=blocks, bs=bs, rows=len(prompts) * W), prompts, W, new, m.vocab, eos)
+    for _ in range(steps):
+        b.step()
+    return b
+
+
+@pytest.mark.parametrize("eos", [-1, 190])
+def test_beams_of_a_request_that_the_pool_cannot_serve_stop_and_the_others_go_on(eos):
+    prompts, W = [[5, 9, 7], [11, 4, 8]], 2
+    first = beams_of(prompts, W, 2, eos=eos)                  # two tokens are selected until the first border
+    start = beams_of(prompts, W, 0)
+    need = start.cache.num_blocks - int(start.cache.n_free[0])
+    want = beams_of(prompts, W, 5, eos=eos)
+    b = beams_of(prompts, W, 5, blocks=need + W, eos=eos)     # there are blocks for one request more
+    assert want.error() == 0 and b.error() == cpu_library.ERR_CAPACITY and b.stopped.tolist() == [False, True]
+    assert torch.equal(b.tokens[0], want.tokens[0]) and torch.equal(b.score[0], want.score[0])
+    assert torch.equal(b.tokens[1, :, :5], first.tokens[1, :, :5]) and (b.tokens[1, :, 5:] == -1).all()
+    assert torch.equal(b.score[1], first.score[1])
+    b.release()
+    assert int(b.cache.n_free[0]) == need + W
+
+
 # ------------------------------------------------------------------ the cache's memory
 @pytest.mark.parametrize("dtype,kv_dtype,es", [("f32", None, 4), ("bf16", None, 2), ("f16", "e4m3", 1)])
 def test_a_cache_is_made_in_its_own_type(monkeypatch, dtype, kv_dtype, es):

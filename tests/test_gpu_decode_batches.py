@@ -3,6 +3,7 @@ import numpy as np
 import pytest
 import torch
 
+from eagle_speculative_decoding_step_gb300 import binding as lib
 from eagle_speculative_decoding_step_gb300 import decode
 
 pytestmark = pytest.mark.gpu
@@ -66,3 +67,26 @@ def test_finished_requests_give_their_blocks_back_and_a_batch_is_used_again():
     assert int(b.cache.n_free[0]) == 200 - 3 * (4 - len(ended))
     b.release()
     assert b.decode(ids(*FIRST[::-1]), 20).tolist() == want[::-1] and b.error() == 0
+
+
+def beams(prompts, W, steps, blocks=200, bs=8):
+    m = small()
+    b = decode.BeamBatch(m, decode.PagedCache(2, blocks, bs, m.nq, m.nkv, m.hd, dtype="f32", max_rows=W * len(prompts)), prompts, W,
+                         20, m.vocab)
+    for _ in range(steps):
+        b.step()
+    return b
+
+
+def test_beams_of_a_request_that_the_pool_cannot_serve_stop_and_the_others_go_on():
+    prompts, W = [[5, 9, 7], [11, 4, 8]], 3
+    first, want, start = beams(prompts, W, 6), beams(prompts, W, 12), beams(prompts, W, 0)
+    need = 200 - int(start.cache.n_free[0])
+    b = beams(prompts, W, 12, blocks=need + W)               # at the first border, after six tokens, there is room for one
+    assert want.error() == 0 and lib.spec_get_device_error(b.tws) == ERR_CAPACITY and b.cache.error() == 0
+    assert b.stopped.tolist() == [False, True]
+    assert torch.equal(b.tokens[0], want.tokens[0]) and torch.equal(b.score[0], want.score[0])
+    assert torch.equal(b.tokens[1, :, :9], first.tokens[1, :, :9]) and (b.tokens[1, :, 9:] == -1).all()
+    assert torch.equal(b.score[1], first.score[1])
+    b.release()
+    assert int(b.cache.n_free[0]) == need + W
