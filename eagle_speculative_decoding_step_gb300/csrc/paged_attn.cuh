@@ -506,8 +506,8 @@ template <typename T, bool F8, int HD, int NT> struct MmaMath {
           c[u][nt][2 + j] = exp2_fast(c[u][nt][2 + j] - b);
           s.l[nt * 2 + j] += c[u][nt][j] + c[u][nt][2 + j];
         }
-        // a weight enters the second product as two 16-bit parts: one alone (2^-9 of it in bf16)
-        // would cost as much as the output's own rounding.  Two bf16 parts lose 2^-18 of it; two f16 parts 2^-22, or
+        // a weight enters the second product as two 16-bit parts: one alone (2^-8 of it in bf16)
+        // would cost as much as the output's own rounding.  Two bf16 parts lose 2^-17 of it; two f16 parts 2^-23, or
         // where the lower one is subnormal 2^-25, 2^-40 of the largest weight (kBelow)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -557,9 +557,9 @@ template <typename T, bool F8, int HD, int NT> struct MmaMath {
 // their number at every step and leaves a lane with one key's NQ / 4 scores; a lane
 // takes keys and queries in an order of its own (its number's bits flipped), so that what it
 // keeps is always the first half.  Queries go in pairs through packed multiply-adds.
-// Measured: 32 requests of 2000 keys on 8 heads of 128, 32 / 64 / 128 queries 84 / 102 / 184
-// us (77 at the copy bandwidth): by the latency of a step, its multiply-adds, shuffles
-// and shared-memory reads each ~60 us of the 184.  (Lanes with a key each and queries in
+// Measured: 32 requests of 2000 keys on 8 heads of 128, 32 / 64 / 128 queries 83 / 103 / 186
+// us (77 at the copy bandwidth): a warp's step runs its multiply-adds, shuffles and
+// shared-memory reads one after another, each ~60 us of the 186 (above 8 queries two warps read the same rows).  (Lanes with a key each and queries in
 // shared memory: 64 queries 127 us; three tf32 products per product 122.)
 template <int HD, int NQ> struct F32Math {
   using In = float;
@@ -831,8 +831,8 @@ struct Walk {
 // One pass over K and V with running maxima m and sums l (log2 units): o <- o 2^(m - m') + sum p v,
 // p = 2^(s - m').  Bound by the bytes of K and V, which the ring (up to 220 KB an SM) keeps in
 // flight.  Measured, 64 requests on 8 K/V heads of 128, 4 queries each: bf16, 4000 keys 155 us (6.75
-// TB/s, the copy bandwidth), e4m3 85 (6.1 TB/s: the warps' chain from shared memory through the conversion
-// and two products); one request of 131071 keys 84 (152 pieces and their join); 4 of 256 keys 7.1 (launch and
+// TB/s, the copy bandwidth), e4m3 87 (6.0 TB/s: the warps' chain from shared memory through the conversion
+// and two products); one request of 131071 keys 85 (152 pieces and their join); 4 of 256 keys 7.3 (launch and
 // ~10 dependent steps).  A tile's values and the next tile's scores run as one stretch of
 // instructions without a branch, so that two independent chains fill each other's gaps (one after the other:
 // e4m3 98 us; 256 components 224 -> 162).

@@ -47,8 +47,8 @@ SPEC_DEV int first_above(const int* a, int n, int x) {
 // one thread only, which writes to it afterwards, and the update is safe in
 // place without a grid-wide barrier.  What all CTAs read and one of them
 // replaces (len_old, n_free_in) is written by the last CTA to have read it.
-// Bound by latency (lengths, scan, bisection, table entry, slots): 64 requests that grow by a few tokens 4.1 us,
-// 512 requests with 0.8 million new tokens 8.7 us, 1.7 of them at the copy bandwidth.
+// Bound by latency (lengths, scan, bisection, table entry, slots): 64 requests that grow by a few tokens 4.0 us,
+// 512 requests with 0.8 million new tokens 8.4 us, 1.7 of them at the copy bandwidth.
 __global__ void __launch_bounds__(kTabThreads) block_tables_kernel(const TabArgs g) {
   SPEC_TL(kTLTables);
   pdl_wait();
@@ -313,7 +313,7 @@ static bool power_of_two(float s) {
 
 // Rows to slots, bound by the bytes moved.  2^lg lanes share a row (as many as it
 // has vectors of eight elements, at most a warp), blockIdx.y picks K or V.  Measured: 32768 rows of 1024 bf16,
-// slices of a fused product, into 8 bits 27.9 us (7.2 TB/s: the last writes stay in L2), 256 rows 1.9 us.
+// slices of a fused product, into 8 bits 27.9 us (7.2 TB/s: the last writes stay in L2), 256 rows 1.8 us.
 template <typename T, typename C, bool VEC, bool EXACT>
 __global__ void __launch_bounds__(256) cache_append_kernel(const T* __restrict__ k, const T* __restrict__ v,
                                                            long long k_ld, long long v_ld,

@@ -417,7 +417,9 @@ spec_status spec_gather_rows(const void *src, int32_t n_src, int32_t row_bytes, 
 /* the cache and its slot mapping ([NEURON] "KV Cache Sharing",          */
 /* "EagleProposer": slot_mapping from the block table); these calls make */
 /* the tables, fill the cache and decode the requests that are not       */
-/* speculated on.                                                        */
+/* speculated on.  The workspaces of the block tables, the attention and */
+/* the selection keep counters: each serves calls of its own kind, of    */
+/* any sizes that it is large enough for.                                */
 
 /* Workspace of spec_block_tables: 256-byte header (error word first) and a
  * completion counter.  Zero-filled before its first use; every call leaves the
@@ -511,9 +513,9 @@ size_t spec_attention_workspace_bytes(const spec_attn_desc *desc, int32_t max_B)
  * < 2^30.  q, out, the cache and, with ld's, every row of q and out 16-byte
  * aligned (SPEC_ERR_ALIGN).
  * Sums and softmax statistics are fp32.  A softmax weight enters the product with
- * v in fp32 (F32 cache), as two bf16 parts (BF16 cache: 2^-18 of it lost) or as two
- * f16 parts (F16 and E4M3 caches: 2^-22 of it lost, or 2^-40 of the largest weight
- * where that is more).  BF16 queries on an E4M3 cache: components 2^-28 times a
+ * v in fp32 (F32 cache), as two bf16 parts (BF16 cache: 2^-17 of it lost) or as two
+ * f16 parts (F16 and E4M3 caches: 2^-23 of it lost, or 2^-40 of the largest weight
+ * where that is more).  BF16 queries on an E4M3 cache: components under 2^-28 of a
  * query's largest lose bits.
  * A score of +infinity or NaN (a K or q value that is not finite) makes its head's
  * outputs and lse not finite; one of -infinity is a weight of 0, and a row that has

@@ -9,8 +9,9 @@ With s_j the scores (natural units), M the largest, p_j = e^(s_j - lse) and o = 
   by sum p_j E_j.
 * The exponential is 2^-22 off; so is each of the factors that a running maximum's growth brings, at most one for
   every 16 keys and a few for the joins: D of a weight.
-* A weight enters the product with v as a pair of bf16 parts (2^-18 of it lost), a pair of f16 parts of 2^15 times it
-  (2^-22 of it, and 2^-25 of 2^-15 of the largest weight where the parts are subnormal) or in fp32.
+* A weight w, 2^e <= w < 2^(e+1), enters the product with v as a pair of bf16 parts (the first leaves up to 2^(e-8), of
+  which the second loses up to 2^(e-17)), a pair of f16 parts of 2^15 times it (2^(e-11), 2^(e-23); where the second is
+  subnormal 2^-25, 2^-40 of the largest weight) or in fp32.
 * A sum over the keys is added up in steps of 16 keys and two parts, each 2^-23 of what there is; then one division,
   one product, and one rounding to the output's type.
 """
@@ -35,7 +36,7 @@ def bound(q, k, v, scale, t, ct):
     n, hd = k.shape
     E = (hd + 4) * 2.0 ** -24 * scale * (np.abs(k) @ np.abs(q)) + np.abs(s) * 2.0 ** -21 + (np.abs(s) + abs(s.max())) * 2.0 ** -23
     D = (n / 16 + 12) * 1.25 * 2.0 ** -22
-    pair = {"f32": 0.0, "bf16": 2.0 ** -18}.get(ct, 2.0 ** -22)
+    pair = {"f32": 0.0, "bf16": 2.0 ** -17}.get(ct, 2.0 ** -23)
     small = 2.0 ** -40 * p.max() if ct in ("f16", "e4m3") else 0.0
     steps = (n / 8 + 20) * 2.0 ** -23
     mass = p @ np.abs(v)
