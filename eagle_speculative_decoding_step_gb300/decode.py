@@ -145,10 +145,15 @@ class Batch:
         self.length = _ints(B, device=dev)
         self.table = _ints(B, mb, device=dev, fill=-1)
         self.kvs = cache.views(self.table)
-        self.slots, self.pos, self.cu = _ints(B, device=dev), _ints(B, device=dev), _ints(B + 1, device=dev)
+        self.slots, self.pos = _ints(B + 1, device=dev), _ints(B + 1, device=dev)      # (one past the end for cu's last)
+        self.cu = _ints(B + 1, device=dev)
         self.tws = torch.zeros(lib.spec_block_tables_workspace_bytes(B), dtype=torch.uint8, device=dev)
-        self.stopped = torch.zeros(B, dtype=torch.bool, device=dev)
+        self.live, self.kept = _ints(B, device=dev, fill=1), _ints(B, device=dev, fill=1)    # takes tokens; keeps its blocks
         self.select = _Select(B, 1, vocab, eos, dev)
+
+    @property
+    def stopped(self):
+        return self.kept > self.live
 
     def resize(self, want):
         """Grow to (or give back down to) want [B] tokens by at most B new ones in all: their slots and
@@ -157,36 +162,34 @@ class Batch:
         c = self.cache
         lib.spec_block_tables(self.B, c.block_size, self.table.shape[1], c.num_blocks, self.length, want, self.table,
                               self.table, c.free, c.n_free, c.free, c.n_free, self.length, self.cu, self.slots, self.pos,
-                              self.B, self.tws)
+                              self.B + 1, self.tws)
 
     def feed(self, tok):
         """One more token of every request that can take one, tok [B] (of a row that has none: below 0);
         logits [B, V], which mean nothing in the other rows."""
-        done = self.select.done[self.select.at][:, 0] != 0
-        want = torch.where(self.stopped, self.length, torch.where(done, 0, self.length + 1))
+        want = torch.addcmul(self.live, self.length, self.kept)         # a token more; the same; none
         self.resize(want)
-        self.stopped = self.stopped | (self.length != want)
-        fed = ~(self.stopped | done)
-        slots = torch.where(fed, self.slots[self.cu[:-1].clamp(max=self.B - 1).long()], -1)
-        length = torch.where(fed, self.length, 0)
-        return self.model(tok.clamp(min=0), (length - 1).clamp(min=0),
-                          self.cache.attend(self.kvs, slots, length, self.max_len))
+        self.live = self.live * (self.length == want)
+        slots = torch.where(self.live.bool(), self.slots.index_select(0, self.cu[:-1]), -1)
+        length = self.length * self.live
+        return self.model(tok.clamp(min=0), length - self.live, self.cache.attend(self.kvs, slots, length, self.max_len))
 
     def decode(self, tok, steps):
         """Feeds tok [B] and then each step's best token: tokens [B, steps]."""
         out = []
         for _ in range(steps):
             logits = self.feed(tok)
-            self.select.finish(self.stopped[:, None])
             self.select(logits)
             tok = torch.where(self.stopped, -1, self.select.tok[:, 0])
             out.append(tok)
+            done = self.select.done[self.select.at].view(-1)
+            self.kept, self.live = (torch.addcmul(x, self.live, done, value=-1) for x in (self.kept, self.live))
         return torch.stack(out, 1)
 
     def release(self):
         """Gives all blocks back; the batch can take other requests."""
         self.resize(torch.zeros_like(self.length))
-        self.stopped = torch.zeros_like(self.stopped)
+        self.live, self.kept = torch.ones_like(self.live), torch.ones_like(self.kept)
         self.select.begin()
 
     def error(self):
@@ -283,17 +286,17 @@ class BeamBatch:
     def step(self):
         """One token a beam."""
         W, bs = self.W, self.cache.block_size
-        pos = self.length.repeat_interleave(W)
+        pos, length = self.length.repeat_interleave(W), self.length + 1
         kvs = self.kvs[self.at]
-        seen = torch.where(self.stopped, 0, self.length + 1).repeat_interleave(W)
+        seen = length.masked_fill(self.stopped, 0).repeat_interleave(W)
         logits = self.model(self.tok, pos, self.cache.attend(kvs, self.slots, seen, self.max_len))
         stopped = self.stopped[:, None]
         self.select.finish(stopped)
         self.select(logits)
         tok = torch.where(stopped, -1, self.select.tok)
-        self.length = self.length + 1
+        self.length = length
         # a request that comes to a block border needs W more blocks
-        border = (self.length % bs == 0) & ~self.stopped
+        border = (length % bs == 0) > self.stopped
         need = (self.length // bs - self.whole + 1) * W + W + self.whole
         self.want = torch.where(border, torch.maximum(self.held, need * bs), self.held).int()
         self._own()
