@@ -78,6 +78,12 @@ class BeamState(ctypes.Structure):
                                        "spare_in", "spare_out", "slots", "hist_in", "hist_out"]])
 
 
+class BlockState(ctypes.Structure):
+    _fields_ = ([(n, c_i32) for n in ["B", "block_size", "max_blocks", "num_blocks"]]
+                + [(n, c_vp) for n in ["table_in", "table_out", "len_in", "len_out", "shared_in", "shared_out", "free_in",
+                                       "free_out", "n_free_in", "n_free_out"]])
+
+
 EXPORTS = {
     # name: (restype, argtypes)
     "spec_status_string": (ctypes.c_char_p, [c_i32]),
@@ -124,6 +130,17 @@ EXPORTS = {
     "spec_beam_select": (c_i32, [c_i32, c_i32, c_i32, c_i32, c_vp, c_i64, c_vp, c_vp, c_i32, c_vp, c_vp, c_vp, c_vp,
                                  c_vp, c_size, c_vp]),
     "spec_beam_reorder": (c_i32, [ctypes.POINTER(BeamState), c_i32, ctypes.POINTER(KV), c_i32, c_vp, c_vp]),
+    "spec_chunk_attention_workspace_bytes": (c_size, [ctypes.POINTER(AttnDesc), c_i32, c_i32]),
+    "spec_chunk_attention": (c_i32, [ctypes.POINTER(AttnDesc), c_vp, c_i64, ctypes.POINTER(KV), c_vp, c_vp, c_i32, c_i32,
+                                     c_i32, c_i32, c_vp, c_i64, c_vp, c_vp, c_size, c_vp]),
+    "spec_token_logprobs_workspace_bytes": (c_size, [c_i32, c_i32, c_i32]),
+    "spec_token_logprobs": (c_i32, [c_i32, c_i32, c_i32, c_vp, c_i64, c_vp, c_i32, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp,
+                                    c_vp, c_size, c_vp]),
+    "spec_block_state_workspace_bytes": (c_size, [c_i32, c_i32]),
+    "spec_block_fork": (c_i32, [ctypes.POINTER(BlockState), c_i32, c_vp, c_vp, c_i32, ctypes.POINTER(KV), c_i32, c_vp,
+                                c_size, c_vp]),
+    "spec_block_release": (c_i32, [ctypes.POINTER(BlockState), c_vp, c_vp, c_size, c_vp]),
+    "spec_block_compact": (c_i32, [ctypes.POINTER(BlockState), c_i32, ctypes.POINTER(KV), c_i32, c_vp, c_size, c_vp]),
 }
 
 _LIB = None
@@ -230,6 +247,15 @@ def make_beam_state(B, W, block_size, max_blocks, parent, tok, seq_len, prompt_b
     ts = (parent, tok, seq_len, prompt_blocks, owned, table_in, table_out, spare_in, spare_out, slots, hist_in, hist_out)
     st = BeamState(B, W, block_size, max_blocks, owned.shape[-1],
                    hist_in.shape[-1] if hist_in is not None else 0, *[_p(t) for t in ts])
+    st._keep = ts
+    return st
+
+
+def make_block_state(block_size, table_in, table_out, len_in, len_out, shared_in, shared_out, free_in, free_out, n_free_in,
+                     n_free_out) -> BlockState:
+    """The blocks of a batch (spec_block_fork, _release, _compact); an *_out may be its *_in."""
+    ts = (table_in, table_out, len_in, len_out, shared_in, shared_out, free_in, free_out, n_free_in, n_free_out)
+    st = BlockState(table_in.shape[0], block_size, table_in.shape[1], free_in.numel(), *[_p(t) for t in ts])
     st._keep = ts
     return st
 
@@ -391,3 +417,42 @@ def spec_beam_select(B, W, V, dtype, logits, score, done, eos, parent, tok, scor
 def spec_beam_reorder(state, kv_layers, row_bytes, ws=None):
     _check(_lib().spec_beam_reorder(ctypes.byref(state), len(kv_layers), kv_layers, row_bytes, _p(ws), _stream()),
            "spec_beam_reorder")
+
+
+def spec_chunk_attention_workspace_bytes(desc, max_B, max_rows):
+    return _lib().spec_chunk_attention_workspace_bytes(ctypes.byref(desc), max_B, max_rows)
+
+
+def spec_chunk_attention(desc, q, kv, cu_rows, seq_len, B, n_rows, out, lse, ws, max_chunk=0, max_len=0, q_ld=0, out_ld=0):
+    _check(_lib().spec_chunk_attention(ctypes.byref(desc), _p(q), q_ld, ctypes.byref(kv), _p(cu_rows), _p(seq_len), B, n_rows,
+                                       max_chunk, max_len, _p(out), out_ld, _p(lse), _p(ws), ws.numel() * ws.element_size(),
+                                       _stream()), "spec_chunk_attention")
+
+
+def spec_token_logprobs_workspace_bytes(n, V, k):
+    return _lib().spec_token_logprobs_workspace_bytes(n, V, k)
+
+
+def spec_token_logprobs(n, V, dtype, logits, tok, k, logprob, rank, entropy, lse, top_ids, top_logprob, ws, ld=0):
+    _check(_lib().spec_token_logprobs(n, V, DTYPES[dtype], _p(logits), ld, _p(tok), k, _p(logprob), _p(rank), _p(entropy),
+                                      _p(lse), _p(top_ids), _p(top_logprob), _p(ws), ws.numel() * ws.element_size(),
+                                      _stream()), "spec_token_logprobs")
+
+
+def spec_block_state_workspace_bytes(B, num_blocks):
+    return _lib().spec_block_state_workspace_bytes(B, num_blocks)
+
+
+def spec_block_fork(state, n, src, dst, kv_layers, row_bytes, ws):
+    _check(_lib().spec_block_fork(ctypes.byref(state), n, _p(src), _p(dst), len(kv_layers), kv_layers, row_bytes, _p(ws),
+                                  ws.numel() * ws.element_size(), _stream()), "spec_block_fork")
+
+
+def spec_block_release(state, drop, ws):
+    _check(_lib().spec_block_release(ctypes.byref(state), _p(drop), _p(ws), ws.numel() * ws.element_size(), _stream()),
+           "spec_block_release")
+
+
+def spec_block_compact(state, kv_layers, row_bytes, ws):
+    _check(_lib().spec_block_compact(ctypes.byref(state), len(kv_layers), kv_layers, row_bytes, _p(ws),
+                                     ws.numel() * ws.element_size(), _stream()), "spec_block_compact")

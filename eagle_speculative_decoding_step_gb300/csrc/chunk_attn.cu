@@ -1,0 +1,397 @@
+// Attention of a chunk of new tokens per request over the paged cache: checks and
+// launch, and the kernel on fp32 multiply-adds.
+//
+// [NEURON] "KV Cache Sharing": the paged cache the draft layer and the target
+// share; this is a target's pass over several tokens of a request (a prompt's
+// chunk, or a verified chain's tokens).
+#include <algorithm>
+#include <cmath>
+
+#include "chunk_attn.cuh"
+
+namespace spec {
+namespace ca {
+
+// ---------------------------------------------------------------- elements
+template <typename T> struct Elem;
+template <> struct Elem<float> {
+  static SPEC_DEV float4 load4(const float* p) { return __ldg(reinterpret_cast<const float4*>(p)); }
+  static SPEC_DEV void store4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
+};
+template <> struct Elem<__nv_bfloat16> {
+  static SPEC_DEV float4 load4(const __nv_bfloat16* p) {
+    const uint2 u = __ldg(reinterpret_cast<const uint2*>(p));
+    const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.x));
+    const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.y));
+    return make_float4(a.x, a.y, b.x, b.y);
+  }
+  static SPEC_DEV void store4(__nv_bfloat16* p, float4 v) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
+    *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+  }
+};
+template <> struct Elem<__half> {
+  static SPEC_DEV float4 load4(const __half* p) {
+    const uint2 u = __ldg(reinterpret_cast<const uint2*>(p));
+    const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&u.x));
+    const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&u.y));
+    return make_float4(a.x, a.y, b.x, b.y);
+  }
+  static SPEC_DEV void store4(__half* p, float4 v) {
+    const __half2 a = __floats2half2_rn(v.x, v.y), b = __floats2half2_rn(v.z, v.w);
+    *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+  }
+};
+template <> struct Elem<__nv_fp8_e4m3> {
+  static SPEC_DEV float4 load4(const __nv_fp8_e4m3* p) {
+    const uint32_t u = __ldg(reinterpret_cast<const uint32_t*>(p));
+    const __half2 a = __half2_raw(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(u & 0xffffu), __NV_E4M3));
+    const __half2 b = __half2_raw(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(u >> 16), __NV_E4M3));
+    const float2 x = __half22float2(a), y = __half22float2(b);
+    return make_float4(x.x, x.y, y.x, y.y);
+  }
+};
+
+// ---------------------------------------------------------------- kernel on fp32 multiply-adds
+constexpr int kFmaThreads = 256, kFmaRows = 64, kFmaKeys = 64;
+constexpr int kFmaEdges = kFmaRows / kFmaKeys + 2;     // edge tiles at either end of an item's keys
+
+template <int HD> struct FmaSmem {
+  Plan plan;
+  alignas(16) float q[kFmaRows][HD + 4];
+  float kv[kFmaKeys][HD + 4];                          // keys, then values
+  float p[kFmaRows][kFmaKeys + 4];
+  int slot[kFmaKeys];                                  // cache slot of a tile's keys, -1: none
+  uint32_t poison[2 * kFmaEdges][kFmaKeys / 32];       // keys of edge tiles whose value is not finite
+  int poisoned, last;
+};
+
+// Keys of a tile -> cache slots.  A block id outside the cache, or a slot past its end, is reported and left out.
+SPEC_DEV int slot_for(const Args& g, const Item& it, int key) {
+  if (key < it.lo || key >= it.hi) return -1;
+  const long long s = slot_of(g.kv, g.b0 + it.b, key);
+  if (s < 0) report(g.ws, SPEC_ERR_DEVICE, g.b0 + it.b, key);
+  return (int)s;
+}
+
+// Bound by the multiply-add pipes (2 of 4 operands of each from shared memory, 4 x 4 outputs a thread).
+template <typename TQ, typename TK, int HD> __global__ void __launch_bounds__(kFmaThreads)
+    chunk_fma_kernel(const __grid_constant__ Args g) {
+  SPEC_TL(kTLChunkAttn);
+  constexpr int BM = kFmaRows, KT = kFmaKeys, NJ = HD / 64;
+  extern __shared__ __align__(16) uint8_t raw[];
+  FmaSmem<HD>& sm = *reinterpret_cast<FmaSmem<HD>*>(raw);
+  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+  pdl_wait();
+  pdl_trigger();
+  make_plan<BM, KT>(g, sm.plan, tid, kFmaThreads);
+  const Plan& plan = sm.plan;
+  Walk<BM, KT> walk(g, plan);
+  Item it;
+  const TK* kc = static_cast<const TK*>(g.kv.k);
+  const TK* vc = static_cast<const TK*>(g.kv.v);
+  const int units = g.hd / 4;
+  while (walk.next(it)) {
+    __syncthreads();
+    if (tid < 2 * kFmaEdges * (KT / 32)) (&sm.poison[0][0])[tid] = 0;
+    if (tid == 0) sm.poisoned = 0;
+    for (int i = tid; i < BM * (HD / 4); i += kFmaThreads) {
+      const int r = i / (HD / 4), u = i % (HD / 4);
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (r < it.rows && u < units) {
+        const int tok = (it.r0 + r) / g.G, head = it.h * g.G + (it.r0 + r) % g.G;
+        v = Elem<TQ>::load4(static_cast<const TQ*>(g.q) + (it.row0 + tok) * g.q_ld + (long long)head * g.hd + 4 * u);
+      }
+      *reinterpret_cast<float4*>(&sm.q[r][4 * u]) = v;
+    }
+    float m[4], l[4], o[4][4 * NJ];
+    int klo[4], khi[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      m[i] = -INFINITY, l[i] = 0.f;
+      keys_of(g, it, ty + 16 * i, &klo[i], &khi[i]);
+#pragma unroll
+      for (int j = 0; j < 4 * NJ; ++j) o[i][j] = 0.f;
+    }
+    for (int k = it.k0; k < it.k1; ++k) {
+      const int tile = it.tile0 + k, key0 = tile * KT;
+      const bool edge = edge_tile(g, it, tile, KT);
+      __syncthreads();
+      if (tid < KT) sm.slot[tid] = slot_for(g, it, key0 + tid);
+      __syncthreads();
+      for (int i = tid; i < KT * (HD / 4); i += kFmaThreads) {
+        const int r = i / (HD / 4), u = i % (HD / 4), s = sm.slot[r];
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (s >= 0 && u < units) v = Elem<TK>::load4(kc + ((long long)s * g.nkv + it.h) * g.hd + 4 * u);
+        *reinterpret_cast<float4*>(&sm.kv[r][4 * u]) = v;
+      }
+      __syncthreads();
+      float s[4][4] = {};
+#pragma unroll 4
+      for (int d = 0; d < HD; d += 4) {
+        float4 a[4], b[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<const float4*>(&sm.q[ty + 16 * i][d]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) b[j] = *reinterpret_cast<const float4*>(&sm.kv[tx + 16 * j][d]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            s[i][j] += a[i].x * b[j].x + a[i].y * b[j].y + a[i].z * b[j].z + a[i].w * b[j].w;
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float top = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int key = key0 + tx + 16 * j;
+          const bool seen = key >= klo[i] && key < khi[i] && sm.slot[tx + 16 * j] >= 0;
+          s[i][j] = seen ? s[i][j] * g.scale2 : -INFINITY;
+          top = fmaxf(top, s[i][j]);
+        }
+#pragma unroll
+        for (int w = 8; w > 0; w >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
+        const float now = fmaxf(m[i], top), base = base_of(now), keep = exp2_fast(base_of(m[i]) - base);
+        float sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float e = exp2_fast(s[i][j] - base);
+          sum += e;
+          sm.p[ty + 16 * i][tx + 16 * j] = e;
+        }
+#pragma unroll
+        for (int w = 8; w > 0; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
+        m[i] = now;
+        l[i] = l[i] * keep + sum;
+#pragma unroll
+        for (int j = 0; j < 4 * NJ; ++j) o[i][j] *= keep;
+      }
+      __syncthreads();
+      for (int i = tid; i < KT * (HD / 4); i += kFmaThreads) {
+        const int r = i / (HD / 4), u = i % (HD / 4), s = sm.slot[r];
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (s >= 0 && u < units) {
+          v = Elem<TK>::load4(vc + ((long long)s * g.nkv + it.h) * g.hd + 4 * u);
+          // a value that is not finite must not reach the rows that do not attend to its key (0 * inf)
+          if (edge && (not_finite(v.x) || not_finite(v.y) || not_finite(v.z) || not_finite(v.w))) {
+            atomicOr(&sm.poison[edge_slot<kFmaEdges, KT>(g, it, tile)][r / 32], 1u << (r % 32));
+            sm.poisoned = 1;
+            if (not_finite(v.x)) v.x = 0.f;
+            if (not_finite(v.y)) v.y = 0.f;
+            if (not_finite(v.z)) v.z = 0.f;
+            if (not_finite(v.w)) v.w = 0.f;
+          }
+        }
+        *reinterpret_cast<float4*>(&sm.kv[r][4 * u]) = v;
+      }
+      __syncthreads();
+#pragma unroll 4
+      for (int kk = 0; kk < KT; ++kk) {
+        float p[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) p[i] = sm.p[ty + 16 * i][kk];
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+          const float4 v = *reinterpret_cast<const float4*>(&sm.kv[kk][4 * tx + 64 * j]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            o[i][4 * j] += p[i] * v.x, o[i][4 * j + 1] += p[i] * v.y;
+            o[i][4 * j + 2] += p[i] * v.z, o[i][4 * j + 3] += p[i] * v.w;
+          }
+        }
+      }
+    }
+    __syncthreads();
+    if (sm.poisoned) {
+      for (int e = 0; e < 2 * kFmaEdges; ++e)
+        for (int w = 0; w < KT / 32; ++w)
+          for (uint32_t bits = sm.poison[e][w]; bits; bits &= bits - 1) {
+            const int key = edge_tile_of<kFmaEdges, KT>(g, it, e) * KT + 32 * w + __ffs(bits) - 1;
+            const long long s = slot_of(g.kv, g.b0 + it.b, key);
+            for (int i = 0; i < 4; ++i) {
+              if (key < klo[i] || key >= khi[i]) continue;
+              for (int j = 0; j < NJ; ++j) {
+                if (4 * tx + 64 * j >= g.hd) continue;
+                const float4 v = Elem<TK>::load4(vc + (s * g.nkv + it.h) * g.hd + 4 * tx + 64 * j);
+                const float x[4] = {v.x, v.y, v.z, v.w};
+                for (int c = 0; c < 4; ++c)
+                  if (not_finite(x[c])) o[i][4 * j + c] = NAN;
+              }
+            }
+          }
+    }
+    const Pieces pc(plan, it);
+    if (pc.c0 != pc.c1) {
+      const size_t piece = piece_floats(BM, g.hd);
+      float* mine = g.part + pc.slot(plan, it, blockIdx.x) * piece;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = ty + 16 * i;
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+          if (4 * tx + 64 * j < g.hd)
+            *reinterpret_cast<float4*>(mine + ((size_t)(tx + 16 * j) * BM + r) * 4) =
+                make_float4(o[i][4 * j], o[i][4 * j + 1], o[i][4 * j + 2], o[i][4 * j + 3]);
+        if (tx == 0) mine[(size_t)BM * g.hd + r] = m[i], mine[(size_t)BM * (g.hd + 1) + r] = l[i];
+      }
+      __threadfence();
+      __syncthreads();
+      if (tid == 0) {
+        int* counter = g.counters + (long long)it.h * plan.pairs[g.B] + plan.pairs[it.b] + it.t;
+        const int before = atomicAdd(counter, 1);
+        sm.last = before == pc.c1 - pc.c0;
+        if (sm.last) *counter = 0;
+      }
+      __syncthreads();
+      if (!sm.last) continue;
+      __threadfence();
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        m[i] = -INFINITY, l[i] = 0.f;
+#pragma unroll
+        for (int j = 0; j < 4 * NJ; ++j) o[i][j] = 0.f;
+      }
+      for (int c = pc.c0; c <= pc.c1; ++c) {
+        const float* x = g.part + pc.slot(plan, it, c) * piece;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = ty + 16 * i;
+          const float mc = __ldcg(x + (size_t)BM * g.hd + r), lc = __ldcg(x + (size_t)BM * (g.hd + 1) + r);
+          const float now = fmaxf(m[i], mc), base = base_of(now);
+          const float a = exp2_fast(base_of(m[i]) - base), b = exp2_fast(base_of(mc) - base);
+          m[i] = now;
+          l[i] = l[i] * a + lc * b;
+#pragma unroll
+          for (int j = 0; j < NJ; ++j) {
+            if (4 * tx + 64 * j >= g.hd) continue;
+            const float4 v = __ldcg(reinterpret_cast<const float4*>(x + ((size_t)(tx + 16 * j) * BM + r) * 4));
+            o[i][4 * j] = o[i][4 * j] * a + v.x * b, o[i][4 * j + 1] = o[i][4 * j + 1] * a + v.y * b;
+            o[i][4 * j + 2] = o[i][4 * j + 2] * a + v.z * b, o[i][4 * j + 3] = o[i][4 * j + 3] * a + v.w * b;
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = ty + 16 * i;
+      if (r >= it.rows) continue;
+      const int tok = (it.r0 + r) / g.G, head = it.h * g.G + (it.r0 + r) % g.G;
+      // l = 0: no key; a NaN stays one
+      const float inv = l[i] == 0.f ? 0.f : g.v_scale / l[i];
+      TQ* dst = static_cast<TQ*>(g.out) + (it.row0 + tok) * g.out_ld + (long long)head * g.hd;
+#pragma unroll
+      for (int j = 0; j < NJ; ++j)
+        if (4 * tx + 64 * j < g.hd)
+          Elem<TQ>::store4(dst + 4 * tx + 64 * j,
+                           make_float4(o[i][4 * j] * inv, o[i][4 * j + 1] * inv, o[i][4 * j + 2] * inv, o[i][4 * j + 3] * inv));
+      if (g.lse && tx == 0)
+        g.lse[(long long)(it.row0 + tok) * g.nq + head] = l[i] == 0.f ? -INFINITY : (m[i] + log2f(l[i])) * kLn2;
+    }
+  }
+}
+
+// ---------------------------------------------------------------- dispatch
+struct Kernel {
+  void (*fn)(Args);
+  int rows, threads, per_sm;   // packed rows of an item; CTAs an SM
+  size_t smem;
+};
+
+template <typename TQ, typename TK, int HD> static Kernel fma_of() {
+  return Kernel{chunk_fma_kernel<TQ, TK, HD>, kFmaRows, kFmaThreads, HD > 128 ? 1 : 2, sizeof(FmaSmem<HD>)};
+}
+template <typename TQ, typename TK> static Kernel fma_for(int hd) {
+  return hd <= 64 ? fma_of<TQ, TK, 64>() : hd <= 128 ? fma_of<TQ, TK, 128>() : fma_of<TQ, TK, 256>();
+}
+
+static Kernel kernel_for(const spec_attn_desc& d) {
+  const bool e4m3 = d.kv_dtype == SPEC_DTYPE_E4M3;
+  if (d.dtype == SPEC_DTYPE_F32) return fma_for<float, float>(d.head_dim);
+  if (d.dtype == SPEC_DTYPE_BF16)
+    return e4m3 ? fma_for<__nv_bfloat16, __nv_fp8_e4m3>(d.head_dim) : fma_for<__nv_bfloat16, __nv_bfloat16>(d.head_dim);
+  return e4m3 ? fma_for<__half, __nv_fp8_e4m3>(d.head_dim) : fma_for<__half, __half>(d.head_dim);
+}
+
+static bool check(const spec_attn_desc* d) {
+  return d && d->n_q_heads > 0 && d->n_kv_heads > 0 && d->n_q_heads % d->n_kv_heads == 0 &&
+         d->n_q_heads / d->n_kv_heads <= 128 && d->head_dim > 0 && d->head_dim % 16 == 0 && d->head_dim <= 256 &&
+         d->window >= 0;
+}
+static bool check_types(const spec_attn_desc& d) {
+  if (d.dtype < SPEC_DTYPE_F32 || d.dtype > SPEC_DTYPE_F16) return false;
+  return d.kv_dtype == d.dtype || (d.kv_dtype == SPEC_DTYPE_E4M3 && d.dtype != SPEC_DTYPE_F32);
+}
+
+// Pieces (two a CTA) come first, at the size of the largest kernel's, so that the counters lie in the same place for every call
+// that shares the workspace and stay zero between calls.
+static size_t part_bytes(int sms) { return align_up((size_t)sms * 2 * kPieceFloats * 4, 256); }
+
+// Counters: an item has at least 64 packed rows, or ends its request; two of one with 256 rows.
+static long long most_items(const spec_attn_desc& d, long long B, long long rows) {
+  return d.n_kv_heads * (2 * B + (rows * (d.n_q_heads / d.n_kv_heads) + kFmaRows - 1) / kFmaRows);
+}
+
+static spec_status launch_fma(const spec_attn_desc& d, const Args& g, int sms, cudaStream_t st) {
+  const Kernel k = kernel_for(d);
+  if (cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)k.smem) != cudaSuccess) return SPEC_ERR_CUDA;
+  return cuda_status(launch_pdl(k.fn, dim3(sms * k.per_sm), dim3(k.threads), k.smem, st, g));
+}
+
+}  // namespace ca
+}  // namespace spec
+
+using namespace spec;
+
+extern "C" size_t spec_chunk_attention_workspace_bytes(const spec_attn_desc* desc, int32_t max_B, int32_t max_rows) {
+  if (!ca::check(desc) || !ca::check_types(*desc) || max_B <= 0 || max_rows <= 0 ||
+      (long long)max_rows * desc->n_q_heads >= (1ll << 31))
+    return 0;
+  return kWsHeader + ca::part_bytes(sm_count()) + align_up((size_t)ca::most_items(*desc, max_B, max_rows) * 4, 256);
+}
+
+extern "C" spec_status spec_chunk_attention(const spec_attn_desc* desc, const void* q, int64_t q_ld, const spec_kv* kv,
+                                            const int32_t* cu_rows, const int32_t* seq_len, int32_t B, int32_t n_rows,
+                                            int32_t max_chunk, int32_t max_len, void* out, int64_t out_ld, float* lse,
+                                            void* ws, size_t ws_bytes, spec_stream_t stream) {
+  if (!desc || !q || !kv || !kv->k || !kv->v || !kv->block_table || !cu_rows || !seq_len || !out) return SPEC_ERR_ARG;
+  const spec_attn_desc& d = *desc;
+  if (!ca::check(desc) || B <= 0 || n_rows <= 0 || max_chunk < 0 || max_len < 0 || kv->block_size <= 0 ||
+      kv->max_blocks <= 0 || kv->num_slots <= 0 || (long long)kv->max_blocks * kv->block_size >= (1ll << 30))
+    return SPEC_ERR_SHAPE;
+  if (!ca::check_types(d)) return SPEC_ERR_UNSUPPORTED;
+  const bool e4m3 = d.kv_dtype == SPEC_DTYPE_E4M3;
+  if (!(d.scale >= 0) || std::isinf(d.scale) ||
+      (e4m3 && !(d.k_scale > 0 && d.v_scale > 0 && std::isfinite(d.k_scale) && std::isfinite(d.v_scale))))
+    return SPEC_ERR_ARG;
+  const long long width = (long long)d.n_q_heads * d.head_dim;
+  if (q_ld == 0) q_ld = width;
+  if (out_ld == 0) out_ld = width;
+  if (q_ld < width || out_ld < width) return SPEC_ERR_SHAPE;
+  if ((long long)n_rows * d.n_q_heads >= (1ll << 31)) return SPEC_ERR_CAPACITY;
+  const int es = d.dtype == SPEC_DTYPE_F32 ? 4 : 2;
+  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(kv->k, 16) || !aligned(kv->v, 16) || q_ld * es % 16 ||
+      out_ld * es % 16)
+    return SPEC_ERR_ALIGN;
+  if (!ws || !aligned(ws, 256) || ws_bytes < spec_chunk_attention_workspace_bytes(desc, B, n_rows)) return SPEC_ERR_WORKSPACE;
+  const int sms = sm_count();
+  ca::Args g{};
+  g.kv = *kv, g.q = q, g.out = out, g.lse = lse, g.cu = cu_rows, g.seq_len = seq_len, g.q_ld = q_ld, g.out_ld = out_ld;
+  g.n_rows = n_rows, g.nq = d.n_q_heads, g.nkv = d.n_kv_heads, g.G = d.n_q_heads / d.n_kv_heads, g.hd = d.head_dim;
+  g.window = d.window < kv->max_blocks * kv->block_size ? d.window : 0, g.min_tiles = 1;
+  g.scale2 = (d.scale > 0 ? d.scale : 1.f / sqrtf((float)d.head_dim)) * (e4m3 ? d.k_scale : 1.f) * ca::kLog2e;
+  g.v_scale = e4m3 ? d.v_scale : 1.f;
+  g.part = reinterpret_cast<float*>(static_cast<char*>(ws) + kWsHeader);
+  g.counters = reinterpret_cast<int*>(static_cast<char*>(ws) + kWsHeader + ca::part_bytes(sms));
+  g.ws = ws;
+  for (int b0 = 0; b0 < B; b0 += ca::kMaxB) {
+    g.b0 = b0;
+    g.B = std::min(B - b0, ca::kMaxB);
+    const spec_status r = ca::launch_fma(d, g, sms, stream);
+    if (r != SPEC_OK) return r;
+  }
+  return last_launch();
+}
+
+// per-unit log setter of the instrumented build (no-op otherwise)
+SPEC_TL_SETTER(chunk_attn)

@@ -602,6 +602,137 @@ typedef struct {
 spec_status spec_beam_reorder(const spec_beam_state *st, int32_t n_layers, const spec_kv *kv, int32_t row_bytes,
                               void *ws, spec_stream_t stream);
 
+/* ------------------------------------------------------------------ */
+/* Prompts and samples over the paged cache: attention of a chunk of new */
+/* tokens, log-probabilities, blocks that several requests share.        */
+
+/* Workspace of spec_chunk_attention for at most max_B requests and max_rows new
+ * tokens: header, partial results, counters.  Zero-filled before its first use;
+ * every call leaves the counters at zero.  Calls that share a workspace must not
+ * overlap on the GPU; each workspace serves calls of its own kind, of any sizes
+ * that it is large enough for.  0 for an invalid descriptor. */
+size_t spec_chunk_attention_workspace_bytes(const spec_attn_desc *desc, int32_t max_B, int32_t max_rows);
+
+/* Attention of a chunk of new tokens per request over the paged cache (a target's
+ * pass over a prompt's chunk, or over the tokens of a verified chain): the batch's
+ * new tokens are rows of q, those of request b rows cu_rows[b] .. cu_rows[b + 1]
+ * (spec_block_tables' cu_new).  With n of them, row i is the token at cache index
+ * p = seq_len[b] - n + i (its own K/V row is appended before the call) and attends,
+ * with query head h and kv head h / (n_q_heads / n_kv_heads), to the keys at cache
+ * indices max(0, p - window + 1) .. p:
+ *   s_j = scale * q . k_j;  lse = log(sum_j exp(s_j));
+ *   out = sum_j exp(s_j - lse) v_j.
+ * A row without keys (p < 0: a request that holds fewer tokens than it has rows)
+ * gets out = 0 and lse = -infinity.  A request may have no rows.  Rows from
+ * cu_rows[B] on are left as they are.
+ * q, out [n_rows, n_q_heads, head_dim] in desc->dtype, q_ld / out_ld elements from
+ * one row to the next (0 = n_q_heads * head_dim); lse [n_rows, n_q_heads] fp32 or
+ * NULL.  cu_rows [B + 1], seq_len [B].  max_chunk and max_len: upper bounds of a
+ * request's new tokens and of seq_len, or 0 if unknown; they only choose how work
+ * is laid out.  Any block_size; max_blocks * block_size < 2^30, n_rows * n_q_heads
+ * < 2^31.  q, out, the cache and, with ld's, every row of q and out 16-byte aligned
+ * (SPEC_ERR_ALIGN).  out does not overlap q or the cache.
+ * A score of +infinity or NaN, or one of -infinity, and a V value that is not finite
+ * act as in spec_paged_attention, on the rows that attend to their key; other rows
+ * are as they would be without.
+ * Error word: SPEC_ERR_DEVICE for cu_rows that fall or leave [0, n_rows], a seq_len
+ * outside [0, max_blocks * block_size] (both clamped) or a slot out of range (such
+ * keys are left out). */
+spec_status spec_chunk_attention(const spec_attn_desc *desc, const void *q, int64_t q_ld, const spec_kv *kv,
+                                 const int32_t *cu_rows, const int32_t *seq_len, int32_t B, int32_t n_rows,
+                                 int32_t max_chunk, int32_t max_len, void *out, int64_t out_ld, float *lse,
+                                 void *ws, size_t ws_bytes, spec_stream_t stream);
+
+/* Workspace of spec_token_logprobs for at most n rows of V logits with k
+ * alternatives: header, counters, per-chunk records.  Zero-filled before its first
+ * use; every call leaves the counters at zero.  Calls that share a workspace must
+ * not overlap on the GPU; it serves every call with no more rows, logits and
+ * alternatives, of any type. */
+size_t spec_token_logprobs_workspace_bytes(int32_t n, int32_t V, int32_t k);
+
+/* Log-probabilities of given tokens under their rows' logits, with rank, entropy
+ * and the k best alternatives, in one pass.  logits [n, V] in dtype (F32, BF16 or
+ * F16), ld elements from one row to the next (0 = V), rows of any alignment.  A
+ * logit that is not finite is masked: its probability is 0.  Per row, over the
+ * finite logits x:
+ *   lse = log(sum exp(x));   entropy = lse - sum p x, p = exp(x - lse);
+ *   logprob = x[tok] - lse;
+ *   rank = the tokens before tok: larger logits, and equal ones with a smaller id;
+ *   top_ids / top_logprob [n, k]: the k first in that order, -1 and -infinity past
+ *   the finite ones.
+ * tok [n]: -1 for none; a row without a token, or whose token is masked, gets
+ * logprob = -infinity and rank = -1 (a token outside the vocabulary also sets
+ * SPEC_ERR_DEVICE).  A row without a finite logit has lse = -infinity, entropy 0.
+ * Each of logprob, rank, entropy and lse may be NULL; tok may be if logprob and rank
+ * are.  0 <= k <= 32 (0: top_ids and top_logprob are not written), V <= 2^20
+ * (SPEC_ERR_CAPACITY).  Sums are fp32; logits are compared as they are. */
+spec_status spec_token_logprobs(int32_t n, int32_t V, int32_t dtype, const void *logits, int64_t ld,
+                                const int32_t *tok, int32_t k, float *logprob, int32_t *rank, float *entropy,
+                                float *lse, int32_t *top_ids, float *top_logprob,
+                                void *ws, size_t ws_bytes, spec_stream_t stream);
+
+/* The blocks of a batch whose requests may share them.  Row b of the table holds
+ * ceil(len[b] / block_size) blocks; a block that several rows hold has
+ * shared[id] = the holders beyond the first, every other 0.  So spec_block_tables
+ * grows such rows as any other (a block off the pool has one holder); it does not
+ * shrink them: spec_block_release does.  Only full blocks are shared.
+ * Each *_out may be its *_in (an update in place) or must not overlap any input. */
+typedef struct {
+  int32_t B;
+  int32_t block_size;
+  int32_t max_blocks;             /* entries of a table row */
+  int32_t num_blocks;             /* ids are 0 <= id < num_blocks */
+  const int32_t *table_in;        /* [B, max_blocks] */
+  int32_t *table_out;
+  const int32_t *len_in;          /* [B] tokens a row holds */
+  int32_t *len_out;
+  const int32_t *shared_in;       /* [num_blocks] */
+  int32_t *shared_out;
+  const int32_t *free_in;         /* [num_blocks] the pool: free ids, -1 past its end */
+  int32_t *free_out;
+  const int32_t *n_free_in;       /* [1] */
+  int32_t *n_free_out;
+} spec_block_state;
+
+/* Workspace of the three calls below (header and scratch; nothing in it is kept
+ * between calls).  Calls that share a workspace must not overlap on the GPU. */
+size_t spec_block_state_workspace_bytes(int32_t B, int32_t num_blocks);
+
+/* Forks requests: row dst[i] (empty) becomes a copy of row src[i], i < n, both as
+ * they are before the call.  Full blocks are held once more (shared + 1).  A last,
+ * partial block of r slots is copied: a block is taken off the top of the pool (the
+ * i-th taken, in the order of the forks, is free_in[n_free_in - 1 - i]) and gets its
+ * r slots in every layer.  Forks that need a block are served in their order until
+ * the pool is empty; one that is not served leaves its row empty (SPEC_ERR_CAPACITY).
+ * table_out's entries past the row's blocks are -1.  kv: n_layers descriptors
+ * (1 .. 64), host memory, of st->block_size and at least num_blocks blocks;
+ * row_bytes: bytes of one slot of k (and of v) in each; block tables in kv are not
+ * read.  1 <= n <= B <= 8192.  Error word: SPEC_ERR_DEVICE for a row outside [0, B),
+ * a dst that is not empty or that an earlier fork named, a length out of range (these
+ * forks are refused, without a block), or a block id out of range (its entry
+ * becomes -1, nothing is copied for it). */
+spec_status spec_block_fork(const spec_block_state *st, int32_t n, const int32_t *src, const int32_t *dst,
+                            int32_t n_layers, const spec_kv *kv, int32_t row_bytes,
+                            void *ws, size_t ws_bytes, spec_stream_t stream);
+
+/* Releases rows: every block of a row with drop[b] != 0 loses a holder, and goes to
+ * the pool when it has none left (on top, in the order of the last entries that let
+ * go of them: row, then block order).  The row becomes empty, its table entries -1.
+ * Error word: SPEC_ERR_DEVICE for a length out of range (the row is left as it is), a
+ * block id out of range (skipped), or a block that more rows let go of than hold it. */
+spec_status spec_block_release(const spec_block_state *st, const int32_t *drop, void *ws, size_t ws_bytes,
+                               spec_stream_t stream);
+
+/* Compacts the cache: with U blocks in use, those with ids of U and over move to the
+ * unused ids below U (the smallest to the smallest, and so on), with their slots in
+ * every layer; tables and shared follow; the pool becomes num_blocks - 1 down to U.
+ * Entries past a row's blocks become -1.  All rows that hold blocks of the pool must
+ * be in the table: if U + n_free_in is not num_blocks (SPEC_ERR_CAPACITY), or a
+ * length or block id is out of range (SPEC_ERR_DEVICE), nothing moves.  kv and
+ * row_bytes as in spec_block_fork. */
+spec_status spec_block_compact(const spec_block_state *st, int32_t n_layers, const spec_kv *kv, int32_t row_bytes,
+                               void *ws, size_t ws_bytes, spec_stream_t stream);
+
 /* Greedy verification without caller-provided scratch.  The paper has no
  * counterpart: this entry point exists for callers that cannot allocate device
  * memory -- a host framework that owns every device buffer and passes only
