@@ -7,52 +7,14 @@
 #include <algorithm>
 #include <cmath>
 
-#include "chunk_attn.cuh"
+#include "chunk_attn_tc.cuh"
 
 namespace spec {
 namespace ca {
 
-// ---------------------------------------------------------------- elements
-template <typename T> struct Elem;
-template <> struct Elem<float> {
-  static SPEC_DEV float4 load4(const float* p) { return __ldg(reinterpret_cast<const float4*>(p)); }
-  static SPEC_DEV void store4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
-};
-template <> struct Elem<__nv_bfloat16> {
-  static SPEC_DEV float4 load4(const __nv_bfloat16* p) {
-    const uint2 u = __ldg(reinterpret_cast<const uint2*>(p));
-    const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.x));
-    const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.y));
-    return make_float4(a.x, a.y, b.x, b.y);
-  }
-  static SPEC_DEV void store4(__nv_bfloat16* p, float4 v) {
-    const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
-    *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
-  }
-};
-template <> struct Elem<__half> {
-  static SPEC_DEV float4 load4(const __half* p) {
-    const uint2 u = __ldg(reinterpret_cast<const uint2*>(p));
-    const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&u.x));
-    const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&u.y));
-    return make_float4(a.x, a.y, b.x, b.y);
-  }
-  static SPEC_DEV void store4(__half* p, float4 v) {
-    const __half2 a = __floats2half2_rn(v.x, v.y), b = __floats2half2_rn(v.z, v.w);
-    *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
-  }
-};
-template <> struct Elem<__nv_fp8_e4m3> {
-  static SPEC_DEV float4 load4(const __nv_fp8_e4m3* p) {
-    const uint32_t u = __ldg(reinterpret_cast<const uint32_t*>(p));
-    const __half2 a = __half2_raw(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(u & 0xffffu), __NV_E4M3));
-    const __half2 b = __half2_raw(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(u >> 16), __NV_E4M3));
-    const float2 x = __half22float2(a), y = __half22float2(b);
-    return make_float4(x.x, x.y, y.x, y.y);
-  }
-};
-
 // ---------------------------------------------------------------- kernel on fp32 multiply-adds
+SPEC_DEV float4 load4(const float* p) { return __ldg(reinterpret_cast<const float4*>(p)); }
+
 constexpr int kFmaThreads = 256, kFmaRows = 64, kFmaKeys = 64;
 constexpr int kFmaEdges = kFmaRows / kFmaKeys + 2;     // edge tiles at either end of an item's keys
 
@@ -75,7 +37,7 @@ SPEC_DEV int slot_for(const Args& g, const Item& it, int key) {
 }
 
 // Bound by the multiply-add pipes (2 of 4 operands of each from shared memory, 4 x 4 outputs a thread).
-template <typename TQ, typename TK, int HD> __global__ void __launch_bounds__(kFmaThreads)
+template <int HD> __global__ void __launch_bounds__(kFmaThreads)
     chunk_fma_kernel(const __grid_constant__ Args g) {
   SPEC_TL(kTLChunkAttn);
   constexpr int BM = kFmaRows, KT = kFmaKeys, NJ = HD / 64;
@@ -88,8 +50,8 @@ template <typename TQ, typename TK, int HD> __global__ void __launch_bounds__(kF
   const Plan& plan = sm.plan;
   Walk<BM, KT> walk(g, plan);
   Item it;
-  const TK* kc = static_cast<const TK*>(g.kv.k);
-  const TK* vc = static_cast<const TK*>(g.kv.v);
+  const float* kc = static_cast<const float*>(g.kv.k);
+  const float* vc = static_cast<const float*>(g.kv.v);
   const int units = g.hd / 4;
   while (walk.next(it)) {
     __syncthreads();
@@ -100,7 +62,7 @@ template <typename TQ, typename TK, int HD> __global__ void __launch_bounds__(kF
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
       if (r < it.rows && u < units) {
         const int tok = (it.r0 + r) / g.G, head = it.h * g.G + (it.r0 + r) % g.G;
-        v = Elem<TQ>::load4(static_cast<const TQ*>(g.q) + (it.row0 + tok) * g.q_ld + (long long)head * g.hd + 4 * u);
+        v = load4(static_cast<const float*>(g.q) + (it.row0 + tok) * g.q_ld + (long long)head * g.hd + 4 * u);
       }
       *reinterpret_cast<float4*>(&sm.q[r][4 * u]) = v;
     }
@@ -122,7 +84,7 @@ template <typename TQ, typename TK, int HD> __global__ void __launch_bounds__(kF
       for (int i = tid; i < KT * (HD / 4); i += kFmaThreads) {
         const int r = i / (HD / 4), u = i % (HD / 4), s = sm.slot[r];
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (s >= 0 && u < units) v = Elem<TK>::load4(kc + ((long long)s * g.nkv + it.h) * g.hd + 4 * u);
+        if (s >= 0 && u < units) v = load4(kc + ((long long)s * g.nkv + it.h) * g.hd + 4 * u);
         *reinterpret_cast<float4*>(&sm.kv[r][4 * u]) = v;
       }
       __syncthreads();
@@ -172,7 +134,7 @@ template <typename TQ, typename TK, int HD> __global__ void __launch_bounds__(kF
         const int r = i / (HD / 4), u = i % (HD / 4), s = sm.slot[r];
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
         if (s >= 0 && u < units) {
-          v = Elem<TK>::load4(vc + ((long long)s * g.nkv + it.h) * g.hd + 4 * u);
+          v = load4(vc + ((long long)s * g.nkv + it.h) * g.hd + 4 * u);
           // a value that is not finite must not reach the rows that do not attend to its key (0 * inf)
           if (edge && (not_finite(v.x) || not_finite(v.y) || not_finite(v.z) || not_finite(v.w))) {
             atomicOr(&sm.poison[edge_slot<kFmaEdges, KT>(g, it, tile)][r / 32], 1u << (r % 32));
@@ -213,7 +175,7 @@ template <typename TQ, typename TK, int HD> __global__ void __launch_bounds__(kF
               if (key < klo[i] || key >= khi[i]) continue;
               for (int j = 0; j < NJ; ++j) {
                 if (4 * tx + 64 * j >= g.hd) continue;
-                const float4 v = Elem<TK>::load4(vc + (s * g.nkv + it.h) * g.hd + 4 * tx + 64 * j);
+                const float4 v = load4(vc + (s * g.nkv + it.h) * g.hd + 4 * tx + 64 * j);
                 const float x[4] = {v.x, v.y, v.z, v.w};
                 for (int c = 0; c < 4; ++c)
                   if (not_finite(x[c])) o[i][4 * j + c] = NAN;
@@ -279,12 +241,12 @@ template <typename TQ, typename TK, int HD> __global__ void __launch_bounds__(kF
       const int tok = (it.r0 + r) / g.G, head = it.h * g.G + (it.r0 + r) % g.G;
       // l = 0: no key; a NaN stays one
       const float inv = l[i] == 0.f ? 0.f : g.v_scale / l[i];
-      TQ* dst = static_cast<TQ*>(g.out) + (it.row0 + tok) * g.out_ld + (long long)head * g.hd;
+      float* dst = static_cast<float*>(g.out) + (it.row0 + tok) * g.out_ld + (long long)head * g.hd;
 #pragma unroll
       for (int j = 0; j < NJ; ++j)
         if (4 * tx + 64 * j < g.hd)
-          Elem<TQ>::store4(dst + 4 * tx + 64 * j,
-                           make_float4(o[i][4 * j] * inv, o[i][4 * j + 1] * inv, o[i][4 * j + 2] * inv, o[i][4 * j + 3] * inv));
+          *reinterpret_cast<float4*>(dst + 4 * tx + 64 * j) =
+              make_float4(o[i][4 * j] * inv, o[i][4 * j + 1] * inv, o[i][4 * j + 2] * inv, o[i][4 * j + 3] * inv);
       if (g.lse && tx == 0)
         g.lse[(long long)(it.row0 + tok) * g.nq + head] = l[i] == 0.f ? -INFINITY : (m[i] + log2f(l[i])) * kLn2;
     }
@@ -298,19 +260,11 @@ struct Kernel {
   size_t smem;
 };
 
-template <typename TQ, typename TK, int HD> static Kernel fma_of() {
-  return Kernel{chunk_fma_kernel<TQ, TK, HD>, kFmaRows, kFmaThreads, HD > 128 ? 1 : 2, sizeof(FmaSmem<HD>)};
+template <int HD> static Kernel fma_of() {
+  return Kernel{chunk_fma_kernel<HD>, kFmaRows, kFmaThreads, HD > 128 ? 1 : 2, sizeof(FmaSmem<HD>)};
 }
-template <typename TQ, typename TK> static Kernel fma_for(int hd) {
-  return hd <= 64 ? fma_of<TQ, TK, 64>() : hd <= 128 ? fma_of<TQ, TK, 128>() : fma_of<TQ, TK, 256>();
-}
-
-static Kernel kernel_for(const spec_attn_desc& d) {
-  const bool e4m3 = d.kv_dtype == SPEC_DTYPE_E4M3;
-  if (d.dtype == SPEC_DTYPE_F32) return fma_for<float, float>(d.head_dim);
-  if (d.dtype == SPEC_DTYPE_BF16)
-    return e4m3 ? fma_for<__nv_bfloat16, __nv_fp8_e4m3>(d.head_dim) : fma_for<__nv_bfloat16, __nv_bfloat16>(d.head_dim);
-  return e4m3 ? fma_for<__half, __nv_fp8_e4m3>(d.head_dim) : fma_for<__half, __half>(d.head_dim);
+static Kernel fma_for(int hd) {
+  return hd <= 64 ? fma_of<64>() : hd <= 128 ? fma_of<128>() : fma_of<256>();
 }
 
 static bool check(const spec_attn_desc* d) {
@@ -332,10 +286,30 @@ static long long most_items(const spec_attn_desc& d, long long B, long long rows
   return d.n_kv_heads * (2 * B + (rows * (d.n_q_heads / d.n_kv_heads) + kFmaRows - 1) / kFmaRows);
 }
 
+// Both sides measured: see the table at the modes.
+static int mode_for(const spec_attn_desc& d, int longest) {
+  if (d.head_dim > 128) return kWide;
+  return (long long)longest * (d.n_q_heads / d.n_kv_heads) <= 128 ? kOneQ : kTwoQ;
+}
+
 static spec_status launch_fma(const spec_attn_desc& d, const Args& g, int sms, cudaStream_t st) {
-  const Kernel k = kernel_for(d);
+  const Kernel k = fma_for(d.head_dim);
   if (cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)k.smem) != cudaSuccess) return SPEC_ERR_CUDA;
   return cuda_status(launch_pdl(k.fn, dim3(sms * k.per_sm), dim3(k.threads), k.smem, st, g));
+}
+
+// always the same limit: another thread may be launching the same kernel with another head size
+constexpr int kTcSmem = 208 * 1024;
+
+static spec_status launch_tc(const spec_attn_desc& d, const Args& g, int longest, int sms, cudaStream_t st) {
+  const bool f8 = d.kv_dtype == SPEC_DTYPE_E4M3;
+  const int mode = mode_for(d, longest);
+  TcArgs a;
+  a.g = g;
+  a.l = mode == kTwoQ ? layout<kTwoQ>(d.head_dim, f8) : mode == kOneQ ? layout<kOneQ>(d.head_dim, f8) : layout<kWide>(d.head_dim, f8);
+  const TcFn fn = d.dtype == SPEC_DTYPE_BF16 ? tc_kernel_bf16(f8, mode) : tc_kernel_f16(f8, mode);
+  if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kTcSmem) != cudaSuccess) return SPEC_ERR_CUDA;
+  return cuda_status(launch_pdl(fn, dim3(sms), dim3(kTcThreads), a.l.smem, st, a));
 }
 
 }  // namespace ca
@@ -375,6 +349,7 @@ extern "C" spec_status spec_chunk_attention(const spec_attn_desc* desc, const vo
     return SPEC_ERR_ALIGN;
   if (!ws || !aligned(ws, 256) || ws_bytes < spec_chunk_attention_workspace_bytes(desc, B, n_rows)) return SPEC_ERR_WORKSPACE;
   const int sms = sm_count();
+  const int longest = max_chunk > 0 ? std::min(max_chunk, n_rows) : n_rows;
   ca::Args g{};
   g.kv = *kv, g.q = q, g.out = out, g.lse = lse, g.cu = cu_rows, g.seq_len = seq_len, g.q_ld = q_ld, g.out_ld = out_ld;
   g.n_rows = n_rows, g.nq = d.n_q_heads, g.nkv = d.n_kv_heads, g.G = d.n_q_heads / d.n_kv_heads, g.hd = d.head_dim;
@@ -387,7 +362,7 @@ extern "C" spec_status spec_chunk_attention(const spec_attn_desc* desc, const vo
   for (int b0 = 0; b0 < B; b0 += ca::kMaxB) {
     g.b0 = b0;
     g.B = std::min(B - b0, ca::kMaxB);
-    const spec_status r = ca::launch_fma(d, g, sms, stream);
+    const spec_status r = d.dtype == SPEC_DTYPE_F32 ? ca::launch_fma(d, g, sms, stream) : ca::launch_tc(d, g, longest, sms, stream);
     if (r != SPEC_OK) return r;
   }
   return last_launch();

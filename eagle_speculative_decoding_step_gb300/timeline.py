@@ -26,7 +26,7 @@ NAMES = [None, "tc_kernel (GEMMs, LM head)", "attn_ws_kernel", "attn_mma_kernel"
 DECODE_NAMES = {24: "block_tables_kernel", 25: "cache_append_kernel", 26: "paged_attention_kernel",
                 27: "beam_select_kernel", 28: "beam_reorder_kernel", 29: "chunk_attention_kernel", 30: "logprobs_kernel",
                 31: "block_fork_kernel", 32: "block_release_kernel", 33: "block_compact_kernel", 34: "block_copy_kernel"}
-UNITS = ("beam", "blocks", "chunk_attn", "layer", "lmhead", "logprobs",
+UNITS = ("beam", "blocks", "chunk_attn", "chunk_attn_bf16", "chunk_attn_f16", "layer", "lmhead", "logprobs",
          "metadata", "paged_attn", "paged_attn_bf16", "paged_attn_f16", "prefill", "tables", "tc_gemm", "tree", "verify")
 SLOTS = 1 << 20
 LOG_WORDS = 8 + 4 * SLOTS
