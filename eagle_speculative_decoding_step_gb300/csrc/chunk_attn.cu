@@ -66,6 +66,7 @@ template <int HD> __global__ void __launch_bounds__(kFmaThreads)
       }
       *reinterpret_cast<float4*>(&sm.q[r][4 * u]) = v;
     }
+    const Edges<KT> edges(g, it);
     float m[4], l[4], o[4][4 * NJ];
     int klo[4], khi[4];
 #pragma unroll
@@ -77,7 +78,7 @@ template <int HD> __global__ void __launch_bounds__(kFmaThreads)
     }
     for (int k = it.k0; k < it.k1; ++k) {
       const int tile = it.tile0 + k, key0 = tile * KT;
-      const bool edge = edge_tile(g, it, tile, KT);
+      const bool edge = edges.has(tile);
       __syncthreads();
       if (tid < KT) sm.slot[tid] = slot_for(g, it, key0 + tid);
       __syncthreads();
@@ -137,7 +138,7 @@ template <int HD> __global__ void __launch_bounds__(kFmaThreads)
           v = load4(vc + ((long long)s * g.nkv + it.h) * g.hd + 4 * u);
           // a value that is not finite must not reach the rows that do not attend to its key (0 * inf)
           if (edge && (not_finite(v.x) || not_finite(v.y) || not_finite(v.z) || not_finite(v.w))) {
-            atomicOr(&sm.poison[edge_slot<kFmaEdges, KT>(g, it, tile)][r / 32], 1u << (r % 32));
+            atomicOr(&sm.poison[edges.slot<kFmaEdges>(tile)][r / 32], 1u << (r % 32));
             sm.poisoned = 1;
             if (not_finite(v.x)) v.x = 0.f;
             if (not_finite(v.y)) v.y = 0.f;
@@ -169,7 +170,7 @@ template <int HD> __global__ void __launch_bounds__(kFmaThreads)
       for (int e = 0; e < 2 * kFmaEdges; ++e)
         for (int w = 0; w < KT / 32; ++w)
           for (uint32_t bits = sm.poison[e][w]; bits; bits &= bits - 1) {
-            const int key = edge_tile_of<kFmaEdges, KT>(g, it, e) * KT + 32 * w + __ffs(bits) - 1;
+            const int key = edges.tile<kFmaEdges>(e) * KT + 32 * w + __ffs(bits) - 1;
             const long long s = slot_of(g.kv, g.b0 + it.b, key);
             for (int i = 0; i < 4; ++i) {
               if (key < klo[i] || key >= khi[i]) continue;
@@ -301,12 +302,37 @@ static spec_status launch_fma(const spec_attn_desc& d, const Args& g, int sms, c
 // always the same limit: another thread may be launching the same kernel with another head size
 constexpr int kTcSmem = 208 * 1024;
 
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// The cache as [slots][nkv][hd], boxes of 16 slots of one head and 64 components; past a head's or the cache's end: zeros
+static bool run_map(CUtensorMap* tm, const void* ptr, const spec_attn_desc& d, const spec_kv& kv) {
+  static const EncodeTiledFn enc = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    const bool ok = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) ==
+                        cudaSuccess && q == cudaDriverEntryPointSuccess;
+    return ok ? reinterpret_cast<EncodeTiledFn>(f) : nullptr;
+  }();
+  if (!enc) return false;
+  cuuint64_t dims[3] = {(cuuint64_t)d.head_dim, (cuuint64_t)d.n_kv_heads, (cuuint64_t)kv.num_slots};
+  cuuint64_t strides[2] = {(cuuint64_t)d.head_dim * 2, (cuuint64_t)d.n_kv_heads * d.head_dim * 2};
+  cuuint32_t box[3] = {64, 1, 16};
+  cuuint32_t es[3] = {1, 1, 1};
+  return enc(tm, d.kv_dtype == SPEC_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+             const_cast<void*>(ptr), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 static spec_status launch_tc(const spec_attn_desc& d, const Args& g, int longest, int sms, cudaStream_t st) {
   const bool f8 = d.kv_dtype == SPEC_DTYPE_E4M3;
   const int mode = mode_for(d, longest);
-  TcArgs a;
+  TcArgs a{};
   a.g = g;
   a.l = mode == kTwoQ ? layout<kTwoQ>(d.head_dim, f8) : mode == kOneQ ? layout<kOneQ>(d.head_dim, f8) : layout<kWide>(d.head_dim, f8);
+  a.l.runs = !f8 && g.kv.block_size % 16 == 0;
+  if (a.l.runs && (!run_map(&a.tmk, g.kv.k, d, g.kv) || !run_map(&a.tmv, g.kv.v, d, g.kv))) return SPEC_ERR_CUDA;
   const TcFn fn = d.dtype == SPEC_DTYPE_BF16 ? tc_kernel_bf16(f8, mode) : tc_kernel_f16(f8, mode);
   if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kTcSmem) != cudaSuccess) return SPEC_ERR_CUDA;
   return cuda_status(launch_pdl(fn, dim3(sms), dim3(kTcThreads), a.l.smem, st, a));

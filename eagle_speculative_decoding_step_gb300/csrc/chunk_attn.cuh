@@ -97,6 +97,7 @@ SPEC_DEV int owner(const Plan& p, long long x) { return (int)(((x + 1) * p.ctas 
 
 // All threads of the block.  A few thousand integers at most are read, from L2.
 template <int BM, int KT> SPEC_DEV void make_plan(const Args& g, Plan& p, int tid, int threads) {
+#pragma unroll 1
   for (int b = tid; b < g.B; b += threads) {
     bool bad;
     const Req r = request(g, b, &bad);
@@ -108,6 +109,7 @@ template <int BM, int KT> SPEC_DEV void make_plan(const Args& g, Plan& p, int ti
   __syncthreads();
   if (tid < 32) {
     int run = 0;
+#pragma unroll 1
     for (int b0 = 0; b0 < g.B; b0 += 32) {
       int x = b0 + tid < g.B ? p.pairs[b0 + tid + 1] : 0;
 #pragma unroll
@@ -121,6 +123,7 @@ template <int BM, int KT> SPEC_DEV void make_plan(const Args& g, Plan& p, int ti
   }
   __syncthreads();
   const int items = p.pairs[g.B];
+#pragma unroll 1
   for (int i = tid; i < items; i += threads) {
     int lo = 0, hi = g.B;      // the request whose items hold i
     while (hi - lo > 1) {
@@ -135,6 +138,7 @@ template <int BM, int KT> SPEC_DEV void make_plan(const Args& g, Plan& p, int ti
   __syncthreads();
   if (tid < 32) {
     long long run = 0;
+#pragma unroll 1
     for (int b0 = 0; b0 < g.B; b0 += 32) {
       long long x = b0 + tid < g.B ? p.work[b0 + tid + 1] : 0;
 #pragma unroll
@@ -165,6 +169,7 @@ template <int BM, int KT> SPEC_DEV void make_plan(const Args& g, Plan& p, int ti
       rem -= p.work[b];
       const Req r = request(g, b);
       const int n = p.pairs[b + 1] - p.pairs[b];
+#pragma unroll 1
       for (int t0 = 0; t0 < n; t0 += 32) {
         Item it;
         it.tiles = 0;
@@ -233,21 +238,22 @@ SPEC_DEV void keys_of(const Args& g, const Item& it, int r, int* lo, int* hi) {
   *lo = g.window > 0 ? max(0, p + 1 - g.window) : 0;
 }
 
-// Tiles that some row of the item does not attend to all keys of.
-SPEC_DEV bool edge_tile(const Args& g, const Item& it, int tile, int kt) {
-  const int p0 = it.first + it.r0 / g.G, p1 = it.first + (it.r0 + it.rows - 1) / g.G;
-  return (tile + 1) * kt > p0 + 1 || (g.window > 0 && tile * kt < p1 + 1 - g.window);
-}
-
-// Edge tiles of an item by number: those at its newest keys, then those at its window's start (EDGES each).
-template <int EDGES, int KT> SPEC_DEV int edge_slot(const Args& g, const Item& it, int tile) {
-  const int p0 = it.first + it.r0 / g.G;
-  return (tile + 1) * KT > p0 + 1 ? tile - max(0, p0 + 1) / KT : EDGES + tile - it.tile0;
-}
-template <int EDGES, int KT> SPEC_DEV int edge_tile_of(const Args& g, const Item& it, int slot) {
-  const int p0 = it.first + it.r0 / g.G;
-  return slot < EDGES ? max(0, p0 + 1) / KT + slot : it.tile0 + slot - EDGES;
-}
+// An item's edge tiles: those that some row does not attend to all keys of.  By number: the ones at its newest keys,
+// then (from EDGES on) the ones at its window's start.
+template <int KT> struct Edges {
+  int from, below, tile_a, tile_b;     // keys at or past `from`, and below `below`, are not for all rows
+  SPEC_DEV Edges() {}
+  SPEC_DEV Edges(const Args& g, const Item& it) {
+    const int p0 = it.first + it.r0 / g.G, p1 = it.first + (it.r0 + it.rows - 1) / g.G;
+    from = p0 + 1;
+    below = g.window > 0 ? p1 + 1 - g.window : 0;
+    tile_a = max(0, from) / KT;
+    tile_b = it.tile0;
+  }
+  SPEC_DEV bool has(int tile) const { return (tile + 1) * KT > from || tile * KT < below; }
+  template <int EDGES> SPEC_DEV int slot(int tile) const { return (tile + 1) * KT > from ? tile - tile_a : EDGES + tile - tile_b; }
+  template <int EDGES> SPEC_DEV int tile(int slot) const { return slot < EDGES ? tile_a + slot : tile_b + slot - EDGES; }
+};
 
 // reference of the exponents: finite also where nothing has been seen
 SPEC_DEV float base_of(float m) { return m == -INFINITY ? 0.f : m; }

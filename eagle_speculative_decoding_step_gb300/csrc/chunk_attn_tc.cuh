@@ -45,6 +45,7 @@ struct Layout {
   int chunks;        // 64-component (128-byte) chunks of a head
   int q_bytes, stage_bytes, stages, raw_bytes;
   int smem;
+  int runs;          // keys come in runs of 16 slots of a block, by tensor copies
 };
 template <int MODE> static inline Layout layout(int hd, bool f8) {
   using S = Shape<MODE>;
@@ -60,6 +61,7 @@ template <int MODE> static inline Layout layout(int hd, bool f8) {
 }
 
 struct TcArgs {
+  CUtensorMap tmk, tmv;        // runs: [slots][nkv][hd] views of the cache, boxes of 16 slots x 64 components
   Args g;
   Layout l;
 };
@@ -81,17 +83,61 @@ SPEC_DEV void sts128(uint32_t a, uint4 v) {
 template <int R> SPEC_DEV void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R)); }
 template <int R> SPEC_DEV void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
 
-// D[tmem] (+)= A[tmem] * B[smem]
-SPEC_DEV void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+// Whether a phase is over, at once (mbarrier.try_wait may hold the warp for a while).
+SPEC_DEV bool test(uint64_t& bar, uint32_t parity) {
+  uint32_t ok;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(tc::su32(&bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+// Bounded wait, in few instructions: the roles' loops share the SM's instruction cache.
+SPEC_DEV bool wait_for(uint64_t& bar, uint32_t parity, volatile int* abort) {
+  const uint32_t a = tc::su32(&bar);
+  if (tc::mbar_try(a, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+#pragma unroll 1
+  while (!tc::mbar_try(a, parity)) {
+    if (*abort) return false;
+    if (globaltimer_ns() - t0 > tc::kWaitNs) {
+      *abort = 1;
+      return false;
+    }
+  }
+  return true;
+}
+
+SPEC_DEV void copy_run(uint32_t dst, const CUtensorMap* tm, uint32_t mbar, int x, int head, int slot, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(head), "r"(slot), "r"(mbar), "l"(policy)
       : "memory");
 }
-SPEC_DEV void tmem_ld32(uint32_t a, float* r) {
-  uint32_t* u = reinterpret_cast<uint32_t*>(r);
+
+// D[tmem] (+)= A[smem] * B[smem]^T; descriptors by their low halves, the high ones do not change
+template <bool ACC> SPEC_DEV void mma_ss(uint32_t d, uint32_t a, uint32_t a_hi, uint32_t b, uint32_t b_hi, uint32_t idesc) {
+  asm volatile(
+      "{\n\t.reg .b64 x, y;\n\t.reg .pred p;\n\t"
+      "mov.b64 x, {%1, %2};\n\tmov.b64 y, {%3, %4};\n\tsetp.ne.u32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %5, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(a_hi), "r"(b), "r"(b_hi), "r"(idesc), "n"(ACC ? 1 : 0)
+      : "memory");
+}
+// D[tmem] (+)= A[tmem] * B[smem]
+SPEC_DEV void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t b_hi, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .b64 y;\n\t.reg .pred p;\n\t"
+      "mov.b64 y, {%2, %3};\n\tsetp.ne.u32 p, %5, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %4, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(b_hi), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+SPEC_DEV void tmem_ld32(uint32_t a, uint32_t* u) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
       "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
@@ -159,7 +205,7 @@ template <typename T> SPEC_DEV uint2 widen4(uint32_t x) {
 
 struct TcSmem {
   Plan plan;
-  uint64_t full[kMaxStages], empty[kMaxStages], q_full, q_empty, drain, s_full[2], p_full[2], o_done[2], o_free[2], group[2];
+  uint64_t full[kMaxStages], empty[kMaxStages], q_full, q_empty, drain, landed[4], s_full[2], p_full[2], o_done[2], o_free[2], group[2];
   alignas(16) uint32_t bits[kTileBits][4];   // keys of a tile that are there
   uint32_t poison[kItems][2 * 6][4];   // keys of an item's edge tiles whose value is not finite
   int poisoned[kItems];
@@ -171,133 +217,103 @@ struct TcSmem {
 };
 
 // ---------------------------------------------------------------- loader
+// Four warps copy a tile's rows in 16-byte pieces (cp.async): any block size, rows of any number of pieces, and 512 bytes
+// an instruction.  U: pieces of a cache row, where that is 4, 8, 16 or 32 (a lane's piece and its step from row to row do
+// not change then), or 0.
+template <int N> struct Units {
+  const int n, inv;                    // 2^16 / n rounded up: quotients of numbers below 2^11 are exact
+  SPEC_DEV explicit Units(int n_) : n(N ? N : n_), inv(N ? 0 : (65536 + n_ - 1) / n_) {}
+  SPEC_DEV int row(int i) const { return N ? i / (N ? N : 1) : (i * inv) >> 16; }
+};
+
 template <typename T, bool F8, int MODE> struct Loader {
   using S = Shape<MODE>;
   static constexpr int KT = S::KT, RW = KT / 4;        // key rows of a warp
-  static constexpr int EW = 16 / (F8 ? 1 : 2);         // components of 16 bytes of the cache
-  static constexpr int kLag = F8 ? kRawStages - 1 : 2; // stages under way behind the newest
-  const Args& g;
-  const Layout& l;
-  TcSmem& sm;
-  uint32_t q0, ring0, raw0;
-  int warp, lane, units, inv;          // 16-byte units of a cache row, and 2^16 / units rounded up
-  int issued = 0, finished = 0, stage = 0, f_stage = 0;
-  uint32_t phase = 0;
-  int raw = 0, f_raw = 0, q_at = -1;   // the stage that the item's Q came with
-  bool ok = true;
+  static constexpr int ES = F8 ? 1 : 2;
+  static constexpr int kLag = 1;       // stages under way behind the newest
 
-  SPEC_DEV Loader(const TcArgs& a, TcSmem& s, uint32_t base, int w, int ln)
-      : g(a.g), l(a.l), sm(s), q0(base), ring0(base + a.l.q_bytes), raw0(base + a.l.q_bytes + a.l.stages * a.l.stage_bytes),
-        warp(w), lane(ln) {
-    units = g.hd / EW;
-    inv = (65536 + units - 1) / units;
-  }
-  // rows of 16-byte units: row of item i (i < 32 * 32)
-  SPEC_DEV int row_of(int i) const { return (i * inv) >> 16; }
-  SPEC_DEV uint32_t place(int row, int u) const {      // of a 16-bit 16-byte unit in a stage
-    return (uint32_t)((u >> 3) * KT * 128 + row * 128 + (((u ^ row) & 7) << 4));
-  }
-  SPEC_DEV bool wait(uint64_t& bar, uint32_t parity) {
-    const uint32_t a = tc::su32(&bar);
-    if (tc::mbar_try(a, parity)) return true;
-    drain();                                           // what has been asked for may be what frees the stage
-    return tc::mbar_wait(a, parity, &sm.abort);
-  }
-  SPEC_DEV void drain() {
-    while (finished < issued && ok) {
-      cp_wait<0>();
-      finish();
-    }
-  }
-  // Copies of the next stage, K or V of the tile whose slots the lanes hold.
-  SPEC_DEV void issue(const void* cache, int slot, int h, int info) {
-    if constexpr (!F8) {
-      if (ok && !wait(sm.empty[stage], phase ^ 1u)) ok = false;
-    }
-    if (!ok) return;
-    const uint32_t to = F8 ? raw0 + (uint32_t)raw * l.raw_bytes : ring0 + (uint32_t)stage * l.stage_bytes;
-    const char* c = static_cast<const char*>(cache);
-    for (int i = lane; i < RW * units + lane; i += 32) {   // (every lane takes part in the shuffles)
-      const int row = min(row_of(i), RW - 1), u = i - row * units;
-      const int s = __shfl_sync(0xffffffffu, slot, row);
-      if (i < RW * units) {
-        const long long at = (((long long)max(s, 0) * g.nkv + h) * units + u) * 16;
-        const uint32_t dst = F8 ? to + (uint32_t)((warp * RW + row) * units + u) * 16 : to + place(warp * RW + row, u);
-        cp16(dst, c + at, s >= 0);
-      }
-    }
-    cp_commit();
-    if (lane == 0) sm.info[warp][issued % kTileBits] = info;
-    __syncwarp();
-    ++issued;
-    if constexpr (F8) {
-      if (++raw == kRawStages) raw = 0;
-    } else {
-      if (++stage == l.stages) stage = 0, phase ^= 1u;
-    }
-    if (issued - finished > kLag) {
-      cp_wait<kLag>();
-      finish();
-    }
-  }
-  // The oldest stage under way has come: widened (8 bits), cleared of values that are not finite (info: in an edge tile),
-  // handed to the MMA thread.
-  SPEC_DEV void finish() {
-    const int info = sm.info[warp][finished % kTileBits];
-    if constexpr (F8) {
-      // (not through wait(): it must not come back here)
-      if (!tc::mbar_wait(tc::su32(&sm.empty[stage]), phase ^ 1u, &sm.abort)) {
-        ok = false;
-        return;
-      }
-      const uint32_t from = raw0 + (uint32_t)f_raw * l.raw_bytes, to = ring0 + (uint32_t)stage * l.stage_bytes;
-      for (int i = lane; i < RW * units; i += 32) {
-        const int row = row_of(i), u = i - row * units, r = warp * RW + row;
-        const uint4 x = lds128(from + (uint32_t)(r * units + u) * 16);
-        const uint2 a = widen4<T>(x.x), b = widen4<T>(x.y), c = widen4<T>(x.z), d = widen4<T>(x.w);
-        uint4 lo = make_uint4(a.x, a.y, b.x, b.y), hi = make_uint4(c.x, c.y, d.x, d.y);
-        if (info >= 0) lo = clean(lo, info, r), hi = clean(hi, info, r);
-        sts128(to + place(r, 2 * u), lo);
-        sts128(to + place(r, 2 * u + 1), hi);
-      }
-      if (++f_raw == kRawStages) f_raw = 0;
-    } else if (info >= 0) {
-      const uint32_t at = ring0 + (uint32_t)f_stage * l.stage_bytes;
-      for (int i = lane; i < RW * units; i += 32) {    // the units that this lane copied
-        const int row = row_of(i), u = i - row * units, r = warp * RW + row;
-        const uint32_t a = at + place(r, u);
-        sts128(a, clean(lds128(a), info, r));
-      }
-    }
-    proxy_fence();
-    __syncwarp();
-    if (lane == 0) {
-      tc::mbar_arrive(tc::su32(&sm.full[F8 ? stage : f_stage]));
-      if (finished == q_at) tc::mbar_arrive(tc::su32(&sm.q_full));
-    }
-    if (finished == q_at) q_at = -1;
-    ++finished;
-    if constexpr (F8) {
-      if (++stage == l.stages) stage = 0, phase ^= 1u;
-    } else {
-      if (++f_stage == l.stages) f_stage = 0;
-    }
+  // where 16-byte piece u of a row of 16-bit components is in a tile of `rows` rows
+  static SPEC_DEV uint32_t place(int row, int u, int rows) {
+    return (uint32_t)((u >> 3) * rows * 128 + row * 128 + (((u ^ row) & 7) << 4));
   }
   // A weight of 0 times a value that is not finite is a NaN in rows that do not attend to the key: in edge tiles such
   // components are zeros, and the rows that do attend to the key get theirs at the end.
-  SPEC_DEV uint4 clean(uint4 v, int info, int key) {
+  static SPEC_DEV void mark(TcSmem& sm, int info, int key) {
+    atomicOr(&sm.poison[info >> 8][info & 255][key >> 5], 1u << (key & 31));
+    sm.poisoned[info >> 8] = 1;
+  }
+  static SPEC_DEV uint4 clean(TcSmem& sm, uint4 v, int info, int key) {
     const uint32_t a = odd_halves<T>(v.x), b = odd_halves<T>(v.y), c = odd_halves<T>(v.z), d = odd_halves<T>(v.w);
     if (a | b | c | d) {
-      const int item = info >> 8, e = info & 255;
-      atomicOr(&sm.poison[item][e][key >> 5], 1u << (key & 31));
-      sm.poisoned[item] = 1;
+      mark(sm, info, key);
       v.x &= ~a, v.y &= ~b, v.z &= ~c, v.w &= ~d;
     }
     return v;
   }
-  SPEC_DEV void load_q(const Item& it) {
+  // rows r0 .. of a warp, whose slots (-1: none) its lanes hold
+  template <int U> static SPEC_DEV void copy_rows(const char* base, uint32_t stride, int slot, uint32_t to, int r0, int lane,
+                                                  int units) {
+    const Units<U> un(units);
+    const int n = RW * un.n;
+    constexpr int B = U ? 8 : 2;                       // slots looked up together
+    static_assert(!U || RW * U % (32 * B) == 0 || RW * U < 32 * B, "");
+    const int i0 = lane, u0 = U ? lane % (U ? U : 1) : 0;
+#pragma unroll 1
+    for (int j = 0; j < n; j += 32 * B) {              // (every lane takes part in the shuffles)
+      int s[B];
+#pragma unroll
+      for (int q = 0; q < B; ++q) s[q] = __shfl_sync(0xffffffffu, slot, un.row(i0 + j + 32 * q) & 31);
+#pragma unroll
+      for (int q = 0; q < B; ++q) {
+        const int i = i0 + j + 32 * q, row = un.row(i), u = U ? u0 : i - row * un.n;
+        const char* src = base + (uint64_t)(uint32_t)max(s[q], 0) * stride + u * 16;
+        if (i < n) cp16(to + (F8 ? (uint32_t)((r0 + row) * un.n + u) * 16 : place(r0 + row, u, KT)), src, s[q] >= 0);
+      }
+    }
+  }
+  static SPEC_DEV void widen_rows(TcSmem& sm, uint32_t from, uint32_t to, int r0, int lane, int units, int info) {
+    const Units<0> un(units);
+    const int n = RW * units;
+#pragma unroll 2
+    for (int i = lane; i < n; i += 32) {
+      const int row = un.row(i), u = i - row * units, r = r0 + row;
+      const uint4 x = lds128(from + (uint32_t)(r * units + u) * 16);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint2 a = widen4<T>(h ? x.z : x.x), b = widen4<T>(h ? x.w : x.y);
+        uint4 v = make_uint4(a.x, a.y, b.x, b.y);
+        if (info >= 0) v = clean(sm, v, info, r);
+        sts128(to + place(r, 2 * u + h, KT), v);
+      }
+    }
+  }
+  // Rows r0 .. of a tile in an edge (info), of which `there` are keys (others hold whatever the cache has there).
+  static SPEC_DEV void clean_rows(TcSmem& sm, uint32_t at, int r0, int lane, int units, int info, uint32_t there) {
+    const Units<0> un(units);
+#pragma unroll 4
+    for (int i = lane; i < RW * units; i += 32) {
+      const int row = un.row(i), u = i - row * units;
+      const uint32_t to = at + place(r0 + row, u, KT);
+      uint4 v = lds128(to);
+      const uint32_t a = odd_halves<T>(v.x), b = odd_halves<T>(v.y), c = odd_halves<T>(v.z), d = odd_halves<T>(v.w);
+      if (a | b | c | d) {
+        v.x &= ~a, v.y &= ~b, v.z &= ~c, v.w &= ~d;
+        sts128(to, v);
+        if (there >> row & 1u) mark(sm, info, r0 + row);
+      }
+    }
+  }
+  static SPEC_DEV void zero_rows(uint32_t at, int r0, int lane, int units, uint32_t which) {
+    const Units<0> un(units);
+#pragma unroll 1
+    for (int i = lane; i < RW * units; i += 32) {
+      const int row = un.row(i), u = i - row * units;
+      if (which >> row & 1u) sts128(at + place(r0 + row, u, KT), make_uint4(0, 0, 0, 0));
+    }
+  }
+  static SPEC_DEV void load_q(const Args& g, const Item& it, uint32_t q0, int chunks, int warp, int lane) {
     constexpr int RQ = S::BM / 4;                      // rows of a warp
-    const int qu = g.hd / 8, qinv = (65536 + qu - 1) / qu;
+    const Units<0> un(g.hd / 8);
     const T* q = static_cast<const T*>(g.q);
     for (int r0 = 0; r0 < RQ; r0 += 32) {
       const int r = warp * RQ + r0 + lane;
@@ -306,121 +322,356 @@ template <typename T, bool F8, int MODE> struct Loader {
         const int tok = (it.r0 + r) / g.G, head = it.h * g.G + (it.r0 + r) - tok * g.G;
         off = (it.row0 + tok) * g.q_ld + (long long)head * g.hd;
       }
-      for (int i = lane; i < 32 * qu + lane; i += 32) {
-        const int row = min((i * qinv) >> 16, 31), u = i - row * qu;
+#pragma unroll 2
+      for (int j = 0; j < 32 * un.n; j += 32) {
+        const int i = j + lane, row = un.row(i), u = i - row * un.n;
         const long long o = __shfl_sync(0xffffffffu, off, row);
-        if (i < 32 * qu) {
-          const int m = warp * RQ + r0 + row, t = m >> 7, mr = m & 127;
-          cp16(q0 + (uint32_t)(t * l.chunks * 16384 + (u >> 3) * 16384 + mr * 128 + (((u ^ mr) & 7) << 4)),
-               q + max(o, 0ll) + 8 * u, o >= 0);
-        }
+        const int m = warp * RQ + r0 + row;
+        cp16(q0 + (uint32_t)((m >> 7) * chunks * 16384) + place(m & 127, u, 128), q + max(o, 0ll) + 8 * u, o >= 0);
       }
     }
-    q_at = issued;                                     // with the next stage's copies
   }
-  SPEC_DEV void run() {
+
+  // Keys in runs of 16 slots: tensor copies, a lane a run and 64 components, that report to the MMA warp by themselves; in
+  // edge tiles the values come by way of this warp.
+  static SPEC_DEV void run_tensor(const TcArgs& a, TcSmem& sm, uint32_t q0, int warp, int lane) {
+    const Args& g = a.g;
+    const int chunks = a.l.chunks, stages = a.l.stages, units = g.hd / 8, r0 = warp * RW;
+    const uint32_t stage_bytes = a.l.stage_bytes, ring0 = q0 + a.l.q_bytes;
+    volatile int* abort = &sm.abort;
     Walk<S::BM, KT> walk(g, sm.plan);
     Item it;
-    int tiles = 0, items = 0;
-    uint32_t q_phase = 0;
+    int tiles = 0, items = 0, stage = 0, filled = 0;
+    uint32_t phase = 0, q_phase = 0, l_phase = 0;
+    // this lane's copy: run and chunk
+    const int run = lane / chunks, chunk = lane - run * chunks;
+    const bool copier = run < RW / 16;
+    const uint32_t lane_to = (uint32_t)(chunk * KT * 128 + (r0 + run * 16) * 128), run_mask = copier ? 0xffffu << (run * 16) : 0u;
+    const uint64_t policy = tc::policy_evict_last();
+    const int step_b = KT / g.kv.block_size, step_i = KT % g.kv.block_size;
+    const bool mine = lane < RW;
+    bool ok = true;
     while (ok && walk.next(it)) {
-      const int im = items % kItems;
-      if (items > 0) {
-        if (!wait(sm.q_empty, q_phase)) break;
-        q_phase ^= 1u;
+      const Edges<KT> edges(g, it);
+      const int32_t* table = g.kv.block_table + (long long)(g.b0 + it.b) * g.kv.max_blocks;
+      int key = (it.tile0 + it.k0) * KT + r0 + lane, block = key / g.kv.block_size, in_block = key % g.kv.block_size;
+      auto entry = [&] { return mine && key >= it.lo && key < it.hi ? __ldg(table + block) : -1; };
+      int e = entry();
+      for (int k = it.k0; ok && k < it.k1; ++k, ++tiles) {
+        int slot = -1;
+        if (mine && key >= it.lo && key < it.hi) {
+          const long long s = (long long)e * g.kv.block_size + in_block;
+          if (s >= 0 && s < g.kv.num_slots) slot = (int)s;
+          else report(g.ws, SPEC_ERR_DEVICE, g.b0 + it.b, key);
+        }
+        key += KT, block += step_b, in_block += step_i;
+        if (in_block >= g.kv.block_size) in_block -= g.kv.block_size, ++block;
+        if (k + 1 < it.k1) e = entry();
+        const uint32_t there = __ballot_sync(0xffffffffu, slot >= 0);
+        if (lane == 0) {
+          if constexpr (RW == 32) sm.bits[tiles % kTileBits][warp] = there;
+          else reinterpret_cast<uint16_t*>(sm.bits[tiles % kTileBits])[warp] = (uint16_t)there;
+        }
+        // the slot that the lane's run begins with
+        const uint32_t keys = there & run_mask;
+        const int from = keys ? __ffs(keys) - 1 : 0;
+        const int first = __shfl_sync(0xffffffffu, slot, from) - (from & 15);
+        const uint32_t runs = (there & 0xffffu ? 1u : 0u) + (RW == 32 && there >> 16 ? 1u : 0u);
+        const uint32_t bytes = runs * chunks * 2048u;
+        const uint32_t absent = (there & 0xffffu ? 0u : 0xffffu) | (RW == 32 && there >> 16 ? 0u : RW == 32 ? 0xffff0000u : 0u);
+        const int tile = it.tile0 + k;
+        const bool edge = edges.has(tile);
+#pragma unroll 1
+        for (int value = 0; value < 2; ++value) {
+          if (!__all_sync(0xffffffffu, wait_for(sm.empty[stage], phase ^ 1u, abort))) {
+            ok = false;
+            break;
+          }
+          const uint32_t at = ring0 + (uint32_t)stage * stage_bytes;
+          const bool by_way = value && edge;
+          if (value && absent) {                       // nothing is copied there: weights of 0 must meet numbers
+            zero_rows(at, r0, lane, units, absent);
+            proxy_fence();
+          }
+          uint64_t& bar = by_way ? sm.landed[warp] : sm.full[stage];
+          __syncwarp();
+          if (lane == 0) tc::mbar_expect_tx(tc::su32(&bar), bytes);
+          __syncwarp();
+          if (keys) copy_run(at + lane_to, value ? &a.tmv : &a.tmk, tc::su32(&bar), 64 * chunk, it.h, first, policy);
+          if (by_way) {
+            __syncwarp();
+            if (!__all_sync(0xffffffffu, wait_for(bar, l_phase, abort))) {
+              ok = false;
+              break;
+            }
+            l_phase ^= 1u;
+            clean_rows(sm, at, r0, lane, units, (items % kItems) << 8 | edges.template slot<S::EDGES>(tile), there);
+            proxy_fence();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(tc::su32(&sm.full[stage]));
+          }
+          filled = min(filled + 1, stages);
+          if (++stage == stages) stage = 0, phase ^= 1u;
+        }
+        if (k == it.k0 && ok) {
+          // Q, once the first keys are on their way
+          if (items > 0) {
+            ok = __all_sync(0xffffffffu, wait_for(sm.q_empty, q_phase, abort));
+            q_phase ^= 1u;
+          }
+          if (ok) {
+            load_q(g, it, q0, chunks, warp, lane);
+            cp_commit();
+            cp_wait<0>();
+            proxy_fence();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(tc::su32(&sm.q_full));
+          }
+        }
       }
       ++items;
-      load_q(it);
-      for (int k = it.k0; ok && k < it.k1; ++k, ++tiles) {
-        const int tile = it.tile0 + k, key = tile * KT + warp * RW + lane;
-        int slot = -1;
-        if (lane < RW && key >= it.lo && key < it.hi) {
-          const long long s = slot_of(g.kv, g.b0 + it.b, key);
-          slot = (int)s;
-          if (s < 0) report(g.ws, SPEC_ERR_DEVICE, g.b0 + it.b, key);
+    }
+    cp_wait<0>();
+    if (!ok || sm.abort) {
+      // gives up: the copies under way land first (or the limit passes)
+      for (int i = 0; i < filled; ++i) {
+        if (--stage < 0) stage = stages - 1, phase ^= 1u;
+        tc::mbar_wait(tc::su32(&sm.full[stage]), phase, abort, false);
+      }
+    }
+  }
+
+  // One loop, a step of which either hands over the oldest stage under way or asks for the next one, so that each is in
+  // the code once.
+  static SPEC_DEV void run(const TcArgs& a, TcSmem& sm, uint32_t q0, int warp, int lane) {
+    const Args& g = a.g;
+    const int chunks = a.l.chunks, stages = a.l.stages, units = g.hd * ES / 16, r0 = warp * RW;
+    const uint32_t stage_bytes = a.l.stage_bytes, raw_bytes = a.l.raw_bytes, ring0 = q0 + a.l.q_bytes,
+                   raw0 = ring0 + (uint32_t)stages * stage_bytes, stride = (uint32_t)(g.nkv * g.hd * ES);
+    volatile int* abort = &sm.abort;
+    Walk<S::BM, KT> walk(g, sm.plan);
+    Item it;
+    it.k0 = it.k1 = 0;
+    // stage: the next to be filled; f_stage: of the oldest copies under way (8 bits: raw, f_raw)
+    int tiles = 0, items = 0, issued = 0, finished = 0, stage = 0, f_stage = 0, raw = 0, f_raw = 0, q_at = -1;
+    uint32_t phase = 0, q_phase = 0;
+    int k = 0, key = 0, e = -1, slot = -1, info = -1;
+    int block = 0, in_block = 0;       // of the lane's key in the tile whose entry has been asked for
+    const int step_b = KT / g.kv.block_size, step_i = KT % g.kv.block_size;
+    const int32_t* table = nullptr;
+    bool value = false, more = true, q_due = false;
+    // A key's entry of the block table, asked for a tile ahead; -1 where no row attends to it.
+    const bool mine = lane < RW;
+    auto entry = [&](int key_) { return mine && key_ >= it.lo && key_ < it.hi ? __ldg(table + block) : -1; };
+    Edges<KT> edges;
+#pragma unroll 1
+    for (;;) {
+      if (!value && k == it.k1 && more && !q_due) {
+        more = walk.next(it);
+        if (more) {
+          q_due = true;
+          k = it.k0;
+          key = (it.tile0 + k) * KT + r0 + lane;
+          table = g.kv.block_table + (long long)(g.b0 + it.b) * g.kv.max_blocks;
+          block = key / g.kv.block_size, in_block = key % g.kv.block_size;
+          edges = Edges<KT>(g, it);
+          e = entry(key);
+        }
+      }
+      bool hand = issued - finished > kLag;
+      if (hand) {
+        cp_wait<kLag>();
+      } else if (!more) {
+        if (issued == finished) break;
+        cp_wait<0>();
+        hand = true;
+      } else if (q_due || !F8) {
+        // what has been asked for may be what frees the place that is waited for
+        uint64_t& bar = q_due ? sm.q_empty : sm.empty[stage];
+        const uint32_t parity = q_due ? q_phase : phase ^ 1u;
+        if (!(q_due && items == 0) && !test(bar, parity)) {
+          if (issued > finished) {
+            cp_wait<0>();
+            hand = true;
+          } else if (!wait_for(bar, parity, abort)) {
+            break;
+          }
+        }
+      }
+      if (hand) {
+        // it has come: widened (8 bits), cleared of values that are not finite (in an edge tile), handed to the MMA thread
+        const int edge = sm.info[warp][finished % kTileBits];
+        if constexpr (F8) {
+          if (!wait_for(sm.empty[stage], phase ^ 1u, abort)) break;
+          widen_rows(sm, raw0 + (uint32_t)f_raw * raw_bytes, ring0 + (uint32_t)stage * stage_bytes, r0, lane, units, edge);
+          if (++f_raw == kRawStages) f_raw = 0;
+        } else if (edge >= 0) {
+          clean_rows(sm, ring0 + (uint32_t)f_stage * stage_bytes, r0, lane, units, edge, 0xffffffffu);   // (others are zeros)
+        }
+        proxy_fence();
+        __syncwarp();
+        if (lane == 0) {
+          tc::mbar_arrive(tc::su32(&sm.full[F8 ? stage : f_stage]));
+          if (finished == q_at) tc::mbar_arrive(tc::su32(&sm.q_full));
+        }
+        ++finished;
+        if constexpr (F8) {
+          if (++stage == stages) stage = 0, phase ^= 1u;
+        } else {
+          if (++f_stage == stages) f_stage = 0;
+        }
+        continue;
+      }
+      if (q_due) {
+        if (items > 0) q_phase ^= 1u;
+        ++items;
+        q_due = false;
+        load_q(g, it, q0, chunks, warp, lane);
+        q_at = issued;                                 // comes with the next stage's copies
+        if (!F8 && !test(sm.empty[stage], phase ^ 1u)) continue;
+      }
+      if (!value) {                                    // a new tile: its slots
+        const int tile = it.tile0 + k;
+        slot = -1;
+        if (mine && key >= it.lo && key < it.hi) {
+          const long long s = (long long)e * g.kv.block_size + in_block;
+          if (s >= 0 && s < g.kv.num_slots) slot = (int)s;
+          else report(g.ws, SPEC_ERR_DEVICE, g.b0 + it.b, key);
+        }
+        if (k + 1 < it.k1) {
+          block += step_b, in_block += step_i;
+          if (in_block >= g.kv.block_size) in_block -= g.kv.block_size, ++block;
+          e = entry(key + KT);
         }
         const uint32_t there = __ballot_sync(0xffffffffu, slot >= 0);
         if (lane == 0) {
           if constexpr (RW == 32) sm.bits[tiles % kTileBits][warp] = there;
           else reinterpret_cast<uint16_t*>(sm.bits[tiles % kTileBits])[warp] = (uint16_t)there;
         }
-        const bool edge = edge_tile(g, it, tile, KT);
-        issue(g.kv.k, slot, it.h, -1);
-        issue(g.kv.v, slot, it.h, edge ? im << 8 | edge_slot<S::EDGES, KT>(g, it, tile) : -1);
+        info = edges.has(tile) ? ((items - 1) % kItems) << 8 | edges.template slot<S::EDGES>(tile) : -1;
       }
+      const uint32_t to = F8 ? raw0 + (uint32_t)raw * raw_bytes : ring0 + (uint32_t)stage * stage_bytes;
+      const char* base = static_cast<const char*>(value ? g.kv.v : g.kv.k) + (long long)it.h * g.hd * ES;
+      if (units == 16) copy_rows<16>(base, stride, slot, to, r0, lane, units);
+      else if (units == 8) copy_rows<8>(base, stride, slot, to, r0, lane, units);
+      else copy_rows<0>(base, stride, slot, to, r0, lane, units);
+      cp_commit();
+      if (lane == 0) sm.info[warp][issued % kTileBits] = value ? info : -1;
+      __syncwarp();
+      ++issued;
+      if constexpr (F8) {
+        if (++raw == kRawStages) raw = 0;
+      } else {
+        if (++stage == stages) stage = 0, phase ^= 1u;
+      }
+      if (value) ++k, ++tiles, key += KT;
+      value = !value;
     }
-    drain();
     cp_wait<0>();                                      // nothing in flight when the CTA ends, or gives up
   }
 };
 
-// ---------------------------------------------------------------- MMA thread
-template <typename T, int MODE> SPEC_DEV void issue_mmas(const TcArgs& a, TcSmem& sm, uint32_t base, uint32_t tmem) {
+// ---------------------------------------------------------------- MMA warp
+// The whole warp walks the items, with values that are the same in all lanes (uniform()), and one lane issues: a lane on a
+// path of its own would move every operand of every instruction into uniform registers first (80 cycles an MMA).
+SPEC_DEV int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+SPEC_DEV bool elect_one() {
+  uint32_t one;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+  return one != 0;
+}
+SPEC_DEV bool warp_wait(uint64_t& bar, uint32_t parity, volatile int* abort) {
+  return __all_sync(0xffffffffu, wait_for(bar, parity, abort));
+}
+
+template <typename T, int MODE> SPEC_DEV void issue_mmas(const TcArgs& a, TcSmem& sm, uint32_t base_, uint32_t tmem_) {
   using S = Shape<MODE>;
   constexpr int KT = S::KT;
   const Args& g = a.g;
   const Layout& l = a.l;
-  const uint32_t ring0 = base + l.q_bytes;
+  const uint32_t base = uniform(base_), tmem = uniform(tmem_), ring0 = base + l.q_bytes;
   const int ks = g.hd / 16;
   const uint32_t id_s = idesc_of<T>(KT, false), id_o = idesc_of<T>(g.hd, true);
   volatile int* abort = &sm.abort;
   Walk<S::BM, KT> walk(g, sm.plan);
   Item it;
-  uint32_t q_phase = 0, p_phase[2] = {0, 0}, free_phase[2] = {0, 0};
-  int tile0 = 0;               // tiles before the item's
+  uint32_t q_phase = 0, p_phase = 0, free_phase = 0;   // (of two barriers: a bit each)
+  // K and V tiles take turns in the ring; their next places, and what is added to a descriptor there
+  int k_st = 0, v_st = 1;
+  uint32_t k_ph = 0, v_ph = 0;
+  const uint64_t q_desc = tc::desc_sw128(base), k_desc = tc::desc_sw128(ring0), v_desc = desc_values(ring0, KT * 128);
+  const uint32_t q_lo = (uint32_t)q_desc, k_lo = (uint32_t)k_desc, v_lo = (uint32_t)v_desc;
+  const uint32_t s_hi = (uint32_t)(k_desc >> 32), v_hi = (uint32_t)(v_desc >> 32), stage16 = (uint32_t)l.stage_bytes >> 4;
   bool first = true, ok = true;
-  while (ok && walk.next(it)) {
-    const int nt = it.k1 - it.k0, jobs = MODE == kTwoQ ? 2 * nt : nt;
-    if (!tc::mbar_wait(tc::su32(&sm.q_full), q_phase, abort)) break;
+  while (ok && __any_sync(0xffffffffu, walk.next(it))) {
+    const int jobs = uniform((it.k1 - it.k0) * (MODE == kTwoQ ? 2 : 1));
+    if (!warp_wait(sm.q_full, q_phase, abort)) break;
     q_phase ^= 1u;
-    auto scores = [&](int k) {
-      const int t = tile0 + (MODE == kTwoQ ? k >> 1 : k), idx = 2 * t, st = idx % l.stages;
-      if (!tc::mbar_wait(tc::su32(&sm.full[st]), (uint32_t)(idx / l.stages) & 1u, abort)) return false;
-      tc::tc_fence_after();
-      const uint32_t q = base + (MODE == kTwoQ ? (uint32_t)(k & 1) * l.chunks * 16384 : 0u);
-      const uint64_t da = tc::desc_sw128(q), db = tc::desc_sw128(ring0 + (uint32_t)st * l.stage_bytes);
-      const uint32_t d = tmem + (uint32_t)((k & 1) * KT);
-      for (int kk = 0; kk < ks; ++kk)
-        tc::tc_mma(d, da + (uint64_t)(((kk >> 2) * 16384 + (kk & 3) * 32) >> 4),
-                   db + (uint64_t)(((kk >> 2) * KT * 128 + (kk & 3) * 32) >> 4), id_s, kk > 0);
-      tc::tc_commit(tc::su32(&sm.s_full[k & 1]));
-      if (MODE != kTwoQ || (k & 1)) tc::tc_commit(tc::su32(&sm.empty[st]));
-      if (k == jobs - 1) tc::tc_commit(tc::su32(&sm.q_empty));
-      return true;
-    };
-    ok = scores(0) && (jobs < 2 || scores(1));
-    for (int k = 0; ok && k < jobs; ++k) {
-      const int buf = k & 1, acc = MODE == kWide ? 0 : buf;
-      if (!(ok = tc::mbar_wait(tc::su32(&sm.p_full[buf]), p_phase[buf], abort))) break;
-      p_phase[buf] ^= 1u;
-      const bool fresh = MODE == kWide ? k == 0 : k < 2;
-      // the last item's accumulator has been read
-      if (fresh && !first) {
-        if (!(ok = tc::mbar_wait(tc::su32(&sm.o_free[acc]), free_phase[acc], abort))) break;
-        free_phase[acc] ^= 1u;
-      }
-      const int t = tile0 + (MODE == kTwoQ ? k >> 1 : k), idx = 2 * t + 1, st = idx % l.stages;
-      if (!(ok = tc::mbar_wait(tc::su32(&sm.full[st]), (uint32_t)(idx / l.stages) & 1u, abort))) break;
-      tc::tc_fence_after();
-      const uint64_t db = desc_values(ring0 + (uint32_t)st * l.stage_bytes, KT * 128);
-      const uint32_t d = tmem + (uint32_t)(acc ? S::O1 : S::O0), p = tmem + (uint32_t)(buf * KT);
+    // Jobs k: the scores are two ahead of the products with V.
+#pragma unroll 1
+    for (int k = -2; k < jobs; ++k) {
+      const int buf = k & 1;
+      if (k >= 0) {
+        const int acc = MODE == kWide ? 0 : buf;
+        const bool fresh = MODE == kWide ? k == 0 : k < 2;
+        if (!(ok = warp_wait(sm.full[v_st], v_ph, abort))) break;
+        if (fresh && !first) {         // the last item's accumulator has been read
+          if (!(ok = warp_wait(sm.o_free[acc], free_phase >> acc & 1u, abort))) break;
+          free_phase ^= 1u << acc;
+        }
+        if (!(ok = warp_wait(sm.p_full[buf], p_phase >> buf & 1u, abort))) break;
+        p_phase ^= 1u << buf;
+        tc::tc_fence_after();
+        if (elect_one()) {
+          const uint32_t b = v_lo + v_st * stage16;
+          const uint32_t d = tmem + (uint32_t)(acc ? S::O1 : S::O0), p = tmem + (uint32_t)(buf * KT);
 #pragma unroll
-      for (int kk = 0; kk < KT / 16; ++kk)
-        tc_mma_ts(d, p + 8 * kk, db + (uint64_t)(kk * 2048 >> 4), id_o, !fresh || kk > 0);
-      if (MODE != kTwoQ || buf) tc::tc_commit(tc::su32(&sm.empty[st]));
-      if (MODE == kWide || k >= jobs - 2) tc::tc_commit(tc::su32(&sm.o_done[acc]));
-      if (k + 2 < jobs) ok = scores(k + 2);
+          for (int kk = 0; kk < KT / 16; ++kk)
+            mma_ts(d, p + 8 * kk, b + (kk * 2048 >> 4), v_hi, id_o, kk > 0 ? 1u : fresh ? 0u : 1u);
+          if (MODE != kTwoQ || buf) tc::tc_commit(tc::su32(&sm.empty[v_st]));
+          if (MODE == kWide || k >= jobs - 2) tc::tc_commit(tc::su32(&sm.o_done[acc]));
+        }
+        __syncwarp();
+        if (MODE != kTwoQ || buf) {
+          v_st += 2;
+          if (v_st >= l.stages) v_st -= l.stages, v_ph ^= 1u;
+        }
+      }
+      if (k + 2 < jobs) {
+        if (!(ok = warp_wait(sm.full[k_st], k_ph, abort))) break;
+        tc::tc_fence_after();
+        if (elect_one()) {
+          uint32_t qa = q_lo + (MODE == kTwoQ ? (uint32_t)(buf * l.chunks) * (16384 >> 4) : 0u), kb = k_lo + k_st * stage16;
+          const uint32_t d = tmem + (uint32_t)(buf * KT);
+          mma_ss<false>(d, qa, s_hi, kb, s_hi, id_s);
+#pragma unroll 1
+          for (int c = 0, n = ks; c < l.chunks; ++c, n -= 4, qa += 16384 >> 4, kb += KT * 128 >> 4) {
+            if (c) mma_ss<true>(d, qa, s_hi, kb, s_hi, id_s);
+            if (n > 1) mma_ss<true>(d, qa + 2, s_hi, kb + 2, s_hi, id_s);
+            if (n > 2) mma_ss<true>(d, qa + 4, s_hi, kb + 4, s_hi, id_s);
+            if (n > 3) mma_ss<true>(d, qa + 6, s_hi, kb + 6, s_hi, id_s);
+          }
+          tc::tc_commit(tc::su32(&sm.s_full[buf]));
+          if (MODE != kTwoQ || buf) tc::tc_commit(tc::su32(&sm.empty[k_st]));
+          if (k + 2 == jobs - 1) tc::tc_commit(tc::su32(&sm.q_empty));
+        }
+        __syncwarp();
+        if (MODE != kTwoQ || buf) {
+          k_st += 2;
+          if (k_st >= l.stages) k_st -= l.stages, k_ph ^= 1u;
+        }
+      }
     }
     // (kOneQ with a single tile: the second accumulator is not used, nor waited for)
     if (MODE == kOneQ && jobs == 1 && ok && !first) {
-      ok = tc::mbar_wait(tc::su32(&sm.o_free[1]), free_phase[1], abort);
-      free_phase[1] ^= 1u;
+      ok = warp_wait(sm.o_free[1], free_phase >> 1, abort);
+      free_phase ^= 2u;
     }
     first = false;
-    tile0 += nt;
   }
   // the copies' stages and TMEM are given back only when every MMA has ended
-  tc::tc_commit(tc::su32(&sm.drain));
+  if (elect_one()) tc::tc_commit(tc::su32(&sm.drain));
+  __syncwarp();
   tc::mbar_wait(tc::su32(&sm.drain), 0, abort, false);
 }
 
@@ -449,10 +700,10 @@ template <typename T, bool F8, int MODE> struct Softmax {
   // The warps that write an item together: a warpgroup, or both (kOneQ).  Bounded as every wait.
   uint32_t group_phase = 0;
   SPEC_DEV bool group_sync() {
-    const uint32_t a = tc::su32(&sm.group[MODE == kOneQ ? 0 : w]);
+    uint64_t& bar = sm.group[MODE == kOneQ ? 0 : w];
     __syncwarp();
-    if (lane == 0) tc::mbar_arrive(a);
-    const bool ok = tc::mbar_wait(a, group_phase, &sm.abort);
+    if (lane == 0) tc::mbar_arrive(tc::su32(&bar));
+    const bool ok = wait_for(bar, group_phase, &sm.abort);
     group_phase ^= 1u;
     __syncwarp();
     return ok;
@@ -472,28 +723,49 @@ template <typename T, bool F8, int MODE> struct Softmax {
 
   // One tile: scores in TMEM columns s0 -> weights there.  o0: the accumulator; fresh: nothing is in it.
   // done: waits until the products of the last tile are in the accumulator (kWide).
-  template <typename Done> SPEC_DEV void tile(const Item& it, int tile, int bits, uint32_t s0, uint32_t o0, bool fresh,
+  // The scores are read from TMEM twice, 32 columns at a time in short loops: holding 128 of them in registers unrolls
+  // the code to 17 KB, and the roles' loops then push one another out of the SM's instruction cache (every role ran
+  // three times slower).
+  template <typename Done> SPEC_DEV void tile(const Edges<KT>& edges, int tile, int bits, uint32_t s0, uint32_t o0, bool fresh,
                                               int klo, int khi, Done&& done) {
-    float s[KT];
+    const uint32_t at = tm + s0;
     __syncwarp();
-#pragma unroll
-    for (int i = 0; i < KT / 32; ++i) tmem_ld32(tm + s0 + 32 * i, s + 32 * i);
-    tc::tmem_ld_wait();
     const uint4 there = *reinterpret_cast<const uint4*>(sm.bits[bits]);
     const uint32_t all = KT == 128 ? there.x & there.y & there.z & there.w : there.x & there.y;
-    if (edge_tile(g, it, tile, KT) || all != 0xffffffffu) {
+    if (edges.has(tile) || all != 0xffffffffu) {
       const int key0 = tile * KT;
-#pragma unroll
+#pragma unroll 1
       for (int i = 0; i < KT / 32; ++i) {
         const uint32_t seen = span(klo - key0, khi - key0, i) & (i == 0 ? there.x : i == 1 ? there.y : i == 2 ? there.z : there.w);
+        if (__all_sync(0xffffffffu, seen == 0xffffffffu)) continue;
+        uint32_t s[32];
+        tmem_ld32(at + 32 * i, s);
+        tc::tmem_ld_wait();
 #pragma unroll
-        for (int j = 0; j < 32; ++j) s[32 * i + j] = seen & (1u << j) ? s[32 * i + j] : -INFINITY;
+        for (int j = 0; j < 32; ++j) s[j] = seen & (1u << j) ? s[j] : 0xff800000u;
+        tmem_st16(at + 32 * i, s);
+        tmem_st16(at + 32 * i + 16, s + 16);
+      }
+      tmem_st_wait();
+    }
+    uint32_t x[2][32];
+    float top = -INFINITY, other = -INFINITY;
+    tmem_ld32(at, x[0]);
+#pragma unroll 1
+    for (int i = 0; i < KT / 32; i += 2) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        tc::tmem_ld_wait();
+        // the next columns; at the end the first ones again, for the second pass
+        tmem_ld32(at + 32 * ((i + h + 1) & (KT / 32 - 1)), x[1 - h]);
+#pragma unroll
+        for (int j = 0; j < 32; j += 4) {
+          top = fmaxf(fmaxf(top, __uint_as_float(x[h][j])), __uint_as_float(x[h][j + 1]));
+          other = fmaxf(fmaxf(other, __uint_as_float(x[h][j + 2])), __uint_as_float(x[h][j + 3]));
+        }
       }
     }
-    float top[4] = {s[0], s[1], s[2], s[3]};
-#pragma unroll
-    for (int i = 4; i < KT; ++i) top[i & 3] = fmaxf(top[i & 3], s[i]);
-    const float now = fmaxf(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * g.scale2, m);
+    const float now = fmaxf(fmaxf(top, other) * g.scale2, m);
     bool in = fresh;
     if (fresh) {
       m = now;
@@ -501,7 +773,9 @@ template <typename T, bool F8, int MODE> struct Softmax {
       const float f = m == -INFINITY ? 1.f : exp2_fast(m - now);
       if (!done()) return;
       in = true;
+      tc::tmem_ld_wait();
       tc::tc_fence_after();
+#pragma unroll 1
       for (int c = 0; c < g.hd; c += 16) {
         uint32_t o[16];
         tc::tmem_ld16(tm + o0 + c, o);
@@ -514,38 +788,51 @@ template <typename T, bool F8, int MODE> struct Softmax {
       m = now;
     }
     const float base = W::kShift - base_of(m);
-    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+    float sum0 = 0.f, sum1 = 0.f;
+#pragma unroll 1
+    for (int i = 0; i < KT / 32; i += 2) {
 #pragma unroll
-    for (int i = 0; i < KT / 32; ++i) {
-      uint32_t p[16];
+      for (int h = 0; h < 2; ++h) {
+        tc::tmem_ld_wait();
+        // (the weights of columns 32 i go to columns 16 i, which have been read)
+        if (h == 0 || i + 2 < KT / 32) tmem_ld32(at + 32 * (i + h + 1), x[1 - h]);
+        uint32_t p[16];
 #pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        const float a = exp2_fast(fmaf(s[32 * i + 2 * j], g.scale2, base));
-        const float b = exp2_fast(fmaf(s[32 * i + 2 * j + 1], g.scale2, base));
-        sum[(2 * j) & 3] += a, sum[(2 * j + 1) & 3] += b;
-        p[j] = pack2<T>(a, b);
+        for (int j = 0; j < 16; ++j) {
+          const float u = exp2_fast(fmaf(__uint_as_float(x[h][2 * j]), g.scale2, base));
+          const float v = exp2_fast(fmaf(__uint_as_float(x[h][2 * j + 1]), g.scale2, base));
+          sum0 += u, sum1 += v;
+          p[j] = pack2<T>(u, v);
+        }
+        tmem_st16(at + 16 * (i + h), p);
       }
-      tmem_st16(tm + s0 + 16 * i, p);
     }
     tmem_st_wait();
-    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+    l += sum0 + sum1;
     if (!in) done();                       // every phase is waited for in its turn
   }
 
   // A value that is not finite, of a key of an edge tile that the row attends to
   SPEC_DEV void mend(const Item& it, int item, int klo, int khi, int c0, float* o) {
+#pragma unroll 1
     for (int e = 0; e < 2 * S::EDGES; ++e)
+#pragma unroll 1
       for (int i = 0; i < KT / 32; ++i)
+#pragma unroll 1
         for (uint32_t b = sm.poison[item][e][i]; b; b &= b - 1) {
-          const int key = edge_tile_of<S::EDGES, KT>(g, it, e) * KT + 32 * i + __ffs(b) - 1;
+          const int key = Edges<KT>(g, it).template tile<S::EDGES>(e) * KT + 32 * i + __ffs(b) - 1;
           if (key < klo || key >= khi) continue;
           const long long at = (slot_of(g.kv, g.b0 + it.b, key) * g.nkv + it.h) * g.hd + c0;
+          uint32_t odd = 0;
+#pragma unroll 1
           for (int j = 0; j < 16; ++j) {
             float v;
             if constexpr (F8) v = (float)static_cast<const __nv_fp8_e4m3*>(g.kv.v)[at + j];
             else v = (float)static_cast<const T*>(g.kv.v)[at + j];
-            if (not_finite(v)) o[j] = NAN;
+            odd |= not_finite(v) ? 1u << j : 0u;
           }
+#pragma unroll
+          for (int j = 0; j < 16; ++j) o[j] = odd >> j & 1u ? NAN : o[j];
         }
   }
 
@@ -608,6 +895,7 @@ template <typename T, bool F8, int MODE> struct Softmax {
     const Pieces pc(sm.plan, it);
     if (pc.c0 == pc.c1) {
       const float inv = l == 0.f ? 0.f : g.v_scale / l;
+#pragma unroll 1
       for (int c = c0; c < c1; c += 16) {
         float o[16];
         take(o, c, f0, f1, two);
@@ -620,6 +908,7 @@ template <typename T, bool F8, int MODE> struct Softmax {
     }
     const size_t piece = piece_floats(BM, g.hd);
     float* mine = g.part + pc.slot(sm.plan, it, blockIdx.x) * piece;
+#pragma unroll 1
     for (int c = c0; c < c1; c += 16) {
       float o[16];
       take(o, c, f0, f1, two);
@@ -648,19 +937,23 @@ template <typename T, bool F8, int MODE> struct Softmax {
     if (!last || !valid) return true;
     __threadfence();
     float M = -INFINITY;
+#pragma unroll 1
     for (int c = pc.c0; c <= pc.c1; ++c)
       M = fmaxf(M, __ldcg(g.part + pc.slot(sm.plan, it, c) * piece + (size_t)BM * g.hd + r));
     float L = 0.f;
+#pragma unroll 1
     for (int c = pc.c0; c <= pc.c1; ++c) {
       const float* x = g.part + pc.slot(sm.plan, it, c) * piece + (size_t)BM * g.hd + r;
       const float mc = __ldcg(x);
       L += __ldcg(x + BM) * (mc == -INFINITY ? 0.f : exp2_fast(mc - base_of(M)));
     }
     const float inv = L == 0.f ? 0.f : g.v_scale / L;
+#pragma unroll 1
     for (int c = c0; c < c1; c += 16) {
       float o[16];
 #pragma unroll
       for (int j = 0; j < 16; ++j) o[j] = 0.f;
+#pragma unroll 1
       for (int p = pc.c0; p <= pc.c1; ++p) {
         const float* x = g.part + pc.slot(sm.plan, it, p) * piece;
         const float mc = __ldcg(x + (size_t)BM * g.hd + r), f = mc == -INFINITY ? 1.f : exp2_fast(mc - base_of(M));
@@ -696,18 +989,19 @@ template <typename T, bool F8, int MODE> struct Softmax {
       const int nt = it.k1 - it.k0, item = items % kItems;
       int klo, khi;
       keys_of(g, it, MODE == kTwoQ ? w * 128 + row : row, &klo, &khi);
+      const Edges<KT> edges(g, it);
       m = -INFINITY, l = 0.f;
       bool fresh = true;
       for (int k = MODE == kOneQ ? w : 0; k < nt; k += MODE == kOneQ ? 2 : 1) {
         const int buf = MODE == kWide ? k & 1 : w;
-        if (!tc::mbar_wait(tc::su32(&sm.s_full[buf]), s_phase[buf], abort)) return;
+        if (!wait_for(sm.s_full[buf], s_phase[buf], abort)) return;
         s_phase[buf] ^= 1u;
         tc::tc_fence_after();
         bool ok = true;
-        tile(it, it.tile0 + it.k0 + k, (tiles + k) % kTileBits, (uint32_t)(buf * KT),
+        tile(edges, it.tile0 + it.k0 + k, (tiles + k) % kTileBits, (uint32_t)(buf * KT),
              MODE == kWide ? S::O0 : w ? S::O1 : S::O0, fresh, klo, khi, [&] {
                // kTwoQ, kOneQ: the scores were asked for after those products
-               if (MODE == kWide) ok = tc::mbar_wait(tc::su32(&sm.o_done[0]), o_phase[0] ^ (uint32_t)((k - 1) & 1), abort);
+               if (MODE == kWide) ok = wait_for(sm.o_done[0], o_phase[0] ^ (uint32_t)((k - 1) & 1), abort);
                return ok;
              });
         if (!ok) return;
@@ -715,18 +1009,18 @@ template <typename T, bool F8, int MODE> struct Softmax {
         fresh = false;
       }
       if (MODE == kTwoQ) {
-        if (!tc::mbar_wait(tc::su32(&sm.o_done[w]), o_phase[w], abort)) return;
+        if (!wait_for(sm.o_done[w], o_phase[w], abort)) return;
         o_phase[w] ^= 1u;
       } else if (MODE == kOneQ) {
-        if (!tc::mbar_wait(tc::su32(&sm.o_done[0]), o_phase[0], abort)) return;
+        if (!wait_for(sm.o_done[0], o_phase[0], abort)) return;
         o_phase[0] ^= 1u;
         if (nt > 1) {
-          if (!tc::mbar_wait(tc::su32(&sm.o_done[1]), o_phase[1], abort)) return;
+          if (!wait_for(sm.o_done[1], o_phase[1], abort)) return;
           o_phase[1] ^= 1u;
         }
       } else {
         // a phase a tile
-        if (!tc::mbar_wait(tc::su32(&sm.o_done[0]), o_phase[0] ^ (uint32_t)((nt - 1) & 1), abort)) return;
+        if (!wait_for(sm.o_done[0], o_phase[0] ^ (uint32_t)((nt - 1) & 1), abort)) return;
         o_phase[0] ^= (uint32_t)(nt & 1);
       }
       tc::tc_fence_after();
@@ -750,7 +1044,7 @@ template <typename T, bool F8, int MODE> __global__ void __launch_bounds__(kTcTh
   using S = Shape<MODE>;
   extern __shared__ uint8_t dyn[];
   __shared__ __align__(16) TcSmem sm;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
   const uint32_t base = (tc::su32(dyn) + 1023u) & ~1023u;
   if (tid == 0) {
     sm.abort = 0;
@@ -761,6 +1055,7 @@ template <typename T, bool F8, int MODE> __global__ void __launch_bounds__(kTcTh
     tc::mbar_init(tc::su32(&sm.q_full), 4);
     tc::mbar_init(tc::su32(&sm.q_empty), 1);
     tc::mbar_init(tc::su32(&sm.drain), 1);
+    for (int i = 0; i < 4; ++i) tc::mbar_init(tc::su32(&sm.landed[i]), 1);
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(tc::su32(&sm.s_full[i]), 1);
       tc::mbar_init(tc::su32(&sm.p_full[i]), 4);
@@ -788,11 +1083,11 @@ template <typename T, bool F8, int MODE> __global__ void __launch_bounds__(kTcTh
     if (MODE != kWide || warp < 4) Softmax<T, F8, MODE>(a.g, sm, tmem, warp >> 2, warp & 3, lane).run();
   } else if (warp < 12) {
     regs_dec<kLoaderRegs>();
-    Loader<T, F8, MODE>(a, sm, base, warp - 8, lane).run();
+    if (!F8 && a.l.runs) Loader<T, F8, MODE>::run_tensor(a, sm, base, warp - 8, lane);
+    else Loader<T, F8, MODE>::run(a, sm, base, warp - 8, lane);
   } else {
     regs_dec<kMmaRegs>();
-    if (warp == 12 && lane == 0) issue_mmas<T, MODE>(a, sm, base, tmem);
-    __syncwarp();
+    if (warp == 12) issue_mmas<T, MODE>(a, sm, base, tmem);
   }
   tc::tc_fence_before();
   __syncthreads();
