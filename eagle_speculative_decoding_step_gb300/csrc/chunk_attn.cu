@@ -299,9 +299,6 @@ static spec_status launch_fma(const spec_attn_desc& d, const Args& g, int sms, c
   return cuda_status(launch_pdl(k.fn, dim3(sms * k.per_sm), dim3(k.threads), k.smem, st, g));
 }
 
-// always the same limit: another thread may be launching the same kernel with another head size
-constexpr int kTcSmem = 208 * 1024;
-
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);

@@ -7,9 +7,8 @@
 // a row: no shuffles, its maximum and sum in registers.
 //   warps 0-3, 4-7   two softmax warpgroups
 //   warps 8-11       K/V and Q into shared memory (any block size, any alignment of runs)
-//   warp 12          one thread issues all MMAs
-// The MMA thread keeps two S buffers in flight: while a warpgroup works on one job's
-// scores, the tensor cores do the other's products.
+//   warp 12          issues the MMAs
+// While one warpgroup works on its scores, the tensor cores do the other's products.
 #pragma once
 #include <type_traits>
 
@@ -28,10 +27,13 @@ constexpr int kTcThreads = 512;
 // 512 threads are launched with 128 registers each and share them out: 2 x 128 x 200 + 128 x 72 + 128 x 40
 constexpr int kSoftmaxRegs = 200, kLoaderRegs = 72, kMmaRegs = 40;
 static_assert(2 * kSoftmaxRegs + kLoaderRegs + kMmaRegs <= 4 * 128, "");
+// dynamic shared memory of a launch, at most; the attribute is always this: another thread may be launching the same kernel
+// with another head size
+constexpr int kTcSmem = 208 * 1024;
 constexpr int kMaxStages = 8, kTileBits = 8;
 constexpr int kRawStages = 2;            // 8-bit tiles under way, before they are widened
-// An item's masks are used again 8 items later: the loader is at most two items ahead of a warpgroup, and the
-// warpgroups at most one apart, so the first of them may clear those of two items ago.
+// An item's masks are used again 8 items later: the streams are at most two items apart (one's next-but-one Q waits for the
+// other's scores of the item before it) and the loader one ahead of the first, so that stream clears those of four items ago.
 constexpr int kItems = 8;
 
 template <int MODE> struct Shape {
@@ -54,7 +56,7 @@ template <int MODE> static inline Layout layout(int hd, bool f8) {
   l.q_bytes = S::BM * 128 * l.chunks;
   l.stage_bytes = S::KT * 128 * l.chunks;
   l.raw_bytes = f8 ? S::KT * hd : 0;
-  const int room = 208 * 1024 - 1024 - l.q_bytes - kRawStages * l.raw_bytes;
+  const int room = kTcSmem - 1024 - l.q_bytes - kRawStages * l.raw_bytes;
   l.stages = room / l.stage_bytes < kMaxStages ? room / l.stage_bytes : kMaxStages;
   l.smem = 1024 + l.q_bytes + l.stages * l.stage_bytes + kRawStages * l.raw_bytes;
   return l;
@@ -173,6 +175,29 @@ template <typename T> SPEC_DEV uint32_t idesc_of(int N, bool b_mn) {
   return (1u << 4) | (f << 7) | (f << 10) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | (8u << 24);
 }
 
+// two floats in an instruction
+struct Two {
+  unsigned long long x;
+  SPEC_DEV Two() {}
+  SPEC_DEV Two(float a, float b) { asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(a), "f"(b)); }
+  SPEC_DEV void get(float& a, float& b) const { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x)); }
+};
+SPEC_DEV Two add2(Two a, Two b) {
+  Two d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d.x) : "l"(a.x), "l"(b.x));
+  return d;
+}
+SPEC_DEV Two fma2(Two a, Two b, Two c) {
+  Two d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d.x) : "l"(a.x), "l"(b.x), "l"(c.x));
+  return d;
+}
+SPEC_DEV float max3(float a, uint32_t b, uint32_t c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(__uint_as_float(b)), "f"(__uint_as_float(c)));
+  return d;
+}
+
 template <typename T> SPEC_DEV uint32_t pack2(float lo, float hi) {
   if constexpr (std::is_same_v<T, __half>) {
     const __half2 h = __floats2half2_rn(lo, hi);
@@ -205,7 +230,7 @@ template <typename T> SPEC_DEV uint2 widen4(uint32_t x) {
 
 struct TcSmem {
   Plan plan;
-  uint64_t full[kMaxStages], empty[kMaxStages], q_full, q_empty, drain, landed[4], s_full[2], p_full[2], o_done[2], o_free[2], group[2];
+  uint64_t full[kMaxStages], empty[kMaxStages], q_full, q_empty, drain, landed[4], s_full[2], p_full[2][2], o_done[2], o_free[2], group[2];
   alignas(16) uint32_t bits[kTileBits][4];   // keys of a tile that are there
   uint32_t poison[kItems][2 * 6][4];   // keys of an item's edge tiles whose value is not finite
   int poisoned[kItems];
@@ -580,10 +605,15 @@ SPEC_DEV bool elect_one() {
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
   return one != 0;
 }
-SPEC_DEV bool warp_wait(uint64_t& bar, uint32_t parity, volatile int* abort) {
-  return __all_sync(0xffffffffu, wait_for(bar, parity, abort));
-}
+// Waits without an answer, so that the warp's path does not depend on it: after a timeout every wait returns at once, and
+// what is issued meanwhile works on whatever is there.  (A path that does is 100 cycles longer a wait.)
+SPEC_DEV void settle(uint64_t& bar, uint32_t parity, volatile int* abort) { (void)wait_for(bar, parity, abort); }
 
+// Jobs of an item, in the order of their MMAs: kTwoQ: (tile 0, rows 0-127), (tile 0, rows 128-255), (tile 1, ...), ...;
+// otherwise the tiles, for two streams in turns (kOneQ) or one (kWide).  The products of job k with V, then the scores of
+// job k + 2, which go over its weights: one warp for both streams, so that they stay half a period apart and their softmax
+// warps do not all want the special function units at the same time.
+// The weights of a job come in halves, so that the products begin with whichever half is there.
 template <typename T, int MODE> SPEC_DEV void issue_mmas(const TcArgs& a, TcSmem& sm, uint32_t base_, uint32_t tmem_) {
   using S = Shape<MODE>;
   constexpr int KT = S::KT;
@@ -602,44 +632,51 @@ template <typename T, int MODE> SPEC_DEV void issue_mmas(const TcArgs& a, TcSmem
   const uint64_t q_desc = tc::desc_sw128(base), k_desc = tc::desc_sw128(ring0), v_desc = desc_values(ring0, KT * 128);
   const uint32_t q_lo = (uint32_t)q_desc, k_lo = (uint32_t)k_desc, v_lo = (uint32_t)v_desc;
   const uint32_t s_hi = (uint32_t)(k_desc >> 32), v_hi = (uint32_t)(v_desc >> 32), stage16 = (uint32_t)l.stage_bytes >> 4;
-  bool first = true, ok = true;
-  while (ok && __any_sync(0xffffffffu, walk.next(it))) {
+  bool first = true;
+  while (__any_sync(0xffffffffu, walk.next(it)) && !__any_sync(0xffffffffu, *abort != 0)) {
     const int jobs = uniform((it.k1 - it.k0) * (MODE == kTwoQ ? 2 : 1));
-    if (!warp_wait(sm.q_full, q_phase, abort)) break;
+    settle(sm.q_full, q_phase, abort);
     q_phase ^= 1u;
-    // Jobs k: the scores are two ahead of the products with V.
 #pragma unroll 1
     for (int k = -2; k < jobs; ++k) {
       const int buf = k & 1;
+      const bool last_use = MODE != kTwoQ || buf;      // of the K and V tiles
       if (k >= 0) {
         const int acc = MODE == kWide ? 0 : buf;
         const bool fresh = MODE == kWide ? k == 0 : k < 2;
-        if (!(ok = warp_wait(sm.full[v_st], v_ph, abort))) break;
+        if (MODE != kTwoQ || !buf) settle(sm.full[v_st], v_ph, abort);
         if (fresh && !first) {         // the last item's accumulator has been read
-          if (!(ok = warp_wait(sm.o_free[acc], free_phase >> acc & 1u, abort))) break;
+          settle(sm.o_free[acc], free_phase >> acc & 1u, abort);
           free_phase ^= 1u << acc;
         }
-        if (!(ok = warp_wait(sm.p_full[buf], p_phase >> buf & 1u, abort))) break;
-        p_phase ^= 1u << buf;
-        tc::tc_fence_after();
-        if (elect_one()) {
-          const uint32_t b = v_lo + v_st * stage16;
-          const uint32_t d = tmem + (uint32_t)(acc ? S::O1 : S::O0), p = tmem + (uint32_t)(buf * KT);
+        const uint32_t b = v_lo + v_st * stage16;
+        const uint32_t d = tmem + (uint32_t)(acc ? S::O1 : S::O0), p = tmem + (uint32_t)(buf * KT);
 #pragma unroll
-          for (int kk = 0; kk < KT / 16; ++kk)
-            mma_ts(d, p + 8 * kk, b + (kk * 2048 >> 4), v_hi, id_o, kk > 0 ? 1u : fresh ? 0u : 1u);
-          if (MODE != kTwoQ || buf) tc::tc_commit(tc::su32(&sm.empty[v_st]));
-          if (MODE == kWide || k >= jobs - 2) tc::tc_commit(tc::su32(&sm.o_done[acc]));
+        for (int h = 0; h < 2; ++h) {
+          settle(sm.p_full[buf][h], p_phase >> buf & 1u, abort);
+          tc::tc_fence_after();
+          if (elect_one()) {
+#pragma unroll
+            for (int i = 0; i < KT / 32; ++i) {
+              const int kk = h * (KT / 32) + i;
+              mma_ts(d, p + 8 * kk, b + (kk * 2048 >> 4), v_hi, id_o, kk > 0 ? 1u : fresh ? 0u : 1u);
+            }
+            if (h && last_use) tc::tc_commit(tc::su32(&sm.empty[v_st]));
+            if (h && (MODE == kWide || k >= jobs - 2)) tc::tc_commit(tc::su32(&sm.o_done[acc]));
+          }
+          __syncwarp();
         }
-        __syncwarp();
-        if (MODE != kTwoQ || buf) {
+        p_phase ^= 1u << buf;
+        if (last_use) {
           v_st += 2;
           if (v_st >= l.stages) v_st -= l.stages, v_ph ^= 1u;
         }
       }
       if (k + 2 < jobs) {
-        if (!(ok = warp_wait(sm.full[k_st], k_ph, abort))) break;
-        tc::tc_fence_after();
+        if (MODE != kTwoQ || !buf) {
+          settle(sm.full[k_st], k_ph, abort);
+          tc::tc_fence_after();
+        }
         if (elect_one()) {
           uint32_t qa = q_lo + (MODE == kTwoQ ? (uint32_t)(buf * l.chunks) * (16384 >> 4) : 0u), kb = k_lo + k_st * stage16;
           const uint32_t d = tmem + (uint32_t)(buf * KT);
@@ -652,19 +689,19 @@ template <typename T, int MODE> SPEC_DEV void issue_mmas(const TcArgs& a, TcSmem
             if (n > 3) mma_ss<true>(d, qa + 6, s_hi, kb + 6, s_hi, id_s);
           }
           tc::tc_commit(tc::su32(&sm.s_full[buf]));
-          if (MODE != kTwoQ || buf) tc::tc_commit(tc::su32(&sm.empty[k_st]));
+          if (last_use) tc::tc_commit(tc::su32(&sm.empty[k_st]));
           if (k + 2 == jobs - 1) tc::tc_commit(tc::su32(&sm.q_empty));
         }
         __syncwarp();
-        if (MODE != kTwoQ || buf) {
+        if (last_use) {
           k_st += 2;
           if (k_st >= l.stages) k_st -= l.stages, k_ph ^= 1u;
         }
       }
     }
     // (kOneQ with a single tile: the second accumulator is not used, nor waited for)
-    if (MODE == kOneQ && jobs == 1 && ok && !first) {
-      ok = warp_wait(sm.o_free[1], free_phase >> 1, abort);
+    if (MODE == kOneQ && jobs == 1 && !first) {
+      settle(sm.o_free[1], free_phase >> 1, abort);
       free_phase ^= 2u;
     }
     first = false;
@@ -721,14 +758,11 @@ template <typename T, bool F8, int MODE> struct Softmax {
     return below_b & ~below_a;
   }
 
-  // One tile: scores in TMEM columns s0 -> weights there.  o0: the accumulator; fresh: nothing is in it.
+  // One tile: scores in an S buffer -> weights there, handed over by halves.  o0: the accumulator; fresh: nothing is in it.
   // done: waits until the products of the last tile are in the accumulator (kWide).
-  // The scores are read from TMEM twice, 32 columns at a time in short loops: holding 128 of them in registers unrolls
-  // the code to 17 KB, and the roles' loops then push one another out of the SM's instruction cache (every role ran
-  // three times slower).
-  template <typename Done> SPEC_DEV void tile(const Edges<KT>& edges, int tile, int bits, uint32_t s0, uint32_t o0, bool fresh,
+  template <typename Done> SPEC_DEV void tile(const Edges<KT>& edges, int tile, int bits, int buf, uint32_t o0, bool fresh,
                                               int klo, int khi, Done&& done) {
-    const uint32_t at = tm + s0;
+    const uint32_t at = tm + (uint32_t)(buf * KT);
     __syncwarp();
     const uint4 there = *reinterpret_cast<const uint4*>(sm.bits[bits]);
     const uint32_t all = KT == 128 ? there.x & there.y & there.z & there.w : there.x & there.y;
@@ -748,24 +782,17 @@ template <typename T, bool F8, int MODE> struct Softmax {
       }
       tmem_st_wait();
     }
-    uint32_t x[2][32];
-    float top = -INFINITY, other = -INFINITY;
-    tmem_ld32(at, x[0]);
-#pragma unroll 1
-    for (int i = 0; i < KT / 32; i += 2) {
+    uint32_t x[KT];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        tc::tmem_ld_wait();
-        // the next columns; at the end the first ones again, for the second pass
-        tmem_ld32(at + 32 * ((i + h + 1) & (KT / 32 - 1)), x[1 - h]);
+    for (int i = 0; i < KT / 32; ++i) tmem_ld32(at + 32 * i, x + 32 * i);
+    tc::tmem_ld_wait();
+    float t0 = -INFINITY, t1 = -INFINITY, t2 = -INFINITY, t3 = -INFINITY;
 #pragma unroll
-        for (int j = 0; j < 32; j += 4) {
-          top = fmaxf(fmaxf(top, __uint_as_float(x[h][j])), __uint_as_float(x[h][j + 1]));
-          other = fmaxf(fmaxf(other, __uint_as_float(x[h][j + 2])), __uint_as_float(x[h][j + 3]));
-        }
-      }
+    for (int j = 0; j < KT; j += 8) {
+      t0 = max3(t0, x[j], x[j + 1]), t1 = max3(t1, x[j + 2], x[j + 3]);
+      t2 = max3(t2, x[j + 4], x[j + 5]), t3 = max3(t3, x[j + 6], x[j + 7]);
     }
-    const float now = fmaxf(fmaxf(top, other) * g.scale2, m);
+    const float now = fmaxf(fmaxf(fmaxf(t0, t1), fmaxf(t2, t3)) * g.scale2, m);
     bool in = fresh;
     if (fresh) {
       m = now;
@@ -788,28 +815,30 @@ template <typename T, bool F8, int MODE> struct Softmax {
       m = now;
     }
     const float base = W::kShift - base_of(m);
-    float sum0 = 0.f, sum1 = 0.f;
-#pragma unroll 1
-    for (int i = 0; i < KT / 32; i += 2) {
+    const Two b2(base, base), scale(g.scale2, g.scale2);
+    Two sum(0.f, 0.f);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        tc::tmem_ld_wait();
-        // (the weights of columns 32 i go to columns 16 i, which have been read)
-        if (h == 0 || i + 2 < KT / 32) tmem_ld32(at + 32 * (i + h + 1), x[1 - h]);
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int i = h * (KT / 64); i < (h + 1) * (KT / 64); ++i) {
         uint32_t p[16];
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
-          const float u = exp2_fast(fmaf(__uint_as_float(x[h][2 * j]), g.scale2, base));
-          const float v = exp2_fast(fmaf(__uint_as_float(x[h][2 * j + 1]), g.scale2, base));
-          sum0 += u, sum1 += v;
+          float u, v;
+          fma2(Two(__uint_as_float(x[32 * i + 2 * j]), __uint_as_float(x[32 * i + 2 * j + 1])), scale, b2).get(u, v);
+          u = exp2_fast(u), v = exp2_fast(v);
+          sum = add2(sum, Two(u, v));
           p[j] = pack2<T>(u, v);
         }
-        tmem_st16(at + 16 * (i + h), p);
+        tmem_st16(at + 16 * i, p);
       }
+      tmem_st_wait();
+      if (h == 1 && !in) done();           // (every phase is waited for in its turn)
+      arrive(sm.p_full[buf][h]);
     }
-    tmem_st_wait();
-    l += sum0 + sum1;
-    if (!in) done();                       // every phase is waited for in its turn
+    float u, v;
+    sum.get(u, v);
+    l += u + v;
   }
 
   // A value that is not finite, of a key of an edge tile that the row attends to
@@ -858,19 +887,12 @@ template <typename T, bool F8, int MODE> struct Softmax {
     }
   }
 
-  SPEC_DEV void write(const Item& it, int r, int c, const float* o, float inv) {
-    const int tok = (it.r0 + r) / g.G, head = it.h * g.G + (it.r0 + r) - tok * g.G;
-    uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(g.out) + (it.row0 + tok) * g.out_ld + (long long)head * g.hd + c);
+  static SPEC_DEV void write(T* dst, const float* o, float inv) {
     uint32_t u[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) u[j] = pack2<T>(o[2 * j] * inv, o[2 * j + 1] * inv);
-    dst[0] = make_uint4(u[0], u[1], u[2], u[3]);
-    dst[1] = make_uint4(u[4], u[5], u[6], u[7]);
-  }
-  SPEC_DEV void write_lse(const Item& it, int r, float m_, float l_) {
-    if (!g.lse) return;
-    const int tok = (it.r0 + r) / g.G, head = it.h * g.G + (it.r0 + r) - tok * g.G;
-    g.lse[(long long)(it.row0 + tok) * g.nq + head] = l_ == 0.f ? -INFINITY : (m_ - W::kShift + log2f(l_)) * kLn2;
+    reinterpret_cast<uint4*>(dst)[0] = make_uint4(u[0], u[1], u[2], u[3]);
+    reinterpret_cast<uint4*>(dst)[1] = make_uint4(u[4], u[5], u[6], u[7]);
   }
 
   // The item's rows, or their piece; the last piece to come joins all.
@@ -892,6 +914,9 @@ template <typename T, bool F8, int MODE> struct Softmax {
     const int c0 = MODE == kOneQ && w ? 16 * half : 0, c1 = MODE == kOneQ && !w ? 16 * half : g.hd;
     const int r = MODE == kTwoQ ? w * 128 + row : row;
     const bool valid = r < it.rows, poisoned = sm.poisoned[item] != 0;
+    const int tok = (it.r0 + r) / g.G, head = it.h * g.G + (it.r0 + r) - tok * g.G;
+    T* dst = static_cast<T*>(g.out) + (it.row0 + tok) * g.out_ld + (long long)head * g.hd;
+    float* lse = g.lse && c0 == 0 ? g.lse + (long long)(it.row0 + tok) * g.nq + head : nullptr;
     const Pieces pc(sm.plan, it);
     if (pc.c0 == pc.c1) {
       const float inv = l == 0.f ? 0.f : g.v_scale / l;
@@ -900,9 +925,9 @@ template <typename T, bool F8, int MODE> struct Softmax {
         float o[16];
         take(o, c, f0, f1, two);
         if (poisoned && valid) mend(it, item, klo, khi, c, o);
-        if (valid) write(it, r, c, o, inv);
+        if (valid) write(dst + c, o, inv);
       }
-      if (valid && c0 == 0) write_lse(it, r, m, l);
+      if (valid && lse) *lse = l == 0.f ? -INFINITY : (m - W::kShift + log2f(l)) * kLn2;
       release();
       return true;
     }
@@ -964,9 +989,9 @@ template <typename T, bool F8, int MODE> struct Softmax {
           o[4 * j + 2] = fmaf(v.z, f, o[4 * j + 2]), o[4 * j + 3] = fmaf(v.w, f, o[4 * j + 3]);
         }
       }
-      write(it, r, c, o, inv);
+      write(dst + c, o, inv);
     }
-    if (c0 == 0) write_lse(it, r, M, L);
+    if (lse) *lse = L == 0.f ? -INFINITY : (M - W::kShift + log2f(L)) * kLn2;
     return true;
   }
   // the accumulators have been read
@@ -998,14 +1023,13 @@ template <typename T, bool F8, int MODE> struct Softmax {
         s_phase[buf] ^= 1u;
         tc::tc_fence_after();
         bool ok = true;
-        tile(edges, it.tile0 + it.k0 + k, (tiles + k) % kTileBits, (uint32_t)(buf * KT),
+        tile(edges, it.tile0 + it.k0 + k, (tiles + k) % kTileBits, buf,
              MODE == kWide ? S::O0 : w ? S::O1 : S::O0, fresh, klo, khi, [&] {
                // kTwoQ, kOneQ: the scores were asked for after those products
                if (MODE == kWide) ok = wait_for(sm.o_done[0], o_phase[0] ^ (uint32_t)((k - 1) & 1), abort);
                return ok;
              });
         if (!ok) return;
-        arrive(sm.p_full[buf]);
         fresh = false;
       }
       if (MODE == kTwoQ) {
@@ -1028,7 +1052,7 @@ template <typename T, bool F8, int MODE> struct Softmax {
       __syncwarp();
       if (!ok) return;
       if (w == 0) {
-        const int old = (items + kItems - 2) % kItems;
+        const int old = (items + kItems - 4) % kItems;
         if (row < 2 * 6 * 4) (&sm.poison[old][0][0])[row] = 0;
         if (row == 0) sm.poisoned[old] = 0;
       }
@@ -1058,7 +1082,8 @@ template <typename T, bool F8, int MODE> __global__ void __launch_bounds__(kTcTh
     for (int i = 0; i < 4; ++i) tc::mbar_init(tc::su32(&sm.landed[i]), 1);
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(tc::su32(&sm.s_full[i]), 1);
-      tc::mbar_init(tc::su32(&sm.p_full[i]), 4);
+      tc::mbar_init(tc::su32(&sm.p_full[i][0]), 4);
+      tc::mbar_init(tc::su32(&sm.p_full[i][1]), 4);
       tc::mbar_init(tc::su32(&sm.o_done[i]), 1);
       tc::mbar_init(tc::su32(&sm.o_free[i]), MODE == kOneQ ? 8 : 4);
       tc::mbar_init(tc::su32(&sm.group[i]), MODE == kOneQ ? 8 : 4);
@@ -1097,6 +1122,8 @@ template <typename T, bool F8, int MODE> __global__ void __launch_bounds__(kTcTh
   }
   if (tid == 0 && sm.abort) report(a.g.ws, SPEC_ERR_TIMEOUT, blockIdx.x, 0);
 }
+
+static_assert(kTcSmem + sizeof(TcSmem) <= 227 * 1024, "");
 
 typedef void (*TcFn)(TcArgs);
 // by type (chunk_attn_<type>.cu)
