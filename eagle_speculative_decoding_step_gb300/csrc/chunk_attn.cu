@@ -376,7 +376,7 @@ extern "C" spec_status spec_chunk_attention(const spec_attn_desc* desc, const vo
   ca::Args g{};
   g.kv = *kv, g.q = q, g.out = out, g.lse = lse, g.cu = cu_rows, g.seq_len = seq_len, g.q_ld = q_ld, g.out_ld = out_ld;
   g.n_rows = n_rows, g.nq = d.n_q_heads, g.nkv = d.n_kv_heads, g.G = d.n_q_heads / d.n_kv_heads, g.hd = d.head_dim;
-  g.window = d.window < kv->max_blocks * kv->block_size ? d.window : 0, g.min_tiles = 1;
+  g.window = d.window < kv->max_blocks * kv->block_size ? d.window : 0;
   g.scale2 = (d.scale > 0 ? d.scale : 1.f / sqrtf((float)d.head_dim)) * (e4m3 ? d.k_scale : 1.f) * ca::kLog2e;
   g.v_scale = e4m3 ? d.v_scale : 1.f;
   g.part = reinterpret_cast<float*>(static_cast<char*>(ws) + kWsHeader);

@@ -21,6 +21,7 @@ namespace ca {
 enum : unsigned { kTLChunkAttn = 29 };   // after the other units' ids
 
 constexpr int kMaxB = 1024;              // requests of a launch
+constexpr int kWhole = 4;                // tiles of an item that is not cut while there are CTAs for all
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 struct Args {
@@ -31,7 +32,6 @@ struct Args {
   const int32_t *cu, *seq_len;
   long long q_ld, out_ld;
   int B, b0, n_rows, nq, nkv, G, hd, window;
-  int min_tiles;               // tiles of a share, at least
   float scale2;                // softmax scale (and k_scale) times log2(e)
   float v_scale;
   float* part;                 // [grid][2] pieces of piece_floats()
@@ -89,6 +89,8 @@ struct Plan {
   int pairs[kMaxB + 1];        // prefix sums of the items of a kv head by request
   long long total, begin, end; // tiles in all, and this CTA's
   int ctas;
+  int longest;                 // tiles of an item, at most
+  bool whole;                  // an item a CTA
   int h, b, t, off;            // where this CTA begins
 };
 
@@ -105,7 +107,7 @@ template <int BM, int KT> SPEC_DEV void make_plan(const Args& g, Plan& p, int ti
     p.pairs[b + 1] = (int)(((long long)r.n * g.G + BM - 1) / BM);
     p.work[b + 1] = 0;
   }
-  if (tid == 0) p.pairs[0] = 0, p.work[0] = 0;
+  if (tid == 0) p.pairs[0] = 0, p.work[0] = 0, p.longest = 0;
   __syncthreads();
   if (tid < 32) {
     int run = 0;
@@ -134,6 +136,7 @@ template <int BM, int KT> SPEC_DEV void make_plan(const Args& g, Plan& p, int ti
     Item it;
     geometry<BM, KT>(g, request(g, lo), i - p.pairs[lo], it);
     atomicAdd(reinterpret_cast<unsigned long long*>(&p.work[lo + 1]), (unsigned long long)it.tiles);
+    atomicMax(&p.longest, it.tiles);
   }
   __syncthreads();
   if (tid < 32) {
@@ -150,13 +153,31 @@ template <int BM, int KT> SPEC_DEV void make_plan(const Args& g, Plan& p, int ti
       run += __shfl_sync(0xffffffffu, x, 31);
     }
     __syncwarp();
-    const long long one = run, total = one * g.nkv;
-    const int ctas = (int)max(1ll, min((long long)gridDim.x, total / g.min_tiles));
+    const long long one = run, total = one * g.nkv, all_items = (long long)items * g.nkv;
     const int c = blockIdx.x;
-    const long long begin = c < ctas ? total * c / ctas : total, end = c < ctas ? total * (c + 1) / ctas : total;
+    // Short items that have a CTA each stay whole: 32 items of 2 or 3 tiles, in shares of one tile 24 us, whole 19.
+    const bool whole = all_items <= gridDim.x && p.longest <= kWhole;
+    const int ctas = whole ? (int)max(1ll, all_items) : (int)max(1ll, min((long long)gridDim.x, total));
+    long long begin = c < ctas ? total * c / ctas : total, end = c < ctas ? total * (c + 1) / ctas : total;
     int h = 0, b = 0, t = 0;
     long long rem = 0;
-    if (begin < end) {
+    if (whole) {
+      begin = end = 0;
+      if (c < all_items) {
+        h = c / items;
+        const int i = c - h * items;
+        int lo = 0, hi = g.B;
+        while (hi - lo > 1) {
+          const int mid = (lo + hi) >> 1;
+          if (p.pairs[mid] <= i) lo = mid;
+          else hi = mid;
+        }
+        b = lo, t = i - p.pairs[lo];
+        Item it;
+        geometry<BM, KT>(g, request(g, b), t, it);
+        end = it.tiles;
+      }
+    } else if (begin < end) {
       h = (int)(begin / one);
       rem = begin - h * one;
       int lo = 0, hi = g.B;    // the last request whose prefix is at or below: it has tiles
@@ -192,7 +213,7 @@ template <int BM, int KT> SPEC_DEV void make_plan(const Args& g, Plan& p, int ti
       }
     }
     if (tid == 0) {
-      p.total = total, p.begin = begin, p.end = end, p.ctas = ctas;
+      p.total = total, p.begin = begin, p.end = end, p.ctas = ctas, p.whole = whole;
       p.h = h, p.b = b, p.t = t, p.off = (int)rem;
     }
   }
@@ -227,7 +248,8 @@ template <int BM, int KT> struct Walk {
 // Where the pieces of an item are: CTAs c0 .. c1, each in its first or second slot.
 struct Pieces {
   int c0, c1;
-  SPEC_DEV Pieces(const Plan& p, const Item& it) : c0(owner(p, it.pos)), c1(owner(p, it.pos + it.tiles - 1)) {}
+  SPEC_DEV Pieces(const Plan& p, const Item& it)
+      : c0(p.whole ? 0 : owner(p, it.pos)), c1(p.whole ? 0 : owner(p, it.pos + it.tiles - 1)) {}
   SPEC_DEV int slot(const Plan& p, const Item& it, int c) const { return 2 * c + (it.pos < share_begin(p, c) ? 0 : 1); }
 };
 

@@ -267,14 +267,6 @@ template <typename T, bool F8, int MODE> struct Loader {
     atomicOr(&sm.poison[info >> 8][info & 255][key >> 5], 1u << (key & 31));
     sm.poisoned[info >> 8] = 1;
   }
-  static SPEC_DEV uint4 clean(TcSmem& sm, uint4 v, int info, int key) {
-    const uint32_t a = odd_halves<T>(v.x), b = odd_halves<T>(v.y), c = odd_halves<T>(v.z), d = odd_halves<T>(v.w);
-    if (a | b | c | d) {
-      mark(sm, info, key);
-      v.x &= ~a, v.y &= ~b, v.z &= ~c, v.w &= ~d;
-    }
-    return v;
-  }
   // rows r0 .. of a warp, whose slots (-1: none) its lanes hold
   template <int U> static SPEC_DEV void copy_rows(const char* base, uint32_t stride, int slot, uint32_t to, int r0, int lane,
                                                   int units) {
@@ -296,19 +288,24 @@ template <typename T, bool F8, int MODE> struct Loader {
       }
     }
   }
-  static SPEC_DEV void widen_rows(TcSmem& sm, uint32_t from, uint32_t to, int r0, int lane, int units, int info) {
-    const Units<0> un(units);
-    const int n = RW * units;
-#pragma unroll 2
-    for (int i = lane; i < n; i += 32) {
-      const int row = un.row(i), u = i - row * units, r = r0 + row;
-      const uint4 x = lds128(from + (uint32_t)(r * units + u) * 16);
+  // 8-bit rows -> 16-bit ones in the ring, four pieces of a lane at a time (one warp's latencies are what this takes)
+  template <int U> static SPEC_DEV void widen_rows(uint32_t from, uint32_t to, int r0, int lane, int units) {
+    const Units<U> un(units);
+    const int n = RW * un.n;
+    constexpr int B = U ? 4 : 2;
+#pragma unroll 1
+    for (int j = lane; j < n; j += 32 * B) {
+      uint4 x[B];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint2 a = widen4<T>(h ? x.z : x.x), b = widen4<T>(h ? x.w : x.y);
-        uint4 v = make_uint4(a.x, a.y, b.x, b.y);
-        if (info >= 0) v = clean(sm, v, info, r);
-        sts128(to + place(r, 2 * u + h, KT), v);
+      for (int q = 0; q < B; ++q)
+        if (j + 32 * q < n) x[q] = lds128(from + (uint32_t)(r0 * un.n + j + 32 * q) * 16);
+#pragma unroll
+      for (int q = 0; q < B; ++q) {
+        const int i = j + 32 * q, row = un.row(i), u = U ? lane % (U ? U : 1) : i - row * un.n;
+        if (i >= n) break;
+        const uint2 a = widen4<T>(x[q].x), b = widen4<T>(x[q].y), c = widen4<T>(x[q].z), d = widen4<T>(x[q].w);
+        sts128(to + place(r0 + row, 2 * u, KT), make_uint4(a.x, a.y, b.x, b.y));
+        sts128(to + place(r0 + row, 2 * u + 1, KT), make_uint4(c.x, c.y, d.x, d.y));
       }
     }
   }
@@ -528,10 +525,15 @@ template <typename T, bool F8, int MODE> struct Loader {
         const int edge = sm.info[warp][finished % kTileBits];
         if constexpr (F8) {
           if (!wait_for(sm.empty[stage], phase ^ 1u, abort)) break;
-          widen_rows(sm, raw0 + (uint32_t)f_raw * raw_bytes, ring0 + (uint32_t)stage * stage_bytes, r0, lane, units, edge);
+          const uint32_t from = raw0 + (uint32_t)f_raw * raw_bytes, to = ring0 + (uint32_t)stage * stage_bytes;
+          if (units == 8) widen_rows<8>(from, to, r0, lane, units);
+          else if (units == 4) widen_rows<4>(from, to, r0, lane, units);
+          else widen_rows<0>(from, to, r0, lane, units);
           if (++f_raw == kRawStages) f_raw = 0;
-        } else if (edge >= 0) {
-          clean_rows(sm, ring0 + (uint32_t)f_stage * stage_bytes, r0, lane, units, edge, 0xffffffffu);   // (others are zeros)
+        }
+        if (edge >= 0) {
+          __syncwarp();
+          clean_rows(sm, ring0 + (uint32_t)(F8 ? stage : f_stage) * stage_bytes, r0, lane, g.hd / 8, edge, 0xffffffffu);   // (others are zeros)
         }
         proxy_fence();
         __syncwarp();
