@@ -303,8 +303,10 @@ typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t,
                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
-// The cache as [slots][nkv][hd], boxes of 16 slots of one head and 64 components; past a head's or the cache's end: zeros
-static bool run_map(CUtensorMap* tm, const void* ptr, const spec_attn_desc& d, const spec_kv& kv) {
+// ptr as [rows][heads][hd] of 16-bit components with ld of them from a row to the next, boxes of box_heads x box_rows x 64;
+// past a head's or the last row's end: zeros
+static bool rows_map(CUtensorMap* tm, const void* ptr, int dtype, int hd, int heads, long long rows, long long ld, int box_heads,
+                     int box_rows) {
   static const EncodeTiledFn enc = [] {
     void* f = nullptr;
     cudaDriverEntryPointQueryResult q;
@@ -313,11 +315,11 @@ static bool run_map(CUtensorMap* tm, const void* ptr, const spec_attn_desc& d, c
     return ok ? reinterpret_cast<EncodeTiledFn>(f) : nullptr;
   }();
   if (!enc) return false;
-  cuuint64_t dims[3] = {(cuuint64_t)d.head_dim, (cuuint64_t)d.n_kv_heads, (cuuint64_t)kv.num_slots};
-  cuuint64_t strides[2] = {(cuuint64_t)d.head_dim * 2, (cuuint64_t)d.n_kv_heads * d.head_dim * 2};
-  cuuint32_t box[3] = {64, 1, 16};
+  cuuint64_t dims[3] = {(cuuint64_t)hd, (cuuint64_t)heads, (cuuint64_t)rows};
+  cuuint64_t strides[2] = {(cuuint64_t)hd * 2, (cuuint64_t)ld * 2};
+  cuuint32_t box[3] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_rows};
   cuuint32_t es[3] = {1, 1, 1};
-  return enc(tm, d.kv_dtype == SPEC_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+  return enc(tm, dtype == SPEC_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
              const_cast<void*>(ptr), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -329,7 +331,15 @@ static spec_status launch_tc(const spec_attn_desc& d, const Args& g, int longest
   a.g = g;
   a.l = mode == kTwoQ ? layout<kTwoQ>(d.head_dim, f8) : mode == kOneQ ? layout<kOneQ>(d.head_dim, f8) : layout<kWide>(d.head_dim, f8);
   a.l.runs = !f8 && g.kv.block_size % 16 == 0;
-  if (a.l.runs && (!run_map(&a.tmk, g.kv.k, d, g.kv) || !run_map(&a.tmv, g.kv.v, d, g.kv))) return SPEC_ERR_CUDA;
+  const long long slot = (long long)d.n_kv_heads * d.head_dim;
+  if (a.l.runs)
+    for (int i = 0; i < 2; ++i)
+      if (!rows_map(i ? &a.tmv : &a.tmk, i ? g.kv.v : g.kv.k, d.kv_dtype, d.head_dim, d.n_kv_heads, g.kv.num_slots, slot, 1, 16))
+        return SPEC_ERR_CUDA;
+  // (a row stride of 2^40 bytes and over is no tensor map's)
+  a.l.q_boxes = 128 % g.G == 0 && g.q_ld < (1ll << 38);
+  if (a.l.q_boxes && !rows_map(&a.tmq, g.q, d.dtype, d.head_dim, d.n_q_heads, g.n_rows, g.q_ld, g.G, 128 / g.G))
+    return SPEC_ERR_CUDA;
   const TcFn fn = d.dtype == SPEC_DTYPE_BF16 ? tc_kernel_bf16(f8, mode) : tc_kernel_f16(f8, mode);
   if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kTcSmem) != cudaSuccess) return SPEC_ERR_CUDA;
   return cuda_status(launch_pdl(fn, dim3(sms), dim3(kTcThreads), a.l.smem, st, a));

@@ -48,6 +48,7 @@ struct Layout {
   int q_bytes, stage_bytes, stages, raw_bytes;
   int smem;
   int runs;          // keys come in runs of 16 slots of a block, by tensor copies
+  int q_boxes;       // rows of Q come in boxes of 128 / G tokens
 };
 template <int MODE> static inline Layout layout(int hd, bool f8) {
   using S = Shape<MODE>;
@@ -64,6 +65,7 @@ template <int MODE> static inline Layout layout(int hd, bool f8) {
 
 struct TcArgs {
   CUtensorMap tmk, tmv;        // runs: [slots][nkv][hd] views of the cache, boxes of 16 slots x 64 components
+  CUtensorMap tmq;             // q_boxes: [n_rows][nq][hd] of q, boxes of 128 packed rows x 64 components
   Args g;
   Layout l;
 };
@@ -333,6 +335,26 @@ template <typename T, bool F8, int MODE> struct Loader {
       if (which >> row & 1u) sts128(at + place(r0 + row, u, KT), make_uint4(0, 0, 0, 0));
     }
   }
+  // Q by tensor copies: 128 packed rows are 128 / G tokens of G heads, in this order in a box (rows of other requests and
+  // zeros past the last token among them).  Every warp arrives at q_full.
+  static SPEC_DEV void copy_q(const TcArgs& a, TcSmem& sm, const Item& it, uint32_t q0, int warp, int lane) {
+    const uint32_t bar = tc::su32(&sm.q_full);
+    if (lane == 0) {
+      if (warp == 0) {
+        tc::mbar_expect_tx(bar, S::NQ * a.l.chunks * 16384);
+        const int token = it.row0 + it.r0 / a.g.G, per = 128 / a.g.G;
+        const uint64_t policy = tc::policy_evict_first();
+#pragma unroll 1
+        for (int i = 0; i < S::NQ * a.l.chunks; ++i) {
+          const int t = i / a.l.chunks, c = i - t * a.l.chunks;
+          copy_run(q0 + (uint32_t)i * 16384, &a.tmq, bar, 64 * c, it.h * a.g.G, token + t * per, policy);
+        }
+      } else {
+        tc::mbar_arrive(bar);
+      }
+    }
+    __syncwarp();
+  }
   static SPEC_DEV void load_q(const Args& g, const Item& it, uint32_t q0, int chunks, int warp, int lane) {
     constexpr int RQ = S::BM / 4;                      // rows of a warp
     const Units<0> un(g.hd / 8);
@@ -441,7 +463,9 @@ template <typename T, bool F8, int MODE> struct Loader {
             ok = __all_sync(0xffffffffu, wait_for(sm.q_empty, q_phase, abort));
             q_phase ^= 1u;
           }
-          if (ok) {
+          if (ok && a.l.q_boxes) {
+            copy_q(a, sm, it, q0, warp, lane);
+          } else if (ok) {
             load_q(g, it, q0, chunks, warp, lane);
             cp_commit();
             cp_wait<0>();
@@ -454,6 +478,7 @@ template <typename T, bool F8, int MODE> struct Loader {
       ++items;
     }
     cp_wait<0>();
+    if (a.l.q_boxes && warp == 0 && items > 0 && sm.abort) tc::mbar_wait(tc::su32(&sm.q_full), (uint32_t)(items - 1) & 1u, abort, false);
     if (!ok || sm.abort) {
       // gives up: the copies under way land first (or the limit passes)
       for (int i = 0; i < filled; ++i) {
@@ -553,8 +578,12 @@ template <typename T, bool F8, int MODE> struct Loader {
         if (items > 0) q_phase ^= 1u;
         ++items;
         q_due = false;
-        load_q(g, it, q0, chunks, warp, lane);
-        q_at = issued;                                 // comes with the next stage's copies
+        if (a.l.q_boxes) {
+          copy_q(a, sm, it, q0, warp, lane);
+        } else {
+          load_q(g, it, q0, chunks, warp, lane);
+          q_at = issued;                               // comes with the next stage's copies
+        }
         if (!F8 && !test(sm.empty[stage], phase ^ 1u)) continue;
       }
       if (!value) {                                    // a new tile: its slots
@@ -595,6 +624,7 @@ template <typename T, bool F8, int MODE> struct Loader {
       value = !value;
     }
     cp_wait<0>();                                      // nothing in flight when the CTA ends, or gives up
+    if (a.l.q_boxes && warp == 0 && items > 0 && sm.abort) tc::mbar_wait(tc::su32(&sm.q_full), (uint32_t)(items - 1) & 1u, abort, false);
   }
 };
 
