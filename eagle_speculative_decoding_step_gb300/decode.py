@@ -5,7 +5,9 @@ that are too many to speculate on, or that ask for beams.
 workspaces.  ``Batch`` decodes one continuation a request: every step the block
 tables grow (and finished requests give their blocks back), the new rows are
 appended, each new token attends to its request's cache, and the best token is
-selected.  ``BeamBatch`` decodes W beams a request: after every selection the beams'
+selected.  Its prompts enter in chunks (``extend``, ``score``), its requests are
+forked, dropped and their cache compacted (``fork``, ``drop``, ``compact``).
+``BeamBatch`` decodes W beams a request: after every selection the beams'
 tables, histories and partial blocks are reordered.  [NEURON] "Speculative Decoding
 (EAGLE3) in the vLLM Neuron Framework", "KV Cache Sharing" and "EagleProposer": the
 cache, its block tables and slot mapping.
@@ -47,6 +49,18 @@ def _rows(x, n, heads, hd, dtype, name):
     return x, x.stride(0) if n > 1 else heads * hd
 
 
+def _logits(logits, n, V):
+    """logits as n rows of V (copied if a row is not in one piece): the type's name, the rows, the elements from one to the
+    next."""
+    name = _LOGITS.get(logits.dtype)
+    if name is None or logits.numel() != n * V or logits.shape[-1] != V:
+        raise ValueError("logits are %s %s, not %s of floats" % (logits.dtype, tuple(logits.shape), (n, V)))
+    x = logits.reshape(n, V)
+    if x.stride(1) != 1 or (n > 1 and x.stride(0) < V):
+        x = x.contiguous()
+    return name, x, x.stride(0) if n > 1 else V
+
+
 class PagedCache:
     """K/V of ``layers`` layers in ``num_blocks`` blocks of ``block_size`` slots, and the
     pool of free blocks."""
@@ -64,8 +78,10 @@ class PagedCache:
         self.row_bytes = n_kv_heads * head_dim * self.k.element_size()
         self.free = torch.arange(num_blocks - 1, -1, -1, dtype=torch.int32, device=device)
         self.n_free = _ints(1, device=device, fill=num_blocks)
+        self.shared = _ints(num_blocks, device=device)         # holders of a block beyond the first
         self.ws = torch.zeros(lib.spec_attention_workspace_bytes(self.desc, max_rows), dtype=torch.uint8, device=device)
         self.max_rows = max_rows
+        self.chunk_ws = None                                   # made for the first chunks, and for larger ones
 
     def views(self, table):
         """KV structs of all layers under a block table."""
@@ -91,9 +107,30 @@ class PagedCache:
             return out
         return call
 
+    def attend_chunks(self, kvs, slots, cu, seq_len, max_chunk=0, max_len=0):
+        """The ``attend`` of a model whose row i writes slot slots[i], and whose rows cu[b] .. cu[b + 1] are the last
+        tokens of request b's first seq_len[b]: each attends to what its request holds up to itself."""
+        n, B = slots.numel(), seq_len.numel()
+        need = lib.spec_chunk_attention_workspace_bytes(self.desc, B, n)
+        if self.chunk_ws is None or self.chunk_ws.numel() < need:
+            error = 0 if self.chunk_ws is None else lib.spec_get_device_error(self.chunk_ws)
+            self.chunk_ws = torch.zeros(need, dtype=torch.uint8, device=self.device)
+            self.chunk_ws[:4].view(torch.int32).fill_(error)
+
+        def call(layer, q, k, v):
+            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            q, q_ld = _rows(q, n, self.n_q_heads, self.head_dim, self.dtype, "q")
+            k, k_ld = _rows(k, n, self.n_kv_heads, self.head_dim, self.dtype, "k")
+            v, v_ld = _rows(v, n, self.n_kv_heads, self.head_dim, self.dtype, "v")
+            lib.spec_cache_append(self.desc, k, v, k_ld, slots, n, kvs[layer], self.ws, v_ld=v_ld)
+            lib.spec_chunk_attention(self.desc, q, kvs[layer], cu, seq_len, B, n, out, None, self.chunk_ws,
+                                     max_chunk=max_chunk, max_len=max_len, q_ld=q_ld)
+            return out
+        return call
+
     def error(self):
         """The attention's error word (synchronises)."""
-        return lib.spec_get_device_error(self.ws)
+        return lib.spec_get_device_error(self.ws) or (lib.spec_get_device_error(self.chunk_ws) if self.chunk_ws is not None else 0)
 
 
 class _Select:
@@ -109,15 +146,10 @@ class _Select:
 
     def __call__(self, logits):
         """logits [B * W, V] in fp32, bf16 or fp16 (copied if a row is not in one piece)."""
-        n, V, a, b = self.B * self.W, self.V, self.at, 1 - self.at
-        name = _LOGITS.get(logits.dtype)
-        if name is None or logits.numel() != n * V or logits.shape[-1] != V:
-            raise ValueError("logits are %s %s, not %s of floats" % (logits.dtype, tuple(logits.shape), (n, V)))
-        x = logits.reshape(n, V)
-        if x.stride(1) != 1 or (n > 1 and x.stride(0) < V):
-            x = x.contiguous()
+        V, a, b = self.V, self.at, 1 - self.at
+        name, x, ld = _logits(logits, self.B * self.W, V)
         lib.spec_beam_select(self.B, self.W, V, name, x, self.score[a], self.done[a], self.eos, self.parent, self.tok,
-                             self.score[b], self.done[b], self.ws, ld=x.stride(0) if n > 1 else V)
+                             self.score[b], self.done[b], self.ws, ld=ld)
         self.at = b
 
     def begin(self):
@@ -150,6 +182,13 @@ class Batch:
         self.tws = torch.zeros(lib.spec_block_tables_workspace_bytes(B), dtype=torch.uint8, device=dev)
         self.live, self.kept = _ints(B, device=dev, fill=1), _ints(B, device=dev, fill=1)    # takes tokens; keeps its blocks
         self.select = _Select(B, 1, vocab, eos, dev)
+        self.vocab = vocab
+        self.forked = False                                 # blocks may have several holders
+        self.bws = torch.zeros(lib.spec_block_state_workspace_bytes(B, cache.num_blocks), dtype=torch.uint8, device=dev)
+        self.lws = None
+        c = cache
+        self.blocks = lib.make_block_state(c.block_size, self.table, self.table, self.length, self.length, c.shared, c.shared,
+                                           c.free, c.free, c.n_free, c.n_free)
 
     @property
     def stopped(self):
@@ -159,10 +198,15 @@ class Batch:
         """Grow to (or give back down to) want [B] tokens by at most B new ones in all: their slots and
         positions are in ``slots`` and ``pos``, those of request b from ``cu``[b] on (a request that is
         refused for its length has none there)."""
+        self._resize(want, self.slots, self.pos)
+
+    def _resize(self, want, slots, pos):
         c = self.cache
+        if self.forked:                                     # what others hold stays
+            lib.spec_block_release(self.blocks, (want == 0).int(), self.bws)
         lib.spec_block_tables(self.B, c.block_size, self.table.shape[1], c.num_blocks, self.length, want, self.table,
-                              self.table, c.free, c.n_free, c.free, c.n_free, self.length, self.cu, self.slots, self.pos,
-                              self.B + 1, self.tws)
+                              self.table, c.free, c.n_free, c.free, c.n_free, self.length, self.cu, slots, pos,
+                              slots.numel(), self.tws)
 
     def feed(self, tok):
         """One more token of every request that can take one, tok [B] (of a row that has none: below 0);
@@ -186,6 +230,110 @@ class Batch:
             self.kept, self.live = (torch.addcmul(x, self.live, done, value=-1) for x in (self.kept, self.live))
         return torch.stack(out, 1)
 
+    def _chunks(self, tokens, chunk):
+        """Feeds tokens (a host list of ids a request, which may be empty) in chunks of at most ``chunk`` a request.  After
+        each: the logits of its rows, and of every request the rows [from, to) and the tokens before them."""
+        if len(tokens) != self.B:
+            raise ValueError("tokens of %d requests, the batch has %d" % (len(tokens), self.B))
+        if chunk < 1:
+            raise ValueError("chunks of %d tokens" % chunk)
+        dev = self.cache.device
+        # a row that was dropped, or whose request ended and gave its blocks back, takes another one
+        fresh = torch.tensor([len(t) > 0 for t in tokens], device=dev) & (self.length == 0)
+        self.live, self.kept = (torch.where(fresh, 1, x) for x in (self.live, self.kept))
+        for x in (self.select.score, self.select.done):
+            x[self.select.at].masked_fill_(fresh[:, None], 0)
+        longest = max((len(t) for t in tokens), default=0)
+        for at in range(0, longest, chunk):
+            part = [list(t[at:at + chunk]) for t in tokens]
+            n = [len(p) for p in part]
+            ends = np.cumsum([0] + n)
+            total = int(ends[-1])
+            tok, count, cu = (torch.tensor(x, dtype=torch.int32, device=dev) for x in ([t for p in part for t in p], n, ends))
+            req = torch.repeat_interleave(torch.arange(self.B, device=dev), count.long(), output_size=total)
+            nth = torch.arange(total, device=dev, dtype=torch.int32) - cu[req]
+            want = torch.addcmul(self.live * count, self.length, self.kept)
+            slots = _ints(total + 1, device=dev)
+            self._resize(want, slots, None)
+            self.live = self.live * (self.length == want)
+            mine = self.live[req].bool()
+            slots = torch.where(mine, slots[(self.cu[req] + nth).clamp(max=total)], -1)
+            length = self.length * self.live
+            pos = (length[req] - count[req] + nth).clamp(min=0)
+            attend = self.cache.attend_chunks(self.kvs, slots, cu, length, max(n), self.max_len)
+            yield self.model(tok, pos, attend), ends, at, n
+
+    def extend(self, tokens, chunk=512):
+        """Appends tokens (a host list of ids a request, which may be empty) to the requests: logits [B, V] after each
+        request's last one, zeros where there was none to feed.  A row without a request takes a new one; one that cannot
+        take all its tokens stops, as in ``feed``."""
+        out = None
+        for logits, ends, at, n in self._chunks(tokens, chunk):
+            if out is None:
+                out = torch.zeros(self.B, logits.shape[-1], dtype=logits.dtype, device=logits.device)
+            last = [b for b in range(self.B) if n[b] and at + n[b] == len(tokens[b])]
+            if last:
+                where = torch.tensor(last, device=logits.device)
+                out[where] = logits[torch.tensor([int(ends[b + 1]) - 1 for b in last], device=logits.device)]
+        if out is None:
+            raise ValueError("no tokens")
+        return out
+
+    def score(self, tokens, k=0, chunk=512):
+        """Appends tokens as ``extend`` does, and says what the model made of them: for each request a dict of tensors over
+        its tokens, entry i of what it expected after token i: logprob and rank of token i + 1 (-infinity and -1 for the
+        last one, and in requests that stopped), entropy, lse, and top_ids and top_logprob [len, k], the best alternatives."""
+        parts = [[] for _ in tokens]
+        for logits, ends, at, n in self._chunks(tokens, chunk):
+            name, x, ld = _logits(logits, int(ends[-1]), self.vocab)
+            rows, dev = x.shape[0], x.device
+            after = [t for b, seq in enumerate(tokens) for t in (list(seq[at + 1:at + n[b] + 1]) + [-1])[:n[b]]]
+            need = lib.spec_token_logprobs_workspace_bytes(rows, self.vocab, k)
+            if self.lws is None or self.lws.numel() < need:
+                self.lws = torch.zeros(need, dtype=torch.uint8, device=dev)
+            f = {key: torch.empty(rows, device=dev) for key in ("logprob", "entropy", "lse")}
+            r = dict(f, rank=_ints(rows, device=dev), top_ids=_ints(rows, k, device=dev), top_logprob=torch.empty(rows, k, device=dev))
+            lib.spec_token_logprobs(rows, self.vocab, name, x, torch.tensor(after, dtype=torch.int32, device=dev), k, ws=self.lws,
+                                    ld=ld, **r)
+            ok = torch.repeat_interleave(self.live.bool(), torch.tensor(n, device=dev), output_size=rows)
+            r["logprob"], r["rank"] = torch.where(ok, r["logprob"], -float("inf")), torch.where(ok, r["rank"], -1)
+            for b in range(self.B):
+                if n[b]:
+                    parts[b].append({key: v[int(ends[b]):int(ends[b + 1])] for key, v in r.items()})
+        return [{key: torch.cat([p[key] for p in ps]) for key in ps[0]} if ps else {} for ps in parts]
+
+    def fork(self, src, dst):
+        """Rows dst (host lists of row numbers), which hold no request, become copies of rows src: their blocks are shared,
+        a last partial one copied.  A row that the pool has no block for stays empty, and ``error`` says so."""
+        if len(src) != len(dst) or not dst:
+            raise ValueError("%d rows to fork to, from %d" % (len(dst), len(src)))
+        if len(set(dst)) != len(dst) or not all(0 <= i < self.B for i in [*src, *dst]):
+            raise ValueError("rows %s of %d" % (dst, self.B))
+        dev, c = self.cache.device, self.cache
+        a, d = (torch.tensor(x, dtype=torch.int32, device=dev) for x in (src, dst))
+        empty = self.length[d.long()] == 0
+        self.forked = True
+        lib.spec_block_fork(self.blocks, len(dst), a, d, c.views(self.table), c.row_bytes, self.bws)
+        a, d = a.long(), d.long()
+        there = empty & (self.length[d] > 0)
+        for x in (self.live, self.kept):
+            x[d] = torch.where(there, x[a], torch.where(empty, 0, x[d]))
+        for x in (self.select.score[self.select.at], self.select.done[self.select.at]):
+            x[d] = torch.where(there[:, None], x[a], x[d])
+
+    def drop(self, rows):
+        """Ends the requests of the given rows (a host list); blocks that no other row holds go back to the pool."""
+        which = torch.zeros(self.B, dtype=torch.int32, device=self.cache.device)
+        which[torch.tensor(rows, dtype=torch.long, device=self.cache.device)] = 1
+        lib.spec_block_release(self.blocks, which, self.bws)
+        self.live, self.kept = (x * (1 - which) for x in (self.live, self.kept))
+
+    def compact(self):
+        """Moves the blocks in use to the cache's lowest ids.  Only where no other batch holds blocks of the cache:
+        otherwise nothing moves, and ``error`` says so."""
+        c = self.cache
+        lib.spec_block_compact(self.blocks, c.views(self.table), c.row_bytes, self.bws)
+
     def release(self):
         """Gives all blocks back; the batch can take other requests."""
         self.resize(torch.zeros_like(self.length))
@@ -193,7 +341,8 @@ class Batch:
         self.select.begin()
 
     def error(self):
-        return lib.spec_get_device_error(self.tws) or self.cache.error()
+        words = [self.tws, self.bws] + ([self.lws] if self.lws is not None else [])
+        return next((e for e in map(lib.spec_get_device_error, words) if e), 0) or self.cache.error()
 
 
 class BeamBatch:
@@ -377,6 +526,18 @@ def main():
     for i in range(2):
         print("request %d: score %.3f, tokens %s" % (i, float(beams.score[i, 0]), beams.tokens[i, 0, len(prompts[i]):].tolist()))
     beams.release()
+    # prompts in one chunk, scored; the first one is continued from its four best next tokens
+    batch = Batch(model, cache, B + W - 1, 128, model.vocab, eos=2)
+    scores = batch.score(prompts + [[]] * (W - 1), k=W)
+    print("prompt 0: %d tokens, mean log-probability %.3f" % (len(prompts[0]), float(scores[0]["logprob"][:-1].mean())))
+    batch.fork([0] * (W - 1), list(range(B, B + W - 1)))
+    first = torch.stack([s["top_ids"][-1, 0] for s in scores[:B]] + list(scores[0]["top_ids"][-1, 1:]))
+    out = batch.decode(first, new)
+    for i in (0, *range(B, B + W - 1)):
+        print("from token %d: %s" % (int(first[i]), out[i].tolist()))
+    if batch.error():
+        raise RuntimeError("device error word %d" % batch.error())
+    batch.release()
     print("free blocks: %d of %d" % (int(cache.n_free[0]), cache.num_blocks))
 
 
