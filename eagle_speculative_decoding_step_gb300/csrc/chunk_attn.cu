@@ -303,8 +303,8 @@ typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t,
                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
-// ptr as [rows][heads][hd] of 16-bit components with ld of them from a row to the next, boxes of box_heads x box_rows x 64;
-// past a head's or the last row's end: zeros
+// ptr as [rows][heads][hd] with ld components from a row to the next, boxes of box_heads x box_rows x 64 (8 bits: x hd, as
+// they lie); past a head's or the last row's end: zeros
 static bool rows_map(CUtensorMap* tm, const void* ptr, int dtype, int hd, int heads, long long rows, long long ld, int box_heads,
                      int box_rows) {
   static const EncodeTiledFn enc = [] {
@@ -316,12 +316,17 @@ static bool rows_map(CUtensorMap* tm, const void* ptr, int dtype, int hd, int he
   }();
   if (!enc) return false;
   cuuint64_t dims[3] = {(cuuint64_t)hd, (cuuint64_t)heads, (cuuint64_t)rows};
-  cuuint64_t strides[2] = {(cuuint64_t)hd * 2, (cuuint64_t)ld * 2};
-  cuuint32_t box[3] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_rows};
+  const bool f8 = dtype == SPEC_DTYPE_E4M3;
+  const cuuint64_t es_bytes = f8 ? 1 : 2;
+  cuuint64_t strides[2] = {hd * es_bytes, ld * es_bytes};
+  cuuint32_t box[3] = {f8 ? (cuuint32_t)hd : 64u, (cuuint32_t)box_heads, (cuuint32_t)box_rows};
   cuuint32_t es[3] = {1, 1, 1};
-  return enc(tm, dtype == SPEC_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
-             const_cast<void*>(ptr), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  const CUtensorMapDataType type = f8                          ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                   : dtype == SPEC_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                              : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  return enc(tm, type, 3, const_cast<void*>(ptr), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             f8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 static spec_status launch_tc(const spec_attn_desc& d, const Args& g, int longest, int sms, cudaStream_t st) {
@@ -330,7 +335,7 @@ static spec_status launch_tc(const spec_attn_desc& d, const Args& g, int longest
   TcArgs a{};
   a.g = g;
   a.l = mode == kTwoQ ? layout<kTwoQ>(d.head_dim, f8) : mode == kOneQ ? layout<kOneQ>(d.head_dim, f8) : layout<kWide>(d.head_dim, f8);
-  a.l.runs = !f8 && g.kv.block_size % 16 == 0;
+  a.l.runs = g.kv.block_size % 16 == 0;
   const long long slot = (long long)d.n_kv_heads * d.head_dim;
   if (a.l.runs)
     for (int i = 0; i < 2; ++i)

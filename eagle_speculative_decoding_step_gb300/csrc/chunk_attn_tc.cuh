@@ -232,7 +232,7 @@ template <typename T> SPEC_DEV uint2 widen4(uint32_t x) {
 
 struct TcSmem {
   Plan plan;
-  uint64_t full[kMaxStages], empty[kMaxStages], q_full, q_empty, drain, landed[4], s_full[2], p_full[2][2], o_done[2], o_free[2], group[2];
+  uint64_t full[kMaxStages], empty[kMaxStages], q_full, q_empty, drain, landed[4][kRawStages], s_full[2], p_full[2][2], o_done[2], o_free[2], group[2];
   alignas(16) uint32_t bits[kTileBits][4];   // keys of a tile that are there
   uint32_t poison[kItems][2 * 6][4];   // keys of an item's edge tiles whose value is not finite
   int poisoned[kItems];
@@ -376,25 +376,62 @@ template <typename T, bool F8, int MODE> struct Loader {
     }
   }
 
-  // Keys in runs of 16 slots: tensor copies, a lane a run and 64 components, that report to the MMA warp by themselves; in
-  // edge tiles the values come by way of this warp.
+  // Keys in runs of 16 slots: tensor copies, a lane a run (and 64 components).  16-bit ones report to the MMA warp by
+  // themselves, but for the values of edge tiles, which come by way of this warp; 8-bit ones land in raw stages of the warp's
+  // rows, and are widened while the next ones are under way.
+  struct Way {                         // a stage that comes by way of the warp
+    uint32_t there, absent;            // of its rows: keys; rows that nothing was copied to
+    int info;                          // an edge tile's values: item and slot, otherwise -1
+    bool value;
+  };
   static SPEC_DEV void run_tensor(const TcArgs& a, TcSmem& sm, uint32_t q0, int warp, int lane) {
     const Args& g = a.g;
     const int chunks = a.l.chunks, stages = a.l.stages, units = g.hd / 8, r0 = warp * RW;
-    const uint32_t stage_bytes = a.l.stage_bytes, ring0 = q0 + a.l.q_bytes;
+    const uint32_t stage_bytes = a.l.stage_bytes, raw_bytes = a.l.raw_bytes, ring0 = q0 + a.l.q_bytes,
+                   raw0 = ring0 + (uint32_t)stages * stage_bytes;
     volatile int* abort = &sm.abort;
     Walk<S::BM, KT> walk(g, sm.plan);
     Item it;
-    int tiles = 0, items = 0, stage = 0, filled = 0;
-    uint32_t phase = 0, q_phase = 0, l_phase = 0;
+    int tiles = 0, items = 0, stage = 0, filled = 0, raw = 0, l_raw = 0;
+    uint32_t phase = 0, q_phase = 0, l_phase = 0;   // l_phase: of landed[warp], a bit each
     // this lane's copy: run and chunk
-    const int run = lane / chunks, chunk = lane - run * chunks;
+    const int per = F8 ? 1 : chunks, run = lane / per, chunk = lane - run * per;
     const bool copier = run < RW / 16;
-    const uint32_t lane_to = (uint32_t)(chunk * KT * 128 + (r0 + run * 16) * 128), run_mask = copier ? 0xffffu << (run * 16) : 0u;
+    const uint32_t lane_to = F8 ? (uint32_t)((r0 + run * 16) * g.hd) : (uint32_t)(chunk * KT * 128 + (r0 + run * 16) * 128);
+    const uint32_t run_mask = copier ? 0xffffu << (run * 16) : 0u, run_bytes = F8 ? 16u * g.hd : chunks * 2048u;
     const uint64_t policy = tc::policy_evict_last();
     const int step_b = KT / g.kv.block_size, step_i = KT % g.kv.block_size;
     const bool mine = lane < RW;
-    bool ok = true;
+    bool ok = true, pending = false;
+    Way way{};
+    auto free_stage = [&] { return __all_sync(0xffffffffu, wait_for(sm.empty[stage], phase ^ 1u, abort)); };
+    auto next_stage = [&] {
+      filled = min(filled + 1, stages);
+      if (++stage == stages) stage = 0, phase ^= 1u;
+    };
+    // The stage that is to come by way of this warp: waits for its copies, widens and clears it, hands it over.
+    auto hand = [&](const Way& w) {
+      if (F8 && !free_stage()) return false;
+      if (!__all_sync(0xffffffffu, wait_for(sm.landed[warp][l_raw], l_phase >> l_raw & 1u, abort))) return false;
+      l_phase ^= 1u << l_raw;
+      const uint32_t at = ring0 + (uint32_t)stage * stage_bytes;
+      if constexpr (F8) {
+        const uint32_t from = raw0 + (uint32_t)l_raw * raw_bytes;
+        if (units == 16) widen_rows<8>(from, at, r0, lane, 8);
+        else if (units == 8) widen_rows<4>(from, at, r0, lane, 4);
+        else widen_rows<0>(from, at, r0, lane, units / 2);
+        if (++l_raw == kRawStages) l_raw = 0;
+        __syncwarp();
+        if (w.value && w.absent) zero_rows(at, r0, lane, units, w.absent);
+        __syncwarp();
+      }
+      if (w.info >= 0) clean_rows(sm, at, r0, lane, units, w.info, w.there);
+      proxy_fence();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(tc::su32(&sm.full[stage]));
+      next_stage();
+      return true;
+    };
     while (ok && walk.next(it)) {
       const Edges<KT> edges(g, it);
       const int32_t* table = g.kv.block_table + (long long)(g.b0 + it.b) * g.kv.max_blocks;
@@ -420,42 +457,38 @@ template <typename T, bool F8, int MODE> struct Loader {
         const uint32_t keys = there & run_mask;
         const int from = keys ? __ffs(keys) - 1 : 0;
         const int first = __shfl_sync(0xffffffffu, slot, from) - (from & 15);
-        const uint32_t runs = (there & 0xffffu ? 1u : 0u) + (RW == 32 && there >> 16 ? 1u : 0u);
-        const uint32_t bytes = runs * chunks * 2048u;
-        const uint32_t absent = (there & 0xffffu ? 0u : 0xffffu) | (RW == 32 && there >> 16 ? 0u : RW == 32 ? 0xffff0000u : 0u);
+        const uint32_t bytes = ((there & 0xffffu ? 1u : 0u) + (RW == 32 && there >> 16 ? 1u : 0u)) * run_bytes;
+        const uint32_t absent = (there & 0xffffu ? 0u : 0xffffu) | (RW == 32 && !(there >> 16) ? 0xffff0000u : 0u);
         const int tile = it.tile0 + k;
-        const bool edge = edges.has(tile);
+        const int info = edges.has(tile) ? (items % kItems) << 8 | edges.template slot<S::EDGES>(tile) : -1;
 #pragma unroll 1
-        for (int value = 0; value < 2; ++value) {
-          if (!__all_sync(0xffffffffu, wait_for(sm.empty[stage], phase ^ 1u, abort))) {
+        for (int value = 0; ok && value < 2; ++value) {
+          const Way now{there, absent, value ? info : -1, value != 0};
+          const bool by_way = F8 || now.info >= 0;
+          if (!F8 && !free_stage()) {
             ok = false;
             break;
           }
-          const uint32_t at = ring0 + (uint32_t)stage * stage_bytes;
-          const bool by_way = value && edge;
-          if (value && absent) {                       // nothing is copied there: weights of 0 must meet numbers
+          const uint32_t at = F8 ? raw0 + (uint32_t)raw * raw_bytes : ring0 + (uint32_t)stage * stage_bytes;
+          if (!F8 && value && absent) {                // nothing is copied there: weights of 0 must meet numbers
             zero_rows(at, r0, lane, units, absent);
             proxy_fence();
           }
-          uint64_t& bar = by_way ? sm.landed[warp] : sm.full[stage];
+          uint64_t& bar = by_way ? sm.landed[warp][F8 ? raw : 0] : sm.full[stage];
           __syncwarp();
           if (lane == 0) tc::mbar_expect_tx(tc::su32(&bar), bytes);
           __syncwarp();
           if (keys) copy_run(at + lane_to, value ? &a.tmv : &a.tmk, tc::su32(&bar), 64 * chunk, it.h, first, policy);
-          if (by_way) {
-            __syncwarp();
-            if (!__all_sync(0xffffffffu, wait_for(bar, l_phase, abort))) {
-              ok = false;
-              break;
-            }
-            l_phase ^= 1u;
-            clean_rows(sm, at, r0, lane, units, (items % kItems) << 8 | edges.template slot<S::EDGES>(tile), there);
-            proxy_fence();
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(tc::su32(&sm.full[stage]));
+          __syncwarp();
+          if constexpr (F8) {
+            if (++raw == kRawStages) raw = 0;
+            if (pending) ok = hand(way);
+            way = now, pending = true;
+          } else if (by_way) {
+            ok = hand(now);
+          } else {
+            next_stage();
           }
-          filled = min(filled + 1, stages);
-          if (++stage == stages) stage = 0, phase ^= 1u;
         }
         if (k == it.k0 && ok) {
           // Q, once the first keys are on their way
@@ -477,13 +510,18 @@ template <typename T, bool F8, int MODE> struct Loader {
       }
       ++items;
     }
+    if (ok && pending) ok = hand(way);
     cp_wait<0>();
-    if (a.l.q_boxes && warp == 0 && items > 0 && sm.abort) tc::mbar_wait(tc::su32(&sm.q_full), (uint32_t)(items - 1) & 1u, abort, false);
     if (!ok || sm.abort) {
       // gives up: the copies under way land first (or the limit passes)
-      for (int i = 0; i < filled; ++i) {
-        if (--stage < 0) stage = stages - 1, phase ^= 1u;
-        tc::mbar_wait(tc::su32(&sm.full[stage]), phase, abort, false);
+      if (a.l.q_boxes && warp == 0 && items > 0) tc::mbar_wait(tc::su32(&sm.q_full), (uint32_t)(items - 1) & 1u, abort, false);
+      if constexpr (F8) {
+        for (int i = 0; i < kRawStages; ++i) tc::mbar_wait(tc::su32(&sm.landed[warp][i]), l_phase >> i & 1u, abort, false);
+      } else {
+        for (int i = 0; i < filled; ++i) {
+          if (--stage < 0) stage = stages - 1, phase ^= 1u;
+          tc::mbar_wait(tc::su32(&sm.full[stage]), phase, abort, false);
+        }
       }
     }
   }
@@ -1111,7 +1149,8 @@ template <typename T, bool F8, int MODE> __global__ void __launch_bounds__(kTcTh
     tc::mbar_init(tc::su32(&sm.q_full), 4);
     tc::mbar_init(tc::su32(&sm.q_empty), 1);
     tc::mbar_init(tc::su32(&sm.drain), 1);
-    for (int i = 0; i < 4; ++i) tc::mbar_init(tc::su32(&sm.landed[i]), 1);
+    for (int i = 0; i < 4; ++i)
+      for (int j = 0; j < kRawStages; ++j) tc::mbar_init(tc::su32(&sm.landed[i][j]), 1);
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(tc::su32(&sm.s_full[i]), 1);
       tc::mbar_init(tc::su32(&sm.p_full[i][0]), 4);
@@ -1140,7 +1179,7 @@ template <typename T, bool F8, int MODE> __global__ void __launch_bounds__(kTcTh
     if (MODE != kWide || warp < 4) Softmax<T, F8, MODE>(a.g, sm, tmem, warp >> 2, warp & 3, lane).run();
   } else if (warp < 12) {
     regs_dec<kLoaderRegs>();
-    if (!F8 && a.l.runs) Loader<T, F8, MODE>::run_tensor(a, sm, base, warp - 8, lane);
+    if (a.l.runs) Loader<T, F8, MODE>::run_tensor(a, sm, base, warp - 8, lane);
     else Loader<T, F8, MODE>::run(a, sm, base, warp - 8, lane);
   } else {
     regs_dec<kMmaRegs>();
