@@ -294,7 +294,7 @@ template <typename T, bool F8, int MODE> struct Loader {
   template <int U> static SPEC_DEV void widen_rows(uint32_t from, uint32_t to, int r0, int lane, int units) {
     const Units<U> un(units);
     const int n = RW * un.n;
-    constexpr int B = U ? 4 : 2;
+    constexpr int B = U ? U : 2;                       // U: RW U pieces are B 32 of them, or half of that
 #pragma unroll 1
     for (int j = lane; j < n; j += 32 * B) {
       uint4 x[B];
@@ -311,10 +311,22 @@ template <typename T, bool F8, int MODE> struct Loader {
       }
     }
   }
-  // Rows r0 .. of a tile in an edge (info), of which `there` are keys (others hold whatever the cache has there).
+  // Rows r0 .. of a tile in an edge (info), of which `there` are keys (others hold whatever the cache has there).  Looked
+  // over first: the largest magnitude of the lane's pieces, NaN if there is one.
   static SPEC_DEV void clean_rows(TcSmem& sm, uint32_t at, int r0, int lane, int units, int info, uint32_t there) {
+    using T2 = std::conditional_t<std::is_same_v<T, __half>, __half2, __nv_bfloat162>;
     const Units<0> un(units);
-#pragma unroll 4
+    const uint32_t zero = 0;
+    T2 top = *reinterpret_cast<const T2*>(&zero);
+#pragma unroll 8
+    for (int i = lane; i < RW * units; i += 32) {
+      const int row = un.row(i), u = i - row * units;
+      const uint4 v = lds128(at + place(r0 + row, u, KT));
+      const T2* x = reinterpret_cast<const T2*>(&v);
+      top = __hmax2_nan(top, __hmax2_nan(__hmax2_nan(__habs2(x[0]), __habs2(x[1])), __hmax2_nan(__habs2(x[2]), __habs2(x[3]))));
+    }
+    if (!__any_sync(0xffffffffu, odd_halves<T>(*reinterpret_cast<const uint32_t*>(&top)) != 0)) return;
+#pragma unroll 1
     for (int i = lane; i < RW * units; i += 32) {
       const int row = un.row(i), u = i - row * units;
       const uint32_t to = at + place(r0 + row, u, KT);
