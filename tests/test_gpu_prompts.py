@@ -627,7 +627,8 @@ def test_block_fork_bad_forks(in_place):
 
 @pytest.mark.parametrize("in_place", [False, True])
 @pytest.mark.parametrize("live,fan,bs,most,share", [(1, 1, 16, 40, 1.0), (6, 4, 16, 300, 0.5), (200, 5, 8, 200, 0.6),
-                                                    (1500, 5, 16, 60, 0.3), (3, 40, 1, 50, 0.9), (20, 3, 16, 500, 0.0)])
+                                                    (1500, 5, 16, 60, 0.3), (3, 40, 1, 50, 0.9), (20, 3, 16, 500, 0.0),
+                                                    (300, 5, 8, 900, 0.5)])
 def test_block_release(live, fan, bs, most, share, in_place):
     st, _, r = pool_case(live, families_of(live, live, fan, most, 3 * bs), bs, 10)
     drop = (r.random(len(st["length"])) < share).astype(int) * 5
