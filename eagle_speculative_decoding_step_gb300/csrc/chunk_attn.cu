@@ -184,10 +184,10 @@ template <int HD> __global__ void __launch_bounds__(kFmaThreads)
             }
           }
     }
-    const Pieces pc(plan, it);
-    if (pc.c0 != pc.c1) {
+    if (it.k0 > 0 || it.k1 < it.tiles) {
+      const Pieces pc(plan, it);
       const size_t piece = piece_floats(BM, g.hd);
-      float* mine = g.part + pc.slot(plan, it, blockIdx.x) * piece;
+      float* mine = g.part + pc.slot(blockIdx.x) * piece;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int r = ty + 16 * i;
@@ -216,7 +216,7 @@ template <int HD> __global__ void __launch_bounds__(kFmaThreads)
         for (int j = 0; j < 4 * NJ; ++j) o[i][j] = 0.f;
       }
       for (int c = pc.c0; c <= pc.c1; ++c) {
-        const float* x = g.part + pc.slot(plan, it, c) * piece;
+        const float* x = g.part + pc.slot(c) * piece;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int r = ty + 16 * i;

@@ -94,7 +94,6 @@ struct Plan {
   int h, b, t, off;            // where this CTA begins
 };
 
-SPEC_DEV long long share_begin(const Plan& p, int c) { return p.total * c / p.ctas; }
 SPEC_DEV int owner(const Plan& p, long long x) { return (int)(((x + 1) * p.ctas - 1) / p.total); }
 
 // All threads of the block.  A few thousand integers at most are read, from L2.
@@ -250,7 +249,8 @@ struct Pieces {
   int c0, c1;
   SPEC_DEV Pieces(const Plan& p, const Item& it)
       : c0(p.whole ? 0 : owner(p, it.pos)), c1(p.whole ? 0 : owner(p, it.pos + it.tiles - 1)) {}
-  SPEC_DEV int slot(const Plan& p, const Item& it, int c) const { return 2 * c + (it.pos < share_begin(p, c) ? 0 : 1); }
+  // (the first CTA's share begins before the item or with it, the others' inside)
+  SPEC_DEV int slot(int c) const { return 2 * c + (c == c0 ? 1 : 0); }
 };
 
 // keys that packed row r of an item attends to: [lo, hi)

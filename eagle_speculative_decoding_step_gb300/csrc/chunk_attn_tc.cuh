@@ -947,25 +947,24 @@ template <typename T, bool F8, int MODE> struct Softmax {
         }
   }
 
-  // 16 components of the row's unnormalised output
-  SPEC_DEV void take(float* o, int c, float f0, float f1, bool two) {
+  // 16 components of the row's unnormalised output, or 32
+  SPEC_DEV void take(float* o, int c, float f0, float f1, bool two, bool more) {
     __syncwarp();
-    uint32_t a[16];
-    if (MODE == kTwoQ) {
-      tc::tmem_ld16(tm + (w ? S::O1 : S::O0) + c, a);
+    const uint32_t o0 = tm + (MODE == kTwoQ && w ? S::O1 : S::O0) + c;
+    uint32_t a[32];
+    tc::tmem_ld16(o0, a);
+    if (more) tc::tmem_ld16(o0 + 16, a + 16);
+    if (MODE == kOneQ && two) {
+      uint32_t b[32];
+      tc::tmem_ld16(tm + S::O1 + c, b);
+      if (more) tc::tmem_ld16(tm + S::O1 + c + 16, b + 16);
       tc::tmem_ld_wait();
 #pragma unroll
-      for (int j = 0; j < 16; ++j) o[j] = __uint_as_float(a[j]);
+      for (int j = 0; j < 32; ++j) o[j] = fmaf(__uint_as_float(b[j]), f1, __uint_as_float(a[j]) * f0);
     } else {
-      tc::tmem_ld16(tm + S::O0 + c, a);
-      uint32_t b[16];
-      if (MODE == kOneQ && two) tc::tmem_ld16(tm + S::O1 + c, b);
       tc::tmem_ld_wait();
 #pragma unroll
-      for (int j = 0; j < 16; ++j) o[j] = __uint_as_float(a[j]) * f0;
-      if (MODE == kOneQ && two)
-#pragma unroll
-        for (int j = 0; j < 16; ++j) o[j] = fmaf(__uint_as_float(b[j]), f1, o[j]);
+      for (int j = 0; j < 32; ++j) o[j] = MODE == kOneQ ? __uint_as_float(a[j]) * f0 : __uint_as_float(a[j]);
     }
   }
 
@@ -999,33 +998,36 @@ template <typename T, bool F8, int MODE> struct Softmax {
     const int tok = (it.r0 + r) / g.G, head = it.h * g.G + (it.r0 + r) - tok * g.G;
     T* dst = static_cast<T*>(g.out) + (it.row0 + tok) * g.out_ld + (long long)head * g.hd;
     float* lse = g.lse && c0 == 0 ? g.lse + (long long)(it.row0 + tok) * g.nq + head : nullptr;
-    const Pieces pc(sm.plan, it);
-    if (pc.c0 == pc.c1) {
-      const float inv = l == 0.f ? 0.f : g.v_scale / l;
+    const bool whole = it.k0 == 0 && it.k1 == it.tiles;
+    const float inv = l == 0.f ? 0.f : g.v_scale / l;
+    const size_t piece = piece_floats(BM, g.hd);
+    float* mine = g.part + (whole ? 0 : 2 * blockIdx.x + (it.k0 > 0 ? 0 : 1)) * piece;
 #pragma unroll 1
-      for (int c = c0; c < c1; c += 16) {
-        float o[16];
-        take(o, c, f0, f1, two);
-        if (poisoned && valid) mend(it, item, klo, khi, c, o);
-        if (valid) write(dst + c, o, inv);
+    for (int c = c0; c < c1; c += 32) {
+      const bool more = c + 16 < c1;
+      float o[32];
+      take(o, c, f0, f1, two, more);
+      if (poisoned && valid) {
+        mend(it, item, klo, khi, c, o);
+        if (more) mend(it, item, klo, khi, c + 16, o + 16);
       }
+      if (valid && whole) {
+        write(dst + c, o, inv);
+        if (more) write(dst + c + 16, o + 16, inv);
+      }
+      if (valid && !whole)
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (j < 4 || more)
+            *reinterpret_cast<float4*>(mine + ((size_t)(c / 4 + j) * BM + r) * 4) =
+                make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+    }
+    if (whole) {
       if (valid && lse) *lse = l == 0.f ? -INFINITY : (m - W::kShift + log2f(l)) * kLn2;
       release();
       return true;
     }
-    const size_t piece = piece_floats(BM, g.hd);
-    float* mine = g.part + pc.slot(sm.plan, it, blockIdx.x) * piece;
-#pragma unroll 1
-    for (int c = c0; c < c1; c += 16) {
-      float o[16];
-      take(o, c, f0, f1, two);
-      if (poisoned && valid) mend(it, item, klo, khi, c, o);
-      if (valid)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          *reinterpret_cast<float4*>(mine + ((size_t)(c / 4 + j) * BM + r) * 4) =
-              make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
-    }
+    const Pieces pc(sm.plan, it);
     if (valid && c0 == 0) mine[(size_t)BM * g.hd + r] = m, mine[(size_t)BM * (g.hd + 1) + r] = l;
     release();
     __threadfence();
@@ -1041,40 +1043,45 @@ template <typename T, bool F8, int MODE> struct Softmax {
     if (!group_sync()) return false;
     const bool last = sm.last[slot] != 0;
     if (!group_sync()) return false;       // (read before the next item's is written)
-    if (!last || !valid) return true;
+    if (last) join(it, pc);
+    return true;
+  }
+
+  // All pieces of the item's rows, in their order; 16 components of a row a thread at a time.
+  SPEC_DEV void join(const Item& it, const Pieces& pc) {
     __threadfence();
-    float M = -INFINITY;
+    const int base = MODE == kTwoQ ? w * 128 : 0, rows = MODE == kTwoQ ? min(128, it.rows - base) : it.rows;
+    const int tid = MODE == kOneQ ? w * 128 + row : row, threads = MODE == kOneQ ? 256 : 128;
+    const size_t piece = piece_floats(BM, g.hd);
 #pragma unroll 1
-    for (int c = pc.c0; c <= pc.c1; ++c)
-      M = fmaxf(M, __ldcg(g.part + pc.slot(sm.plan, it, c) * piece + (size_t)BM * g.hd + r));
-    float L = 0.f;
-#pragma unroll 1
-    for (int c = pc.c0; c <= pc.c1; ++c) {
-      const float* x = g.part + pc.slot(sm.plan, it, c) * piece + (size_t)BM * g.hd + r;
-      const float mc = __ldcg(x);
-      L += __ldcg(x + BM) * (mc == -INFINITY ? 0.f : exp2_fast(mc - base_of(M)));
-    }
-    const float inv = L == 0.f ? 0.f : g.v_scale / L;
-#pragma unroll 1
-    for (int c = c0; c < c1; c += 16) {
-      float o[16];
+    for (int task = tid; task < rows * (g.hd / 16); task += threads) {
+      const int r = base + task % rows, c = task / rows * 16;
+      float M = -INFINITY;
+#pragma unroll 4
+      for (int p = pc.c0; p <= pc.c1; ++p) M = fmaxf(M, __ldcg(g.part + pc.slot(p) * piece + (size_t)BM * g.hd + r));
+      float L = 0.f, o[16];
 #pragma unroll
       for (int j = 0; j < 16; ++j) o[j] = 0.f;
-#pragma unroll 1
+#pragma unroll 4
       for (int p = pc.c0; p <= pc.c1; ++p) {
-        const float* x = g.part + pc.slot(sm.plan, it, p) * piece;
-        const float mc = __ldcg(x + (size_t)BM * g.hd + r), f = mc == -INFINITY ? 1.f : exp2_fast(mc - base_of(M));
+        const float* x = g.part + pc.slot(p) * piece;
+        const float mc = __ldcg(x + (size_t)BM * g.hd + r), lc = __ldcg(x + (size_t)BM * (g.hd + 1) + r);
+        float4 v[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = __ldcg(reinterpret_cast<const float4*>(x + ((size_t)(c / 4 + j) * BM + r) * 4));
+        const float f = mc == -INFINITY ? 1.f : exp2_fast(mc - base_of(M));   // (1: of zeros)
+        L = fmaf(lc, f, L);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const float4 v = __ldcg(reinterpret_cast<const float4*>(x + ((size_t)(c / 4 + j) * BM + r) * 4));
-          o[4 * j] = fmaf(v.x, f, o[4 * j]), o[4 * j + 1] = fmaf(v.y, f, o[4 * j + 1]);
-          o[4 * j + 2] = fmaf(v.z, f, o[4 * j + 2]), o[4 * j + 3] = fmaf(v.w, f, o[4 * j + 3]);
+          o[4 * j] = fmaf(v[j].x, f, o[4 * j]), o[4 * j + 1] = fmaf(v[j].y, f, o[4 * j + 1]);
+          o[4 * j + 2] = fmaf(v[j].z, f, o[4 * j + 2]), o[4 * j + 3] = fmaf(v[j].w, f, o[4 * j + 3]);
         }
       }
-      write(dst + c, o, inv);
+      const int tok = (it.r0 + r) / g.G, head = it.h * g.G + (it.r0 + r) - tok * g.G;
+      write(static_cast<T*>(g.out) + (it.row0 + tok) * g.out_ld + (long long)head * g.hd + c, o, L == 0.f ? 0.f : g.v_scale / L);
+      if (g.lse && c == 0)
+        g.lse[(long long)(it.row0 + tok) * g.nq + head] = L == 0.f ? -INFINITY : (M - W::kShift + log2f(L)) * kLn2;
     }
-    if (lse) *lse = L == 0.f ? -INFINITY : (M - W::kShift + log2f(L)) * kLn2;
-    return true;
   }
   // the accumulators have been read
   SPEC_DEV void release() {
