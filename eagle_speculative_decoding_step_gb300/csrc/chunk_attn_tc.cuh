@@ -8,6 +8,7 @@
 //   warps 0-3, 4-7   two softmax warpgroups
 //   warps 8-11       K/V and Q into shared memory (any block size, any alignment of runs)
 //   warp 12          issues the MMAs
+//   warp 13          asks for 8-bit K/V, which the loader warps widen
 // While one warpgroup works on its scores, the tensor cores do the other's products.
 #pragma once
 #include <type_traits>
@@ -24,8 +25,8 @@ namespace ca {
 enum Mode { kTwoQ = 0, kOneQ = 1, kWide = 2 };
 
 constexpr int kTcThreads = 512;
-// 512 threads are launched with 128 registers each and share them out: 2 x 128 x 200 + 128 x 72 + 128 x 40
-constexpr int kSoftmaxRegs = 200, kLoaderRegs = 72, kMmaRegs = 40;
+// 512 threads are launched with 128 registers each and share them out: 2 x 128 x 192 + 128 x 72 + 128 x 56
+constexpr int kSoftmaxRegs = 192, kLoaderRegs = 72, kMmaRegs = 56;
 static_assert(2 * kSoftmaxRegs + kLoaderRegs + kMmaRegs <= 4 * 128, "");
 // dynamic shared memory of a launch, at most; the attribute is always this: another thread may be launching the same kernel
 // with another head size
@@ -232,10 +233,12 @@ template <typename T> SPEC_DEV uint2 widen4(uint32_t x) {
 
 struct TcSmem {
   Plan plan;
-  uint64_t full[kMaxStages], empty[kMaxStages], q_full, q_empty, drain, landed[4][kRawStages], s_full[2], p_full[2][2], o_done[2], o_free[2], group[2];
+  uint64_t full[kMaxStages], empty[kMaxStages], q_full, q_empty, drain, landed[4], raw_full[kRawStages], raw_empty[kRawStages], s_full[2], p_full[2][2], o_done[2], o_free[2], group[2];
   alignas(16) uint32_t bits[kTileBits][4];   // keys of a tile that are there
   uint32_t poison[kItems][2 * 6][4];   // keys of an item's edge tiles whose value is not finite
   int poisoned[kItems];
+  alignas(16) uint32_t way_there[kRawStages][4];   // an 8-bit stage: its keys, and its info
+  int way_info[kRawStages];
   int info[4][kTileBits];              // loader warps: what a stage under way needs when it has come
   float2 ml[2][128];
   int last[2];
@@ -388,78 +391,83 @@ template <typename T, bool F8, int MODE> struct Loader {
     }
   }
 
-  // Keys in runs of 16 slots: tensor copies, a lane a run (and 64 components).  16-bit ones report to the MMA warp by
-  // themselves, but for the values of edge tiles, which come by way of this warp; 8-bit ones land in raw stages of the warp's
-  // rows, and are widened while the next ones are under way.
-  struct Way {                         // a stage that comes by way of the warp
-    uint32_t there, absent;            // of its rows: keys; rows that nothing was copied to
-    int info;                          // an edge tile's values: item and slot, otherwise -1
-    bool value;
+  // Q of the next item, once the MMAs have read the last one's.  Every loader warp.
+  static SPEC_DEV bool next_q(const TcArgs& a, TcSmem& sm, const Item& it, uint32_t q0, int warp, int lane, int items,
+                              uint32_t& q_phase) {
+    if (items > 0) {
+      if (!__all_sync(0xffffffffu, wait_for(sm.q_empty, q_phase, &sm.abort))) return false;
+      q_phase ^= 1u;
+    }
+    if (a.l.q_boxes) {
+      copy_q(a, sm, it, q0, warp, lane);
+    } else {
+      load_q(a.g, it, q0, a.l.chunks, warp, lane);
+      cp_commit();
+      cp_wait<0>();
+      proxy_fence();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(tc::su32(&sm.q_full));
+    }
+    return true;
+  }
+  // Gives up: Q's copies land first (or the limit passes).
+  static SPEC_DEV void settle_q(const TcArgs& a, TcSmem& sm, int warp, int items) {
+    if (a.l.q_boxes && warp == 0 && items > 0) tc::mbar_wait(tc::su32(&sm.q_full), (uint32_t)(items - 1) & 1u, &sm.abort, false);
+  }
+
+  // Where the keys of consecutive tiles are: the lane's key of a tile, its entry of the block table asked for a tile ahead.
+  struct Keys {
+    const Args& g;
+    const int32_t* table;
+    int b, lo, hi, key, block, in_block, e;
+    bool mine;
+    SPEC_DEV explicit Keys(const Args& g_) : g(g_) {}
+    SPEC_DEV void begin(const Item& it, int first, bool mine_) {
+      table = g.kv.block_table + (long long)(g.b0 + it.b) * g.kv.max_blocks;
+      b = g.b0 + it.b, lo = it.lo, hi = it.hi, key = first, mine = mine_;
+      block = key / g.kv.block_size, in_block = key % g.kv.block_size;
+      ask();
+    }
+    SPEC_DEV void ask() { e = mine && key >= lo && key < hi ? __ldg(table + block) : -1; }
+    // the key's slot, -1 for none; then the next tile's key
+    SPEC_DEV int next(bool more, int step_b, int step_i, int kt) {
+      int slot = -1;
+      if (mine && key >= lo && key < hi) {
+        const long long s = (long long)e * g.kv.block_size + in_block;
+        if (s >= 0 && s < g.kv.num_slots) slot = (int)s;
+        else report(g.ws, SPEC_ERR_DEVICE, b, key);
+      }
+      key += kt, block += step_b, in_block += step_i;
+      if (in_block >= g.kv.block_size) in_block -= g.kv.block_size, ++block;
+      if (more) ask();
+      return slot;
+    }
   };
+
+  // 16-bit keys in runs of 16 slots: tensor copies, a lane a run and 64 components, that report to the MMA warp by themselves;
+  // the values of edge tiles come by way of this warp.
   static SPEC_DEV void run_tensor(const TcArgs& a, TcSmem& sm, uint32_t q0, int warp, int lane) {
     const Args& g = a.g;
     const int chunks = a.l.chunks, stages = a.l.stages, units = g.hd / 8, r0 = warp * RW;
-    const uint32_t stage_bytes = a.l.stage_bytes, raw_bytes = a.l.raw_bytes, ring0 = q0 + a.l.q_bytes,
-                   raw0 = ring0 + (uint32_t)stages * stage_bytes;
+    const uint32_t stage_bytes = a.l.stage_bytes, ring0 = q0 + a.l.q_bytes;
     volatile int* abort = &sm.abort;
     Walk<S::BM, KT> walk(g, sm.plan);
     Item it;
-    int tiles = 0, items = 0, stage = 0, filled = 0, raw = 0, l_raw = 0;
-    uint32_t phase = 0, q_phase = 0, l_phase = 0;   // l_phase: of landed[warp], a bit each
+    int tiles = 0, items = 0, stage = 0, filled = 0;
+    uint32_t phase = 0, q_phase = 0, l_phase = 0;
     // this lane's copy: run and chunk
-    const int per = F8 ? 1 : chunks, run = lane / per, chunk = lane - run * per;
-    const bool copier = run < RW / 16;
-    const uint32_t lane_to = F8 ? (uint32_t)((r0 + run * 16) * g.hd) : (uint32_t)(chunk * KT * 128 + (r0 + run * 16) * 128);
-    const uint32_t run_mask = copier ? 0xffffu << (run * 16) : 0u, run_bytes = F8 ? 16u * g.hd : chunks * 2048u;
+    const int run = lane / chunks, chunk = lane - run * chunks;
+    const uint32_t lane_to = (uint32_t)(chunk * KT * 128 + (r0 + run * 16) * 128);
+    const uint32_t run_mask = run < RW / 16 ? 0xffffu << (run * 16) : 0u;
     const uint64_t policy = tc::policy_evict_last();
     const int step_b = KT / g.kv.block_size, step_i = KT % g.kv.block_size;
-    const bool mine = lane < RW;
-    bool ok = true, pending = false;
-    Way way{};
-    auto free_stage = [&] { return __all_sync(0xffffffffu, wait_for(sm.empty[stage], phase ^ 1u, abort)); };
-    auto next_stage = [&] {
-      filled = min(filled + 1, stages);
-      if (++stage == stages) stage = 0, phase ^= 1u;
-    };
-    // The stage that is to come by way of this warp: waits for its copies, widens and clears it, hands it over.
-    auto hand = [&](const Way& w) {
-      if (F8 && !free_stage()) return false;
-      if (!__all_sync(0xffffffffu, wait_for(sm.landed[warp][l_raw], l_phase >> l_raw & 1u, abort))) return false;
-      l_phase ^= 1u << l_raw;
-      const uint32_t at = ring0 + (uint32_t)stage * stage_bytes;
-      if constexpr (F8) {
-        const uint32_t from = raw0 + (uint32_t)l_raw * raw_bytes;
-        if (units == 16) widen_rows<8>(from, at, r0, lane, 8);
-        else if (units == 8) widen_rows<4>(from, at, r0, lane, 4);
-        else widen_rows<0>(from, at, r0, lane, units / 2);
-        if (++l_raw == kRawStages) l_raw = 0;
-        __syncwarp();
-        if (w.value && w.absent) zero_rows(at, r0, lane, units, w.absent);
-        __syncwarp();
-      }
-      if (w.info >= 0) clean_rows(sm, at, r0, lane, units, w.info, w.there);
-      proxy_fence();
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(tc::su32(&sm.full[stage]));
-      next_stage();
-      return true;
-    };
+    Keys at_key(g);
+    bool ok = true;
     while (ok && walk.next(it)) {
       const Edges<KT> edges(g, it);
-      const int32_t* table = g.kv.block_table + (long long)(g.b0 + it.b) * g.kv.max_blocks;
-      int key = (it.tile0 + it.k0) * KT + r0 + lane, block = key / g.kv.block_size, in_block = key % g.kv.block_size;
-      auto entry = [&] { return mine && key >= it.lo && key < it.hi ? __ldg(table + block) : -1; };
-      int e = entry();
+      at_key.begin(it, (it.tile0 + it.k0) * KT + r0 + lane, lane < RW);
       for (int k = it.k0; ok && k < it.k1; ++k, ++tiles) {
-        int slot = -1;
-        if (mine && key >= it.lo && key < it.hi) {
-          const long long s = (long long)e * g.kv.block_size + in_block;
-          if (s >= 0 && s < g.kv.num_slots) slot = (int)s;
-          else report(g.ws, SPEC_ERR_DEVICE, g.b0 + it.b, key);
-        }
-        key += KT, block += step_b, in_block += step_i;
-        if (in_block >= g.kv.block_size) in_block -= g.kv.block_size, ++block;
-        if (k + 1 < it.k1) e = entry();
+        const int slot = at_key.next(k + 1 < it.k1, step_b, step_i, KT);
         const uint32_t there = __ballot_sync(0xffffffffu, slot >= 0);
         if (lane == 0) {
           if constexpr (RW == 32) sm.bits[tiles % kTileBits][warp] = there;
@@ -469,73 +477,168 @@ template <typename T, bool F8, int MODE> struct Loader {
         const uint32_t keys = there & run_mask;
         const int from = keys ? __ffs(keys) - 1 : 0;
         const int first = __shfl_sync(0xffffffffu, slot, from) - (from & 15);
-        const uint32_t bytes = ((there & 0xffffu ? 1u : 0u) + (RW == 32 && there >> 16 ? 1u : 0u)) * run_bytes;
+        const uint32_t bytes = ((there & 0xffffu ? 1u : 0u) + (RW == 32 && there >> 16 ? 1u : 0u)) * chunks * 2048u;
         const uint32_t absent = (there & 0xffffu ? 0u : 0xffffu) | (RW == 32 && !(there >> 16) ? 0xffff0000u : 0u);
         const int tile = it.tile0 + k;
-        const int info = edges.has(tile) ? (items % kItems) << 8 | edges.template slot<S::EDGES>(tile) : -1;
+        const bool edge = edges.has(tile);
 #pragma unroll 1
-        for (int value = 0; ok && value < 2; ++value) {
-          const Way now{there, absent, value ? info : -1, value != 0};
-          const bool by_way = F8 || now.info >= 0;
-          if (!F8 && !free_stage()) {
+        for (int value = 0; value < 2; ++value) {
+          if (!__all_sync(0xffffffffu, wait_for(sm.empty[stage], phase ^ 1u, abort))) {
             ok = false;
             break;
           }
-          const uint32_t at = F8 ? raw0 + (uint32_t)raw * raw_bytes : ring0 + (uint32_t)stage * stage_bytes;
-          if (!F8 && value && absent) {                // nothing is copied there: weights of 0 must meet numbers
+          const uint32_t at = ring0 + (uint32_t)stage * stage_bytes;
+          const bool by_way = value && edge;
+          if (value && absent) {                       // nothing is copied there: weights of 0 must meet numbers
             zero_rows(at, r0, lane, units, absent);
             proxy_fence();
           }
-          uint64_t& bar = by_way ? sm.landed[warp][F8 ? raw : 0] : sm.full[stage];
+          uint64_t& bar = by_way ? sm.landed[warp] : sm.full[stage];
           __syncwarp();
           if (lane == 0) tc::mbar_expect_tx(tc::su32(&bar), bytes);
           __syncwarp();
           if (keys) copy_run(at + lane_to, value ? &a.tmv : &a.tmk, tc::su32(&bar), 64 * chunk, it.h, first, policy);
-          __syncwarp();
-          if constexpr (F8) {
-            if (++raw == kRawStages) raw = 0;
-            if (pending) ok = hand(way);
-            way = now, pending = true;
-          } else if (by_way) {
-            ok = hand(now);
-          } else {
-            next_stage();
-          }
-        }
-        if (k == it.k0 && ok) {
-          // Q, once the first keys are on their way
-          if (items > 0) {
-            ok = __all_sync(0xffffffffu, wait_for(sm.q_empty, q_phase, abort));
-            q_phase ^= 1u;
-          }
-          if (ok && a.l.q_boxes) {
-            copy_q(a, sm, it, q0, warp, lane);
-          } else if (ok) {
-            load_q(g, it, q0, chunks, warp, lane);
-            cp_commit();
-            cp_wait<0>();
+          if (by_way) {
+            __syncwarp();
+            if (!__all_sync(0xffffffffu, wait_for(bar, l_phase, abort))) {
+              ok = false;
+              break;
+            }
+            l_phase ^= 1u;
+            clean_rows(sm, at, r0, lane, units, (items % kItems) << 8 | edges.template slot<S::EDGES>(tile), there);
             proxy_fence();
             __syncwarp();
-            if (lane == 0) tc::mbar_arrive(tc::su32(&sm.q_full));
+            if (lane == 0) tc::mbar_arrive(tc::su32(&sm.full[stage]));
           }
+          filled = min(filled + 1, stages);
+          if (++stage == stages) stage = 0, phase ^= 1u;
+        }
+        // Q, once the first keys are on their way
+        if (k == it.k0 && ok) ok = next_q(a, sm, it, q0, warp, lane, items, q_phase);
+      }
+      ++items;
+    }
+    cp_wait<0>();
+    if (!ok || sm.abort) {
+      // gives up: the copies under way land first (or the limit passes)
+      settle_q(a, sm, warp, items);
+      for (int i = 0; i < filled; ++i) {
+        if (--stage < 0) stage = stages - 1, phase ^= 1u;
+        tc::mbar_wait(tc::su32(&sm.full[stage]), phase, abort, false);
+      }
+    }
+  }
+
+  // 8-bit keys in runs of 16 slots: one warp asks for them, as they lie, in raw stages ...
+  static SPEC_DEV void ask_raw(const TcArgs& a, TcSmem& sm, uint32_t q0, int lane) {
+    constexpr int N = KT / 32, RUNS = KT / 16;
+    const Args& g = a.g;
+    const uint32_t raw0 = q0 + a.l.q_bytes + (uint32_t)a.l.stages * a.l.stage_bytes;
+    volatile int* abort = &sm.abort;
+    Walk<S::BM, KT> walk(g, sm.plan);
+    Item it;
+    int tiles = 0, items = 0, raw = 0, asked = 0;
+    uint32_t phase = 0;
+    const uint64_t policy = tc::policy_evict_last();
+    const int step_b = KT / g.kv.block_size, step_i = KT % g.kv.block_size;
+    Keys at_key[4] = {Keys(g), Keys(g), Keys(g), Keys(g)};         // (N of them)
+    bool ok = true;
+    while (ok && walk.next(it)) {
+      const Edges<KT> edges(g, it);
+#pragma unroll
+      for (int i = 0; i < N; ++i) at_key[i].begin(it, (it.tile0 + it.k0) * KT + 32 * i + lane, true);
+      for (int k = it.k0; ok && k < it.k1; ++k, ++tiles) {
+        uint32_t there[N], runs = 0, keys = 0;
+        int first = 0;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          const int slot = at_key[i].next(k + 1 < it.k1, step_b, step_i, KT);
+          there[i] = __ballot_sync(0xffffffffu, slot >= 0);
+          // lane r: run r
+          const uint32_t mine = lane >> 1 == i ? there[i] & 0xffffu << (16 * (lane & 1)) : 0u;
+          const int from = mine ? __ffs(mine) - 1 : 0, s = __shfl_sync(0xffffffffu, slot, from);
+          if (mine) first = s - (from & 15), keys = mine;
+          runs += (there[i] & 0xffffu ? 1u : 0u) + (there[i] >> 16 ? 1u : 0u);
+        }
+        const int tile = it.tile0 + k;
+        const int info = edges.has(tile) ? (items % kItems) << 8 | edges.template slot<S::EDGES>(tile) : -1;
+#pragma unroll 1
+        for (int value = 0; value < 2; ++value) {
+          if (!__all_sync(0xffffffffu, wait_for(sm.raw_empty[raw], phase ^ 1u, abort))) {
+            ok = false;
+            break;
+          }
+          if (lane == 0) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+              sm.way_there[raw][i] = there[i];
+              if (!value) sm.bits[tiles % kTileBits][i] = there[i];
+            }
+            sm.way_info[raw] = value ? info : -1;
+            tc::mbar_expect_tx(tc::su32(&sm.raw_full[raw]), runs * 16u * g.hd);
+          }
+          __syncwarp();
+          if (lane < RUNS && keys)
+            copy_run(raw0 + (uint32_t)raw * a.l.raw_bytes + (uint32_t)(lane * 16 * g.hd), value ? &a.tmv : &a.tmk,
+                     tc::su32(&sm.raw_full[raw]), 0, it.h, first, policy);
+          __syncwarp();
+          asked = min(asked + 1, kRawStages);
+          if (++raw == kRawStages) raw = 0, phase ^= 1u;
         }
       }
       ++items;
     }
-    if (ok && pending) ok = hand(way);
-    cp_wait<0>();
-    if (!ok || sm.abort) {
-      // gives up: the copies under way land first (or the limit passes)
-      if (a.l.q_boxes && warp == 0 && items > 0) tc::mbar_wait(tc::su32(&sm.q_full), (uint32_t)(items - 1) & 1u, abort, false);
-      if constexpr (F8) {
-        for (int i = 0; i < kRawStages; ++i) tc::mbar_wait(tc::su32(&sm.landed[warp][i]), l_phase >> i & 1u, abort, false);
-      } else {
-        for (int i = 0; i < filled; ++i) {
-          if (--stage < 0) stage = stages - 1, phase ^= 1u;
-          tc::mbar_wait(tc::su32(&sm.full[stage]), phase, abort, false);
-        }
+    if (!ok || sm.abort)
+      for (int i = 0; i < asked; ++i) {
+        if (--raw < 0) raw = kRawStages - 1, phase ^= 1u;
+        tc::mbar_wait(tc::su32(&sm.raw_full[raw]), phase, abort, false);
       }
+  }
+  // ... and the loader warps widen them.
+  static SPEC_DEV void run_widen(const TcArgs& a, TcSmem& sm, uint32_t q0, int warp, int lane) {
+    const Args& g = a.g;
+    const int stages = a.l.stages, units = g.hd / 8, r0 = warp * RW;
+    const uint32_t stage_bytes = a.l.stage_bytes, ring0 = q0 + a.l.q_bytes, raw0 = ring0 + (uint32_t)stages * stage_bytes;
+    volatile int* abort = &sm.abort;
+    Walk<S::BM, KT> walk(g, sm.plan);
+    Item it;
+    int items = 0, stage = 0, raw = 0;
+    uint32_t phase = 0, r_phase = 0, q_phase = 0;
+    bool ok = true;
+    while (ok && walk.next(it)) {
+      const int jobs = 2 * (it.k1 - it.k0);            // K, V, K, V, ...
+#pragma unroll 1
+      for (int j = 0; ok && j < jobs; ++j) {
+        ok = __all_sync(0xffffffffu, wait_for(sm.raw_full[raw], r_phase, abort)) &&
+             __all_sync(0xffffffffu, wait_for(sm.empty[stage], phase ^ 1u, abort));
+        if (!ok) break;
+        const uint32_t word = sm.way_there[raw][r0 / 32];
+        const uint32_t there = RW == 32 ? word : word >> (r0 % 32) & 0xffffu;
+        const int info = sm.way_info[raw];
+        const uint32_t from = raw0 + (uint32_t)raw * a.l.raw_bytes, at = ring0 + (uint32_t)stage * stage_bytes;
+        if (units == 16) widen_rows<8>(from, at, r0, lane, 8);
+        else if (units == 8) widen_rows<4>(from, at, r0, lane, 4);
+        else widen_rows<0>(from, at, r0, lane, units / 2);
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(tc::su32(&sm.raw_empty[raw]));
+        const uint32_t absent = (there & 0xffffu ? 0u : 0xffffu) | (RW == 32 && !(there >> 16) ? 0xffff0000u : 0u);
+        if (absent) {                                  // (whatever the raw stage held)
+          zero_rows(at, r0, lane, units, absent);
+          __syncwarp();
+        }
+        if (info >= 0) clean_rows(sm, at, r0, lane, units, info, there);
+        proxy_fence();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(tc::su32(&sm.full[stage]));
+        if (++raw == kRawStages) raw = 0, r_phase ^= 1u;
+        if (++stage == stages) stage = 0, phase ^= 1u;
+        // Q, once the first keys are there
+        if (j == 0) ok = next_q(a, sm, it, q0, warp, lane, items, q_phase);
+      }
+      ++items;
     }
+    cp_wait<0>();
+    if (!ok || sm.abort) settle_q(a, sm, warp, items);
   }
 
   // One loop, a step of which either hands over the oldest stage under way or asks for the next one, so that each is in
@@ -1168,8 +1271,11 @@ template <typename T, bool F8, int MODE> __global__ void __launch_bounds__(kTcTh
     tc::mbar_init(tc::su32(&sm.q_full), 4);
     tc::mbar_init(tc::su32(&sm.q_empty), 1);
     tc::mbar_init(tc::su32(&sm.drain), 1);
-    for (int i = 0; i < 4; ++i)
-      for (int j = 0; j < kRawStages; ++j) tc::mbar_init(tc::su32(&sm.landed[i][j]), 1);
+    for (int i = 0; i < 4; ++i) tc::mbar_init(tc::su32(&sm.landed[i]), 1);
+    for (int i = 0; i < kRawStages; ++i) {
+      tc::mbar_init(tc::su32(&sm.raw_full[i]), 1);
+      tc::mbar_init(tc::su32(&sm.raw_empty[i]), 4);
+    }
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(tc::su32(&sm.s_full[i]), 1);
       tc::mbar_init(tc::su32(&sm.p_full[i][0]), 4);
@@ -1198,11 +1304,13 @@ template <typename T, bool F8, int MODE> __global__ void __launch_bounds__(kTcTh
     if (MODE != kWide || warp < 4) Softmax<T, F8, MODE>(a.g, sm, tmem, warp >> 2, warp & 3, lane).run();
   } else if (warp < 12) {
     regs_dec<kLoaderRegs>();
-    if (a.l.runs) Loader<T, F8, MODE>::run_tensor(a, sm, base, warp - 8, lane);
+    if (a.l.runs && F8) Loader<T, F8, MODE>::run_widen(a, sm, base, warp - 8, lane);
+    else if (a.l.runs) Loader<T, F8, MODE>::run_tensor(a, sm, base, warp - 8, lane);
     else Loader<T, F8, MODE>::run(a, sm, base, warp - 8, lane);
   } else {
     regs_dec<kMmaRegs>();
     if (warp == 12) issue_mmas<T, MODE>(a, sm, base, tmem);
+    else if (F8 && warp == 13 && a.l.runs) Loader<T, F8, MODE>::ask_raw(a, sm, base, lane);
   }
   tc::tc_fence_before();
   __syncthreads();
