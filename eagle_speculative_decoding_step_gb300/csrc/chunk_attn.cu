@@ -36,7 +36,7 @@ SPEC_DEV int slot_for(const Args& g, const Item& it, int key) {
   return (int)s;
 }
 
-// Bound by the multiply-add pipes (2 of 4 operands of each from shared memory, 4 x 4 outputs a thread).
+// fp32 rows.  Bound by shared memory: 8 reads of 16 bytes for 64 multiply-adds of a thread (4 x 4 outputs); 31 TFLOP/s.
 template <int HD> __global__ void __launch_bounds__(kFmaThreads)
     chunk_fma_kernel(const __grid_constant__ Args g) {
   SPEC_TL(kTLChunkAttn);
@@ -287,7 +287,7 @@ static long long most_items(const spec_attn_desc& d, long long B, long long rows
   return d.n_kv_heads * (2 * B + (rows * (d.n_q_heads / d.n_kv_heads) + kFmaRows - 1) / kFmaRows);
 }
 
-// Both sides measured: see the table at the modes.
+// 128 packed rows where every request's fit them (32 requests of 8 tokens, 512-2048 keys, kOneQ / kTwoQ: ONEQ / TWOQ us).
 static int mode_for(const spec_attn_desc& d, int longest) {
   if (d.head_dim > 128) return kWide;
   return (long long)longest * (d.n_q_heads / d.n_kv_heads) <= 128 ? kOneQ : kTwoQ;
@@ -346,7 +346,7 @@ static spec_status launch_tc(const spec_attn_desc& d, const Args& g, int longest
   if (a.l.q_boxes && !rows_map(&a.tmq, g.q, d.dtype, d.head_dim, d.n_q_heads, g.n_rows, g.q_ld, g.G, 128 / g.G))
     return SPEC_ERR_CUDA;
   const TcFn fn = d.dtype == SPEC_DTYPE_BF16 ? tc_kernel_bf16(f8, mode) : tc_kernel_f16(f8, mode);
-  if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kTcSmem) != cudaSuccess) return SPEC_ERR_CUDA;
+  if (!fn || cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kTcSmem) != cudaSuccess) return SPEC_ERR_CUDA;
   return cuda_status(launch_pdl(fn, dim3(sms), dim3(kTcThreads), a.l.smem, st, a));
 }
 

@@ -238,6 +238,8 @@ template <int kThreads> SPEC_DEV void best_of(Smem& sm, int n, int k) {
 // are left, about k, are read again (from L2) and ranked by counting.  Where there are too many (logits in an order, or
 // mostly equal) the part is searched k times.  The last CTA of a row to finish joins the parts in their order (a counter,
 // nobody waits).
+// 2048 rows of 151936 fp32 logits: k = 0 208 us (91 % of the copy bandwidth), k = 20 233; bf16, 152 and 190 (13 instructions an
+// element, half of the issue slots' time); 64 rows of 128256 bf16, k = 5: 15 us, a chain of dependent trips.
 template <typename T, int NV> __global__ void __launch_bounds__(threads_of<T>(), kResident / threads_of<T>())
     logprobs_kernel(const __grid_constant__ Args g) {
   SPEC_TL(kTLLogprobs);
