@@ -197,13 +197,15 @@ class Batch:
     def resize(self, want):
         """Grow to (or give back down to) want [B] tokens by at most B new ones in all: their slots and
         positions are in ``slots`` and ``pos``, those of request b from ``cu``[b] on (a request that is
-        refused for its length has none there)."""
+        refused for its length has none there).  Once rows were forked, one gives back all that it holds (want 0) or
+        nothing: a smaller want leaves it as it is."""
         self._resize(want, self.slots, self.pos)
 
     def _resize(self, want, slots, pos):
         c = self.cache
         if self.forked:                                     # what others hold stays
             lib.spec_block_release(self.blocks, (want == 0).int(), self.bws)
+            want = torch.where(want > 0, torch.maximum(want, self.length), want)
         lib.spec_block_tables(self.B, c.block_size, self.table.shape[1], c.num_blocks, self.length, want, self.table,
                               self.table, c.free, c.n_free, c.free, c.n_free, self.length, self.cu, slots, pos,
                               slots.numel(), self.tws)

@@ -184,3 +184,21 @@ def test_refusals():
                  lambda: b.fork([0, 0], [1, 1]), lambda: b.fork([0], [2]), lambda: b.fork([-1], [1])):
         with pytest.raises(ValueError):
             call()
+
+
+def test_a_smaller_size_takes_no_block_from_a_fork():
+    m, p = model(), prompts(10)
+    first, got = torch.tensor([7, 8], dtype=torch.int32), []
+    for shrink in (False, True):
+        b = decode.Batch(m, cache_of(m), 2, 64, m.vocab)
+        b.extend(p + [[]])
+        b.drop([1])
+        b.fork([0], [1])
+        if shrink:
+            b.resize(torch.tensor([3, 10], dtype=torch.int32))
+            assert b.length.tolist() == [10, 10]
+        got.append(b.decode(first, 6)[1])
+        assert b.error() == 0
+        b.release()
+        assert sorted(b.cache.free.tolist()) == list(range(b.cache.num_blocks)) and int(b.cache.shared.sum()) == 0
+    assert torch.equal(*got)
