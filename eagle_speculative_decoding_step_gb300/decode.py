@@ -325,6 +325,8 @@ class Batch:
 
     def drop(self, rows):
         """Ends the requests of the given rows (a host list); blocks that no other row holds go back to the pool."""
+        if not all(0 <= i < self.B for i in rows):
+            raise ValueError("rows %s of %d" % (rows, self.B))
         which = torch.zeros(self.B, dtype=torch.int32, device=self.cache.device)
         which[torch.tensor(rows, dtype=torch.long, device=self.cache.device)] = 1
         lib.spec_block_release(self.blocks, which, self.bws)

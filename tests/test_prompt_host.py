@@ -181,7 +181,7 @@ def test_refusals():
     m = model()
     b = decode.Batch(m, cache_of(m), 2, 64, m.vocab)
     for call in (lambda: b.extend([[1]]), lambda: b.extend([[], []]), lambda: b.extend([[1], [2]], chunk=0), lambda: b.fork([0], []),
-                 lambda: b.fork([0, 0], [1, 1]), lambda: b.fork([0], [2]), lambda: b.fork([-1], [1])):
+                 lambda: b.fork([0, 0], [1, 1]), lambda: b.fork([0], [2]), lambda: b.fork([-1], [1]), lambda: b.drop([2]), lambda: b.drop([0, -1])):
         with pytest.raises(ValueError):
             call()
 
