@@ -96,23 +96,26 @@ struct Plan {
 
 SPEC_DEV int owner(const Plan& p, long long x) { return (int)(((x + 1) * p.ctas - 1) / p.total); }
 
-// All threads of the block.  A few thousand integers at most are read, from L2.
+// All threads of the block.  A few thousand integers at most are read, from L2.  Where rows fall from a request to the
+// next, requests overlap, and their items may be more than there are counters: then none has any.
 template <int BM, int KT> SPEC_DEV void make_plan(const Args& g, Plan& p, int tid, int threads) {
+  int falls = 0;
 #pragma unroll 1
   for (int b = tid; b < g.B; b += threads) {
     bool bad;
+    falls |= g.cu[g.b0 + b + 1] < g.cu[g.b0 + b];
     const Req r = request(g, b, &bad);
     if (bad && blockIdx.x == 0) report(g.ws, SPEC_ERR_DEVICE, g.b0 + b, r.len);
     p.pairs[b + 1] = (int)(((long long)r.n * g.G + BM - 1) / BM);
     p.work[b + 1] = 0;
   }
   if (tid == 0) p.pairs[0] = 0, p.work[0] = 0, p.longest = 0;
-  __syncthreads();
+  falls = __syncthreads_or(falls);
   if (tid < 32) {
     int run = 0;
 #pragma unroll 1
     for (int b0 = 0; b0 < g.B; b0 += 32) {
-      int x = b0 + tid < g.B ? p.pairs[b0 + tid + 1] : 0;
+      int x = b0 + tid < g.B && !falls ? p.pairs[b0 + tid + 1] : 0;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int y = __shfl_up_sync(0xffffffffu, x, o);

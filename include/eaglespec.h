@@ -635,9 +635,9 @@ size_t spec_chunk_attention_workspace_bytes(const spec_attn_desc *desc, int32_t 
  * A score of +infinity or NaN, or one of -infinity, and a V value that is not finite
  * act as in spec_paged_attention, on the rows that attend to their key; other rows
  * are as they would be without.
- * Error word: SPEC_ERR_DEVICE for cu_rows that fall or leave [0, n_rows], a seq_len
- * outside [0, max_blocks * block_size] (both clamped) or a slot out of range (such
- * keys are left out). */
+ * Error word: SPEC_ERR_DEVICE for cu_rows that fall (rows are left as they are),
+ * cu_rows that leave [0, n_rows] or a seq_len outside [0, max_blocks * block_size]
+ * (both clamped), or a slot out of range (such keys are left out). */
 spec_status spec_chunk_attention(const spec_attn_desc *desc, const void *q, int64_t q_ld, const spec_kv *kv,
                                  const int32_t *cu_rows, const int32_t *seq_len, int32_t B, int32_t n_rows,
                                  int32_t max_chunk, int32_t max_len, void *out, int64_t out_ld, float *lse,

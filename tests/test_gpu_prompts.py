@@ -283,6 +283,25 @@ def test_chunk_attention_bad_inputs(t, c):
     assert torch.equal(out[keep], ok[keep]) and torch.equal(lse[keep], olse[keep])
 
 
+@pytest.mark.parametrize("t,c", TYPE_PAIRS)
+def test_chunk_attention_rows_that_fall_again_and_again(t, c):
+    """Requests that overlap would have more items than the workspace has counters: no row is computed, and nothing outside
+    the workspace is written."""
+    x = Chunk([(64, 64)] * 41, 2, 1, 64, t, c, seed=9)
+    x.cu = np.array([0, x.n] * 21)
+    need = lib.spec_chunk_attention_workspace_bytes(x.desc, 41, x.n)
+    room = torch.full((need + 4096,), 85, dtype=torch.uint8, device="cuda")
+    room[:need] = 0
+    out, lse, _ = x.run(ws=room[:need])
+    assert error(room[:need]) == ERR_DEVICE
+    assert (out == 7).all() and (lse == 7).all() and (room[need:] == 85).all()
+    room[:256] = 0                                             # the workspace serves the next call
+    y = Chunk([(64, 64)] * 41, 2, 1, 64, t, c, seed=9)
+    out, lse, _ = y.run(ws=room[:need])
+    assert error(room[:need]) == 0
+    y.check(out, lse)
+
+
 @pytest.mark.parametrize("t", ["bf16", "f32"])
 def test_chunk_attention_output_strides_and_no_lse(t):
     x = Chunk([(37, 90), (5, 60)], 6, 3, 80, t, seed=4)
