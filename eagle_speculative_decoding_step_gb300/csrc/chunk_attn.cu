@@ -381,7 +381,7 @@ extern "C" spec_status spec_chunk_attention(const spec_attn_desc* desc, const vo
   if (q_ld == 0) q_ld = width;
   if (out_ld == 0) out_ld = width;
   if (q_ld < width || out_ld < width) return SPEC_ERR_SHAPE;
-  if ((long long)n_rows * d.n_q_heads >= (1ll << 31)) return SPEC_ERR_CAPACITY;
+  if ((long long)n_rows * d.n_q_heads >= (1ll << 31) || width >= (1ll << 30)) return SPEC_ERR_CAPACITY;
   const int es = d.dtype == SPEC_DTYPE_F32 ? 4 : 2;
   if (!aligned(q, 16) || !aligned(out, 16) || !aligned(kv->k, 16) || !aligned(kv->v, 16) || q_ld * es % 16 ||
       out_ld * es % 16)

@@ -629,8 +629,9 @@ size_t spec_chunk_attention_workspace_bytes(const spec_attn_desc *desc, int32_t 
  * one row to the next (0 = n_q_heads * head_dim); lse [n_rows, n_q_heads] fp32 or
  * NULL.  cu_rows [B + 1], seq_len [B].  max_chunk and max_len: upper bounds of a
  * request's new tokens and of seq_len, or 0 if unknown; they only choose how work
- * is laid out.  Any block_size; max_blocks * block_size < 2^30, n_rows * n_q_heads
- * < 2^31.  q, out, the cache and, with ld's, every row of q and out 16-byte aligned
+ * is laid out.  Any block_size; max_blocks * block_size < 2^30 (SPEC_ERR_SHAPE),
+ * n_rows * n_q_heads < 2^31 and n_q_heads * head_dim < 2^30 (SPEC_ERR_CAPACITY).
+ * q, out, the cache and, with ld's, every row of q and out 16-byte aligned
  * (SPEC_ERR_ALIGN).  out does not overlap q or the cache.
  * A score of +infinity or NaN, or one of -infinity, and a V value that is not finite
  * act as in spec_paged_attention, on the rows that attend to their key; other rows

@@ -50,7 +50,7 @@ def test_chunk_attention_refusals():
     for x in (-1.0, float("nan"), float("inf")):
         assert chunk(d=desc(scale=x)) == ARG
         assert chunk(d=desc(c="e4m3", k_scale=x)) == ARG and chunk(d=desc(c="e4m3", v_scale=x)) == ARG
-    assert chunk(n=1 << 28) == CAPACITY
+    assert chunk(n=1 << 28) == CAPACITY and chunk(d=desc(nq=1 << 24, nkv=1 << 24), n=1) == CAPACITY
     assert chunk(q=F + 8) == ALIGN and chunk(out=F + 2) == ALIGN and chunk(q_ld=516) == ALIGN and chunk(out_ld=516) == ALIGN
     assert chunk(cache=kv(k=F + 8)) == ALIGN and chunk(d=desc(t="f32"), q_ld=514) == ALIGN
     assert chunk(ws=None) == WS and chunk(ws=F + 128) == WS and chunk(wsb=256) == WS
