@@ -16,7 +16,7 @@
 // (1024 of MMA, 1400 with their waits).  128 rows x 128 keys x 128 components: 3060 cycles for
 // two jobs, of which the tensor pipe works 2048.  500 rows of 32 heads over 131071 keys 0.89-0.94 ms
 // (1.14-1.20 PFLOP/s, 59-62 % of a measured cuBLAS bf16 product; the SM clock stays near
-// 1.5 GHz under this load, as it does for cuBLAS), 16 chunks of 100-2048 tokens 0.93-0.96 ms.
+// 1.5 GHz under this load, as it does for cuBLAS), 16 chunks of 100-2048 tokens 0.93 ms.
 #pragma once
 #include <type_traits>
 
@@ -29,7 +29,7 @@ namespace ca {
 // kTwoQ: 256 rows, a warpgroup for each half, every K/V tile used twice (shared memory gives the tensor cores
 // 128 bytes a cycle: scores of 128 x 128 take all of it).  kOneQ: 128 rows, the warpgroups take turns at the
 // tiles with an accumulator each, joined at the end.  kWide: head sizes above 128, whose accumulator leaves no
-// room for a second one: 128 rows, tiles of 64 keys, one warpgroup (256 components: 770 TFLOP/s).
+// room for a second one: 128 rows, tiles of 64 keys, one warpgroup (256 components: 780 TFLOP/s).
 enum Mode { kTwoQ = 0, kOneQ = 1, kWide = 2 };
 
 constexpr int kTcThreads = 512;
@@ -254,7 +254,7 @@ struct TcSmem {
 // Keys come in runs of 16 slots by tensor copies where the block size allows: boxes of 16 slots x 128 bytes, no thread's
 // time.  Otherwise four warps copy a tile's rows in 16-byte pieces (cp.async): any block size, rows of any number of
 // pieces, and 512 bytes an instruction; an SM takes about 27 bytes a cycle that way (8 chunks of 512-1024 tokens, blocks of
-// 16 / 24 / 1 slots: 289 / 410 / 408 us).  U: pieces of a cache row, where that is 4, 8, 16 or 32 (a lane's piece and its step from row to row do
+// 16 / 24 / 1 slots: 280 / 394 / 394 us).  U: pieces of a cache row, where that is 4, 8, 16 or 32 (a lane's piece and its step from row to row do
 // not change then), or 0.
 template <int N> struct Units {
   const int n, inv;                    // 2^16 / n rounded up: quotients of numbers below 2^11 are exact
@@ -1085,6 +1085,25 @@ template <typename T, bool F8, int MODE> struct Softmax {
     reinterpret_cast<uint4*>(dst)[1] = make_uint4(u[4], u[5], u[6], u[7]);
   }
 
+  // 16 components of the rows of a warp, a row a lane: two lanes exchange pieces of 16 bytes, so that a store writes 32 bytes
+  // of each of 16 rows instead of 16 of each of 32 (8 chunks of 512-1024 tokens 287 -> 279 us, 32 of 100-300 tokens
+  // 114 -> 109; four lanes, 64 bytes of 8 rows: as much, but 1-3 % more where items are long, from the code).  Not kOneQ,
+  // whose few rows are written sooner without (4 chunks of 8 tokens 15.4 / 16.1).
+  // at: the lane's piece of the pair's rows (NULL: not written).
+  static SPEC_DEV void write_rows(T* const (&at)[2], int c, const float* o, float inv, bool odd) {
+    uint32_t u[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) u[j] = pack2<T>(o[2 * j] * inv, o[2 * j + 1] * inv);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t x = __shfl_xor_sync(0xffffffffu, odd ? u[j] : u[4 + j], 1);
+      if (odd) u[j] = x;
+      else u[4 + j] = x;
+    }
+    if (at[0]) *reinterpret_cast<uint4*>(at[0] + c) = make_uint4(u[0], u[1], u[2], u[3]);
+    if (at[1]) *reinterpret_cast<uint4*>(at[1] + c) = make_uint4(u[4], u[5], u[6], u[7]);
+  }
+
   // The item's rows, or their piece; the last piece to come joins all.
   SPEC_DEV bool finish(const Item& it, int item, int klo, int khi) {
     const bool two = MODE == kOneQ && it.k1 - it.k0 > 1;
@@ -1111,6 +1130,14 @@ template <typename T, bool F8, int MODE> struct Softmax {
     const float inv = l == 0.f ? 0.f : g.v_scale / l;
     const size_t piece = piece_floats(BM, g.hd);
     float* mine = g.part + (whole ? 0 : 2 * blockIdx.x + (it.k0 > 0 ? 0 : 1)) * piece;
+    const bool odd = lane & 1;
+    T* at[2];
+    if (MODE != kOneQ && whole) {
+      T* const own = valid ? dst : nullptr;
+      T* const other = reinterpret_cast<T*>(__shfl_xor_sync(0xffffffffu, reinterpret_cast<unsigned long long>(own), 1));
+      at[0] = odd ? other : own, at[1] = odd ? own : other;
+      if (odd) at[0] = at[0] ? at[0] + 8 : nullptr, at[1] = at[1] ? at[1] + 8 : nullptr;
+    }
 #pragma unroll 1
     for (int c = c0; c < c1; c += 32) {
       const bool more = c + 16 < c1;
@@ -1120,7 +1147,11 @@ template <typename T, bool F8, int MODE> struct Softmax {
         mend(it, item, klo, khi, c, o);
         if (more) mend(it, item, klo, khi, c + 16, o + 16);
       }
-      if (valid && whole) {
+      if (MODE != kOneQ && whole) {
+        write_rows(at, c, o, inv, odd);
+        if (more) write_rows(at, c + 16, o + 16, inv, odd);
+      }
+      if (MODE == kOneQ && whole && valid) {
         write(dst + c, o, inv);
         if (more) write(dst + c + 16, o + 16, inv);
       }
