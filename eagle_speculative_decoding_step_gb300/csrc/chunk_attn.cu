@@ -115,7 +115,8 @@ template <int HD> __global__ void __launch_bounds__(kFmaThreads)
         }
 #pragma unroll
         for (int w = 8; w > 0; w >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
-        const float now = fmaxf(m[i], top), base = base_of(now), keep = exp2_fast(base_of(m[i]) - base);
+        // (nothing seen yet: m is -infinity and keep 0, whatever the first scores are)
+        const float now = fmaxf(m[i], top), base = base_of(now), keep = exp2_fast(m[i] - base);
         float sum = 0.f;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -222,7 +223,7 @@ template <int HD> __global__ void __launch_bounds__(kFmaThreads)
           const int r = ty + 16 * i;
           const float mc = __ldcg(x + (size_t)BM * g.hd + r), lc = __ldcg(x + (size_t)BM * (g.hd + 1) + r);
           const float now = fmaxf(m[i], mc), base = base_of(now);
-          const float a = exp2_fast(base_of(m[i]) - base), b = exp2_fast(base_of(mc) - base);
+          const float a = exp2_fast(m[i] - base), b = exp2_fast(mc - base);    // (0 for a piece without keys of the row)
           m[i] = now;
           l[i] = l[i] * a + lc * b;
 #pragma unroll
