@@ -240,7 +240,9 @@ class Batch:
         if chunk < 1:
             raise ValueError("chunks of %d tokens" % chunk)
         dev = self.cache.device
-        # a row that was dropped, or whose request ended and gave its blocks back, takes another one
+        # a row that was dropped, or whose request has ended (with the last step, it may be: then it gives its blocks back
+        # first), takes another one
+        self.resize(self.length * self.kept)
         fresh = torch.tensor([len(t) > 0 for t in tokens], device=dev) & (self.length == 0)
         self.live, self.kept = (torch.where(fresh, 1, x) for x in (self.live, self.kept))
         for x in (self.select.score, self.select.done):

@@ -1,0 +1,60 @@
+"""Batches that take prompts, forks and smaller sizes at any point of their requests' lives, on CPU tensors (prompt_library)."""
+import pytest
+import torch
+
+import prompt_library
+from eagle_speculative_decoding_step_gb300 import decode
+from test_prompt_host import cache_of, model, one_by_one, prompts
+
+
+@pytest.fixture(autouse=True)
+def on_cpu(monkeypatch):
+    prompt_library.use(monkeypatch)
+
+
+def ints(*x):
+    return torch.tensor(x, dtype=torch.int32)
+
+
+def all_blocks_are_back(b):
+    return sorted(b.cache.free.tolist()) == list(range(b.cache.num_blocks)) and int(b.cache.shared.sum()) == 0
+
+
+def ended(steps, forked=False):
+    """A batch whose row 0 has just selected the end token, in the last of `steps` steps, and row 1 goes on; the same batch
+    without an end token."""
+    m, p, out = model(), prompts(9, 6), None
+    for eos in (-1, None):
+        b = decode.Batch(m, cache_of(m), 3, 64, m.vocab, eos=eos if eos is not None else int(out[0, steps - 1]))
+        b.extend(p + [[]])
+        if forked:
+            b.drop([2])
+            b.fork([0], [2])
+        first = out
+        out = b.decode(ints(7, 8, 9), steps)
+    end = int(first[0, steps - 1])
+    assert end not in first[0, :steps - 1].tolist() and end not in first[1].tolist() and end not in first[2].tolist()
+    assert int(b.live[0]) == 0 and int(b.length[0]) > 0
+    return m, b
+
+
+@pytest.mark.parametrize("forked", [False, True])
+@pytest.mark.parametrize("chunk", [2, 512])
+def test_a_prompt_right_after_an_end_token(forked, chunk):
+    m, b = ended(3, forked)
+    lengths = b.length.tolist()
+    out = b.extend([[3, 4, 5], [], []], chunk=chunk)
+    torch.testing.assert_close(out[0], one_by_one(m, [3, 4, 5])[-1], atol=1e-4, rtol=1e-4)
+    assert b.length.tolist() == [3] + lengths[1:] and b.live.tolist() == [1, 1, 1] and b.error() == 0
+    logits = b.feed(ints(6, 1, 2))
+    torch.testing.assert_close(logits[0], one_by_one(m, [3, 4, 5, 6])[-1], atol=1e-4, rtol=1e-4)
+    b.release()
+    assert all_blocks_are_back(b) and b.error() == 0
+
+
+def test_scores_of_a_prompt_right_after_an_end_token():
+    m, b = ended(4)
+    s = b.score([[3, 4, 5], [], []], k=2)[0]
+    logp = torch.log_softmax(one_by_one(m, [3, 4, 5]).double(), -1)
+    torch.testing.assert_close(s["logprob"][:2], logp[torch.arange(2), torch.tensor([4, 5])].float(), atol=1e-4, rtol=1e-4)
+    assert (s["top_ids"][:, 0].long() == logp.argmax(-1)).all() and b.error() == 0
