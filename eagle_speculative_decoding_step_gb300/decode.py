@@ -270,7 +270,7 @@ class Batch:
     def extend(self, tokens, chunk=512):
         """Appends tokens (a host list of ids a request, which may be empty) to the requests: logits [B, V] after each
         request's last one, zeros where there was none to feed.  A row without a request takes a new one; one that cannot
-        take all its tokens stops, as in ``feed``."""
+        take all its tokens stops, as in ``feed``, and gets zeros."""
         out = None
         for logits, ends, at, n in self._chunks(tokens, chunk):
             if out is None:
@@ -278,7 +278,8 @@ class Batch:
             last = [b for b in range(self.B) if n[b] and at + n[b] == len(tokens[b])]
             if last:
                 where = torch.tensor(last, device=logits.device)
-                out[where] = logits[torch.tensor([int(ends[b + 1]) - 1 for b in last], device=logits.device)]
+                rows = logits[torch.tensor([int(ends[b + 1]) - 1 for b in last], device=logits.device)]
+                out[where] = torch.where(self.live[where].bool()[:, None], rows, 0)
         if out is None:
             raise ValueError("no tokens")
         return out
@@ -286,7 +287,8 @@ class Batch:
     def score(self, tokens, k=0, chunk=512):
         """Appends tokens as ``extend`` does, and says what the model made of them: for each request a dict of tensors over
         its tokens, entry i of what it expected after token i: logprob and rank of token i + 1 (-infinity and -1 for the
-        last one, and in requests that stopped), entropy, lse, and top_ids and top_logprob [len, k], the best alternatives."""
+        last one), entropy, lse, and top_ids and top_logprob [len, k], the best alternatives.  Tokens that a request did not
+        take, since it stopped, have what a row without a logit has: -infinity, -1 and an entropy of 0."""
         parts = [[] for _ in tokens]
         for logits, ends, at, n in self._chunks(tokens, chunk):
             name, x, ld = _logits(logits, int(ends[-1]), self.vocab)
@@ -300,7 +302,8 @@ class Batch:
             lib.spec_token_logprobs(rows, self.vocab, name, x, torch.tensor(after, dtype=torch.int32, device=dev), k, ws=self.lws,
                                     ld=ld, **r)
             ok = torch.repeat_interleave(self.live.bool(), torch.tensor(n, device=dev), output_size=rows)
-            r["logprob"], r["rank"] = torch.where(ok, r["logprob"], -float("inf")), torch.where(ok, r["rank"], -1)
+            nothing = dict(rank=-1, top_ids=-1, entropy=0.0)
+            r = {key: torch.where(ok.view(-1, *[1] * (v.dim() - 1)), v, nothing.get(key, -float("inf"))) for key, v in r.items()}
             for b in range(self.B):
                 if n[b]:
                     parts[b].append({key: v[int(ends[b]):int(ends[b + 1])] for key, v in r.items()})

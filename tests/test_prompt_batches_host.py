@@ -58,3 +58,22 @@ def test_scores_of_a_prompt_right_after_an_end_token():
     logp = torch.log_softmax(one_by_one(m, [3, 4, 5]).double(), -1)
     torch.testing.assert_close(s["logprob"][:2], logp[torch.arange(2), torch.tensor([4, 5])].float(), atol=1e-4, rtol=1e-4)
     assert (s["top_ids"][:, 0].long() == logp.argmax(-1)).all() and b.error() == 0
+
+
+def test_what_a_request_that_stopped_is_told():
+    """Its tokens were not fed: logits of zeros, and scores as of a row without a logit.  (The pool serves requests in their
+    order, so the one that it cannot serve is the last.)"""
+    m, p = model(), prompts(6, 5, 30)
+    for chunk in (8, 100):
+        b = decode.Batch(m, cache_of(m, blocks=6), 3, 64, m.vocab)
+        out = b.extend(p, chunk=chunk)
+        assert b.stopped.tolist() == [False, False, True] and (out[2] == 0).all() and out[0].any() and out[1].any()
+        b = decode.Batch(m, cache_of(m, blocks=6), 3, 64, m.vocab)
+        s = b.score(p, k=2, chunk=chunk)
+        assert b.stopped.tolist() == [False, False, True]
+        fed = int(b.length[2])                                 # in the chunks before it stopped
+        assert fed == (8 if chunk == 8 else 0)
+        for key, nothing in (("logprob", -float("inf")), ("rank", -1), ("entropy", 0), ("lse", -float("inf")), ("top_ids", -1),
+                             ("top_logprob", -float("inf"))):
+            assert s[2][key].shape[0] == 30 and (s[2][key][fed:] == nothing).all(), key
+        assert s[2]["lse"][:fed].isfinite().all() and s[0]["lse"].isfinite().all() and (s[1]["top_ids"] >= 0).all()
