@@ -134,7 +134,7 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1) for
   for (int i = warp; i < n; i += kWarps) {
     const int l = len[i], a = g.src[i], d = g.dst[i], whole = l / s.block_size, rest = l % s.block_size;
     int4 move = make_int4(0, 0, 0, 0);
-    if (l > 0 && (rest == 0 || nth[i] < n_free)) {
+    if (l >= 0 && (rest == 0 || nth[i] < n_free)) {      // (l = 0: a row of entries -1)
       int fresh = -1;
       if (rest > 0) {
         const int place = n_free - 1 - nth[i];

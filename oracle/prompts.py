@@ -101,8 +101,6 @@ def block_fork(block_size, table, length, shared, free, n_free, src, dst):
         if rest and nth >= n_free:
             r["short"] = True
             continue
-        if old[a] == 0:
-            continue
         row = np.full(mb, -1)
         for j in range(whole):
             i = int(table[a][j])

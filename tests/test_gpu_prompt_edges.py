@@ -3,7 +3,8 @@ import numpy as np
 import pytest
 import torch
 
-from test_gpu_prompts import TYPE_PAIRS, TYPES, Chunk, error
+from oracle import prompts as oracle
+from test_gpu_prompts import TYPE_PAIRS, TYPES, Chunk, caches, error, moved, pool_case, run_blocks, same
 
 pytestmark = pytest.mark.gpu
 
@@ -32,3 +33,21 @@ def test_chunk_attention_scores_far_below_zero(t, c, hd, chunks, window):
     assert error(ws) == 0
     x.check(out, lse)
     assert (lse[:int(x.cu[-1])] < -150).all()
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+def test_block_fork_of_an_empty_row_leaves_no_entries(in_place):
+    """Rows without tokens whose table entries are whatever was there: a copy of one holds nothing, its entries are -1."""
+    st, empty, _ = pool_case(3, [(20, [30, 25]), (0, [9])], 8, 6, empty=4)
+    a = np.nonzero(st["length"] == 30)[0][0]
+    for row in empty:
+        st["table"][row] = np.arange(st["table"].shape[1]) + row
+    src, dst = [empty[0], a, empty[0]], [empty[1], empty[2], empty[3]]
+    kv, args = caches(1, len(st["free"]), 8, 1, 16, "bf16")
+    ref = oracle.block_fork(8, **st, src=src, dst=dst)
+    want = moved(kv, ref["copies"], 8)
+    got, err = run_blocks("fork", 8, st, in_place, src, dst, kv=args)
+    assert err == 0 and not ref["bad"] and same(kv, want)
+    for k in ("table", "length", "shared", "free", "n_free"):
+        np.testing.assert_array_equal(got[k], ref[k], err_msg=k)
+    assert (got["table"][[empty[1], empty[3]]] == -1).all() and (got["table"][empty[0]] == st["table"][empty[0]]).all()
