@@ -183,7 +183,7 @@ class Batch:
         self.live, self.kept = _ints(B, device=dev, fill=1), _ints(B, device=dev, fill=1)    # takes tokens; keeps its blocks
         self.select = _Select(B, 1, vocab, eos, dev)
         self.vocab = vocab
-        self.forked = False                                 # blocks may have several holders
+        self.forked = False                                 # blocks may have several holders (until all are given back)
         self.bws = torch.zeros(lib.spec_block_state_workspace_bytes(B, cache.num_blocks), dtype=torch.uint8, device=dev)
         self.lws = None
         c = cache
@@ -197,15 +197,19 @@ class Batch:
     def resize(self, want):
         """Grow to (or give back down to) want [B] tokens by at most B new ones in all: their slots and
         positions are in ``slots`` and ``pos``, those of request b from ``cu``[b] on (a request that is
-        refused for its length has none there).  Once rows were forked, one gives back all that it holds (want 0) or
-        nothing: a smaller want leaves it as it is."""
+        refused for its length has none there).  A smaller want (not 0) of a row that was forked leaves it as it is
+        where another row holds a block that it would let go of, or write to next."""
+        if self.forked:
+            at, size = torch.arange(self.table.shape[1], device=self.table.device), self.cache.block_size
+            past = (at >= (want // size)[:, None]) & (at * size < self.length[:, None])
+            held = (past & (self.cache.shared[self.table.clamp(min=0).long()] > 0)).any(1)
+            want = torch.where(held & (want > 0), torch.maximum(want, self.length), want)
         self._resize(want, self.slots, self.pos)
 
     def _resize(self, want, slots, pos):
         c = self.cache
         if self.forked:                                     # what others hold stays
             lib.spec_block_release(self.blocks, (want == 0).int(), self.bws)
-            want = torch.where(want > 0, torch.maximum(want, self.length), want)
         lib.spec_block_tables(self.B, c.block_size, self.table.shape[1], c.num_blocks, self.length, want, self.table,
                               self.table, c.free, c.n_free, c.free, c.n_free, self.length, self.cu, slots, pos,
                               slots.numel(), self.tws)
@@ -346,6 +350,7 @@ class Batch:
     def release(self):
         """Gives all blocks back; the batch can take other requests."""
         self.resize(torch.zeros_like(self.length))
+        self.forked = False
         self.live, self.kept = torch.ones_like(self.live), torch.ones_like(self.kept)
         self.select.begin()
 

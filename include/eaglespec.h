@@ -675,8 +675,10 @@ spec_status spec_token_logprobs(int32_t n, int32_t V, int32_t dtype, const void 
 /* The blocks of a batch whose requests may share them.  Row b of the table holds
  * ceil(len[b] / block_size) blocks; a block that several rows hold has
  * shared[id] = the holders beyond the first, every other 0.  So spec_block_tables
- * grows such rows as any other (a block off the pool has one holder); it does not
- * shrink them: spec_block_release does.  Only full blocks are shared.
+ * grows such rows as any other (a block off the pool has one holder).  It does not
+ * look at shared: it may shrink a row only by blocks with one holder, to a length
+ * whose partial block has one; spec_block_release lets go of shared ones.  Only full
+ * blocks are shared.
  * Each *_out may be its *_in (an update in place) or must not overlap any input. */
 typedef struct {
   int32_t B;

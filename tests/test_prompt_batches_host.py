@@ -77,3 +77,56 @@ def test_what_a_request_that_stopped_is_told():
                              ("top_logprob", -float("inf"))):
             assert s[2][key].shape[0] == 30 and (s[2][key][fed:] == nothing).all(), key
         assert s[2]["lse"][:fed].isfinite().all() and s[0]["lse"].isfinite().all() and (s[1]["top_ids"] >= 0).all()
+
+
+def forked_batch(m, p):
+    """Rows 0 and 1: p[0] (10 tokens: two full blocks of 4 are shared, the third is each one's own)."""
+    b = decode.Batch(m, cache_of(m), 2, 64, m.vocab)
+    b.extend(p[:1] + [[]])
+    b.drop([1])
+    b.fork([0], [1])
+    return b
+
+
+@pytest.mark.parametrize("size", [18, 13, 12, 9, 8])
+def test_a_forked_request_gives_back_tokens_that_are_its_own(size):
+    """What comes after equals a request that never had the tokens, and the other row is as it was."""
+    m, p = model(), prompts(10, 9)
+    b = forked_batch(m, p)
+    b.extend([p[1], []])
+    free = int(b.cache.n_free)
+    b.resize(ints(size, 10))
+    assert b.length.tolist() == [size, 10] and int(b.cache.n_free) == free + 5 - -(-size // 4)
+    out = b.extend([[5, 6, 7], [8]])
+    kept = (p[0] + p[1])[:size]
+    torch.testing.assert_close(out[0], one_by_one(m, kept + [5, 6, 7])[-1], atol=1e-4, rtol=1e-4)
+    torch.testing.assert_close(out[1], one_by_one(m, p[0] + [8])[-1], atol=1e-4, rtol=1e-4)
+    b.release()
+    assert all_blocks_are_back(b) and b.error() == 0
+
+
+@pytest.mark.parametrize("size", [1, 3, 4, 7])
+def test_a_forked_request_keeps_blocks_that_another_row_holds(size):
+    m, p = model(), prompts(10, 9)
+    b = forked_batch(m, p)
+    b.resize(ints(size, 10))
+    assert b.length.tolist() == [10, 10]
+    b.drop([1])                                                # nobody else holds them any more
+    b.resize(ints(size, 0))
+    assert b.length.tolist() == [size, 0]
+    out = b.extend([[5, 6], []])
+    torch.testing.assert_close(out[0], one_by_one(m, p[0][:size] + [5, 6])[-1], atol=1e-4, rtol=1e-4)
+    b.release()
+    assert all_blocks_are_back(b) and b.error() == 0
+
+
+def test_a_batch_that_was_released_is_as_one_that_was_never_forked(monkeypatch):
+    m, p = model(), prompts(10, 9)
+    b = forked_batch(m, p)
+    b.release()
+    calls = []
+    monkeypatch.setattr(decode.lib, "spec_block_release", lambda *a: calls.append(a))
+    b.extend(p)
+    b.resize(ints(4, 9))
+    b.feed(ints(1, 2))
+    assert b.length.tolist() == [5, 10] and calls == []
