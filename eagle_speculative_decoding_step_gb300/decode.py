@@ -61,6 +61,16 @@ def _logits(logits, n, V):
     return name, x, x.stride(0) if n > 1 else V
 
 
+def _grown(ws, need, device):
+    """A workspace of at least ``need`` bytes: ws, or a new one with its error word."""
+    if ws is not None and ws.numel() >= need:
+        return ws
+    new = torch.zeros(need, dtype=torch.uint8, device=device)
+    if ws is not None:
+        new[:4] = ws[:4]
+    return new
+
+
 class PagedCache:
     """K/V of ``layers`` layers in ``num_blocks`` blocks of ``block_size`` slots, and the
     pool of free blocks."""
@@ -112,10 +122,7 @@ class PagedCache:
         tokens of request b's first seq_len[b]: each attends to what its request holds up to itself."""
         n, B = slots.numel(), seq_len.numel()
         need = lib.spec_chunk_attention_workspace_bytes(self.desc, B, n)
-        if self.chunk_ws is None or self.chunk_ws.numel() < need:
-            error = 0 if self.chunk_ws is None else lib.spec_get_device_error(self.chunk_ws)
-            self.chunk_ws = torch.zeros(need, dtype=torch.uint8, device=self.device)
-            self.chunk_ws[:4].view(torch.int32).fill_(error)
+        self.chunk_ws = _grown(self.chunk_ws, need, self.device)
 
         def call(layer, q, k, v):
             out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
@@ -299,8 +306,7 @@ class Batch:
             rows, dev = x.shape[0], x.device
             after = [t for b, seq in enumerate(tokens) for t in (list(seq[at + 1:at + n[b] + 1]) + [-1])[:n[b]]]
             need = lib.spec_token_logprobs_workspace_bytes(rows, self.vocab, k)
-            if self.lws is None or self.lws.numel() < need:
-                self.lws = torch.zeros(need, dtype=torch.uint8, device=dev)
+            self.lws = _grown(self.lws, need, dev)
             f = {key: torch.empty(rows, device=dev) for key in ("logprob", "entropy", "lse")}
             r = dict(f, rank=_ints(rows, device=dev), top_ids=_ints(rows, k, device=dev), top_logprob=torch.empty(rows, k, device=dev))
             lib.spec_token_logprobs(rows, self.vocab, name, x, torch.tensor(after, dtype=torch.int32, device=dev), k, ws=self.lws,

@@ -130,3 +130,14 @@ def test_a_batch_that_was_released_is_as_one_that_was_never_forked(monkeypatch):
     b.resize(ints(4, 9))
     b.feed(ints(1, 2))
     assert b.length.tolist() == [5, 10] and calls == []
+
+
+def test_a_score_that_needs_more_room_keeps_the_error_of_the_last_one(monkeypatch):
+    m, p = model(), prompts(3, 30)
+    b = decode.Batch(m, cache_of(m), 2, 64, m.vocab)
+    b.score([p[0], []], k=1)
+    b.lws[:4].view(torch.int32)[0] = -6                        # as a token outside the vocabulary leaves it
+    have = b.lws.numel()
+    monkeypatch.setattr(decode.lib, "spec_token_logprobs_workspace_bytes", lambda *a: 2 * have)
+    b.score([[], p[1]], k=4)
+    assert b.lws.numel() == 2 * have and b.error() == -6
