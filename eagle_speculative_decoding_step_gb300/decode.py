@@ -61,12 +61,18 @@ def _logits(logits, n, V):
     return name, x, x.stride(0) if n > 1 else V
 
 
+def _capturing(device):
+    return torch.device(device).type == "cuda" and torch.cuda.is_current_stream_capturing()
+
+
 def _grown(ws, need, device):
     """A workspace of at least ``need`` bytes: ws, or a new one with its error word."""
     if ws is not None and ws.numel() >= need:
         return ws
+    if _capturing(device):                                 # its zeros would be written by the replays only
+        raise RuntimeError("a workspace of %d bytes is needed: make the call once before it is captured" % need)
     new = torch.zeros(need, dtype=torch.uint8, device=device)
-    if ws is not None:
+    if ws is not None and ws.numel():
         new[:4] = ws[:4]
     return new
 
@@ -92,6 +98,7 @@ class PagedCache:
         self.ws = torch.zeros(lib.spec_attention_workspace_bytes(self.desc, max_rows), dtype=torch.uint8, device=device)
         self.max_rows = max_rows
         self.chunk_ws = None                                   # made for the first chunks, and for larger ones
+        self.captured_ws = []                                  # those that graphs work on
 
     def views(self, table):
         """KV structs of all layers under a block table."""
@@ -119,7 +126,8 @@ class PagedCache:
 
     def attend_chunks(self, kvs, slots, cu, seq_len, max_chunk=0, max_len=0):
         """The ``attend`` of a model whose row i writes slot slots[i], and whose rows cu[b] .. cu[b + 1] are the last
-        tokens of request b's first seq_len[b]: each attends to what its request holds up to itself."""
+        tokens of request b's first seq_len[b]: each attends to what its request holds up to itself.  Before it is captured into a
+        graph, a call of as many rows and requests is made outside of one."""
         n, B = slots.numel(), seq_len.numel()
         need = lib.spec_chunk_attention_workspace_bytes(self.desc, B, n)
         self.chunk_ws = _grown(self.chunk_ws, need, self.device)
@@ -129,6 +137,8 @@ class PagedCache:
             q, q_ld = _rows(q, n, self.n_q_heads, self.head_dim, self.dtype, "q")
             k, k_ld = _rows(k, n, self.n_kv_heads, self.head_dim, self.dtype, "k")
             v, v_ld = _rows(v, n, self.n_kv_heads, self.head_dim, self.dtype, "v")
+            if _capturing(self.device) and all(self.chunk_ws is not ws for ws in self.captured_ws):
+                self.captured_ws.append(self.chunk_ws)
             lib.spec_cache_append(self.desc, k, v, k_ld, slots, n, kvs[layer], self.ws, v_ld=v_ld)
             lib.spec_chunk_attention(self.desc, q, kvs[layer], cu, seq_len, B, n, out, None, self.chunk_ws,
                                      max_chunk=max_chunk, max_len=max_len, q_ld=q_ld)
@@ -137,7 +147,8 @@ class PagedCache:
 
     def error(self):
         """The attention's error word (synchronises)."""
-        return lib.spec_get_device_error(self.ws) or (lib.spec_get_device_error(self.chunk_ws) if self.chunk_ws is not None else 0)
+        words = [self.ws, *self.captured_ws] + ([self.chunk_ws] if self.chunk_ws is not None else [])
+        return next((e for e in map(lib.spec_get_device_error, words) if e), 0)
 
 
 class _Select:

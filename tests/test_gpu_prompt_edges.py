@@ -3,8 +3,9 @@ import numpy as np
 import pytest
 import torch
 
+from eagle_speculative_decoding_step_gb300 import decode
 from oracle import prompts as oracle
-from test_gpu_prompts import TYPE_PAIRS, TYPES, Chunk, caches, error, moved, pool_case, run_blocks, same
+from test_gpu_prompts import TYPE_PAIRS, TYPES, Chunk, caches, error, i32, moved, pool_case, run_blocks, same
 
 pytestmark = pytest.mark.gpu
 
@@ -51,3 +52,40 @@ def test_block_fork_of_an_empty_row_leaves_no_entries(in_place):
     for k in ("table", "length", "shared", "free", "n_free"):
         np.testing.assert_array_equal(got[k], ref[k], err_msg=k)
     assert (got["table"][[empty[1], empty[3]]] == -1).all() and (got["table"][empty[0]] == st["table"][empty[0]]).all()
+
+
+def test_chunks_in_a_graph_while_other_batches_need_more_room():
+    """A captured pass works on the workspace that it was captured with after larger calls have got another one."""
+    nq, nkv, hd = 4, 2, 64
+    c = decode.PagedCache(1, 400, 16, nq, nkv, hd, max_rows=8)
+    g = torch.Generator(device="cuda").manual_seed(2)
+
+    def chunk(n, first):
+        """Slots of one request's n tokens from block `first` on, and what the attention takes and is called with."""
+        table = torch.arange(first, first + 100, dtype=torch.int32, device="cuda").view(1, 100)
+        slots = torch.arange(first * 16, first * 16 + n, dtype=torch.int32, device="cuda")
+        cu, length = i32([0, n]), i32([n])
+        q, k, v = (torch.randn(n, h, hd, generator=g, device="cuda").bfloat16() for h in (nq, nkv, nkv))
+        return (c.views(table), slots, cu, length), (0, q, k, v)
+    at, qkv = chunk(200, 0)
+    want = c.attend_chunks(*at)(*qkv).clone()
+    old = c.chunk_ws
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = c.attend_chunks(*at)(*qkv)
+    data = old.data_ptr()
+    del old
+    big, other = chunk(1500, 150)
+    c.attend_chunks(*big)(*other)
+    assert c.chunk_ws.data_ptr() != data and [w.data_ptr() for w in c.captured_ws] == [data]
+    mine = torch.full((64 << 20,), 85, dtype=torch.uint8, device="cuda")          # what the pool would have given that memory to
+    for _ in range(2):
+        got.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
+    assert (mine == 85).all() and c.error() == 0
+    table, slots, cu, length = chunk(5000 // 16 * 16, 0)[0]
+    with pytest.raises(RuntimeError, match="before it is captured"):
+        with torch.cuda.graph(torch.cuda.CUDAGraph()):
+            c.attend_chunks(table, slots, cu, length)

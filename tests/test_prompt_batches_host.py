@@ -1,4 +1,7 @@
 """Batches that take prompts, forks and smaller sizes at any point of their requests' lives, on CPU tensors (prompt_library)."""
+import gc
+import weakref
+
 import pytest
 import torch
 
@@ -141,3 +144,39 @@ def test_a_score_that_needs_more_room_keeps_the_error_of_the_last_one(monkeypatc
     monkeypatch.setattr(decode.lib, "spec_token_logprobs_workspace_bytes", lambda *a: 2 * have)
     b.score([[], p[1]], k=4)
     assert b.lws.numel() == 2 * have and b.error() == -6
+
+
+def test_a_replaced_workspace_outlives_a_graph_that_was_captured_with_it(monkeypatch):
+    """The graph's replays still work on it after a larger call has got another one."""
+    m = model()
+    kept = []
+    for captured in (True, False):
+        b = decode.Batch(m, cache_of(m), 1, 64, m.vocab)
+        b.extend([[1, 2, 3]])
+        c = b.cache
+        attend = c.attend_chunks(b.kvs, ints(-1), ints(0, 1), ints(3))
+        monkeypatch.setattr(decode, "_capturing", lambda device: captured)
+        attend(0, torch.zeros(1, m.nq, m.hd), torch.zeros(1, m.nkv, m.hd), torch.zeros(1, m.nkv, m.hd))
+        monkeypatch.setattr(decode, "_capturing", lambda device: False)
+        old = weakref.ref(c.chunk_ws)
+        have = c.chunk_ws.numel()
+        with monkeypatch.context() as patch:
+            patch.setattr(decode.lib, "spec_chunk_attention_workspace_bytes", lambda *a: 2 * have)
+            b.extend([[4, 5]])
+        gc.collect()
+        assert c.chunk_ws.numel() == 2 * have and b.error() == 0
+        kept.append(old() is not None)
+    assert kept == [True, False]                               # (and no other is kept)
+
+
+def test_a_workspace_is_not_made_while_a_graph_is_captured(monkeypatch):
+    """Its zeros would be written by the replays only, and an eager call before the first one would find what was there."""
+    m = model()
+    c = cache_of(m)
+    monkeypatch.setattr(decode, "_capturing", lambda device: True)
+    with pytest.raises(RuntimeError):
+        c.attend_chunks(c.views(torch.zeros(1, 4, dtype=torch.int32)), ints(0, 1), ints(0, 2), ints(2))
+    monkeypatch.setattr(decode, "_capturing", lambda device: False)
+    c.attend_chunks(c.views(torch.zeros(1, 4, dtype=torch.int32)), ints(0, 1), ints(0, 2), ints(2))
+    monkeypatch.setattr(decode, "_capturing", lambda device: True)
+    c.attend_chunks(c.views(torch.zeros(1, 4, dtype=torch.int32)), ints(0), ints(0, 1), ints(2))      # it is there
