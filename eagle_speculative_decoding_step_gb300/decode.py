@@ -339,11 +339,11 @@ class Batch:
             raise ValueError("rows %s of %d" % (dst, self.B))
         dev, c = self.cache.device, self.cache
         a, d = (torch.tensor(x, dtype=torch.int32, device=dev) for x in (src, dst))
-        empty = self.length[d.long()] == 0
+        empty, size = self.length[d.long()] == 0, self.length[a.long()]
         self.forked = True
         lib.spec_block_fork(self.blocks, len(dst), a, d, c.views(self.table), c.row_bytes, self.bws)
         a, d = a.long(), d.long()
-        there = empty & (self.length[d] > 0)
+        there = empty & (self.length[d] == size)
         for x in (self.live, self.kept):
             x[d] = torch.where(there, x[a], torch.where(empty, 0, x[d]))
         for x in (self.select.score[self.select.at], self.select.done[self.select.at]):

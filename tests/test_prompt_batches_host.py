@@ -180,3 +180,24 @@ def test_a_workspace_is_not_made_while_a_graph_is_captured(monkeypatch):
     c.attend_chunks(c.views(torch.zeros(1, 4, dtype=torch.int32)), ints(0, 1), ints(0, 2), ints(2))
     monkeypatch.setattr(decode, "_capturing", lambda device: True)
     c.attend_chunks(c.views(torch.zeros(1, 4, dtype=torch.int32)), ints(0), ints(0, 1), ints(2))      # it is there
+
+
+def test_the_fork_of_a_row_without_tokens_is_as_that_row():
+    """One that takes tokens from its first on, one that was dropped, and one that the pool has no block for."""
+    m, p = model(), prompts(6)
+    b = decode.Batch(m, cache_of(m), 5, 64, m.vocab)
+    b.extend(p + [[]] * 4)
+    b.drop([2])
+    b.fork([1, 2], [3, 4])
+    assert b.live.tolist() == [1, 1, 0, 1, 0] and b.length.tolist() == [6, 0, 0, 0, 0] and b.error() == 0
+    logits = b.feed(ints(4, 7, 1, 7, 1))
+    assert b.length.tolist() == [7, 1, 0, 1, 0]
+    torch.testing.assert_close(logits[3], one_by_one(m, [7])[0], atol=1e-4, rtol=1e-4)
+    e = decode.Batch(m, cache_of(m), 3, 64, m.vocab)           # all as they were before the call
+    e.extend(p + [[], []])
+    e.fork([0, 1], [1, 2])
+    assert e.length.tolist() == [6, 6, 0] and e.live.tolist() == [1, 1, 1] and e.error() == 0
+    c = decode.Batch(m, cache_of(m, blocks=2), 2, 64, m.vocab)
+    c.extend(p + [[]])
+    c.fork([0], [1])
+    assert c.length.tolist() == [6, 0] and c.live.tolist() == [1, 0] and c.error() != 0
