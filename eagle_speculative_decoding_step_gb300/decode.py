@@ -340,8 +340,8 @@ class Batch:
         dev, c = self.cache.device, self.cache
         a, d = (torch.tensor(x, dtype=torch.int32, device=dev) for x in (src, dst))
         empty, size = self.length[d.long()] == 0, self.length[a.long()]
-        self.forked = True
         lib.spec_block_fork(self.blocks, len(dst), a, d, c.views(self.table), c.row_bytes, self.bws)
+        self.forked = True
         a, d = a.long(), d.long()
         there = empty & (self.length[d] == size)
         for x in (self.live, self.kept):

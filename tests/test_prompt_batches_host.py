@@ -201,3 +201,16 @@ def test_the_fork_of_a_row_without_tokens_is_as_that_row():
     c.extend(p + [[]])
     c.fork([0], [1])
     assert c.length.tolist() == [6, 0] and c.live.tolist() == [1, 0] and c.error() != 0
+
+
+def test_a_fork_that_is_refused_changes_nothing(monkeypatch):
+    m, p = model(), prompts(6)
+    b = decode.Batch(m, cache_of(m), 2, 64, m.vocab)
+    b.extend(p + [[]])
+
+    def refuse(*a):
+        raise RuntimeError("more layers than one call copies")
+    monkeypatch.setattr(decode.lib, "spec_block_fork", refuse)
+    with pytest.raises(RuntimeError):
+        b.fork([0], [1])
+    assert not b.forked and b.live.tolist() == [1, 1] and b.length.tolist() == [6, 0]
