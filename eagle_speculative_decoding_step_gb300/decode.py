@@ -311,6 +311,8 @@ class Batch:
         its tokens, entry i of what it expected after token i: logprob and rank of token i + 1 (-infinity and -1 for the
         last one), entropy, lse, and top_ids and top_logprob [len, k], the best alternatives.  Tokens that a request did not
         take, since it stopped, have what a row without a logit has: -infinity, -1 and an entropy of 0."""
+        if lib.spec_token_logprobs_workspace_bytes(1, self.vocab, k) == 0:
+            raise ValueError("%d alternatives of %d logits" % (k, self.vocab))
         parts = [[] for _ in tokens]
         for logits, ends, at, n in self._chunks(tokens, chunk):
             name, x, ld = _logits(logits, int(ends[-1]), self.vocab)

@@ -214,3 +214,15 @@ def test_a_fork_that_is_refused_changes_nothing(monkeypatch):
     with pytest.raises(RuntimeError):
         b.fork([0], [1])
     assert not b.forked and b.live.tolist() == [1, 1] and b.length.tolist() == [6, 0]
+
+
+@pytest.mark.parametrize("k", [-1, 33])
+def test_a_score_with_too_many_alternatives_feeds_nothing(monkeypatch, k):
+    m = model()
+    b = decode.Batch(m, cache_of(m), 1, 64, m.vocab)
+    b.extend([[1, 2]])
+    size = decode.lib.spec_token_logprobs_workspace_bytes
+    monkeypatch.setattr(decode.lib, "spec_token_logprobs_workspace_bytes", lambda n, V, k: size(n, V, k) if 0 <= k <= 32 else 0)
+    with pytest.raises(ValueError):
+        b.score([[3, 4]], k=k)
+    assert b.length.tolist() == [2]
