@@ -44,6 +44,7 @@ constexpr int kRawStages = 2;            // 8-bit tiles under way, before they a
 // An item's masks are used again 8 items later: the streams are at most two items apart (one's next-but-one Q waits for the
 // other's scores of the item before it) and the loader one ahead of the first, so that stream clears those of four items ago.
 constexpr int kItems = 8;
+constexpr int kHoldWord = 16;            // of the workspace's header, in words
 
 template <int MODE> struct Shape {
   static constexpr int BM = MODE == kTwoQ ? 256 : 128, KT = MODE == kWide ? 64 : 128;
@@ -96,7 +97,8 @@ SPEC_DEV void sts128(uint32_t a, uint4 v) {
 template <int R> SPEC_DEV void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R)); }
 template <int R> SPEC_DEV void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
 
-// Whether a phase is over, at once (mbarrier.try_wait may hold the warp for a while).
+// Whether a phase is over, at once (mbarrier.try_wait may hold the warp for a while).  The answer is the warp's: what follows
+// is done by all lanes together.
 SPEC_DEV bool test(uint64_t& bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
@@ -106,10 +108,10 @@ SPEC_DEV bool test(uint64_t& bar, uint32_t parity) {
       : "=r"(ok)
       : "r"(tc::su32(&bar)), "r"(parity)
       : "memory");
-  return ok != 0;
+  return __all_sync(0xffffffffu, ok != 0);
 }
 // Bounded wait, in few instructions: the roles' loops share the SM's instruction cache.
-SPEC_DEV bool wait_for(uint64_t& bar, uint32_t parity, volatile int* abort) {
+SPEC_DEV bool wait_lane(uint64_t& bar, uint32_t parity, volatile int* abort) {
   const uint32_t a = tc::su32(&bar);
   if (tc::mbar_try(a, parity)) return true;
   const uint64_t t0 = globaltimer_ns();
@@ -122,6 +124,11 @@ SPEC_DEV bool wait_for(uint64_t& bar, uint32_t parity, volatile int* abort) {
     }
   }
   return true;
+}
+// The same for a whole warp, whose lanes get one answer: a lane that gave up alone would leave the others waiting for it at
+// their next exchange.
+SPEC_DEV bool wait_for(uint64_t& bar, uint32_t parity, volatile int* abort) {
+  return __all_sync(0xffffffffu, wait_lane(bar, parity, abort));
 }
 
 SPEC_DEV void copy_run(uint32_t dst, const CUtensorMap* tm, uint32_t mbar, int x, int head, int slot, uint64_t policy) {
@@ -248,6 +255,7 @@ struct TcSmem {
   int last[2];
   uint32_t tmem;
   int abort;
+  int hold;                            // CTA + 1 that gets no keys (the workspace header's test hook)
 };
 
 // ---------------------------------------------------------------- loader
@@ -401,7 +409,7 @@ template <typename T, bool F8, int MODE> struct Loader {
   static SPEC_DEV bool next_q(const TcArgs& a, TcSmem& sm, const Item& it, uint32_t q0, int warp, int lane, int items,
                               uint32_t& q_phase) {
     if (items > 0) {
-      if (!__all_sync(0xffffffffu, wait_for(sm.q_empty, q_phase, &sm.abort))) return false;
+      if (!wait_for(sm.q_empty, q_phase, &sm.abort)) return false;
       q_phase ^= 1u;
     }
     if (a.l.q_boxes) {
@@ -489,7 +497,7 @@ template <typename T, bool F8, int MODE> struct Loader {
         const bool edge = edges.has(tile);
 #pragma unroll 1
         for (int value = 0; value < 2; ++value) {
-          if (!__all_sync(0xffffffffu, wait_for(sm.empty[stage], phase ^ 1u, abort))) {
+          if (!wait_for(sm.empty[stage], phase ^ 1u, abort)) {
             ok = false;
             break;
           }
@@ -506,7 +514,7 @@ template <typename T, bool F8, int MODE> struct Loader {
           if (keys) copy_run(at + lane_to, value ? &a.tmv : &a.tmk, tc::su32(&bar), 64 * chunk, it.h, first, policy);
           if (by_way) {
             __syncwarp();
-            if (!__all_sync(0xffffffffu, wait_for(bar, l_phase, abort))) {
+            if (!wait_for(bar, l_phase, abort)) {
               ok = false;
               break;
             }
@@ -570,7 +578,7 @@ template <typename T, bool F8, int MODE> struct Loader {
         const int info = edges.has(tile) ? (items % kItems) << 8 | edges.template slot<S::EDGES>(tile) : -1;
 #pragma unroll 1
         for (int value = 0; value < 2; ++value) {
-          if (!__all_sync(0xffffffffu, wait_for(sm.raw_empty[raw], phase ^ 1u, abort))) {
+          if (!wait_for(sm.raw_empty[raw], phase ^ 1u, abort)) {
             ok = false;
             break;
           }
@@ -615,8 +623,8 @@ template <typename T, bool F8, int MODE> struct Loader {
       const int jobs = 2 * (it.k1 - it.k0);            // K, V, K, V, ...
 #pragma unroll 1
       for (int j = 0; ok && j < jobs; ++j) {
-        ok = __all_sync(0xffffffffu, wait_for(sm.raw_full[raw], r_phase, abort)) &&
-             __all_sync(0xffffffffu, wait_for(sm.empty[stage], phase ^ 1u, abort));
+        ok = wait_for(sm.raw_full[raw], r_phase, abort) &&
+             wait_for(sm.empty[stage], phase ^ 1u, abort);
         if (!ok) break;
         const uint32_t word = sm.way_there[raw][r0 / 32];
         const uint32_t there = RW == 32 ? word : word >> (r0 % 32) & 0xffffu;
@@ -798,7 +806,7 @@ SPEC_DEV bool elect_one() {
 }
 // Waits without an answer, so that the warp's path does not depend on it: after a timeout every wait returns at once, and
 // what is issued meanwhile works on whatever is there.  (A path that does is 100 cycles longer a wait.)
-SPEC_DEV void settle(uint64_t& bar, uint32_t parity, volatile int* abort) { (void)wait_for(bar, parity, abort); }
+SPEC_DEV void settle(uint64_t& bar, uint32_t parity, volatile int* abort) { (void)wait_lane(bar, parity, abort); }
 
 // Jobs of an item, in the order of their MMAs: kTwoQ: (tile 0, rows 0-127), (tile 0, rows 128-255), (tile 1, ...), ...;
 // otherwise the tiles, for two streams in turns (kOneQ) or one (kWide).  The products of job k with V, then the scores of
@@ -1331,7 +1339,10 @@ template <typename T, bool F8, int MODE> __global__ void __launch_bounds__(kTcTh
   }
   pdl_wait();
   pdl_trigger();
+  // (asked for before the plan's own reads, and looked at after them)
+  const int hold = tid == 0 ? __ldcg(static_cast<const int*>(a.g.ws) + kHoldWord) : 0;
   make_plan<S::BM, S::KT>(a.g, sm.plan, tid, kTcThreads);
+  if (tid == 0) sm.hold = hold;
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
@@ -1341,7 +1352,8 @@ template <typename T, bool F8, int MODE> __global__ void __launch_bounds__(kTcTh
     if (MODE != kWide || warp < 4) Softmax<T, F8, MODE>(a.g, sm, tmem, warp >> 2, warp & 3, lane).run();
   } else if (warp < 12) {
     regs_dec<kLoaderRegs>();
-    if (a.l.runs && F8) Loader<T, F8, MODE>::run_widen(a, sm, base, warp - 8, lane);
+    if (sm.hold == (int)blockIdx.x + 1) {}             // every wait for them runs out
+    else if (a.l.runs && F8) Loader<T, F8, MODE>::run_widen(a, sm, base, warp - 8, lane);
     else if (a.l.runs) Loader<T, F8, MODE>::run_tensor(a, sm, base, warp - 8, lane);
     else Loader<T, F8, MODE>::run(a, sm, base, warp - 8, lane);
   } else {

@@ -610,7 +610,9 @@ spec_status spec_beam_reorder(const spec_beam_state *st, int32_t n_layers, const
  * tokens: header, partial results, counters.  Zero-filled before its first use;
  * every call leaves the counters at zero.  Calls that share a workspace must not
  * overlap on the GPU; each workspace serves calls of its own kind, of any sizes
- * that it is large enough for.  0 for an invalid descriptor. */
+ * that it is large enough for.  0 for an invalid descriptor.  Header bytes 64..67
+ * are a test hook, zero otherwise: a value k > 0 keeps CTA k - 1 of a call on 16-bit
+ * rows from its keys, so that its waits run out (2 s: SPEC_ERR_TIMEOUT). */
 size_t spec_chunk_attention_workspace_bytes(const spec_attn_desc *desc, int32_t max_B, int32_t max_rows);
 
 /* Attention of a chunk of new tokens per request over the paged cache (a target's
@@ -638,7 +640,8 @@ size_t spec_chunk_attention_workspace_bytes(const spec_attn_desc *desc, int32_t 
  * are as they would be without.
  * Error word: SPEC_ERR_DEVICE for cu_rows that fall (rows are left as they are),
  * cu_rows that leave [0, n_rows] or a seq_len outside [0, max_blocks * block_size]
- * (both clamped), or a slot out of range (such keys are left out). */
+ * (both clamped), or a slot out of range (such keys are left out); SPEC_ERR_TIMEOUT
+ * where a bounded wait ran out (any row of the call may hold anything then). */
 spec_status spec_chunk_attention(const spec_attn_desc *desc, const void *q, int64_t q_ld, const spec_kv *kv,
                                  const int32_t *cu_rows, const int32_t *seq_len, int32_t B, int32_t n_rows,
                                  int32_t max_chunk, int32_t max_len, void *out, int64_t out_ld, float *lse,

@@ -8,6 +8,7 @@ from oracle import prompts as oracle
 from test_gpu_prompts import TYPE_PAIRS, TYPES, Chunk, caches, error, i32, moved, pool_case, run_blocks, same
 
 pytestmark = pytest.mark.gpu
+ERR_TIMEOUT = -7
 
 
 def far_below_zero(x, at=225.0):
@@ -89,3 +90,62 @@ def test_chunks_in_a_graph_while_other_batches_need_more_room():
     with pytest.raises(RuntimeError, match="before it is captured"):
         with torch.cuda.graph(torch.cuda.CUDAGraph()):
             c.attend_chunks(table, slots, cu, length)
+
+
+SIXTEEN = [p for p in TYPE_PAIRS if p[0] != "f32"]
+# few rows (128 packed ones at most), many, and head sizes above 128: keys that are shared out differently
+FORMS = [(64, [(4, 3000), (8, 40), (1, 1), (0, 9)], 0), (128, [(30, 2500), (1, 700)], 600), (80, [(1, 260)] * 20, 0),
+         (128, [(150, 420), (260, 1500)], 300), (256, [(150, 700), (3, 2500)], 0), (192, [(90, 420), (2, 2)], 70)]
+
+
+@pytest.mark.parametrize("t,c", SIXTEEN)
+@pytest.mark.parametrize("bs", [1, 8, 24])
+@pytest.mark.parametrize("hd,chunks,window", FORMS)
+def test_chunk_attention_blocks_without_runs_of_16(t, c, bs, hd, chunks, window):
+    """Whole and split items, windows, batches of single tokens, in blocks that are no multiple of 16 slots."""
+    x = Chunk(chunks, 4, 2, hd, t, c, bs=bs, window=window, seed=hd + bs)
+    x.poison()
+    out, lse, ws = x.run()
+    assert error(ws) == 0
+    x.check(out, lse)
+
+
+@pytest.mark.parametrize("t,c", SIXTEEN)
+@pytest.mark.parametrize("bs", [8, 16, 24])
+@pytest.mark.parametrize("hd,chunks,window", [(64, [(40, 300), (30, 30), (55, 131)], 0), (128, [(40, 300), (30, 30), (55, 1200)], 50),
+                                              (256, [(90, 300), (40, 40), (30, 900)], 0), (192, [(90, 300), (40, 40), (130, 131)], 70),
+                                              (128, [(90, 300), (40, 40), (130, 900)], 0)])
+def test_chunk_attention_values_that_are_not_finite_in_any_block(t, c, bs, hd, chunks, window):
+    """A key's V that is not finite, among each request's newest keys and where a window begins."""
+    x = Chunk(chunks, 4, 2, hd, t, c, bs=bs, seed=3, window=window)
+    v = x.v.view(torch.uint8) if c == "e4m3" else x.v
+    nan = torch.tensor(float("nan"), device="cuda").to(x.v.dtype).view(v.dtype)
+    for b, (n, length) in enumerate(chunks):
+        first = length - n
+        for key, head, comp in ((first, 0, 3), (first + n // 2, 1, 17), (length - 1, 0, hd - 1), (max(0, first - window + n // 3), 1, 0)):
+            v[x.slot(b, key), head, comp] = nan
+    out, lse, ws = x.run()
+    assert error(ws) == 0
+    x.check(out, lse)
+
+
+def hold(ws, cta):
+    ws[64:68].copy_(torch.tensor([cta], dtype=torch.int32).view(torch.uint8))
+
+
+WAITS = [("bf16", "bf16", 64, [(300, 2000)], 16), ("f16", "f16", 64, [(8, 3000), (8, 40)], 16), ("bf16", "bf16", 256, [(20, 2000)], 24),
+         ("bf16", "e4m3", 128, [(300, 2000)], 16), ("f16", "e4m3", 64, [(4, 3000)], 16), ("bf16", "bf16", 64, [(8, 60)], 16)]
+
+
+@pytest.mark.parametrize("t,c,hd,chunks,bs", WAITS)
+def test_chunk_attention_waits_that_run_out(t, c, hd, chunks, bs):
+    """A CTA that never gets its keys gives up after the limit: the call ends and says so, and the next call is right."""
+    x = Chunk(chunks, 4, 2, hd, t, c, bs=bs, seed=31)
+    ref, rlse, ws = x.run()
+    assert error(ws) == 0
+    hold(ws, 2)
+    x.run(ws=ws)
+    torch.cuda.synchronize()
+    assert error(ws) == ERR_TIMEOUT
+    out, lse, other = x.run()
+    assert error(other) == 0 and torch.equal(out, ref) and torch.equal(lse, rlse)
