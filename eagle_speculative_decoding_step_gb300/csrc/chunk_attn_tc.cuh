@@ -929,6 +929,7 @@ template <typename T, bool F8, int MODE> struct Softmax {
   const int w, warp, lane, row;        // warpgroup, its warp, and the thread's row of 128
   const uint32_t tm;                   // TMEM with the warp's lanes
   float m = -INFINITY, l = 0.f;
+  bool counted = false;                // the item's piece has been counted
 
   SPEC_DEV Softmax(const Args& g_, TcSmem& sm_, uint32_t tmem, int w_, int warp_, int lane_)
       : g(g_), sm(sm_), w(w_), warp(warp_), lane(lane_), row(warp_ * 32 + lane_), tm(tmem + ((uint32_t)(warp_ * 32) << 16)) {}
@@ -1181,18 +1182,32 @@ template <typename T, bool F8, int MODE> struct Softmax {
     __threadfence();
     const int slot = MODE == kOneQ ? 0 : w;
     if (!group_sync()) return false;
-    if (row == 0 && (MODE != kOneQ || w == 0)) {
-      const long long at = (long long)it.h * sm.plan.pairs[g.B] + sm.plan.pairs[it.b] + it.t;
-      int* counter = g.counters + (MODE == kTwoQ ? 2 * at + w : at);
-      const int before = atomicAdd(counter, 1);
-      sm.last[slot] = before == pc.c1 - pc.c0;
-      if (sm.last[slot]) *counter = 0;
-    }
+    if (counts()) sm.last[slot] = count(it, pc);
     if (!group_sync()) return false;
     const bool last = sm.last[slot] != 0;
     if (!group_sync()) return false;       // (read before the next item's is written)
     if (last) join(it, pc);
     return true;
+  }
+
+  // The thread that counts the warpgroups' pieces of an item, and whether this is the last to come.
+  SPEC_DEV bool counts() const { return row == 0 && (MODE != kOneQ || w == 0); }
+  SPEC_DEV bool count(const Item& it, const Pieces& pc) {
+    const long long at = (long long)it.h * sm.plan.pairs[g.B] + sm.plan.pairs[it.b] + it.t;
+    int* counter = g.counters + (MODE == kTwoQ ? 2 * at + w : at);
+    const bool last = atomicAdd(counter, 1) == pc.c1 - pc.c0;
+    if (last) *counter = 0;
+    counted = true;
+    return last;
+  }
+  // After a wait that ran out: what is left of the share counts as pieces that have come, so that all counters are at zero
+  // when the launch ends.
+  SPEC_DEV void give_up(Walk<BM, KT>& walk, Item& it) {
+    if (!counts()) return;
+    do {
+      if (!counted && (it.k0 > 0 || it.k1 < it.tiles)) count(it, Pieces(sm.plan, it));
+      counted = false;
+    } while (walk.next(it));
   }
 
   // All pieces of the item's rows, in their order; 16 components of a row a thread at a time.
@@ -1247,7 +1262,7 @@ template <typename T, bool F8, int MODE> struct Softmax {
     Item it;
     uint32_t s_phase[2] = {0, 0}, o_phase[2] = {0, 0};
     int tiles = 0, items = 0;
-    while (walk.next(it)) {
+    auto item_done = [&]() -> bool {
       const int nt = it.k1 - it.k0, item = items % kItems;
       int klo, khi;
       keys_of(g, it, MODE == kTwoQ ? w * 128 + row : row, &klo, &khi);
@@ -1256,7 +1271,7 @@ template <typename T, bool F8, int MODE> struct Softmax {
       bool fresh = true;
       for (int k = MODE == kOneQ ? w : 0; k < nt; k += MODE == kOneQ ? 2 : 1) {
         const int buf = MODE == kWide ? k & 1 : w;
-        if (!wait_for(sm.s_full[buf], s_phase[buf], abort)) return;
+        if (!wait_for(sm.s_full[buf], s_phase[buf], abort)) return false;
         s_phase[buf] ^= 1u;
         tc::tc_fence_after();
         bool ok = true;
@@ -1266,28 +1281,28 @@ template <typename T, bool F8, int MODE> struct Softmax {
                if (MODE == kWide) ok = wait_for(sm.o_done[0], o_phase[0] ^ (uint32_t)((k - 1) & 1), abort);
                return ok;
              });
-        if (!ok) return;
+        if (!ok) return false;
         fresh = false;
       }
       if (MODE == kTwoQ) {
-        if (!wait_for(sm.o_done[w], o_phase[w], abort)) return;
+        if (!wait_for(sm.o_done[w], o_phase[w], abort)) return false;
         o_phase[w] ^= 1u;
       } else if (MODE == kOneQ) {
-        if (!wait_for(sm.o_done[0], o_phase[0], abort)) return;
+        if (!wait_for(sm.o_done[0], o_phase[0], abort)) return false;
         o_phase[0] ^= 1u;
         if (nt > 1) {
-          if (!wait_for(sm.o_done[1], o_phase[1], abort)) return;
+          if (!wait_for(sm.o_done[1], o_phase[1], abort)) return false;
           o_phase[1] ^= 1u;
         }
       } else {
         // a phase a tile
-        if (!wait_for(sm.o_done[0], o_phase[0] ^ (uint32_t)((nt - 1) & 1), abort)) return;
+        if (!wait_for(sm.o_done[0], o_phase[0] ^ (uint32_t)((nt - 1) & 1), abort)) return false;
         o_phase[0] ^= (uint32_t)(nt & 1);
       }
       tc::tc_fence_after();
       const bool ok = finish(it, item, klo, khi);
       __syncwarp();
-      if (!ok) return;
+      if (!ok) return false;
       if (w == 0) {
         const int old = (items + kItems - 4) % kItems;
         if (row < 2 * 6 * 4) (&sm.poison[old][0][0])[row] = 0;
@@ -1295,6 +1310,14 @@ template <typename T, bool F8, int MODE> struct Softmax {
       }
       ++items;
       tiles += nt;
+      return true;
+    };
+    while (walk.next(it)) {
+      counted = false;
+      if (!item_done()) {
+        give_up(walk, it);
+        return;
+      }
     }
   }
 };

@@ -3,6 +3,7 @@ import numpy as np
 import pytest
 import torch
 
+from eagle_speculative_decoding_step_gb300 import binding as lib
 from eagle_speculative_decoding_step_gb300 import decode
 from oracle import prompts as oracle
 from test_gpu_prompts import TYPE_PAIRS, TYPES, Chunk, caches, error, i32, moved, pool_case, run_blocks, same
@@ -149,3 +150,20 @@ def test_chunk_attention_waits_that_run_out(t, c, hd, chunks, bs):
     assert error(ws) == ERR_TIMEOUT
     out, lse, other = x.run()
     assert error(other) == 0 and torch.equal(out, ref) and torch.equal(lse, rlse)
+
+
+@pytest.mark.parametrize("t,c,hd,chunks,bs", WAITS)
+@pytest.mark.parametrize("cta", [1, 20])
+def test_chunk_attention_after_waits_that_ran_out(t, c, hd, chunks, bs, cta):
+    """Pieces of items that a CTA gave up on are counted all the same: the workspace serves the next call."""
+    x = Chunk(chunks, 4, 2, hd, t, c, bs=bs, seed=31)
+    ref, rlse, ws = x.run()
+    hold(ws, cta)
+    x.run(ws=ws)
+    torch.cuda.synchronize()
+    assert error(ws) == (ERR_TIMEOUT if cta <= 2 or chunks[0][1] > 60 else 0)      # (60 keys: two items, of a CTA each)
+    first = lib.spec_chunk_attention_workspace_bytes(x.desc, 1, 1) - 256           # (a call of one row has a few counters)
+    assert not ws[first:].any()
+    lib.spec_clear_device_error(ws)
+    out, lse, _ = x.run(ws=ws)
+    assert error(ws) == 0 and torch.equal(out, ref) and torch.equal(lse, rlse)
