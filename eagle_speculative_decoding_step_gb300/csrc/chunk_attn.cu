@@ -288,11 +288,12 @@ static long long most_items(const spec_attn_desc& d, long long B, long long rows
   return d.n_kv_heads * (2 * B + (rows * (d.n_q_heads / d.n_kv_heads) + kFmaRows - 1) / kFmaRows);
 }
 
-// 128 packed rows where every request's fit them.  kOneQ / kTwoQ: 4 requests of 8 tokens and 200-256 keys 13.1 / 13.4 us; 32 of
-// 8 tokens and 512-2048 keys 65 / 66; 64 single tokens of 4000 keys 205 / 210.
+// 128 packed rows where every request's fit them, over a 16-bit cache.  kOneQ / kTwoQ: 4 requests of 8 tokens and 200-256 keys
+// 13.0 / 14.0 us; 16 of 32 tokens and 300-4000 keys 59 / 66; 64 single tokens of 4000 keys 194 / 222.  Over an 8-bit cache,
+// where widening bounds both, 20.2 / 19.4 for the first of them and 393 / 310 for the last: always kTwoQ.
 static int mode_for(const spec_attn_desc& d, int longest) {
   if (d.head_dim > 128) return kWide;
-  return (long long)longest * (d.n_q_heads / d.n_kv_heads) <= 128 ? kOneQ : kTwoQ;
+  return d.kv_dtype == d.dtype && (long long)longest * (d.n_q_heads / d.n_kv_heads) <= 128 ? kOneQ : kTwoQ;
 }
 
 static spec_status launch_fma(const spec_attn_desc& d, const Args& g, int sms, cudaStream_t st) {

@@ -1410,7 +1410,7 @@ template <typename T, bool F8, int MODE> TcFn checked() {
 }
 
 template <typename T> TcFn tc_kernel_of(bool f8, int mode) {
-  if (f8) return mode == kTwoQ ? checked<T, true, kTwoQ>() : mode == kOneQ ? checked<T, true, kOneQ>() : checked<T, true, kWide>();
+  if (f8) return mode == kTwoQ ? checked<T, true, kTwoQ>() : checked<T, true, kWide>();
   return mode == kTwoQ ? checked<T, false, kTwoQ>() : mode == kOneQ ? checked<T, false, kOneQ>() : checked<T, false, kWide>();
 }
 
