@@ -586,9 +586,10 @@ extern "C" spec_status spec_block_release(const spec_block_state* st, const int3
   if (r != SPEC_OK) return r;
   bl::Args g = bl::args(st, ws);
   g.drop = drop;
-  // Few entries: one cluster, whose barriers are cheaper than launches; many: a launch a step, whose SMs are more.
-  // 32 rows of up to 140 entries: 10.3 / 11.7 us; 512 of up to 470: 51.6 / 32.7.
-  if ((long long)st->B * st->max_blocks <= 32768) {
+  // A row a warp.  Rows that one cluster's warps hold: its barriers are cheaper than launches; more: a launch a step, whose SMs
+  // are more.  Cluster / launches, 32 rows of up to 138 entries 10.5 / 12.2 us; 128 of 264: 19.5 / 20.5; 256 of 138, 264, 451:
+  // 14.0 / 15.4, 21.5 / 22.3, 33.9 / 32.2; 512 of 138, 451: 21.9 / 16.3, 57 / 35.7.
+  if (st->B <= bl::kWarps) {
     r = bl::plan(bl::release_kernel, g, (size_t)st->B * sizeof(int), bl::kCtas, stream);
   } else {
     void (*const steps[])(bl::Args) = {bl::release_step_kernel<0>, bl::release_step_kernel<1>, bl::release_step_kernel<2>,
