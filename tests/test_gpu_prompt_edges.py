@@ -6,7 +6,7 @@ import torch
 from eagle_speculative_decoding_step_gb300 import binding as lib
 from eagle_speculative_decoding_step_gb300 import decode
 from oracle import prompts as oracle
-from test_gpu_prompts import TYPE_PAIRS, TYPES, Chunk, caches, error, i32, moved, pool_case, run_blocks, same
+from test_gpu_prompts import HALF, TYPE_PAIRS, TYPES, Chunk, caches, error, i32, moved, pool_case, run_blocks, same
 
 pytestmark = pytest.mark.gpu
 ERR_TIMEOUT = -7
@@ -167,3 +167,29 @@ def test_chunk_attention_after_waits_that_ran_out(t, c, hd, chunks, bs, cta):
     lib.spec_clear_device_error(ws)
     out, lse, _ = x.run(ws=ws)
     assert error(ws) == 0 and torch.equal(out, ref) and torch.equal(lse, rlse)
+
+
+@pytest.mark.parametrize("t,c", TYPE_PAIRS)
+def test_chunks_of_one_token_and_the_decode_step(t, c):
+    """spec_paged_attention's answer, up to what the two lose: a weight's rounding to the type of the rows here (u of it, and in
+    f16 2^-34 of the largest) and 2^-17 of it there, of M = sum p |v|; both outputs' rounding, u of them; and the scores' and
+    sums' (test_gpu_prompts), which the two do in different orders."""
+    x = Chunk([(1, n) for n in (700, 1, 33, 64, 1500, 260)], 8, 2, 128, t, c, seed=9, pad=0)
+    out, lse, _ = x.run()
+    o, le = torch.empty_like(out), torch.empty_like(lse)
+    ws = torch.zeros(lib.spec_attention_workspace_bytes(x.desc, 6), dtype=torch.uint8, device="cuda")
+    kv = lib.make_kv(dict(k=x.k, v=x.v, block_table=i32(x.table), block_size=x.bs, max_blocks=x.table.shape[1],
+                          num_slots=x.num_slots))
+    lib.spec_paged_attention(x.desc, x.q, kv, i32(x.length), 6, o, le, ws, q_ld=x.wide.stride(0))
+    q = x.q.double().cpu().numpy().reshape(x.n, x.nq, x.hd)
+    k, v = x.k.double().cpu().numpy() * x.ks, x.v.double().cpu().numpy() * x.vs
+    ref, rlse, mass, size = oracle.chunk_attention(q, k, v, x.table, x.bs, x.cu, x.length, spread=True)
+    n, u = 1500.0, HALF[t]
+    ds = 2 * ((x.hd + 4) * 2.0 ** -23 * size + 2.0 ** -21)
+    tol = mass * ((0.0 if t == "f32" else u + 2.0 ** -17) + 2 * ds[..., None] + 2 * n * 2.0 ** -23) + 2 * u * np.abs(ref)
+    if t == "f16":
+        tol = tol + n * 2.0 ** -34 * np.abs(v).max() + 2 * 2.0 ** -24
+    tol = tol * (1 + 4 * u)                                    # (products of two of these)
+    far, lfar = (np.abs(a.double().cpu().numpy() - b.double().cpu().numpy()) for a, b in ((out, o), (lse, le)))
+    assert (far / tol).max() <= 1.0, "%.3f of the tolerance" % (far / tol).max()
+    assert (lfar <= ds + 2 * n * 2.0 ** -23 + np.abs(rlse) * 2.0 ** -21).all()
