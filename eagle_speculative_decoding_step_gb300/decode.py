@@ -15,8 +15,10 @@ cache, its block tables and slot mapping.
 A model is a callable ``model(tok, pos, attend) -> logits``: tok and pos [n] int32,
 logits [n, V]; in each layer it calls ``attend(layer, q, k, v)`` with q [n, nq, hd],
 k and v [n, nkv, hd] of the new tokens and gets [n, nq, hd].  Everything between the
-model's own operators is a library call on the current stream, without a host
-synchronisation.
+model's own operators is a library call on the current stream; a step (``feed``,
+``decode``, ``step``) has no host synchronisation.  What takes host lists (prompts,
+``extend``, ``score``, ``fork``, ``drop``) copies them to the device, and such a copy waits
+for the stream.
 
 ``python -m eagle_speculative_decoding_step_gb300.decode`` decodes with a small
 random model (``RandomModel``).

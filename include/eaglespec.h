@@ -629,12 +629,18 @@ size_t spec_chunk_attention_workspace_bytes(const spec_attn_desc *desc, int32_t 
  * cu_rows[B] on are left as they are.
  * q, out [n_rows, n_q_heads, head_dim] in desc->dtype, q_ld / out_ld elements from
  * one row to the next (0 = n_q_heads * head_dim); lse [n_rows, n_q_heads] fp32 or
- * NULL.  cu_rows [B + 1], seq_len [B].  max_chunk and max_len: upper bounds of a
- * request's new tokens and of seq_len, or 0 if unknown; they only choose how work
- * is laid out.  Any block_size; max_blocks * block_size < 2^30 (SPEC_ERR_SHAPE),
+ * NULL.  cu_rows [B + 1], seq_len [B].  max_chunk: an upper bound of a request's new
+ * tokens, or 0 if unknown; it only chooses how work is laid out (16-bit rows and
+ * cache).  max_len: reserved for a bound of seq_len, and not read but for its sign
+ * (0 or more).  Any block_size; max_blocks * block_size < 2^30 (SPEC_ERR_SHAPE),
  * n_rows * n_q_heads < 2^31 and n_q_heads * head_dim < 2^30 (SPEC_ERR_CAPACITY).
  * q, out, the cache and, with ld's, every row of q and out 16-byte aligned
  * (SPEC_ERR_ALIGN).  out does not overlap q or the cache.
+ * Scores, sums and softmax statistics are fp32.  A softmax weight enters the product
+ * with v in fp32 (F32 rows) or as one number of the rows' type: up to 2^-8 (BF16) or
+ * 2^-11 (F16) of it is lost, as of an output when it is rounded, and in F16 what is
+ * under 2^-34 of the largest; weights are summed before that.  spec_paged_attention
+ * keeps 2^-17 and better.
  * A score of +infinity or NaN, or one of -infinity, and a V value that is not finite
  * act as in spec_paged_attention, on the rows that attend to their key; other rows
  * are as they would be without.
@@ -715,8 +721,9 @@ size_t spec_block_state_workspace_bytes(int32_t B, int32_t num_blocks);
  * row_bytes: bytes of one slot of k (and of v) in each; block tables in kv are not
  * read.  1 <= n <= B <= 8192.  Error word: SPEC_ERR_DEVICE for a row outside [0, B),
  * a dst that is not empty or that an earlier fork named, a length out of range (these
- * forks are refused, without a block), or a block id out of range (its entry
- * becomes -1, nothing is copied for it). */
+ * forks are refused, without a block), or a block id out of range (the entry of a
+ * full block becomes -1, as one from the pool does; a partial block's is the pool's
+ * block all the same, with nothing copied to it). */
 spec_status spec_block_fork(const spec_block_state *st, int32_t n, const int32_t *src, const int32_t *dst,
                             int32_t n_layers, const spec_kv *kv, int32_t row_bytes,
                             void *ws, size_t ws_bytes, spec_stream_t stream);
