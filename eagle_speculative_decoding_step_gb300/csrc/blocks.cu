@@ -460,7 +460,7 @@ struct CopyArgs {
 
 // A block's slots are one piece of memory in each K and V: kPiece bytes of it a CTA at a
 // time, 8 vectors a thread under way.  Bound by the copy bandwidth (1.2 GB moved within
-// the cache: 390 us, 95 % of it).  Sources are never another move's target.
+// the cache: 390-403 us from one GPU to another, 91-94 % of it).  Sources are never another move's target.
 template <typename V> __global__ void __launch_bounds__(kCopyThreads) block_copy_kernel(const __grid_constant__ CopyArgs g) {
   SPEC_TL(kTLBlockCopy);
   pdl_wait();

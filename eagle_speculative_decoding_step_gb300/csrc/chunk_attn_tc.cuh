@@ -16,7 +16,8 @@
 // (1024 of MMA, 1400 with their waits).  128 rows x 128 keys x 128 components: 3060 cycles for
 // two jobs, of which the tensor pipe works 2048.  500 rows of 32 heads over 131071 keys 0.89-0.94 ms
 // (1.14-1.20 PFLOP/s, 59-62 % of a measured cuBLAS bf16 product; the SM clock stays near
-// 1.5 GHz under this load, as it does for cuBLAS), 16 chunks of 100-2048 tokens 0.93 ms.
+// 1.5 GHz under this load, as it does for cuBLAS), 16 chunks of 100-2048 tokens 0.92-0.95 ms from one GPU to another.
+// Spilled, bytes a thread: kTwoQ 92, kOneQ 292, kWide 48 over 16-bit caches, kTwoQ 362-386, kWide 132-156 over 8-bit ones.
 #pragma once
 #include <type_traits>
 
@@ -29,7 +30,7 @@ namespace ca {
 // kTwoQ: 256 rows, a warpgroup for each half, every K/V tile used twice (shared memory gives the tensor cores
 // 128 bytes a cycle: scores of 128 x 128 take all of it).  kOneQ: 128 rows, the warpgroups take turns at the
 // tiles with an accumulator each, joined at the end.  kWide: head sizes above 128, whose accumulator leaves no
-// room for a second one: 128 rows, tiles of 64 keys, one warpgroup (256 components: 780 TFLOP/s).
+// room for a second one: 128 rows, tiles of 64 keys, one warpgroup (256 components: 800 TFLOP/s).
 enum Mode { kTwoQ = 0, kOneQ = 1, kWide = 2 };
 
 constexpr int kTcThreads = 512;
@@ -262,7 +263,7 @@ struct TcSmem {
 // Keys come in runs of 16 slots by tensor copies where the block size allows: boxes of 16 slots x 128 bytes, no thread's
 // time.  Otherwise four warps copy a tile's rows in 16-byte pieces (cp.async): any block size, rows of any number of
 // pieces, and 512 bytes an instruction; an SM takes about 27 bytes a cycle that way (8 chunks of 512-1024 tokens, blocks of
-// 16 / 24 / 1 slots: 280 / 394 / 394 us).  U: pieces of a cache row, where that is 4, 8, 16 or 32 (a lane's piece and its step from row to row do
+// 16 / 24 / 1 slots: 280 / 386 / 387 us).  U: pieces of a cache row, where that is 4, 8, 16 or 32 (a lane's piece and its step from row to row do
 // not change then), or 0.
 template <int N> struct Units {
   const int n, inv;                    // 2^16 / n rounded up: quotients of numbers below 2^11 are exact
@@ -914,7 +915,10 @@ template <typename T, int MODE> SPEC_DEV void issue_mmas(const TcArgs& a, TcSmem
 // ---------------------------------------------------------------- softmax warpgroups
 // Weights are 2^(s - m + kShift) against a reference m, which follows the running maximum only when that has gone more
 // than kSlack past it: then the sums and outputs are rescaled, as they seldom are.  f16 weights stay below 2^15 and lose
-// what is under 2^-34 of the largest; bf16 has fp32's exponents.
+// what is under 2^-34 of the largest; bf16 has fp32's exponents.  A weight goes into the product with V as one 16-bit number,
+// rounded: 2^-8 (bf16) or 2^-11 of it is lost at most, as of an output by its own rounding, and what different keys lose does not
+// add up in one direction (against 64 bits 0.0021-0.0023 of the output, 0.0017 by its rounding alone; f16 0.00030 / 0.00021).  A second part
+// of each weight would be half as much tensor work again.  The sum l is of the weights as they were before.
 template <typename T> struct Weights {
   static constexpr bool kHalf = std::is_same_v<T, __half>;
   static constexpr float kShift = kHalf ? 10.f : 0.f, kSlack = kHalf ? 5.f : 8.f;
@@ -1097,7 +1101,7 @@ template <typename T, bool F8, int MODE> struct Softmax {
   // 16 components of the rows of a warp, a row a lane: two lanes exchange pieces of 16 bytes, so that a store writes 32 bytes
   // of each of 16 rows instead of 16 of each of 32 (8 chunks of 512-1024 tokens 287 -> 279 us, 32 of 100-300 tokens
   // 114 -> 109; four lanes, 64 bytes of 8 rows: as much, but 1-3 % more where items are long, from the code).  Not kOneQ,
-  // whose few rows are written sooner without (4 chunks of 8 tokens 15.4 / 16.1).
+  // whose few rows are written sooner without (4 chunks of 8 tokens 13.0 / 14.2).
   // at: the lane's piece of the pair's rows (NULL: not written).
   static SPEC_DEV void write_rows(T* const (&at)[2], int c, const float* o, float inv, bool odd) {
     uint32_t u[8];

@@ -18,7 +18,7 @@ enum : unsigned { kTLLogprobs = 30 };    // after the other units' ids
 
 constexpr int kResident = 1024;          // threads of an SM
 // Threads of a CTA.  More of them: fewer ends of parts, where the k best are found; fewer: their warps wait less for one
-// another.  2048 rows of 151936 fp32 logits, k = 20, 256 / 512: 267 / 246 us; of 32000 f16, k = 5: 62 / 72.
+// another.  When it was chosen, 2048 rows of 151936 fp32 logits, k = 20, 256 / 512: 267 / 246 us; of 32000 f16, k = 5: 62 / 72.
 template <typename T> constexpr int threads_of() { return sizeof(T) == 4 ? 512 : 256; }
 constexpr int kHits = 1024;              // threads of a few tiles that hold candidates
 constexpr int kMaxK = 32, kMaxV = 1 << 20;
@@ -238,8 +238,9 @@ template <int kThreads> SPEC_DEV void best_of(Smem& sm, int n, int k) {
 // are left, about k, are read again (from L2) and ranked by counting.  Where there are too many (logits in an order, or
 // mostly equal) the part is searched k times.  The last CTA of a row to finish joins the parts in their order (a counter,
 // nobody waits).
-// 2048 rows of 151936 fp32 logits: k = 0 208 us (91 % of the copy bandwidth), k = 20 233; bf16, 152 and 190 (13 instructions an
-// element, half of the issue slots' time); 64 rows of 128256 bf16, k = 5: 15 us, a chain of dependent trips.
+// 2048 rows of 151936 fp32 logits: k = 0 194-208 us (89-95 % of the copy bandwidth), k = 20 233; bf16, k = 0 and 5: 146 and 181 (13
+// instructions an element, half of the issue slots' time, 224-232 bytes a thread spilled at 64 registers; fp32: none); of 32000 f16,
+// k = 5: 52, mostly the ends of parts; 64 rows of 128256 bf16, k = 5: 15 us, a chain of dependent trips.
 template <typename T, int NV> __global__ void __launch_bounds__(threads_of<T>(), kResident / threads_of<T>())
     logprobs_kernel(const __grid_constant__ Args g) {
   SPEC_TL(kTLLogprobs);
