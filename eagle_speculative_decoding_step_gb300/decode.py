@@ -188,7 +188,7 @@ class Batch:
     A request that cannot take another token, because its table is full or the pool has no block for
     it, is ``stopped`` [B]: it keeps its blocks and length, its tokens are -1 from there on, and
     ``error`` says what was missing.  The others go on.  A request that has selected the end token gives
-    its blocks back with the next ``feed`` and goes on selecting that token; ``release`` ends all of them."""
+    its blocks back with the next ``feed``, ``extend`` or ``score`` and goes on selecting that token; ``release`` ends all of them."""
 
     def __init__(self, model, cache, B, max_len, vocab, eos=-1):
         self.model, self.cache, self.B = model, cache, B
@@ -354,7 +354,8 @@ class Batch:
             x[d] = torch.where(there[:, None], x[a], x[d])
 
     def drop(self, rows):
-        """Ends the requests of the given rows (a host list); blocks that no other row holds go back to the pool."""
+        """Ends the requests of the given rows (a host list); blocks that no other row holds go back to the pool.  What
+        ``decode`` says of such a row means nothing until it takes another request."""
         if not all(0 <= i < self.B for i in rows):
             raise ValueError("rows %s of %d" % (rows, self.B))
         which = torch.zeros(self.B, dtype=torch.int32, device=self.cache.device)
